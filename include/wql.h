@@ -81,8 +81,9 @@ const char* wql_last_error(void);
 int wql_version(void);
 
 /* Synchronises `stream`, then reports and clears the device-side error word of the current
- * device: WQL_ETIMEOUT if a kernel abandoned a bounded wait since the last check, WQL_ECUDA if
- * the synchronisation itself failed, WQL_OK otherwise. */
+ * device: WQL_ETIMEOUT if a kernel abandoned a bounded wait since the last check, WQL_EINVAL if
+ * none did but one met a page, slot or length out of range in device memory, WQL_ECUDA if the
+ * synchronisation itself failed, WQL_OK otherwise. */
 wql_status wql_device_status(void* stream);
 
 /* Diagnostic of the failure path: launches one thread that waits on an on-chip barrier which
@@ -336,6 +337,110 @@ wql_status wql_kv_quant_i8(const uint16_t* kv, int64_t rows, int D, int8_t* q, f
                            void* stream);
 wql_status wql_kv_dequant_i8(const int8_t* q, const float* scales, int64_t rows, int D,
                              uint16_t* out, void* stream);
+
+/* ========================================================================================
+ * Paged KV cache in 4 bits, and attention ([FastLLM] section 5.2 names int4 next to int8 for the
+ * cache and section 3 its pages; [AWQ] section 3 the paged attention.  The pages fix no format;
+ * the readings below are this library's).
+ *
+ * The cache is uint8 [pages, H, page_size / 16, 16 (D + 8)], H the K/V heads: blocks of 16 tokens
+ * of one head, each block
+ *     K codes [16, D / 2]   (channel 2i in the low half of byte i, channel 2i + 1 in the high)
+ *     V codes [16, D / 2]
+ *     K params [16] {fp16 s, fp16 lo}, V params [16] {fp16 s, fp16 lo}
+ * with value = code * s + lo.  Token slot n lies in page n / page_size, block (n % page_size) / 16,
+ * row n % 16.  D is 64 or 128 (WQL_EUNSUPPORTED otherwise); page_size is any multiple of 16;
+ * pages * page_size < 2^31 (the byte offsets may pass 2^32).
+ *
+ * Activations here are token-major with a stride: element (t, h, d) of q, k or v lies at
+ * t * stride + h * D + d, so that views of a fused QKV projection's output are taken as they are.
+ * Strides count elements, are multiples of 8 and at least heads * D.  Outputs are dense.
+ *
+ * Lengths, slots and page numbers are read on the device, so nothing is copied to the host and a
+ * captured call follows their contents.  One that is out of range is left out (see each entry) and
+ * recorded: the next wql_device_status() returns WQL_EINVAL once.
+ * ======================================================================================== */
+
+/* ----------------------------------------------------------------------------------------
+ * kv_plan_pages: block tables and slot maps from request lengths.  Request i holds ctx_lens[i]
+ * tokens in ceil(ctx_lens[i] / page_size) pages, listed in row i of block_table [B, table_width],
+ * and adds new_lens[i] tokens (negative lengths count as 0).  In request order it is given the
+ * pages it lacks from the end of the free list: with n = free_count[0] and `before` the pages that
+ * the requests before it lack, its k-th new page is free_pages[n - 1 - before - k], written
+ * behind the pages it holds.  Requests that exceed table_width pages, and those from the first one
+ * on that the free list cannot serve (except any that lack no page), are refused: they get none.
+ *     cu_new [B + 1]   exclusive sums of new_lens: the first new token of each request
+ *     kv_lens [B]      ctx_lens + new_lens; 0 for a refused request
+ *     slots [T]        slot of each new token, in the packed order of cu_new; -1 for tokens of
+ *                      refused requests and behind the last token (T may exceed cu_new[B]; tokens
+ *                      from T on get no slot)
+ *     free_count_out   [1]: pages left, which are free_pages[0 .. free_count_out - 1]
+ * Only the entries of new pages are written in block_table.  free_capacity is free_pages' size, and
+ * free_count is taken as at most that.  Repeating a call gives the same result.
+ * Requires B <= 4096, sum(new_lens) < 2^31, table_width * page_size < 2^31; slots 16-byte, the
+ * others 4-byte aligned; no output may overlap an input (block_table, read and written, aside).
+ * ---------------------------------------------------------------------------------------- */
+wql_status wql_kv_plan_pages(const int32_t* ctx_lens, const int32_t* new_lens, int B, int page_size,
+                             const int32_t* free_pages, int free_capacity, const int32_t* free_count,
+                             int32_t* block_table, int table_width, int T, int32_t* cu_new,
+                             int32_t* kv_lens, int32_t* slots, int32_t* free_count_out, void* stream);
+
+/* ----------------------------------------------------------------------------------------
+ * kv_append_i4: quantise rows k, v [T, H, D] fp16 into the cache at slots [T].  Per row x [D]:
+ *     lo = min x;  s = fp16((max x - lo) / 15)   (1.0 if that is zero)
+ *     code = clamp(round_half_even((x - lo) / s), 0, 15)
+ * Differences and quotients are the real ones, rounded once, so the cache is bit-exact with this
+ * definition.  A row that holds an infinity or a NaN gets s = lo = NaN and reads back as NaN.
+ * Negative slots are passed over (padding); slots behind the last page are left out and recorded.
+ * No slot may occur twice in a call: what such a slot then holds is unspecified.
+ * kv_read_i4: k, v [T, H, D] fp16 (dense) = fp16(code * s + lo) of the rows at slots, one rounding;
+ * zeros for negative slots and slots out of range.  A slot may occur any number of times.
+ * ---------------------------------------------------------------------------------------- */
+wql_status wql_kv_append_i4(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride,
+                            int T, int H, int D, const int32_t* slots, uint8_t* cache, int64_t pages,
+                            int page_size, void* stream);
+wql_status wql_kv_read_i4(const uint8_t* cache, int64_t pages, int page_size, int H, int D,
+                          const int32_t* slots, int T, uint16_t* k, uint16_t* v, void* stream);
+
+/* ----------------------------------------------------------------------------------------
+ * attention_kv_i4: attention of the last Lq tokens of each of B sequences over the cache.
+ * Sequence b has kv_lens[b] tokens (the Lq queried ones among them) in the pages of row b of
+ * block_table [B, table_width].  For row r < Lq and query head h, with k and v of K/V head
+ * h / (Hq / Hkv):
+ *     out[b, r, h] = sum_t softmax_t(scale * q[b, r, h] . k[t]) v[t],   t <= kv_lens[b] - Lq + r
+ * and zeros where no t is visible (kv_lens[b] = 0, or fewer tokens than rows).  q is [B * Lq, Hq,
+ * D] fp16 with q_stride, out [B, Lq, Hq, D] fp16, dense.  Lq = 1 is the decode step; more rows verify
+ * drafted tokens or run a chunk of a prompt over its cached beginning.
+ * Score and value sums are fp32; a weight times its token's s is rounded to fp16 for the product
+ * with the codes.  The result does not depend on what lies behind a sequence's last token.
+ * A length beyond table_width * page_size is cut there and recorded; a page number out of range
+ * among the pages in use is recorded, and the outputs of that sequence are then unspecified.
+ * workspace: device scratch of at least wql_attention_kv_i4_workspace_bytes(B, Lq, Hq, Hkv, D)
+ * bytes (the current device's), with no contents to keep; calls that may run at the same time
+ * need one each.  out must overlap no input.  Calls and results are deterministic.
+ * ---------------------------------------------------------------------------------------- */
+size_t wql_attention_kv_i4_workspace_bytes(int B, int Lq, int Hq, int Hkv, int D);
+wql_status wql_attention_kv_i4(const uint16_t* q, int64_t q_stride, int B, int Lq, int Hq, int Hkv,
+                               int D, const uint8_t* cache, int64_t pages, int page_size,
+                               const int32_t* block_table, int table_width, const int32_t* kv_lens,
+                               float scale, uint16_t* out, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* ----------------------------------------------------------------------------------------
+ * attention_prompt: causal attention over B packed prompts.  Sequence b is rows cu_seqlens[b] ..
+ * cu_seqlens[b + 1] - 1 of q [T, Hq, D], k and v [T, Hkv, D] (fp16, strided); for its row r and
+ * query head h, with k and v of K/V head h / (Hq / Hkv):
+ *     out[r, h] = sum_{j <= r} softmax_j(scale * q[r, h] . k[j]) v[j]
+ * out [T, Hq, D] fp16, dense; rows of no sequence are left as they were.  cu_seqlens [B + 1]: a
+ * sequence with a negative start, a negative length or an end beyond T is left out and recorded.
+ * Sums are fp32, weights fp16.  A row depends on nothing but the rows up to it of its sequence: an
+ * infinity or a NaN elsewhere does not reach it; one in v that it does see makes that channel of
+ * it infinite or NaN.  No workspace.  Requires Hq <= 65535; out must overlap no input.
+ * ---------------------------------------------------------------------------------------- */
+wql_status wql_attention_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                                int64_t k_stride, const uint16_t* v, int64_t v_stride, int T, int Hq,
+                                int Hkv, int D, const int32_t* cu_seqlens, int B, float scale,
+                                uint16_t* out, void* stream);
 
 #ifdef __cplusplus
 }

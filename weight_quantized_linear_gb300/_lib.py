@@ -22,6 +22,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+_I64 = ctypes.c_int64
 
 # name -> (restype, argtypes); this list is also what the export test checks against wql.h
 SIGNATURES = {
@@ -52,6 +53,12 @@ SIGNATURES = {
     "wql_w8a8_gemm_fp8": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
     "wql_kv_quant_i8": (_I, [_P, ctypes.c_int64, _I, _P, _P, _P]),
     "wql_kv_dequant_i8": (_I, [_P, _P, ctypes.c_int64, _I, _P, _P]),
+    "wql_kv_plan_pages": (_I, [_P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P]),
+    "wql_kv_append_i4": (_I, [_P, _P, _I64, _I64, _I, _I, _I, _P, _P, _I64, _I, _P]),
+    "wql_kv_read_i4": (_I, [_P, _I64, _I, _I, _I, _P, _I, _P, _P, _P]),
+    "wql_attention_kv_i4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "wql_attention_kv_i4": (_I, [_P, _I64, _I, _I, _I, _I, _I, _P, _I64, _I, _P, _I, _P, _F, _P, _P, _SZ, _P]),
+    "wql_attention_prompt": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I, _F, _P, _P]),
 }
 
 _lock = threading.Lock()
@@ -496,4 +503,177 @@ def kv_dequant_i8(q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | Non
         out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
     _need(out, "out", torch.float16, tuple(q.shape))
     _check(load().wql_kv_dequant_i8(_ptr(q), _ptr(scales), rows, D, _ptr(out), _stream(q.device)), "wql_kv_dequant_i8")
+    return out
+
+
+# ---- paged KV cache in 4 bits, and attention -----------------------------------------------------
+
+def _rows(t: torch.Tensor, name: str, heads: int | None = None, dim: int | None = None) -> int:
+    """Check an fp16 CUDA tensor [T, heads, D] whose rows [heads, D] are dense (a view of a fused projection's
+    output); returns its token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must have dtype {torch.float16}, got {t.dtype}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name} must have shape [tokens, {heads or 'heads'}, {dim or 'D'}], got {tuple(t.shape)}")
+    T, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} must be dense within a token (strides [any, {D}, 1], got {tuple(t.stride())})")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _cache_dims(cache: torch.Tensor):
+    """(pages, heads, page size, D) of a 4-bit cache."""
+    if not isinstance(cache, torch.Tensor):
+        raise TypeError("cache must be a torch.Tensor")
+    if cache.dim() != 4 or cache.shape[3] % 16 != 0:
+        raise ValueError("cache must be [pages, heads, page_size / 16, 16 (D + 8)]; see kv_cache_i4")
+    _need(cache, "cache", torch.uint8, tuple(cache.shape))
+    pages, H, blocks, nbytes = cache.shape
+    return pages, H, 16 * blocks, nbytes // 16 - 8
+
+
+def _same_device(ref: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+
+
+def kv_cache_i4(pages: int, heads: int, head_dim: int, page_size: int, device=None) -> torch.Tensor:
+    """A zeroed 4-bit KV cache, uint8 [pages, heads, page_size / 16, 16 (head_dim + 8)]."""
+    if head_dim not in (64, 128):
+        raise ValueError("head_dim must be 64 or 128")
+    if page_size < 16 or page_size % 16:
+        raise ValueError("page_size must be a positive multiple of 16")
+    return torch.zeros((pages, heads, page_size // 16, 16 * (head_dim + 8)), dtype=torch.uint8, device=device or "cuda")
+
+
+def kv_plan_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                  free_count: torch.Tensor, page_size: int, tokens: int):
+    """Block tables and slot maps on the GPU: gives every request the pages it lacks for its new tokens.
+
+    ctx_lens, new_lens [B] int32 (tokens held, tokens added); block_table [B, width] int32, whose entries of new
+    pages are written in place; free_pages [F] int32 with free_count [1] int32 of them free.  Returns (slots
+    [tokens], cu_new [B + 1], kv_lens [B], free_count_out [1]), int32; slots behind the last new token and those of
+    refused requests are -1, kv_lens of refused requests 0.  See wql_kv_plan_pages in include/wql.h."""
+    B = ctx_lens.shape[0]
+    _need(ctx_lens, "ctx_lens", torch.int32, (B,))
+    _need(new_lens, "new_lens", torch.int32, (B,))
+    width = block_table.shape[-1]
+    _need(block_table, "block_table", torch.int32, (B, width))
+    F = free_pages.shape[0]
+    _need(free_pages, "free_pages", torch.int32, (F,))
+    _need(free_count, "free_count", torch.int32, (1,))
+    dev = ctx_lens.device
+    _same_device(ctx_lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages, free_count=free_count)
+    # one allocation: slots first (its start is 16-byte aligned), then the small outputs
+    out = torch.empty((tokens + 2 * B + 2,), dtype=torch.int32, device=dev)
+    slots, cu_new = out[:tokens], out[tokens:tokens + B + 1]
+    kv_lens, left = out[tokens + B + 1:tokens + 2 * B + 1], out[tokens + 2 * B + 1:]
+    with torch.cuda.device(dev):
+        _check(load().wql_kv_plan_pages(_ptr(ctx_lens), _ptr(new_lens), B, page_size, _ptr(free_pages), F,
+                                        _ptr(free_count), _ptr(block_table), width, tokens, _ptr(cu_new),
+                                        _ptr(kv_lens), _ptr(slots), _ptr(left), _stream(dev)), "wql_kv_plan_pages")
+    return slots, cu_new, kv_lens, left
+
+
+def kv_append_i4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor) -> torch.Tensor:
+    """Quantise rows k, v [T, heads, D] fp16 (views of a fused QKV output are taken as they are) into the 4-bit
+    cache at slots [T] int32; negative slots are passed over.  Returns cache."""
+    pages, H, ps, D = _cache_dims(cache)
+    T = k.shape[0]
+    ks, vs = _rows(k, "k", H, D), _rows(v, "v", H, D)
+    if v.shape[0] != T:
+        raise ValueError(f"v must have {T} tokens, got {v.shape[0]}")
+    _need(slots, "slots", torch.int32, (T,))
+    _same_device(cache, k=k, v=v, slots=slots)
+    with torch.cuda.device(cache.device):
+        _check(load().wql_kv_append_i4(_ptr(k), _ptr(v), ks, vs, T, H, D, _ptr(slots), _ptr(cache), pages, ps,
+                                       _stream(cache.device)), "wql_kv_append_i4")
+    return cache
+
+
+def kv_read_i4(cache: torch.Tensor, slots: torch.Tensor, k: torch.Tensor | None = None,
+               v: torch.Tensor | None = None):
+    """(k, v) [T, heads, D] fp16: the values of the 4-bit cache at slots [T] int32; zeros for negative slots."""
+    pages, H, ps, D = _cache_dims(cache)
+    T = slots.shape[0]
+    _need(slots, "slots", torch.int32, (T,))
+    if k is None:
+        k = torch.empty((T, H, D), dtype=torch.float16, device=cache.device)
+    if v is None:
+        v = torch.empty((T, H, D), dtype=torch.float16, device=cache.device)
+    _need(k, "k", torch.float16, (T, H, D))
+    _need(v, "v", torch.float16, (T, H, D))
+    _same_device(cache, k=k, v=v, slots=slots)
+    with torch.cuda.device(cache.device):
+        _check(load().wql_kv_read_i4(_ptr(cache), pages, ps, H, D, _ptr(slots), T, _ptr(k), _ptr(v),
+                                     _stream(cache.device)), "wql_kv_read_i4")
+    return k, v
+
+
+def attention_kv_i4_workspace_bytes(B: int, Lq: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load().wql_attention_kv_i4_workspace_bytes(B, Lq, Hq, Hkv, D))
+
+
+def attention_kv_i4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                    scale: float | None = None, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the last tokens of each sequence over the paged 4-bit cache, grouped heads.
+
+    q [B, Hq, D] (one token each) or [B, Lq, Hq, D] fp16, its tokens evenly strided; block_table [B, width] and
+    kv_lens [B] int32, the queried tokens counted in.  Row r of Lq sees the tokens up to kv_lens - Lq + r; a row that
+    sees none is zero.  scale defaults to D ** -0.5.  Returns out, dense, of q's shape."""
+    pages, Hkv, ps, D = _cache_dims(cache)
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be a tensor [B, Hq, D] or [B, Lq, Hq, D]")
+    B, Lq, Hq = q.shape[0], 1 if q.dim() == 3 else q.shape[1], q.shape[-2]
+    if q.dim() == 4 and B > 1 and Lq > 1 and q.stride(0) != Lq * q.stride(1):
+        raise ValueError("the tokens of q must be evenly strided")
+    rows = q if q.dim() == 3 else q[:, 0] if Lq == 1 else q.as_strided((B * Lq, Hq, q.shape[-1]), q.stride()[1:])
+    qs = _rows(rows, "q", None, D)
+    width = block_table.shape[-1]
+    _need(block_table, "block_table", torch.int32, (B, width))
+    _need(kv_lens, "kv_lens", torch.int32, (B,))
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+    _need(out, "out", torch.float16, tuple(q.shape))
+    _same_device(cache, q=q, block_table=block_table, kv_lens=kv_lens, out=out)
+    with torch.cuda.device(cache.device):
+        if workspace is None:
+            workspace = torch.empty((attention_kv_i4_workspace_bytes(B, Lq, Hq, Hkv, D),), dtype=torch.uint8,
+                                    device=q.device)
+        _same_device(cache, workspace=workspace)
+        _check(load().wql_attention_kv_i4(_ptr(q), qs, B, Lq, Hq, Hkv, D, _ptr(cache), pages, ps, _ptr(block_table),
+                                          width, _ptr(kv_lens), D ** -0.5 if scale is None else scale, _ptr(out),
+                                          _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                          _stream(cache.device)), "wql_attention_kv_i4")
+    return out
+
+
+def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     scale: float | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention over packed prompts, grouped heads: q [T, Hq, D], k and v [T, Hkv, D] fp16 (views of a fused
+    QKV output are taken as they are), cu_seqlens [B + 1] int32.  scale defaults to D ** -0.5.  Returns out
+    [T, Hq, D], dense; rows of no sequence are left as they were (undefined when out is not given)."""
+    qs = _rows(q, "q")
+    T, Hq, D = q.shape
+    ks = _rows(k, "k", None, D)
+    Hkv = k.shape[1]
+    vs = _rows(v, "v", Hkv, D)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"k and v must have {T} tokens, got {k.shape[0]} and {v.shape[0]}")
+    B = cu_seqlens.shape[0] - 1
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.float16, device=q.device)
+    _need(out, "out", torch.float16, (T, Hq, D))
+    _same_device(q, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
+    with torch.cuda.device(q.device):
+        _check(load().wql_attention_prompt(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, T, Hq, Hkv, D, _ptr(cu_seqlens), B,
+                                           D ** -0.5 if scale is None else scale, _ptr(out), _stream(q.device)),
+               "wql_attention_prompt")
     return out

@@ -1,6 +1,8 @@
 // api.cu -- the extern "C" entry points declared in include/wql.h: argument validation, kernel
 // selection by shape, launch-error reporting and the per-device error word of bounded waits.
 #include <atomic>
+#include <climits>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -105,6 +107,8 @@ wql_status wql_device_status(void* stream) {
   if (v != 0) {
     const unsigned zero = 0;
     cudaMemcpy(w, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    if (v == wql::kErrBadIndex)
+      return fail(WQL_EINVAL, "a kernel met a page, slot or length out of range and left it out");
     char buf[96];
     snprintf(buf, sizeof(buf), "a kernel abandoned a bounded wait (error bits 0x%x)", v);
     return fail(WQL_ETIMEOUT, buf);
@@ -452,6 +456,159 @@ wql_status wql_kv_dequant_i8(const int8_t* q, const float* scales, int64_t rows,
               "scales must be a 4-byte aligned device pointer");
   return cuda_status(wql::launch_kv_dequant_i8(q, scales, rows, D, out, static_cast<cudaStream_t>(stream)),
                      "wql_kv_dequant_i8");
+}
+
+namespace {
+
+bool kv_head_dim(int D) { return D == 64 || D == 128; }
+
+// Rows [T, H, D] with `stride` elements between tokens, loaded 16 bytes at a time.
+bool valid_stride(int64_t stride, int H, int D) { return stride >= (int64_t)H * D && stride % 8 == 0; }
+
+#define WQL_REQUIRE_PTR4(p) \
+  WQL_REQUIRE((p) != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0, #p " must be a non-null 4-byte aligned device pointer")
+
+#define WQL_REQUIRE_CACHE()                                                                                        \
+  do {                                                                                                             \
+    if (!kv_head_dim(D)) return fail(WQL_EUNSUPPORTED, "D must be 64 or 128");                                     \
+    WQL_REQUIRE(page_size >= 16 && page_size % 16 == 0, "page_size must be a positive multiple of 16");            \
+    WQL_REQUIRE(pages >= 1 && pages * page_size <= INT_MAX, "pages * page_size must be between 16 and 2^31 - 1");  \
+  } while (0)
+
+}  // namespace
+
+wql_status wql_kv_plan_pages(const int32_t* ctx_lens, const int32_t* new_lens, int B, int page_size,
+                             const int32_t* free_pages, int free_capacity, const int32_t* free_count,
+                             int32_t* block_table, int table_width, int T, int32_t* cu_new, int32_t* kv_lens,
+                             int32_t* slots, int32_t* free_count_out, void* stream) {
+  WQL_REQUIRE(B >= 0 && T >= 0, "B and T must be >= 0");
+  if (B > wql::kPlanMaxB) return fail(WQL_EUNSUPPORTED, "B must be at most 4096");
+  WQL_REQUIRE(page_size >= 16 && page_size % 16 == 0, "page_size must be a positive multiple of 16");
+  WQL_REQUIRE(table_width >= 1 && (int64_t)table_width * page_size <= INT_MAX,
+              "table_width * page_size must be between 16 and 2^31 - 1");
+  WQL_REQUIRE(free_capacity >= 0, "free_capacity must be >= 0");
+  WQL_REQUIRE_PTR4(free_count);
+  WQL_REQUIRE_PTR4(free_count_out);
+  WQL_REQUIRE(free_count != free_count_out, "free_count_out must not be free_count");
+  WQL_REQUIRE_PTR4(cu_new);
+  WQL_REQUIRE(T == 0 || (slots != nullptr && aligned16(slots)), "slots must be a non-null 16-byte aligned device pointer");
+  WQL_REQUIRE(free_capacity == 0 || free_pages != nullptr, "free_pages must not be null");
+  if (B > 0) {
+    WQL_REQUIRE_PTR4(ctx_lens);
+    WQL_REQUIRE_PTR4(new_lens);
+    WQL_REQUIRE_PTR4(block_table);
+    WQL_REQUIRE_PTR4(kv_lens);
+  }
+  return cuda_status(wql::launch_kv_plan(ctx_lens, new_lens, B, page_size, free_pages, free_capacity, free_count,
+                                         block_table, table_width, T, cu_new, kv_lens, slots, free_count_out,
+                                         static_cast<cudaStream_t>(stream)),
+                     "wql_kv_plan_pages");
+}
+
+wql_status wql_kv_append_i4(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int T, int H,
+                            int D, const int32_t* slots, uint8_t* cache, int64_t pages, int page_size, void* stream) {
+  WQL_REQUIRE(T >= 0, "T must be >= 0");
+  WQL_REQUIRE(H >= 1, "H must be >= 1");
+  WQL_REQUIRE_CACHE();
+  if (T == 0) {
+    g_last_error.clear();
+    return WQL_OK;
+  }
+  WQL_REQUIRE_PTR(k);
+  WQL_REQUIRE_PTR(v);
+  WQL_REQUIRE(valid_stride(k_stride, H, D) && valid_stride(v_stride, H, D),
+              "token strides must be multiples of 8 and at least H * D");
+  WQL_REQUIRE_PTR4(slots);
+  WQL_REQUIRE_PTR(cache);
+  unsigned* dev_err = device_error_word();
+  if (!dev_err) return fail(WQL_ECUDA, "wql_kv_append_i4: cannot locate the device error word");
+  return cuda_status(wql::launch_kv_append_i4(k, v, k_stride, v_stride, T, H, D, slots, cache, pages, page_size, dev_err,
+                                              static_cast<cudaStream_t>(stream)),
+                     "wql_kv_append_i4");
+}
+
+wql_status wql_kv_read_i4(const uint8_t* cache, int64_t pages, int page_size, int H, int D, const int32_t* slots, int T,
+                          uint16_t* k, uint16_t* v, void* stream) {
+  WQL_REQUIRE(T >= 0, "T must be >= 0");
+  WQL_REQUIRE(H >= 1, "H must be >= 1");
+  WQL_REQUIRE_CACHE();
+  if (T == 0) {
+    g_last_error.clear();
+    return WQL_OK;
+  }
+  WQL_REQUIRE_PTR(cache);
+  WQL_REQUIRE_PTR4(slots);
+  WQL_REQUIRE_PTR(k);
+  WQL_REQUIRE_PTR(v);
+  unsigned* dev_err = device_error_word();
+  if (!dev_err) return fail(WQL_ECUDA, "wql_kv_read_i4: cannot locate the device error word");
+  return cuda_status(wql::launch_kv_read_i4(cache, pages, page_size, H, D, slots, T, k, v, dev_err,
+                                            static_cast<cudaStream_t>(stream)),
+                     "wql_kv_read_i4");
+}
+
+size_t wql_attention_kv_i4_workspace_bytes(int B, int Lq, int Hq, int Hkv, int D) {
+  if (B < 1 || Lq < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !kv_head_dim(D)) return 0;
+  return wql::attn_kv_i4_workspace_bytes(B, Lq, Hq, Hkv, D);
+}
+
+wql_status wql_attention_kv_i4(const uint16_t* q, int64_t q_stride, int B, int Lq, int Hq, int Hkv, int D,
+                               const uint8_t* cache, int64_t pages, int page_size, const int32_t* block_table,
+                               int table_width, const int32_t* kv_lens, float scale, uint16_t* out, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  WQL_REQUIRE(B >= 0 && Lq >= 0, "B and Lq must be >= 0");
+  WQL_REQUIRE(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0, "Hq must be a positive multiple of Hkv");
+  WQL_REQUIRE_CACHE();
+  WQL_REQUIRE(table_width >= 1 && (int64_t)table_width * page_size <= INT_MAX,
+              "table_width * page_size must be between 16 and 2^31 - 1");
+  WQL_REQUIRE((int64_t)Lq * Hq <= INT_MAX / 256, "Lq * Hq is too large");
+  WQL_REQUIRE(std::isfinite(scale), "scale must be finite");
+  if (B == 0 || Lq == 0) {
+    g_last_error.clear();
+    return WQL_OK;
+  }
+  WQL_REQUIRE_PTR(q);
+  WQL_REQUIRE(valid_stride(q_stride, Hq, D), "the token stride of q must be a multiple of 8 and at least Hq * D");
+  WQL_REQUIRE_PTR(cache);
+  WQL_REQUIRE_PTR4(block_table);
+  WQL_REQUIRE_PTR4(kv_lens);
+  WQL_REQUIRE_PTR(out);
+  WQL_REQUIRE_PTR(workspace);
+  WQL_REQUIRE(workspace_bytes >= wql::attn_kv_i4_workspace_bytes(B, Lq, Hq, Hkv, D),
+              "workspace is smaller than wql_attention_kv_i4_workspace_bytes");
+  unsigned* dev_err = device_error_word();
+  if (!dev_err) return fail(WQL_ECUDA, "wql_attention_kv_i4: cannot locate the device error word");
+  return cuda_status(wql::launch_attn_kv_i4(q, q_stride, B, Lq, Hq, Hkv, D, cache, pages, page_size, block_table,
+                                            table_width, kv_lens, scale, out, workspace, dev_err,
+                                            static_cast<cudaStream_t>(stream)),
+                     "wql_attention_kv_i4");
+}
+
+wql_status wql_attention_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                const uint16_t* v, int64_t v_stride, int T, int Hq, int Hkv, int D,
+                                const int32_t* cu_seqlens, int B, float scale, uint16_t* out, void* stream) {
+  WQL_REQUIRE(T >= 0 && B >= 0, "T and B must be >= 0");
+  WQL_REQUIRE(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0, "Hq must be a positive multiple of Hkv");
+  if (!kv_head_dim(D)) return fail(WQL_EUNSUPPORTED, "D must be 64 or 128");
+  if (Hq > 65535) return fail(WQL_EUNSUPPORTED, "Hq must be at most 65535");
+  WQL_REQUIRE(std::isfinite(scale), "scale must be finite");
+  if (T == 0 || B == 0) {
+    g_last_error.clear();
+    return WQL_OK;
+  }
+  WQL_REQUIRE_PTR(q);
+  WQL_REQUIRE_PTR(k);
+  WQL_REQUIRE_PTR(v);
+  WQL_REQUIRE(valid_stride(q_stride, Hq, D) && valid_stride(k_stride, Hkv, D) && valid_stride(v_stride, Hkv, D),
+              "token strides must be multiples of 8 and at least heads * D");
+  WQL_REQUIRE_PTR4(cu_seqlens);
+  WQL_REQUIRE_PTR(out);
+  unsigned* dev_err = device_error_word();
+  if (!dev_err) return fail(WQL_ECUDA, "wql_attention_prompt: cannot locate the device error word");
+  std::string err;
+  cudaError_t e = wql::launch_attn_prompt(q, q_stride, k, k_stride, v, v_stride, T, Hq, Hkv, D, cu_seqlens, B, scale, out,
+                                          dev_err, static_cast<cudaStream_t>(stream), &err);
+  return cuda_status(e, "wql_attention_prompt", err);
 }
 
 wql_status wql_diag_expire_wait(void* stream) {

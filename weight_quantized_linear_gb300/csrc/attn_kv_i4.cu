@@ -1,0 +1,753 @@
+// attn_kv_i4.cu -- attention of the last Lq tokens of each sequence over the paged 4-bit KV cache, with
+// grouped heads: o = softmax(scale q k^T) v, k and v = code * s + lo, keys t <= len - Lq + r for row r.
+//
+// A unit of work is one (sequence, K/V head, block of 8 NT query rows); the rows of a K/V head are its
+// Lq * G (token, query head) pairs, so a K/V head's cache is read once for all the query heads it serves.
+// Units are cut into steps of 32 tokens.  The steps of all units, in order, are divided evenly over the
+// CTAs (one per SM), whatever the lengths, and a CTA's steps evenly over its warps, each a run of its own.  One
+// more warp requests the copies: its lane w keeps warp w's ring of steps filled, across unit boundaries, so that no
+// warp waits for another while streaming and a short unit costs no synchronisation.  A warp writes a unit that lies in
+// its run; parts of units that span warps are joined in shared memory at the CTA's end, and those that span CTAs are
+// left in the workspace, where a second, small kernel joins them in a fixed order.
+//
+// Mathematics.  Scores: sum_c q_c (code_c s + lo) = s sum_c q_c code_c + lo sum_c q_c, so the matrix product
+// runs on the codes.  Masking a nibble in place makes it an fp16 number without any conversion: a code in
+// bits 0-3 is the subnormal code * 2^-24 and in bits 4-7 code * 2^-20, exactly; the products of the two
+// kinds are kept in two accumulators (or, for V, in different output rows) and scaled apart at the end.
+// Values: sum_t p_t (s_t code_t + lo_t) = sum_t (p_t s_t) code_t + sum_t p_t lo_t, with w_t = p_t s_t as the
+// fp16 weight of the second matrix product and the last sum in fp32.  The running maximum m is that of
+// score + log2 s, i.e. of w itself, so the weights use fp16's range however the scales differ between
+// tokens; m is raised only when a weight would pass 2^15 (the rescaling is skipped while it is idle).
+// What all the codes of a token share is kept out of the sums, which would otherwise grow to hundreds of times the
+// result of a long context and carry their truncation and that of the weights with them.  Every second token enters
+// the product as 15 - code with the weight -w, so that the accumulators stay small; and with w' the rounded, signed
+// weights, 7.5 sum_t w'_t is taken off at the end (one more product, with a matrix of ones, gives that sum where it is
+// needed) while p_t (lo_t + 7.5 s_t) goes to the fp32 sum: a weight's rounding then meets code - 7.5.
+//
+// mma.sync, not tcgen05: operands come out of registers after the unpacking, 8 rows (the query heads of a K/V
+// head) are the narrow side, and a 16-token block needs 16 products of 16 x 8 x 16, which the SM does in a
+// third of the time in which HBM delivers the block.
+#include <atomic>
+#include <climits>
+#include <type_traits>
+
+#include "internal.h"
+#include "kv_i4.cuh"
+#include "tcgen05.cuh"
+
+namespace wql {
+namespace {
+
+constexpr int kStep = 32;                       // tokens per step
+constexpr float kNoMax = -1e30f;                // maximum of nothing
+// Weights are kept below 2^15: at each raise of m the largest becomes 2^7, so that those down to 2^-21 of it are normal
+// fp16 numbers.
+constexpr float kTop = 7.0f, kRaise = 15.0f;
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kWarps = NT == 1 ? 12 : 7;
+  static constexpr int kThreads = 32 * (kWarps + 1);  // and the warp that requests the copies
+  static constexpr int kStepBytes = kStep / kKvBlock * KvI4<D>::kBytes;
+  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kJoinPitch = D + 4;                                  // floats per row of the join buffer
+  static constexpr int kOffJoin = kWarps * kStages * kStepBytes;            // [kWarps][kRows][kJoinPitch] fp32: first parts
+  static constexpr int kOffMl = kOffJoin + kWarps * kRows * kJoinPitch * 4; // [2][kWarps][kRows] {m, l}: first parts, last parts
+  static constexpr int kOffBar = kOffMl + 2 * kWarps * kRows * 8;              // [2][kWarps][kStages] mbarriers: full, empty
+  static_assert(kRows * kJoinPitch * 4 <= kStages * kStepBytes, "a last part takes the warp's ring");
+  static constexpr int kSmem = kOffBar + 2 * kWarps * kStages * 8;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).  Not volatile, unlike its namesake: the products of a step's
+// two blocks may be interleaved.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Division by a number known at launch: n / d for 0 <= n < 2^31 (Granlund and Montgomery's multiplier with l = ceil(log2 d)).
+struct FastDiv {
+  uint32_t d, m, l;
+};
+FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return {d, (uint32_t)((((1ull << l) - d) << 32) / d + 1), l};
+}
+__device__ __forceinline__ uint32_t quot(uint32_t n, const FastDiv& f) { return (__umulhi(n, f.m) + n) >> f.l; }
+
+__device__ __forceinline__ float2 h2f2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+
+// Copy of `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+struct Args {
+  const __half* q;
+  long long q_stride;
+  int B, Lq, Hq, Hkv, G, RB;  // RB: row blocks per K/V head
+  const uint8_t* cache;
+  int pages, ps;
+  const int* table;
+  int width;
+  const int* kv_lens;
+  float scale_log2;
+  FastDiv bpp, rb;  // blocks per page, row blocks per head
+  __half* out;
+  float* part;  // [gridDim][2][kRows][D + 2]: O, m, l of the units that end (0) and go on (1) behind the CTA's range
+  int4* job;    // [gridDim]: {sequence, head and row block, first CTA, last CTA} of a unit to join; sequence -1: none
+  unsigned* err;
+};
+
+__device__ __forceinline__ int seq_len(const Args& a, int b) {
+  const int n = a.kv_lens[b];
+  return n <= 0 ? 0 : (int)min((long long)n, (long long)a.width * a.ps);
+}
+__device__ __forceinline__ int seq_steps(const Args& a, int b) { return (seq_len(a, b) + kStep - 1) / kStep; }
+
+// Position in the order of all steps: unit (b, hr = head * RB + row block), step s of `n` of that unit.
+struct Cursor {
+  int b, hr, s, n;
+};
+__device__ __forceinline__ void advance(const Args& a, Cursor& c, int by) {
+  c.s += by;
+  while (c.s >= c.n) {
+    c.s -= c.n;
+    if (++c.hr == a.Hkv * a.RB) {
+      c.hr = 0;
+      do {
+        if (++c.b >= a.B) {
+          c.n = INT_MAX;  // past the end: nothing is read there
+          return;
+        }
+        c.n = seq_steps(a, c.b);
+      } while (c.n == 0);
+    }
+  }
+}
+
+// The token (of 16) that row r of an 8 x 8 block of weights stands for; K's rows, V's reduction index and the
+// params all use it.  Chosen so that the shared-memory loads of K and V hit every bank once.
+template <int D>
+__device__ __forceinline__ int token_of(int r) {
+  const int c = r >> 1, e = r & 1;
+  return 2 * c + (e ^ (D == 128 ? (c & 1) : (c >> 1)));
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(const Args a) {
+  using C = Cfg<D, NT>;
+  using L = KvI4<D>;
+  constexpr int kW = C::kWarps, kS = C::kStages;
+  constexpr int kKw = D / 32;  // words of K codes per thread and token
+  constexpr int kMt = D / 16;  // 16-channel tiles of the output
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* join = reinterpret_cast<float*>(smem + C::kOffJoin);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  __shared__ long long s_sum[kW + 1];
+  __shared__ long long s_total;
+  __shared__ int4 s_start;
+  __shared__ int4 s_first[kW], s_last[kW];  // {sequence, head and row block, ends here / -, exists} of the warps' parts
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+
+  for (int i = tid; i < 2 * kW * kS; i += C::kThreads) mbar_init(&bars[i], 1);
+  fence_mbarrier_init();
+  grid_dependents_launch();
+
+  // ---- this CTA's range [n0, n1) of the order of all steps -----------------------------------
+  const int per = (a.B + C::kThreads - 1) / C::kThreads;
+  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  const int hr_all = a.Hkv * a.RB;
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = a.kv_lens[b];
+    if (n > 0 && n > (long long)a.width * a.ps) report_error(a.err, kErrBadIndex);
+    mine += (long long)seq_steps(a, b) * hr_all;
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) incl += s_sum[w];
+  if (tid == C::kThreads - 1) s_total = incl;
+  __syncthreads();
+  const long long total = s_total;
+  // at least one step for every warp of a CTA: a short batch uses fewer CTAs and has fewer parts to join
+  long long quota = (total + gridDim.x - 1) / gridDim.x;
+  if (quota < kW) quota = kW;
+  const long long n0 = min(quota * blockIdx.x, total), n1 = min(n0 + quota, total);
+  {
+    long long first = incl - mine;
+    if (n0 < n1 && first <= n0 && n0 < incl)
+      for (int b = b0; b < b1; ++b) {
+        const long long n = seq_steps(a, b);
+        if (n0 < first + n * hr_all) {
+          s_start = make_int4(b, (int)((n0 - first) / n), (int)((n0 - first) % n), (int)n);
+          break;
+        }
+        first += n * hr_all;
+      }
+  }
+  __syncthreads();
+
+  // rows of sequences without any token: zeros
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+    if (seq_len(a, b) == 0)
+      for (int i = tid; i < a.Lq * a.Hq * (D / 8); i += C::kThreads)
+        reinterpret_cast<uint4*>(a.out)[(long long)b * a.Lq * a.Hq * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
+
+  if (n0 >= n1) {
+    if (tid == 0) a.job[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+
+  // warp w's run of steps is [run(w), run(w + 1))
+  const long long quota_w = (n1 - n0 + kW - 1) / kW;
+  auto run = [&](int w) { return min(n0 + quota_w * w, n1); };
+
+  // ---- the warp that requests: lane w keeps warp w's ring filled ---------------------------------
+  if (warp == kW) {
+    if (lane < kW) {
+    const int bpp = (int)a.bpp.d;
+    const uint32_t ring = smem_u32(smem) + lane * kS * C::kStepBytes;
+    uint64_t* full = bars + lane * kS;
+    uint64_t* empty = bars + (kW + lane) * kS;
+    Cursor pc{s_start.x, s_start.y, s_start.z, s_start.w};
+    long long pn = run(lane);  // next step to request
+    const long long pn1 = run(lane + 1);
+    if (pn < pn1) advance(a, pc, (int)(pn - n0));
+    int slot = 0, pg0 = 0, pg1 = 0, blk = 0, col0 = 0, last = 0;
+    uint32_t parity = 1;  // the first round finds every stage free
+    auto look_up = [&]() {  // the pages of the two blocks of the step at pc
+      blk = pc.s * (kStep / kKvBlock);
+      last = (seq_len(a, pc.b) - 1) / kKvBlock;
+      col0 = (int)quot(blk, a.bpp);
+      const int* row = a.table + (long long)pc.b * a.width;
+      pg0 = row[col0];
+      pg1 = blk < last ? row[quot(blk + 1, a.bpp)] : pg0;
+    };
+    if (pn < pn1) look_up();
+    unsigned long long since = globaltimer_ns();
+    while (pn < pn1) {
+      if (!mbar_try_wait(&empty[slot], parity)) {
+        if (globaltimer_ns() - since > kWaitLimitNs) {
+          report_error(a.err, kErrTimeoutEmpty);
+          break;
+        }
+        continue;
+      }
+      if ((unsigned)pg0 >= (unsigned)a.pages || (unsigned)pg1 >= (unsigned)a.pages) {
+        report_error(a.err, kErrBadIndex);
+        if ((unsigned)pg0 >= (unsigned)a.pages) pg0 = 0;
+        if ((unsigned)pg1 >= (unsigned)a.pages) pg1 = 0;
+      }
+      const int head = (int)quot(pc.hr, a.rb), in0 = blk - col0 * bpp, in1 = in0 + 1 < bpp ? in0 + 1 : 0;
+      const bool two = blk < last;
+      const uint32_t dst = ring + slot * C::kStepBytes;
+      const uint8_t* s0 = a.cache + (((long long)pg0 * a.Hkv + head) * bpp + in0) * L::kBytes;
+      mbar_arrive_expect_tx(&full[slot], two ? 2 * L::kBytes : L::kBytes);
+      if (two && in1 > 0) {
+        bulk_load(dst, s0, 2 * L::kBytes, &full[slot]);
+      } else {
+        bulk_load(dst, s0, L::kBytes, &full[slot]);
+        if (two)
+          bulk_load(dst + L::kBytes, a.cache + (((long long)pg1 * a.Hkv + head) * bpp + in1) * L::kBytes, L::kBytes,
+                    &full[slot]);
+      }
+      slot = slot + 1 == kS ? 0 : slot + 1;
+      parity ^= slot == 0;
+      ++pn;
+      if (pn < pn1) {
+        advance(a, pc, 1);
+        look_up();
+      }
+      since = globaltimer_ns();
+    }
+    }
+  } else {
+
+  // ---- the units of a warp's run ---------------------------------------------------------------
+  const uint8_t* ring = smem + warp * kS * C::kStepBytes;
+  uint64_t* full = bars + warp * kS;
+  uint64_t* empty = bars + (kW + warp) * kS;
+  int slot = 0;
+  uint32_t parity = 0;
+  bool alive = true;
+  const long long r0 = run(warp), r1 = run(warp + 1);
+  Cursor u{s_start.x, s_start.y, s_start.z, s_start.w};
+  if (r0 < r1) advance(a, u, (int)(r0 - n0));
+  if (lane == 0) s_first[warp] = s_last[warp] = make_int4(0, 0, 0, 0);
+  for (long long at = r0; at < r1;) {
+    const long long end = min(at + (u.n - u.s), r1);  // of this warp's part of the unit
+    const int len = seq_len(a, u.b), head = (int)quot(u.hr, a.rb), rb = u.hr - head * a.RB;
+    const int rows = a.Lq * a.G, row0 = rb * C::kRows;
+    {
+      // Q fragments: thread (g, c) holds row g's channels of its K words, paired as the codes will be
+      uint32_t qf[NT][kKw][4];
+      float2 qsum[NT];  // of rows 2c and 2c + 1, scaled
+      int lim[NT][2];   // last visible token of those rows
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int row = row0 + 8 * t + g;
+        float sum = 0.f;
+        uint4 raw[kKw];
+#pragma unroll
+        for (int j = 0; j < kKw; ++j) raw[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < rows) {
+          const int r = row / a.G, hq = head * a.G + row % a.G;
+          const __half* src = a.q + ((long long)u.b * a.Lq + r) * a.q_stride + (long long)hq * D + 8 * kKw * c;
+#pragma unroll
+          for (int j = 0; j < kKw; ++j) raw[j] = __ldg(reinterpret_cast<const uint4*>(src) + j);
+        }
+#pragma unroll
+        for (int j = 0; j < kKw; ++j) {
+          // channels 8w + (0,1) (2,3) (4,5) (6,7) -> pairs (0,4) (2,6) of the low nibbles, (1,5) (3,7) of the high
+          qf[t][j][0] = prmt(raw[j].x, raw[j].z, 0x5410u);
+          qf[t][j][1] = prmt(raw[j].y, raw[j].w, 0x5410u);
+          qf[t][j][2] = prmt(raw[j].x, raw[j].z, 0x7632u);
+          qf[t][j][3] = prmt(raw[j].y, raw[j].w, 0x7632u);
+          const float2 f0 = h2f2(raw[j].x), f1 = h2f2(raw[j].y), f2 = h2f2(raw[j].z), f3 = h2f2(raw[j].w);
+          sum += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= a.scale_log2;
+        qsum[t].x = __shfl_sync(0xffffffffu, sum, 8 * c);
+        qsum[t].y = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row_e = row0 + 8 * t + 2 * c + e;
+          lim[t][e] = row_e < rows ? len - a.Lq + row_e / a.G : -1;
+        }
+      }
+      const int all_see = len - a.Lq + row0 / a.G;  // tokens up to here are seen by every row of the unit
+
+      float o[NT][kMt][4];           // fragments: rows 2c and 2c + 1 of the unit in [0, 2) and [2, 4)
+      float ws[NT][4];               // sums of the signed rounded weights of rows 2c and 2c + 1 (twice)
+      float2 m[NT], l[NT], vl[NT];   // of rows 2c and 2c + 1; l and vl: this thread's tokens only
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int i = 0; i < kMt; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
+        m[t] = l[t] = vl[t] = both(0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ws[t][e] = 0.f;
+      }
+      const float c_lo = 16777216.f * a.scale_log2;
+      const int tok = token_of<D>(g);  // this thread's tokens in scores: tok and tok + 8
+      const int tv0 = token_of<D>(2 * c), tv1 = token_of<D>(2 * c + 1);  // in values: those and those + 8
+
+      bool fresh = true;  // no step of this unit yet
+
+      // One step of two blocks of 16 tokens from t0.  kEdge: it may hold tokens that some row does not see, or that lie
+      // behind the sequence (whose bytes are then whatever the page or the ring held).
+      auto step = [&](auto edge_tag, const uint8_t* base, int t0) {
+        constexpr bool kEdge = decltype(edge_tag)::value;
+        constexpr int kB = kStep / kKvBlock;
+        // ---- scores, less the running maximum ----
+        float2 vp[kB][2];  // {signed s, middle of the range} of this thread's two tokens' values
+        float lmax = kNoMax, lv[kB][2];
+        float sc[kB][NT][4];  // rows 2c and 2c + 1 of token tok, then of tok + 8
+        bool raise = fresh;
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+          const uint8_t* b16 = base + b * L::kBytes;
+          uint32_t kw[2][kKw];
+          float kx[2], ky[2];
+          const uint32_t sign = (uint32_t)(g & 1) << 31;  // of this thread's tokens' weights
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint8_t* ad = b16 + (tok + 8 * hh) * L::kRow + 4 * kKw * c;
+            if constexpr (kKw == 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(ad);
+              kw[hh][0] = v.x, kw[hh][1] = v.y, kw[hh][2] = v.z, kw[hh][3] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(ad);
+              kw[hh][0] = v.x, kw[hh][1] = v.y;
+            }
+            float2 kp = h2f2(*reinterpret_cast<const uint32_t*>(b16 + L::kKp + 4 * (tok + 8 * hh)));
+            vp[b][hh] = h2f2(*reinterpret_cast<const uint32_t*>(b16 + L::kVp + 4 * (tok + 8 * hh)));
+            if (kEdge && t0 + b * kKvBlock + tok + 8 * hh >= len) kp = vp[b][hh] = make_float2(1.f, 0.f);
+            vp[b][hh].y = fmaf(7.5f, vp[b][hh].x, vp[b][hh].y);
+            kx[hh] = kp.x * c_lo, ky[hh] = kp.y;
+            lv[b][hh] = lg2(vp[b][hh].x);
+            vp[b][hh].x = __uint_as_float(__float_as_uint(vp[b][hh].x) ^ sign);
+            lmax = fmaxf(lmax, lv[b][hh]);
+          }
+          float lo4[NT][4], hi4[NT][4];
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) lo4[t][e] = hi4[t][e] = 0.f;
+#pragma unroll
+          for (int j = 0; j < kKw; ++j) {
+            const uint32_t x = kw[0][j], y = kw[1][j], x8 = x >> 8, y8 = y >> 8;
+            const uint32_t al[4] = {x & 0x000f000fu, y & 0x000f000fu, x8 & 0x000f000fu, y8 & 0x000f000fu};
+            const uint32_t ah[4] = {x & 0x00f000f0u, y & 0x00f000f0u, x8 & 0x00f000f0u, y8 & 0x00f000f0u};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma16816(lo4[t], al, qf[t][j][0], qf[t][j][1]);
+              mma16816(hi4[t], ah, qf[t][j][2], qf[t][j][3]);
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int hh = e >> 1;
+              const float q = e & 1 ? qsum[t].y : qsum[t].x, top = e & 1 ? m[t].y : m[t].x;
+              const float dot = fmaf(hi4[t][e], 0.0625f, lo4[t][e]);
+              sc[b][t][e] = fmaf(kx[hh], dot, fmaf(ky[hh], q, -top));
+              if (kEdge && t0 + b * kKvBlock + tok + 8 * hh > lim[t][e & 1]) sc[b][t][e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float top = fmaxf(fmaxf(sc[0][t][0], sc[0][t][1]), fmaxf(sc[0][t][2], sc[0][t][3]));
+          top = fmaxf(top, fmaxf(fmaxf(sc[1][t][0], sc[1][t][1]), fmaxf(sc[1][t][2], sc[1][t][3])));
+          raise |= top > kRaise - lmax;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float up[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(fmaxf(sc[0][t][e] + lv[0][0], sc[0][t][e + 2] + lv[0][1]),
+                              fmaxf(sc[1][t][e] + lv[1][0], sc[1][t][e + 2] + lv[1][1]));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              // the first step sets m, whatever it was; a row that sees nothing in it sees nothing later either
+              up[e] = fresh && x > kNoMax ? x - kTop : fmaxf(0.f, x - kTop);
+              const float f = fresh ? 1.f : ex2(-up[e]);  // sums of nothing stay zero
+#pragma unroll
+              for (int i = 0; i < kMt; ++i) o[t][i][e] *= f, o[t][i][e + 2] *= f;
+#pragma unroll
+              for (int b = 0; b < kB; ++b) sc[b][t][e] -= up[e], sc[b][t][e + 2] -= up[e];
+              (e ? l[t].y : l[t].x) *= f;
+              (e ? vl[t].y : vl[t].x) *= f;
+              ws[t][e] *= f;
+            }
+            m[t].x += up[0], m[t].y += up[1];
+          }
+        }
+        fresh = false;
+        // ---- weights and values ----
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+          uint32_t wb[NT][2];
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              float w[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float p = ex2(sc[b][t][2 * hh + e]);
+                w[e] = p * vp[b][hh].x;
+                float& vs = e ? vl[t].y : vl[t].x;
+                if constexpr (kEdge) {  // what a row does not see may hold NaN
+                  const bool sees = t0 + b * kKvBlock + tok + 8 * hh <= lim[t][e];
+                  if (!sees) w[e] = 0.f;
+                  if (sees) vs = fmaf(p, vp[b][hh].y, vs);
+                } else {
+                  vs = fmaf(p, vp[b][hh].y, vs);
+                }
+                (e ? l[t].y : l[t].x) += p;
+              }
+              wb[t][hh] = movmatrix_trans(pack_h2(w[0], w[1]));
+            }
+          // codes: words 2g and 2g + 1 (D = 64: word g) of four tokens, paired by token
+          uint32_t xv[2][2][2];  // [tile rows g / g + 8][token half][low / high 16 bits of the word]
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint8_t* r0 = base + b * L::kBytes + L::kV + (tv0 + 8 * hh) * L::kRow;
+            const uint8_t* r1 = base + b * L::kBytes + L::kV + (tv1 + 8 * hh) * L::kRow;
+            if constexpr (D == 128) {
+              const uint2 p = *reinterpret_cast<const uint2*>(r0 + 8 * g), q = *reinterpret_cast<const uint2*>(r1 + 8 * g);
+              xv[0][hh][0] = prmt(p.x, q.x, 0x5410u), xv[0][hh][1] = prmt(p.x, q.x, 0x7632u);
+              xv[1][hh][0] = prmt(p.y, q.y, 0x5410u), xv[1][hh][1] = prmt(p.y, q.y, 0x7632u);
+            } else {
+              const uint32_t p = *reinterpret_cast<const uint32_t*>(r0 + 4 * g);
+              const uint32_t q = *reinterpret_cast<const uint32_t*>(r1 + 4 * g);
+              xv[0][hh][0] = prmt(p, q, 0x5410u), xv[1][hh][0] = prmt(p, q, 0x7632u);
+            }
+          }
+          const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma16816(ws[t], ones, wb[t][0], wb[t][1]);
+#pragma unroll
+          for (int i = 0; i < kMt; ++i) {
+            // tile i: rows g and g + 8 are nibble i of the two words (D = 128), nibbles i and i + 4 of the one (64)
+            const int half = D == 128 ? i >> 2 : 0, sh = 8 * ((i >> 1) & 1);
+            // the second token of a pair as 15 - code
+            const uint32_t mask = (i & 1) ? 0x00f000f0u : 0x000f000fu, flip = mask & 0xffff0000u;
+            const uint32_t av[4] = {((xv[0][0][half] >> sh) & mask) ^ flip, ((xv[1][0][half] >> sh) & mask) ^ flip,
+                                    ((xv[0][1][half] >> sh) & mask) ^ flip, ((xv[1][1][half] >> sh) & mask) ^ flip};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(o[t][i], av, wb[t][0], wb[t][1]);
+          }
+        }
+      };
+
+      const int s_end = u.s + (int)(end - at);
+      for (int s = u.s; s < s_end; ++s) {
+        if (alive && !mbar_wait_warp(&full[slot], parity)) {
+          alive = false;  // nothing is handed back from here on, so nothing more is requested
+          if (lane == 0) report_error(a.err, kErrTimeoutFull);
+          for (int i = 1; i < kS; ++i) {  // the other copies in flight must not outlive the kernel
+            const int sl = (slot + i) % kS;
+            mbar_wait_bounded(&full[sl], sl < slot ? parity ^ 1 : parity);
+          }
+        }
+        const uint8_t* base = ring + slot * C::kStepBytes;
+        const int t0 = s * kStep;
+        if (t0 + kStep - 1 <= all_see)
+          step(std::false_type{}, base, t0);
+        else
+          step(std::true_type{}, base, t0);
+        fence_proxy_async_smem();  // the loads above before the copy that refills the stage
+        __syncwarp();
+        if (alive && lane == 0) mbar_arrive(&empty[slot]);
+        slot = slot + 1 == kS ? 0 : slot + 1;
+        parity ^= slot == 0;
+      }
+
+      // ---- the unit's result, or this warp's part of it --------------------------------------------
+      const bool open_left = u.s > 0, open_right = at + (u.n - u.s) > r1, whole = !open_left && !open_right;
+      float* dst = open_left ? join + warp * C::kRows * C::kJoinPitch : const_cast<float*>(reinterpret_cast<const float*>(ring));
+      float2* mld = ml + ((open_left ? 0 : kW) + warp) * C::kRows;
+      if (lane == 0 && !whole) (open_left ? s_first : s_last)[warp] = make_int4(u.b, u.hr, !open_right, 1);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) {
+          l[t].x += __shfl_xor_sync(0xffffffffu, l[t].x, d);
+          l[t].y += __shfl_xor_sync(0xffffffffu, l[t].y, d);
+          vl[t].x += __shfl_xor_sync(0xffffffffu, vl[t].x, d);
+          vl[t].y += __shfl_xor_sync(0xffffffffu, vl[t].y, d);
+        }
+        if (!whole && g == 0) {
+          mld[8 * t + 2 * c] = make_float2(l[t].x == 0.f ? kNoMax : m[t].x, l[t].x);
+          mld[8 * t + 2 * c + 1] = make_float2(l[t].y == 0.f ? kNoMax : m[t].y, l[t].y);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float add = e ? vl[t].y : vl[t].x, ls = e ? l[t].y : l[t].x, wsum = ws[t][e];
+          const int row = 8 * t + 2 * c + e, r_all = row0 + row;
+          const float inv = ls == 0.f ? 0.f : 1.f / ls;
+#pragma unroll
+          for (int hi = 0; hi < 2; ++hi) {
+            // D = 128: rows g are channels 16 g + i, rows g + 8 channels 16 g + 8 + i; D = 64: 8 g + i and 8 g + 4 + i
+            float v[kMt];
+#pragma unroll
+            for (int i = 0; i < kMt; ++i) {
+              const float k = (i & 1) ? 1048576.f : 16777216.f;
+              v[i] = fmaf(fmaf(wsum, -7.5f / k, o[t][i][e + 2 * hi]), k, add);
+            }
+            const int ch = (2 * g + hi) * kMt;
+            if (!whole) {
+              float4* d4 = reinterpret_cast<float4*>(dst + row * C::kJoinPitch + ch);
+#pragma unroll
+              for (int i = 0; i < kMt / 4; ++i) d4[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            } else if (r_all < rows) {
+              uint32_t h[kMt / 2];
+#pragma unroll
+              for (int i = 0; i < kMt / 2; ++i) h[i] = pack_h2(v[2 * i] * inv, v[2 * i + 1] * inv);
+              __half* y = a.out + (((long long)u.b * a.Lq + r_all / a.G) * a.Hq + head * a.G + r_all % a.G) * D + ch;
+              if constexpr (kMt == 8)
+                *reinterpret_cast<uint4*>(y) = make_uint4(h[0], h[1], h[2], h[3]);
+              else
+                *reinterpret_cast<uint2*>(y) = make_uint2(h[0], h[1]);
+            }
+          }
+        }
+      }
+    }
+    at = end;
+    if (at < r1) {
+      u.s = u.n - 1;
+      advance(a, u, 1);
+    }
+  }
+  }  // of the warps that compute
+
+  // ---- join the parts of the warps -----------------------------------------------------------------
+  // A unit in parts is a first part of the CTA's first warp (its beginning lies in an earlier CTA) or a warp's last
+  // part, and the first parts of the warps behind it, up to one that ends it or the CTA's end.
+  __syncthreads();
+  const int warps = (int)((n1 - n0 + quota_w - 1) / quota_w);  // with a run
+  if (tid == 0) {  // a unit that spans CTAs is named once, by the second of them
+    int4 j = make_int4(-1, 0, 0, 0);
+    if (s_start.z > 0 && s_start.z <= quota)
+      j = make_int4(s_start.x, s_start.y, (int)blockIdx.x - 1, (int)((n0 + (s_start.w - s_start.z) - 1) / quota));
+    a.job[blockIdx.x] = j;
+  }
+  for (int chain = -1; chain < warps; ++chain) {  // -1: the first warp's first part, w: warp w's last part
+    const int w0 = max(chain, 0);
+    const int4 head_part = chain < 0 ? s_first[0] : s_last[w0];
+    if (!head_part.w) continue;
+    bool ends = head_part.z;
+    int w_end = w0;  // last warp of the unit
+    while (!ends && w_end + 1 < warps) ends = s_first[++w_end].z;
+    const bool begins = chain >= 0, whole = begins && ends;
+    const int head = (int)quot(head_part.y, a.rb), row0 = (head_part.y - head * a.RB) * C::kRows;
+    float* part = a.part + ((long long)blockIdx.x * 2 + (ends ? 0 : 1)) * C::kRows * (D + 2);
+    for (int i = tid; i < C::kRows * (D / 4); i += C::kThreads) {
+      const int row = i / (D / 4), ch = i % (D / 4) * 4, r_all = row0 + row;
+      if (r_all >= a.Lq * a.G) continue;
+      float top = kNoMax, ls = 0.f;
+      for (int w = w0; w <= w_end; ++w) top = fmaxf(top, ml[((begins && w == w0 ? kW : 0) + w) * C::kRows + row].x);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = w0; w <= w_end; ++w) {
+        const bool last = begins && w == w0;
+        const float2 y = ml[((last ? kW : 0) + w) * C::kRows + row];
+        const float f = ex2(y.x - top);
+        ls = fmaf(y.y, f, ls);
+        const float* src = last ? reinterpret_cast<const float*>(smem + w * kS * C::kStepBytes) : join + w * C::kRows * C::kJoinPitch;
+        const float4 z = *reinterpret_cast<const float4*>(src + row * C::kJoinPitch + ch);
+        x.x = fmaf(z.x, f, x.x), x.y = fmaf(z.y, f, x.y), x.z = fmaf(z.z, f, x.z), x.w = fmaf(z.w, f, x.w);
+      }
+      if (whole) {
+        const float inv = ls == 0.f ? 0.f : 1.f / ls;
+        __half* y = a.out + (((long long)head_part.x * a.Lq + r_all / a.G) * a.Hq + head * a.G + r_all % a.G) * D + ch;
+        *reinterpret_cast<uint2*>(y) = make_uint2(pack_h2(x.x * inv, x.y * inv), pack_h2(x.z * inv, x.w * inv));
+      } else {
+        float* p = part + row * (D + 2);
+        p[ch] = x.x, p[ch + 1] = x.y, p[ch + 2] = x.z, p[ch + 3] = x.w;
+        if (ch == 0) p[D] = top, p[D + 1] = ls;
+      }
+    }
+  }
+}
+
+// Joins the parts of the units that span CTAs, in the CTAs' order: CTA (c, row) handles that row of job c.
+template <int D>
+__global__ void __launch_bounds__(D) attn_kv_i4_join_kernel(const Args a, int rows_per_block) {
+  grid_dependency_wait();
+  const int4 job = a.job[blockIdx.x];
+  if (job.x < 0) return;
+  const int row = blockIdx.y, head = (int)quot(job.y, a.rb), rb = job.y - head * a.RB;
+  const int r_all = rb * rows_per_block + row;
+  if (r_all >= a.Lq * a.G) return;
+  // a CTA leaves its part in slot 1 where the unit goes on in the next CTA, in slot 0 where it ends
+  auto part = [&](int cta, bool last) {
+    return a.part + (((long long)cta * 2 + (last ? 1 : 0)) * rows_per_block + row) * (D + 2);
+  };
+  float top = kNoMax;
+  for (int i = job.z; i <= job.w; ++i) top = fmaxf(top, part(i, i < job.w)[D]);
+  float s = 0.f, l = 0.f;
+  for (int i = job.z; i <= job.w; ++i) {
+    const float* p = part(i, i < job.w);
+    const float f = ex2(p[D] - top);
+    s += p[threadIdx.x] * f;
+    l += p[D + 1] * f;
+  }
+  const float y = l == 0.f ? 0.f : s / l;
+  a.out[(((long long)job.x * a.Lq + r_all / a.G) * a.Hq + head * a.G + r_all % a.G) * D + threadIdx.x] = __float2half_rn(y);
+}
+
+int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
+
+template <int D, int NT>
+cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
+  using C = Cfg<D, NT>;
+  static std::atomic<bool> ready[64];  // per device; racing first calls set the same attribute
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(attn_kv_i4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
+  attn_kv_i4_kernel<D, NT><<<ctas, C::kThreads, C::kSmem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || ctas == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, C::kRows < a.Lq * a.G ? C::kRows : a.Lq * a.G, 1);
+  cfg.blockDim = dim3(D, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_kv_i4_join_kernel<D>, a, (int)C::kRows);
+}
+
+}  // namespace
+
+// Two parts per CTA (a CTA's first and its last unit may span CTAs) and a job word per CTA.
+size_t attn_kv_i4_workspace_bytes(int B, int Lq, int Hq, int Hkv, int D) {
+  const int rows = 8 * row_tiles(Lq * (Hq / Hkv));
+  (void)B;
+  return (size_t)num_sms() * (2 * (size_t)rows * (D + 2) * 4 + 16);
+}
+
+cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int Lq, int Hq, int Hkv, int D,
+                              const uint8_t* cache, long long pages, int ps, const int* table, int width,
+                              const int* kv_lens, float scale, uint16_t* out, void* workspace, unsigned* dev_err,
+                              cudaStream_t s) {
+  const int G = Hq / Hkv, nt = row_tiles(Lq * G), sms = num_sms();
+  Args a;
+  a.q = reinterpret_cast<const __half*>(q);
+  a.q_stride = q_stride;
+  a.B = B, a.Lq = Lq, a.Hq = Hq, a.Hkv = Hkv, a.G = G;
+  a.RB = (Lq * G + 8 * nt - 1) / (8 * nt);
+  a.cache = cache;
+  a.pages = (int)pages;
+  a.ps = ps;
+  a.table = table;
+  a.width = width;
+  a.kv_lens = kv_lens;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.bpp = fast_div(ps / kKvBlock);
+  a.rb = fast_div(a.RB);
+  a.out = reinterpret_cast<__half*>(out);
+  a.job = static_cast<int4*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 16 * (size_t)sms);
+  a.err = dev_err;
+  // no more CTAs than the longest possible lengths could use
+  const long long most = (long long)B * Hkv * a.RB * (((long long)width * ps + kStep - 1) / kStep);
+  const int ctas = (int)(most < sms ? (most > 0 ? most : 1) : sms);
+  if (D == 128) return nt == 1 ? launch<128, 1>(a, ctas, s) : launch<128, 2>(a, ctas, s);
+  return nt == 1 ? launch<64, 1>(a, ctas, s) : launch<64, 2>(a, ctas, s);
+}
+
+}  // namespace wql

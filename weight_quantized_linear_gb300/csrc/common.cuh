@@ -17,6 +17,7 @@ enum : unsigned {
   kErrTimeoutMma = 4u,     // MMA / accumulator hand-off wait expired
   kErrTimeoutDrain = 8u,   // exit-time drain of in-flight copies expired
   kErrSmemAlign = 16u,     // dynamic shared memory not 1024-byte aligned where a kernel has no slack for it
+  kErrBadIndex = 32u,      // a page, slot or length read from device memory was out of range and was skipped
 };
 
 // A bounded wait polls for at most this long (nanoseconds of %globaltimer).  Normal waits take

@@ -126,6 +126,25 @@ cudaError_t launch_kv_quant_i8(const uint16_t* kv, long long rows, int D, int8_t
 cudaError_t launch_kv_dequant_i8(const int8_t* q, const float* scales, long long rows, int D, uint16_t* out,
                                  cudaStream_t s);
 
+// Paged 4-bit KV cache (kv_i4.cuh has the layout).  Strides are in elements between tokens.
+constexpr int kPlanMaxB = 4096;  // requests of one kv_plan_pages call
+cudaError_t launch_kv_plan(const int* ctx_lens, const int* new_lens, int B, int ps, const int* free_pages, int free_cap,
+                           const int* free_count, int* table, int width, int T, int* cu_new, int* kv_lens, int* slots,
+                           int* free_count_out, cudaStream_t s);
+cudaError_t launch_kv_append_i4(const uint16_t* k, const uint16_t* v, long long k_stride, long long v_stride, int T,
+                                int H, int D, const int* slots, uint8_t* cache, long long pages, int ps,
+                                unsigned* dev_err, cudaStream_t s);
+cudaError_t launch_kv_read_i4(const uint8_t* cache, long long pages, int ps, int H, int D, const int* slots, int T,
+                              uint16_t* k, uint16_t* v, unsigned* dev_err, cudaStream_t s);
+size_t attn_kv_i4_workspace_bytes(int B, int Lq, int Hq, int Hkv, int D);
+cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int Lq, int Hq, int Hkv, int D,
+                              const uint8_t* cache, long long pages, int ps, const int* table, int width,
+                              const int* kv_lens, float scale, uint16_t* out, void* workspace, unsigned* dev_err,
+                              cudaStream_t s);
+cudaError_t launch_attn_prompt(const uint16_t* q, long long q_stride, const uint16_t* k, long long k_stride,
+                               const uint16_t* v, long long v_stride, int T, int Hq, int Hkv, int D, const int* cu, int B,
+                               float scale, uint16_t* out, unsigned* dev_err, cudaStream_t s, std::string* err);
+
 #ifdef WQL_PHASE_TRACE
 // Phase-trace builds only: register the stamp buffer with the traced kernels of each source file.
 struct TraceDesc;
