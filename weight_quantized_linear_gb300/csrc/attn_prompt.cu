@@ -4,24 +4,56 @@
 //   o[r] = sum_{j <= r} softmax_j(scale q[r] . k[j]) v[j],  k and v those of head h / (Hq / Hkv)
 // One pass over the keys with the running maximum and sum of the softmax in fp32.
 //
-// A CTA takes kTileQ query rows of one head; four warps of 16 rows each; key tiles of kTileK rows in shared
-// memory, products with mma.sync.
+// A CTA takes two tiles of 128 query rows that read the same keys: the same rows of two heads of a group where
+// the group is even, else two consecutive row tiles of one head.  Per key tile of 128, the tensor cores compute
+// S = Q K^T into tensor memory (tcgen05, both operands in shared memory), the tile's four softmax warps turn it
+// into weights P -- thread r owns row r, so neither maximum nor sum needs an exchange -- and write them over S as
+// fp16, and the tensor cores add P V to the tile's accumulator, P from tensor memory.  While one tile's softmax runs,
+// the tensor cores work on the other's products; 2 x (S 128 + O 128) columns fill tensor memory.  K and V tiles arrive
+// by TMA in a ring of kSlots 128-row tiles.
+//
+// The accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last time (the weights
+// are then still below 2^15), by the softmax warps themselves: S(j) complete implies P V(j - 1) complete, since
+// both were issued before the commit that signals S(j).
+//
+// Rows see nothing behind them: scores above the diagonal are replaced, not added to.  V rows behind a row would meet
+// its zero weights in the product, so in the tiles on the diagonal two warps first replace V values that are not
+// finite by zero and note the first such key of each channel; rows from that key on get NaN there at the end.
+#include <atomic>
 #include <climits>
 
 #include "internal.h"
-#include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace wql {
 namespace {
 
-constexpr int kTileQ = 64, kTileK = 64, kThreads = 128;
+constexpr int kTile = 128;                  // query rows and keys of a tile
+constexpr int kThreads = 384;               // warps 0-3, 4-7: softmax of tiles 0, 1; 8: TMA; 9: MMA; 10, 11: V check
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kCheckWarp = 10;
+constexpr float kTop = 7.0f;                // the largest weight after a rescale is 2^7 ...
+constexpr float kRaise = 8.0f;              // ... and before the next at most 2^15
+// registers per thread: launched with 168; the softmax warpgroups take 216, the third gives down to 64
+// (2 x 128 x 216 + 128 x 64 = 63488 <= 384 x 168 = 64512)
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 64;
+
+template <int D>
+struct Cfg {
+  static constexpr int kBox = kTile * 128;            // 128 rows of 64 fp16, 128-byte swizzle
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kBoxes * kBox;    // a Q, K or V tile
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kOffRing = 2 * kTileBytes;
+  static constexpr int kOffBar = kOffRing + kSlots * kTileBytes;
+  static constexpr int kSmem = kOffBar + 1024 + 1024;  // barriers, and alignment of the start
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
 
 struct Args {
-  const __half *q, *k, *v;
-  long long qs, ks, vs;  // elements between tokens
   const int* cu;
-  int B, T, Hq, Hkv, G;
+  int B, T, Hq, G, pair;  // pair: the two tiles are heads 2y and 2y + 1; else row tiles 2x and 2x + 1
   float scale_log2;
+  uint32_t negate;  // bit of the instruction descriptor that negates Q, for a negative scale
   __half* out;
   unsigned* err;
 };
@@ -31,174 +63,381 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Two fp32 at once.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float c) {
+  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n mov.b64 r, {%3, %3};\n"
+      " fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n add.rn.f32x2 p, p, q;\n"
+      " mov.b64 {%0, %1}, p;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
+// Start and length of sequence b; an invalid one has no rows.
+__device__ __forceinline__ int2 sequence(const Args& a, int b) {
+  const int s = a.cu[b], e = a.cu[b + 1];
+  if (s < 0 || e < s || e > a.T) {
+    report_error(a.err, kErrBadIndex);
+    return make_int2(0, 0);
+  }
+  return make_int2(s, e - s);
+}
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) attn_prompt_kernel(const Args a) {
-  constexpr int kPitch = D + 8;  // halves per row in shared memory: 16 bytes off a multiple of 128
-  __shared__ __align__(16) __half sk[kTileK * kPitch], sv[kTileK * kPitch];
-  __shared__ int bad[D];  // first key row whose V value of this channel is not finite
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const Args a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int bad[D];  // first key (in the sequence) whose V value of this channel is not finite
+  __shared__ int any_bad;
   __shared__ int s_sum[kThreads / 32];
   __shared__ int3 s_tile;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* qbar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [1] Q tiles
+  uint64_t* full = qbar + 1;                                        // [kSlots]
+  uint64_t* empty = full + C::kSlots;                               // [kSlots]
+  uint64_t* sbar = empty + C::kSlots;                               // [2] S complete
+  uint64_t* pbar = sbar + 2;                                        // [2] P written (4 warps)
+  uint64_t* obar = pbar + 2;                                        // [2] O complete
+  uint64_t* cbar = obar + 2;                                        // [1] V checked (2 warps)
+  uint64_t* vbar = cbar + 1;                                        // [1] V to be checked has landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vbar + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  // ---- the sequence and first row of this CTA's tile, counted from the last one ----
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  auto seq = [&](int b, int& start) {
-    const int s = a.cu[b], e = a.cu[b + 1];
-    if (s < 0 || e < s || e > a.T) {
-      report_error(a.err, kErrBadIndex);
-      start = 0;
-      return 0;
+  // ---- the sequence and row tiles of this CTA, counted from the last one: the longest rows start first ----
+  const int rows_per = a.pair ? kTile : 2 * kTile;
+  const int nh = a.pair ? a.Hq / 2 : a.Hq, tile_index = blockIdx.x / nh, hx = blockIdx.x - tile_index * nh;
+  {
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += (sequence(a, b).y + rows_per - 1) / rows_per;
+    int incl = mine;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
     }
-    start = s;
-    return e - s;
-  };
-  int mine = 0, start;
-  for (int b = b0; b < b1; ++b) mine += (seq(b, start) + kTileQ - 1) / kTileQ;
-  int incl = mine;
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) incl += s_sum[w];
+      total += s_sum[w];
+    }
+    const int want = total - 1 - tile_index;
+    if (want < 0) return;
+    int first = incl - mine;
+    if (first <= want && want < incl)
+      for (int b = b0; b < b1; ++b) {
+        const int2 s = sequence(a, b);
+        const int n = (s.y + rows_per - 1) / rows_per;
+        if (want < first + n) {
+          s_tile = make_int3(s.x, s.y, (want - first) * rows_per);
+          break;
+        }
+        first += n;
+      }
   }
-  if (lane == 31) s_sum[warp] = incl;
-  if (tid == 0) s_tile = make_int3(0, 0, 0);
+  if (tid == 0) {
+    any_bad = 0;
+    mbar_init(qbar, 1);
+    for (int s = 0; s < C::kSlots; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    for (int x = 0; x < 2; ++x) mbar_init(&sbar[x], 1), mbar_init(&pbar[x], 4), mbar_init(&obar[x], 1);
+    mbar_init(cbar, 2);
+    mbar_init(vbar, 1);
+    fence_mbarrier_init();
+  }
+  for (int i = tid; i < D; i += kThreads) bad[i] = INT_MAX;
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
   __syncthreads();
-  int total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) incl += s_sum[w];
-    total += s_sum[w];
-  }
-  const int want = total - 1 - (int)blockIdx.x;
-  if (want < 0) return;
-  int first = incl - mine;
-  if (first <= want && want < incl)
-    for (int b = b0; b < b1; ++b) {
-      const int len = seq(b, start), n = (len + kTileQ - 1) / kTileQ;
-      if (want < first + n) {
-        s_tile = make_int3(start, len, (want - first) * kTileQ);
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int start = s_tile.x, len = s_tile.y, q0 = s_tile.z;
+  // tile x: head h[x], rows r0[x] .. + 127 of the sequence, n[x] key tiles (0: no such tile)
+  const int h0 = a.pair ? 2 * hx : hx, h1 = a.pair ? h0 + 1 : h0;
+  const int r1 = a.pair ? q0 : q0 + kTile;
+  const int n0 = q0 / kTile + 1, n1 = r1 < len ? r1 / kTile + 1 : 0;
+  const int nmax = max(n0, n1), kvh = h0 / a.G;
+  const int jcheck = (n1 > 0 ? min(n0, n1) : n0) - 1;  // key tiles from here on are on a diagonal
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp && lane == 0) {
+      // ---------------- Q, then K(0), V(0), K(1), V(1) .. into the ring ----------------
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      mbar_arrive_expect_tx(qbar, (n1 > 0 ? 2 : 1) * C::kTileBytes);
+      for (int b = 0; b < C::kBoxes; ++b) tma_load_3d(smem + b * C::kBox, &tm_q, qbar, 64 * b, h0, start + q0);
+      int issued = 0;
+      bool ok = true;
+      for (int i = 0; i < 2 * nmax && ok; ++i) {
+        const int slot = i % C::kSlots;
+        if (!mbar_wait_bounded(&empty[slot], ((i / C::kSlots) & 1) ^ 1)) {
+          report_error(a.err, kErrTimeoutEmpty);
+          ok = false;
+          break;
+        }
+        uint8_t* dst = smem + C::kOffRing + slot * C::kTileBytes;
+        mbar_arrive_expect_tx(&full[slot], C::kTileBytes);
+        for (int b = 0; b < C::kBoxes; ++b)
+          tma_load_3d(dst + b * C::kBox, i & 1 ? &tm_v : &tm_k, &full[slot], 64 * b, kvh, start + (i >> 1) * kTile);
+        if (i == 0 && n1 > 0)  // the second Q tile behind the first K tile
+          for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_3d(smem + C::kTileBytes + b * C::kBox, &tm_q, qbar, 64 * b, h1, start + r1);
+        ++issued;
+      }
+      // copies that may still be in flight land before the kernel ends
+      if (!mbar_wait_bounded(qbar, 0)) report_error(a.err, kErrTimeoutDrain);
+      for (int i = max(0, issued - C::kSlots); i < issued; ++i)
+        if (!mbar_wait_bounded(&full[i % C::kSlots], (i / C::kSlots) & 1)) {
+          report_error(a.err, kErrTimeoutDrain);
+          break;
+        }
+    } else if (warp == kMmaWarp && lane == 0) {
+      // ---------------- the tensor cores' work, issued by one thread ----------------
+      const uint32_t idesc_s = umma_idesc_f16(kTile, kTile, 0, 0) | a.negate;
+      constexpr uint32_t idesc_o = umma_idesc_f16(kTile, D, /*A from TMEM*/ 0, /*B MN-major*/ 1);
+      const uint32_t q_smem = smem_u32(smem), ring = smem_u32(smem + C::kOffRing);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int phase) {
+        if (ok && !mbar_wait_bounded(bar, phase & 1)) {
+          report_error(a.err, kErrTimeoutMma);
+          ok = false;
+        }
+        return ok;
+      };
+      auto qk = [&](int x, int j) {  // S_x = Q_x K(j)^T
+        const uint32_t slot = (uint32_t)(2 * j) % C::kSlots;
+        const uint64_t ad = umma_sdesc_sw128(q_smem + x * C::kTileBytes, 16, 1024);
+        const uint64_t bd = umma_sdesc_sw128(ring + slot * C::kTileBytes, 16, 1024);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint64_t off = (uint64_t)(((s >> 2) * C::kBox + (s & 3) * 32) >> 4);
+          umma_f16(tmem + x * kTile, ad + off, bd + off, idesc_s, s > 0);
+        }
+      };
+      auto pv = [&](int x, int j) {  // O_x += P_x V(j)
+        const uint32_t slot = (uint32_t)(2 * j + 1) % C::kSlots;
+        const uint64_t bd = umma_sdesc_sw128(ring + slot * C::kTileBytes, C::kBox, 1024);
+#pragma unroll
+        for (int s = 0; s < kTile / 16; ++s)
+          umma_f16_ta(tmem + 2 * kTile + x * D, tmem + x * kTile + s * 8, bd + (uint64_t)((s * 2048) >> 4), idesc_o,
+                      j > 0 || s > 0);
+      };
+      wait(qbar, 0);
+      wait(&full[0], 0);
+      if (ok) {
+        tc_fence_after_sync();
+        qk(0, 0);
+        umma_commit(&sbar[0]);
+        if (n1 > 0) {
+          qk(1, 0);
+          umma_commit(&sbar[1]);
+        }
+        if (C::kSlots < 2 * nmax) umma_commit(&empty[0]);
+      }
+      for (int j = 0; j < nmax && ok; ++j) {
+        const int iv = 2 * j + 1, ik = 2 * j + 2;  // ring items V(j) and K(j + 1)
+        wait(&full[iv % C::kSlots], iv / C::kSlots);
+        if (j >= jcheck && ok) mbar_arrive(vbar);
+        if (j + 1 < nmax) wait(&full[ik % C::kSlots], ik / C::kSlots);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int n = x ? n1 : n0;
+          if (j >= n || !wait(&pbar[x], j)) continue;
+          if (j >= jcheck && !wait(cbar, j - jcheck)) continue;
+          tc_fence_after_sync();
+          pv(x, j);
+          if (j + 1 < n) {
+            qk(x, j + 1);
+            umma_commit(&sbar[x]);
+          } else {
+            umma_commit(&obar[x]);
+          }
+        }
+        if (ok && iv + C::kSlots < 2 * nmax) umma_commit(&empty[iv % C::kSlots]);
+        if (ok && ik + C::kSlots < 2 * nmax) umma_commit(&empty[ik % C::kSlots]);
+      }
+    } else if (warp >= kCheckWarp) {
+      // ---------------- V tiles on a diagonal: values that are not finite ----------------
+      for (int j = jcheck; j < nmax; ++j) {
+        const int i = 2 * j + 1;
+        // not on the ring's own barrier, which goes through phases that these warps do not follow
+        if (!mbar_wait_warp(vbar, (j - jcheck) & 1)) {
+          if (lane == 0) report_error(a.err, kErrTimeoutFull);
+          break;
+        }
+        uint4* v = reinterpret_cast<uint4*>(smem + C::kOffRing + (i % C::kSlots) * C::kTileBytes);
+        constexpr int kBatch = 8;
+        for (int at = tid - kCheckWarp * 32; at < C::kTileBytes / 16; at += 64 * kBatch) {
+          uint4 x[kBatch];
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) x[u] = v[at + 64 * u];
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // an exponent of all ones survives the carry into the bit above it
+              hit |= (((w[e] & 0x7c007c00u) + 0x04000400u) & 0x80008000u) != 0;
+            if (!hit) continue;
+            // chunk c of row r (16-byte units, 8 per 128-byte row) holds channels 8 (c ^ r % 8) of the box
+            const int p = at + 64 * u, row = (p >> 3) & (kTile - 1), box = p / (kTile * 8);
+            const int ch = 64 * box + 8 * ((p ^ row) & 7), key = j * kTile + row;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t m = 0x7c00u << (16 * (e & 1));
+              if ((w[e >> 1] & m) != m) continue;
+              w[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
+              if (key < len) {
+                atomicMin(&bad[ch + e], key);
+                any_bad = 1;
+              }
+            }
+            v[p] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cbar);
+      }
+    }
+  } else {
+    // ---------------- softmax and output of tile x: thread r owns row r ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int x = warp >> 2, n = x ? n1 : n0, row = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + x * kTile + lanes, to = tmem + 2 * kTile + x * D + lanes;
+    const float c = a.scale_log2;
+    float m = 0.f, l0 = 0.f, l1 = 0.f;  // m: what is subtracted from the scaled scores
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!mbar_wait_warp(&sbar[x], j & 1)) {
+        if (lane == 0) report_error(a.err, kErrTimeoutMma);
+        ok = false;
         break;
       }
-      first += n;
-    }
-  for (int i = tid; i < D; i += kThreads) bad[i] = INT_MAX;
-  __syncthreads();
-  start = s_tile.x;
-  const int len = s_tile.y, q0 = s_tile.z, head = blockIdx.y, kvh = head / a.G;
-
-  // Q fragments: rows q0 + 16 warp + g and + 8
-  uint32_t qf[D / 16][4];
-  const int r0 = q0 + 16 * warp + g;
+      tc_fence_after_sync();
+      uint32_t s[4][32];
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j)
+      for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
+      tmem_ld_wait();
+      if (j == n - 1) {  // the diagonal tile
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = r0 + 8 * (e & 1);
-      qf[j][e] = r < len ? *reinterpret_cast<const uint32_t*>(a.q + (long long)(start + r) * a.qs + (long long)head * D +
-                                                            16 * j + 2 * c + 8 * (e >> 1))
-                         : 0u;
-    }
-  float o[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-  float m[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f};
-
-  const int last = min(q0 + kTileQ, len);
-  for (int k0 = 0; k0 < last; k0 += kTileK) {
-    __syncthreads();
-    for (int i = tid; i < kTileK * D / 8; i += kThreads) {
-      const int row = i / (D / 8), ch = i % (D / 8) * 8, j = k0 + row;
-      uint4 kk = make_uint4(0u, 0u, 0u, 0u), vv = kk;
-      if (j < len) {
-        kk = *reinterpret_cast<const uint4*>(a.k + (long long)(start + j) * a.ks + (long long)kvh * D + ch);
-        vv = *reinterpret_cast<const uint4*>(a.v + (long long)(start + j) * a.vs + (long long)kvh * D + ch);
+        for (int i = 0; i < 128; ++i)
+          if (i > row) s[i >> 5][i & 31] = 0xff800000u;
       }
-      __half* vh = reinterpret_cast<__half*>(&vv);
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if ((__half_as_ushort(vh[e]) & 0x7c00) == 0x7c00) {  // rows before j must not meet 0 * inf
-          atomicMin(&bad[ch + e], j);
-          vh[e] = __ushort_as_half(0);
+      for (int i = 0; i < 128; i += 2)
+        top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1])));
+      const float up = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c - kTop;
+      if (j == 0) {
+        m = up;
+      } else if (__any_sync(0xffffffffu, up > m + kRaise)) {
+        const float now = fmaxf(m, up), f = ex2(m - now);
+        m = now;
+        l0 *= f, l1 *= f;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(to + i, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tmem_st_32x32b_x32(to + i, o);
         }
-      *reinterpret_cast<uint4*>(sk + row * kPitch + ch) = kk;
-      *reinterpret_cast<uint4*>(sv + row * kPitch + ch) = vv;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float u = __uint_as_float(s[i][2 * e]), v = __uint_as_float(s[i][2 * e + 1]);
+          fma2(u, v, c, -m);
+          u = ex2(u), v = ex2(v);
+          add2(l0, l1, u, v);
+          p[e] = pack_h2(u, v);
+        }
+        tmem_st_32x32b_x16(ts + 16 * i, p);
+      }
+      tmem_st_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pbar[x]);
     }
-    __syncthreads();
-    float s[kTileK / 8][4];
+    if (n > 0 && ok) {
+      if (!mbar_wait_warp(&obar[x], 0)) {
+        if (lane == 0) report_error(a.err, kErrTimeoutMma);
+      } else {
+        mbar_wait_warp(cbar, (nmax - 1 - jcheck) & 1);  // complete already where this tile used it
+        tc_fence_after_sync();
+        const int r = (x ? r1 : q0) + row;
+        const float inv = 1.f / (l0 + l1);
+        __half* dst = a.out + ((long long)(start + r) * a.Hq + (x ? h1 : h0)) * D;
+        const bool poison = any_bad != 0;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(to + i, o);
+          tmem_ld_wait();
+          if (poison) {
 #pragma unroll
-    for (int n = 0; n < kTileK / 8; ++n)
+            for (int e = 0; e < 32; ++e)
+              if (r >= bad[i + e]) o[e] = 0x7fc00000u;
+          }
+          if (r >= len) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t h[4];
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-      for (int n = 0; n < kTileK / 16; ++n) {
-        uint32_t x0, x1, x2, x3;  // two 8-key tiles
-        ldmatrix_x4(smem_u32(sk + (16 * n + (lane & 7) + ((lane >> 4) << 3)) * kPitch + 16 * j + ((lane >> 3) & 1) * 8), x0,
-                    x1, x2, x3);
-        mma_f16_16816(s[2 * n], qf[j], x0, x1);
-        mma_f16_16816(s[2 * n + 1], qf[j], x2, x3);
-      }
-    float mx[2] = {m[0], m[1]};
-#pragma unroll
-    for (int n = 0; n < kTileK / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = k0 + 8 * n + 2 * c + (e & 1), row = r0 + 8 * (e >> 1);
-        s[n][e] = key <= row ? s[n][e] * a.scale_log2 : -INFINITY;
-        mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
-      }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-      const float f = ex2(m[e] - mx[e]);
-      m[e] = mx[e];
-      l[e] *= f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i][2 * e] *= f, o[i][2 * e + 1] *= f;
-    }
-#pragma unroll
-    for (int n = 0; n < kTileK / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[n][e] = ex2(s[n][e] - m[e >> 1]);
-        l[e >> 1] += s[n][e];
-      }
-#pragma unroll
-    for (int n = 0; n < kTileK / 16; ++n) {
-      uint32_t p[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __half2 h = __floats2half2_rn(s[2 * n + (e >> 1)][2 * (e & 1)], s[2 * n + (e >> 1)][2 * (e & 1) + 1]);
-        p[e] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t x0, x1, x2, x3;
-        ldmatrix_x4_trans(smem_u32(sv + (16 * n + (lane & 15)) * kPitch + 16 * i + (lane >> 4) * 8), x0, x1, x2, x3);
-        mma_f16_16816(o[2 * i], p, x0, x1);
-        mma_f16_16816(o[2 * i + 1], p, x2, x3);
+            for (int k = 0; k < 4; ++k)
+              h[k] = pack_h2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+            *reinterpret_cast<uint4*>(dst + i + e) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
       }
     }
   }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-    const int r = r0 + 8 * e;
-    if (r >= len) continue;
-    const float inv = 1.f / l[e];
-    __half* dst = a.out + ((long long)(start + r) * a.Hq + head) * D;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      const int ch = 8 * i + 2 * c;
-      const float x = r >= bad[ch] ? NAN : o[i][2 * e] * inv, y = r >= bad[ch + 1] ? NAN : o[i][2 * e + 1] * inv;
-      *reinterpret_cast<__half2*>(dst + ch) = __floats2half2_rn(x, y);
-    }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+bool tensor_map(CUtensorMap* m, const uint16_t* p, int D, int heads, int T, long long stride, std::string* err) {
+  return make_tmap_3d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, D, heads, T, (uint64_t)D * 2, (uint64_t)stride * 2, 64, 1, kTile,
+                      CU_TENSOR_MAP_SWIZZLE_128B, err);
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const Args& a, dim3 grid, cudaStream_t s) {
+  using C = Cfg<D>;
+  static std::atomic<bool> ready[64];  // per device; racing first calls set the same attribute
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
   }
+  attn_prompt_kernel<D><<<grid, kThreads, C::kSmem, s>>>(q, k, v, a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -206,17 +445,25 @@ __global__ void __launch_bounds__(kThreads) attn_prompt_kernel(const Args a) {
 cudaError_t launch_attn_prompt(const uint16_t* q, long long q_stride, const uint16_t* k, long long k_stride,
                                const uint16_t* v, long long v_stride, int T, int Hq, int Hkv, int D, const int* cu, int B,
                                float scale, uint16_t* out, unsigned* dev_err, cudaStream_t s, std::string* err) {
-  (void)err;
-  Args a{reinterpret_cast<const __half*>(q), reinterpret_cast<const __half*>(k), reinterpret_cast<const __half*>(v),
-         q_stride, k_stride, v_stride, cu, B, T, Hq, Hkv, Hq / Hkv, scale * 1.4426950408889634f,
+  CUtensorMap tq, tk, tv;
+  if (!tensor_map(&tq, q, D, Hq, T, q_stride, err) || !tensor_map(&tk, k, D, Hkv, T, k_stride, err) ||
+      !tensor_map(&tv, v, D, Hkv, T, v_stride, err))
+    return cudaErrorInvalidValue;
+  const int G = Hq / Hkv, pair = G % 2 == 0;
+  // a scale of zero keeps a trace of itself, so that masked scores stay minus infinity
+  const float mag = scale < 0.f ? -scale : scale;
+  Args a{cu, B, T, Hq, G, pair, (mag < 1e-30f ? 1e-30f : mag) * 1.4426950408889634f, scale < 0.f ? 1u << 13 : 0u,
          reinterpret_cast<__half*>(out), dev_err};
-  // no sequence starts more than one ragged tile
-  const dim3 grid((unsigned)(T / kTileQ + (B < T ? B : T)), (unsigned)Hq);
-  if (D == 128)
-    attn_prompt_kernel<128><<<grid, kThreads, 0, s>>>(a);
-  else
-    attn_prompt_kernel<64><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  // every sequence may end in a ragged tile
+  const int rows_per = pair ? kTile : 2 * kTile;
+  const long long tiles = (long long)T / rows_per + (B < T ? B : T);
+  const long long ctas = tiles * (pair ? Hq / 2 : Hq);
+  if (ctas > INT_MAX) {
+    *err = "too many row tiles and heads";
+    return cudaErrorInvalidConfiguration;
+  }
+  const dim3 grid((unsigned)ctas);
+  return D == 128 ? launch<128>(tq, tk, tv, a, grid, s) : launch<64>(tq, tk, tv, a, grid, s);
 }
 
 }  // namespace wql
