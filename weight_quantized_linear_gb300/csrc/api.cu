@@ -578,10 +578,15 @@ wql_status wql_attention_kv_i4(const uint16_t* q, int64_t q_stride, int B, int L
               "workspace is smaller than wql_attention_kv_i4_workspace_bytes");
   unsigned* dev_err = device_error_word();
   if (!dev_err) return fail(WQL_ECUDA, "wql_attention_kv_i4: cannot locate the device error word");
-  return cuda_status(wql::launch_attn_kv_i4(q, q_stride, B, Lq, Hq, Hkv, D, cache, pages, page_size, block_table,
-                                            table_width, kv_lens, scale, out, workspace, dev_err,
-                                            static_cast<cudaStream_t>(stream)),
-                     "wql_attention_kv_i4");
+  // 32-bit counts of 32-token steps in the kernel
+  const int64_t rows = ((int64_t)Lq * (Hq / Hkv) + 7) / 8, steps = ((int64_t)table_width * page_size + 31) / 32;
+  if ((double)B * Hkv * (double)rows * (double)steps > (double)INT_MAX)
+    return fail(WQL_EUNSUPPORTED, "B * Hkv * row blocks * table_width * page_size / 32 must be below 2^31");
+  std::string err;
+  const cudaError_t e = wql::launch_attn_kv_i4(q, q_stride, B, Lq, Hq, Hkv, D, cache, pages, page_size, block_table,
+                                               table_width, kv_lens, scale, out, workspace, dev_err,
+                                               static_cast<cudaStream_t>(stream), &err);
+  return cuda_status(e, "wql_attention_kv_i4", err);
 }
 
 wql_status wql_attention_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,

@@ -116,7 +116,8 @@ struct Args {
   const uint8_t* cache;
   int pages, ps;
   const int* table;
-  int width;
+  int width, cap;  // pages of a row of the table, and their tokens
+  int split;       // 0: a CTA per unit; 1: the steps of all units evenly over the CTAs
   const int* kv_lens;
   float scale_log2;
   FastDiv bpp, rb;  // blocks per page, row blocks per head
@@ -126,10 +127,7 @@ struct Args {
   unsigned* err;
 };
 
-__device__ __forceinline__ int seq_len(const Args& a, int b) {
-  const int n = a.kv_lens[b];
-  return n <= 0 ? 0 : (int)min((long long)n, (long long)a.width * a.ps);
-}
+__device__ __forceinline__ int seq_len(const Args& a, int b) { return min(max(a.kv_lens[b], 0), a.cap); }
 __device__ __forceinline__ int seq_steps(const Args& a, int b) { return (seq_len(a, b) + kStep - 1) / kStep; }
 
 // Position in the order of all steps: unit (b, hr = head * RB + row block), step s of `n` of that unit.
@@ -153,6 +151,17 @@ __device__ __forceinline__ void advance(const Args& a, Cursor& c, int by) {
   }
 }
 
+// Zeros in rows [row0, row0 + count) of a sequence's K/V head, by the whole CTA.
+template <int D>
+__device__ void zero_rows(const Args& a, int b, int head, int row0, int count) {
+  for (int i = threadIdx.x; i < count * (D / 8); i += blockDim.x) {
+    const int r = row0 + i / (D / 8);
+    if (r < a.Lq * a.G)
+      reinterpret_cast<uint4*>(a.out)[(((long long)b * a.Lq + r / a.G) * a.Hq + head * a.G + r % a.G) * (D / 8) + i % (D / 8)] =
+          make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 // The token (of 16) that row r of an 8 x 8 block of weights stands for; K's rows, V's reduction index and the
 // params all use it.  Chosen so that the shared-memory loads of K and V hit every bank once.
 template <int D>
@@ -172,8 +181,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   float* join = reinterpret_cast<float*>(smem + C::kOffJoin);
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  __shared__ long long s_sum[kW + 1];
-  __shared__ long long s_total;
+  __shared__ int s_sum[kW + 1];
+  __shared__ int s_total;
   __shared__ int4 s_start;
   __shared__ int4 s_first[kW], s_last[kW];  // {sequence, head and row block, ends here / -, exists} of the warps' parts
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -182,59 +191,67 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   fence_mbarrier_init();
   grid_dependents_launch();
 
-  // ---- this CTA's range [n0, n1) of the order of all steps -----------------------------------
-  const int per = (a.B + C::kThreads - 1) / C::kThreads;
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  // ---- this CTA's range [n0, n1) of the order of all steps (of its unit's, where each has a CTA) --------
   const int hr_all = a.Hkv * a.RB;
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int n = a.kv_lens[b];
-    if (n > 0 && n > (long long)a.width * a.ps) report_error(a.err, kErrBadIndex);
-    mine += (long long)seq_steps(a, b) * hr_all;
-  }
-  long long incl = mine;
+  int n0, n1, quota;
+  if (!a.split) {
+    const int b = (int)blockIdx.x / hr_all, n = seq_steps(a, b);
+    if (tid == 0) {
+      if (a.kv_lens[b] > a.cap) report_error(a.err, kErrBadIndex);
+      s_start = make_int4(b, (int)blockIdx.x - b * hr_all, 0, n);
+    }
+    n0 = 0, n1 = quota = n;
+    if (n == 0) {
+      const int head = (int)blockIdx.x % hr_all / a.RB, row0 = (int)blockIdx.x % a.RB * C::kRows;
+      zero_rows<D>(a, b, head, row0, C::kRows);
+      return;
+    }
+    __syncthreads();
+  } else {
+    const int per = (a.B + C::kThreads - 1) / C::kThreads;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      if (a.kv_lens[b] > a.cap) report_error(a.err, kErrBadIndex);
+      mine += seq_steps(a, b) * hr_all;
+    }
+    int incl = mine;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) s_sum[warp] = incl;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) incl += s_sum[w];
-  if (tid == C::kThreads - 1) s_total = incl;
-  __syncthreads();
-  const long long total = s_total;
-  // at least one step for every warp of a CTA: a short batch uses fewer CTAs and has fewer parts to join
-  long long quota = (total + gridDim.x - 1) / gridDim.x;
-  if (quota < kW) quota = kW;
-  const long long n0 = min(quota * blockIdx.x, total), n1 = min(n0 + quota, total);
-  {
-    long long first = incl - mine;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += s_sum[w];
+    if (tid == C::kThreads - 1) s_total = incl;
+    __syncthreads();
+    const int total = s_total;
+    // at least one step for every warp of a CTA: a short batch uses fewer CTAs and has fewer parts to join
+    quota = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), kW);
+    n0 = (int)min((unsigned)quota * blockIdx.x, (unsigned)total), n1 = min(n0 + quota, total);
+    int first = incl - mine;
     if (n0 < n1 && first <= n0 && n0 < incl)
       for (int b = b0; b < b1; ++b) {
-        const long long n = seq_steps(a, b);
+        const int n = seq_steps(a, b);
         if (n0 < first + n * hr_all) {
-          s_start = make_int4(b, (int)((n0 - first) / n), (int)((n0 - first) % n), (int)n);
+          s_start = make_int4(b, (n0 - first) / n, (n0 - first) % n, n);
           break;
         }
         first += n * hr_all;
       }
-  }
-  __syncthreads();
-
-  // rows of sequences without any token: zeros
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-    if (seq_len(a, b) == 0)
-      for (int i = tid; i < a.Lq * a.Hq * (D / 8); i += C::kThreads)
-        reinterpret_cast<uint4*>(a.out)[(long long)b * a.Lq * a.Hq * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
-
-  if (n0 >= n1) {
-    if (tid == 0) a.job[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // sequences without any token
+      if (seq_len(a, b) == 0)
+        for (int head = 0; head < a.Hkv; ++head) zero_rows<D>(a, b, head, 0, a.Lq * a.G);
+    if (n0 >= n1) {
+      if (tid == 0) a.job[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      return;
+    }
+    __syncthreads();
   }
 
   // warp w's run of steps is [run(w), run(w + 1))
-  const long long quota_w = (n1 - n0 + kW - 1) / kW;
+  const int quota_w = (n1 - n0 + kW - 1) / kW;
   auto run = [&](int w) { return min(n0 + quota_w * w, n1); };
 
   // ---- the warp that requests: lane w keeps warp w's ring filled ---------------------------------
@@ -245,9 +262,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
     uint64_t* full = bars + lane * kS;
     uint64_t* empty = bars + (kW + lane) * kS;
     Cursor pc{s_start.x, s_start.y, s_start.z, s_start.w};
-    long long pn = run(lane);  // next step to request
-    const long long pn1 = run(lane + 1);
-    if (pn < pn1) advance(a, pc, (int)(pn - n0));
+    int pn = run(lane);  // next step to request
+    const int pn1 = run(lane + 1);
+    if (pn < pn1) advance(a, pc, pn - n0);
     int slot = 0, pg0 = 0, pg1 = 0, blk = 0, col0 = 0, last = 0;
     uint32_t parity = 1;  // the first round finds every stage free
     auto look_up = [&]() {  // the pages of the two blocks of the step at pc
@@ -266,6 +283,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
           report_error(a.err, kErrTimeoutEmpty);
           break;
         }
+        __nanosleep(100);  // the ring holds about 2 us of work; polling without a pause takes issue slots from its users
         continue;
       }
       if ((unsigned)pg0 >= (unsigned)a.pages || (unsigned)pg1 >= (unsigned)a.pages) {
@@ -305,12 +323,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   int slot = 0;
   uint32_t parity = 0;
   bool alive = true;
-  const long long r0 = run(warp), r1 = run(warp + 1);
+  const int r0 = run(warp), r1 = run(warp + 1);
   Cursor u{s_start.x, s_start.y, s_start.z, s_start.w};
-  if (r0 < r1) advance(a, u, (int)(r0 - n0));
+  if (r0 < r1) advance(a, u, r0 - n0);
   if (lane == 0) s_first[warp] = s_last[warp] = make_int4(0, 0, 0, 0);
-  for (long long at = r0; at < r1;) {
-    const long long end = min(at + (u.n - u.s), r1);  // of this warp's part of the unit
+  for (int at = r0; at < r1;) {
+    const int end = min(at + (u.n - u.s), r1);  // of this warp's part of the unit
     const int len = seq_len(a, u.b), head = (int)quot(u.hr, a.rb), rb = u.hr - head * a.RB;
     const int rows = a.Lq * a.G, row0 = rb * C::kRows;
     {
@@ -525,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
         }
       };
 
-      const int s_end = u.s + (int)(end - at);
+      const int s_end = u.s + (end - at);
       for (int s = u.s; s < s_end; ++s) {
         if (alive && !mbar_wait_warp(&full[slot], parity)) {
           alive = false;  // nothing is handed back from here on, so nothing more is requested
@@ -611,11 +629,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   // A unit in parts is a first part of the CTA's first warp (its beginning lies in an earlier CTA) or a warp's last
   // part, and the first parts of the warps behind it, up to one that ends it or the CTA's end.
   __syncthreads();
-  const int warps = (int)((n1 - n0 + quota_w - 1) / quota_w);  // with a run
-  if (tid == 0) {  // a unit that spans CTAs is named once, by the second of them
+  const int warps = (n1 - n0 + quota_w - 1) / quota_w;  // with a run
+  if (a.split && tid == 0) {  // a unit that spans CTAs is named once, by the second of them
     int4 j = make_int4(-1, 0, 0, 0);
     if (s_start.z > 0 && s_start.z <= quota)
-      j = make_int4(s_start.x, s_start.y, (int)blockIdx.x - 1, (int)((n0 + (s_start.w - s_start.z) - 1) / quota));
+      j = make_int4(s_start.x, s_start.y, (int)blockIdx.x - 1, (n0 + (s_start.w - s_start.z) - 1) / quota);
     a.job[blockIdx.x] = j;
   }
   for (int chain = -1; chain < warps; ++chain) {  // -1: the first warp's first part, w: warp w's last part
@@ -698,7 +716,7 @@ cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
   }
   attn_kv_i4_kernel<D, NT><<<ctas, C::kThreads, C::kSmem, s>>>(a);
   e = cudaGetLastError();
-  if (e != cudaSuccess || ctas == 1) return e;
+  if (e != cudaSuccess || !a.split || ctas == 1) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, C::kRows < a.Lq * a.G ? C::kRows : a.Lq * a.G, 1);
   cfg.blockDim = dim3(D, 1, 1);
@@ -723,7 +741,7 @@ size_t attn_kv_i4_workspace_bytes(int B, int Lq, int Hq, int Hkv, int D) {
 cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int Lq, int Hq, int Hkv, int D,
                               const uint8_t* cache, long long pages, int ps, const int* table, int width,
                               const int* kv_lens, float scale, uint16_t* out, void* workspace, unsigned* dev_err,
-                              cudaStream_t s) {
+                              cudaStream_t s, std::string* err) {
   const int G = Hq / Hkv, nt = row_tiles(Lq * G), sms = num_sms();
   Args a;
   a.q = reinterpret_cast<const __half*>(q);
@@ -743,9 +761,17 @@ cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int 
   a.job = static_cast<int4*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 16 * (size_t)sms);
   a.err = dev_err;
-  // no more CTAs than the longest possible lengths could use
-  const long long most = (long long)B * Hkv * a.RB * (((long long)width * ps + kStep - 1) / kStep);
-  const int ctas = (int)(most < sms ? (most > 0 ? most : 1) : sms);
+  a.cap = width * ps;
+  // A CTA per unit where they fit the card at once and none can be long (four steps for every warp): one launch and
+  // nothing to join across CTAs.  Otherwise an even share of all steps for every SM, but no more CTAs than the longest
+  // possible lengths could use, and the joining kernel behind it.
+  const long long units = (long long)B * Hkv * a.RB, most = (a.cap + kStep - 1) / kStep;
+  if (units * most > INT_MAX) {
+    *err = "more than 2^31 - 1 steps of 32 tokens fit the block table";
+    return cudaErrorInvalidValue;
+  }
+  a.split = units > sms || most > 4 * 12;
+  const int ctas = (int)(!a.split ? units : units * most < sms ? units * most : sms);
   if (D == 128) return nt == 1 ? launch<128, 1>(a, ctas, s) : launch<128, 2>(a, ctas, s);
   return nt == 1 ? launch<64, 1>(a, ctas, s) : launch<64, 2>(a, ctas, s);
 }

@@ -140,7 +140,7 @@ size_t attn_kv_i4_workspace_bytes(int B, int Lq, int Hq, int Hkv, int D);
 cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int Lq, int Hq, int Hkv, int D,
                               const uint8_t* cache, long long pages, int ps, const int* table, int width,
                               const int* kv_lens, float scale, uint16_t* out, void* workspace, unsigned* dev_err,
-                              cudaStream_t s);
+                              cudaStream_t s, std::string* err);
 cudaError_t launch_attn_prompt(const uint16_t* q, long long q_stride, const uint16_t* k, long long k_stride,
                                const uint16_t* v, long long v_stride, int T, int Hq, int Hkv, int D, const int* cu, int B,
                                float scale, uint16_t* out, unsigned* dev_err, cudaStream_t s, std::string* err);
