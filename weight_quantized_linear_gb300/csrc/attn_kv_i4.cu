@@ -38,7 +38,9 @@
 namespace wql {
 namespace {
 
+constexpr int kMaxCtas = 256;                   // at most: one per SM
 constexpr int kStep = 32;                       // tokens per step
+constexpr int kLead = 1;                        // steps that stand for a unit's own cost
 constexpr float kNoMax = -1e30f;                // maximum of nothing
 // Weights are kept below 2^15: at each raise of m the largest becomes 2^7, so that those down to 2^-21 of it are normal
 // fp16 numbers.
@@ -72,6 +74,12 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// (a & b) ^ c in one instruction, b and c in registers.
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -109,6 +117,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 struct Args {
   const __half* q;
   long long q_stride;
@@ -128,7 +146,12 @@ struct Args {
 };
 
 __device__ __forceinline__ int seq_len(const Args& a, int b) { return min(max(a.kv_lens[b], 0), a.cap); }
-__device__ __forceinline__ int seq_steps(const Args& a, int b) { return (seq_len(a, b) + kStep - 1) / kStep; }
+// Steps of a unit of sequence b.  Its first kLead steps are no tokens: they stand for what a unit costs beside them (its
+// queries, reductions and output), so that the warps that meet many short units get fewer tokens.
+__device__ __forceinline__ int seq_steps(const Args& a, int b) {
+  const int n = (seq_len(a, b) + kStep - 1) / kStep;
+  return n > 0 ? n + kLead : 0;
+}
 
 // Position in the order of all steps: unit (b, hr = head * RB + row block), step s of `n` of that unit.
 struct Cursor {
@@ -189,13 +212,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
 
   for (int i = tid; i < 2 * kW * kS; i += C::kThreads) mbar_init(&bars[i], 1);
   fence_mbarrier_init();
+  grid_dependency_wait();  // everything before this line overlaps the end of the preceding kernel
   grid_dependents_launch();
 
   // ---- this CTA's range [n0, n1) of the order of all steps (of its unit's, where each has a CTA) --------
   const int hr_all = a.Hkv * a.RB;
   int n0, n1, quota;
   if (!a.split) {
-    const int b = (int)blockIdx.x / hr_all, n = seq_steps(a, b);
+    const int b = (int)blockIdx.x / hr_all, n = seq_steps(a, b);  // the lead step goes to some warp here too
     if (tid == 0) {
       if (a.kv_lens[b] > a.cap) report_error(a.err, kErrBadIndex);
       s_start = make_int4(b, (int)blockIdx.x - b * hr_all, 0, n);
@@ -268,22 +292,32 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
     int slot = 0, pg0 = 0, pg1 = 0, blk = 0, col0 = 0, last = 0;
     uint32_t parity = 1;  // the first round finds every stage free
     auto look_up = [&]() {  // the pages of the two blocks of the step at pc
-      blk = pc.s * (kStep / kKvBlock);
+      blk = (pc.s - kLead) * (kStep / kKvBlock);
       last = (seq_len(a, pc.b) - 1) / kKvBlock;
       col0 = (int)quot(blk, a.bpp);
       const int* row = a.table + (long long)pc.b * a.width;
       pg0 = row[col0];
       pg1 = blk < last ? row[quot(blk + 1, a.bpp)] : pg0;
     };
-    if (pn < pn1) look_up();
+    auto next = [&](int by) {  // to the next step with tokens
+      pn += by;
+      if (pn < pn1) advance(a, pc, by);
+      while (pn < pn1 && pc.s < kLead) {
+        pn += 1;
+        if (pn < pn1) advance(a, pc, 1);
+      }
+      if (pn < pn1) look_up();
+    };
+    next(0);
     unsigned long long since = globaltimer_ns();
     while (pn < pn1) {
-      if (!mbar_try_wait(&empty[slot], parity)) {
+      // a test, not a wait: a lane whose stage is in use must not hold up the others
+      if (!mbar_test_wait(&empty[slot], parity)) {
         if (globaltimer_ns() - since > kWaitLimitNs) {
           report_error(a.err, kErrTimeoutEmpty);
           break;
         }
-        __nanosleep(100);  // the ring holds about 2 us of work; polling without a pause takes issue slots from its users
+        __nanosleep(40);
         continue;
       }
       if ((unsigned)pg0 >= (unsigned)a.pages || (unsigned)pg1 >= (unsigned)a.pages) {
@@ -306,11 +340,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
       }
       slot = slot + 1 == kS ? 0 : slot + 1;
       parity ^= slot == 0;
-      ++pn;
-      if (pn < pn1) {
-        advance(a, pc, 1);
-        look_up();
-      }
+      next(1);
       since = globaltimer_ns();
     }
     }
@@ -390,6 +420,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
       const int tv0 = token_of<D>(2 * c), tv1 = token_of<D>(2 * c + 1);  // in values: those and those + 8
 
       bool fresh = true;  // no step of this unit yet
+      const uint32_t mask0 = 0x000f000fu, mask1 = 0x00f000f0u, flip0 = 0x000f0000u, flip1 = 0x00f00000u;
 
       // One step of two blocks of 16 tokens from t0.  kEdge: it may hold tokens that some row does not see, or that lie
       // behind the sequence (whose bytes are then whatever the page or the ring held).
@@ -532,11 +563,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
 #pragma unroll
           for (int i = 0; i < kMt; ++i) {
             // tile i: rows g and g + 8 are nibble i of the two words (D = 128), nibbles i and i + 4 of the one (64)
-            const int half = D == 128 ? i >> 2 : 0, sh = 8 * ((i >> 1) & 1);
+            const int half = D == 128 ? i >> 2 : 0;
+            if (i % 4 == 2)
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh)
+                xv[0][hh][half] >>= 8, xv[1][hh][half] >>= 8;
             // the second token of a pair as 15 - code
-            const uint32_t mask = (i & 1) ? 0x00f000f0u : 0x000f000fu, flip = mask & 0xffff0000u;
-            const uint32_t av[4] = {((xv[0][0][half] >> sh) & mask) ^ flip, ((xv[1][0][half] >> sh) & mask) ^ flip,
-                                    ((xv[0][1][half] >> sh) & mask) ^ flip, ((xv[1][1][half] >> sh) & mask) ^ flip};
+            const uint32_t mask = i & 1 ? mask1 : mask0, flip = i & 1 ? flip1 : flip0;
+            const uint32_t av[4] = {and_xor(xv[0][0][half], mask, flip), and_xor(xv[1][0][half], mask, flip),
+                                    and_xor(xv[0][1][half], mask, flip), and_xor(xv[1][1][half], mask, flip)};
 #pragma unroll
             for (int t = 0; t < NT; ++t) mma16816(o[t][i], av, wb[t][0], wb[t][1]);
           }
@@ -544,7 +579,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
       };
 
       const int s_end = u.s + (end - at);
-      for (int s = u.s; s < s_end; ++s) {
+      for (int s = max(u.s, kLead) - kLead; s < s_end - kLead; ++s) {
         if (alive && !mbar_wait_warp(&full[slot], parity)) {
           alive = false;  // nothing is handed back from here on, so nothing more is requested
           if (lane == 0) report_error(a.err, kErrTimeoutFull);
@@ -677,6 +712,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
 // Joins the parts of the units that span CTAs, in the CTAs' order: CTA (c, row) handles that row of job c.
 template <int D>
 __global__ void __launch_bounds__(D) attn_kv_i4_join_kernel(const Args a, int rows_per_block) {
+  __shared__ float s_f[kMaxCtas], s_top[D / 32], s_l[D / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependents_launch();
   grid_dependency_wait();
   const int4 job = a.job[blockIdx.x];
   if (job.x < 0) return;
@@ -684,19 +722,41 @@ __global__ void __launch_bounds__(D) attn_kv_i4_join_kernel(const Args a, int ro
   const int r_all = rb * rows_per_block + row;
   if (r_all >= a.Lq * a.G) return;
   // a CTA leaves its part in slot 1 where the unit goes on in the next CTA, in slot 0 where it ends
-  auto part = [&](int cta, bool last) {
-    return a.part + (((long long)cta * 2 + (last ? 1 : 0)) * rows_per_block + row) * (D + 2);
+  auto part = [&](int cta) {
+    return a.part + (((long long)cta * 2 + (cta < job.w ? 1 : 0)) * rows_per_block + row) * (D + 2);
   };
-  float top = kNoMax;
-  for (int i = job.z; i <= job.w; ++i) top = fmaxf(top, part(i, i < job.w)[D]);
-  float s = 0.f, l = 0.f;
-  for (int i = job.z; i <= job.w; ++i) {
-    const float* p = part(i, i < job.w);
-    const float f = ex2(p[D] - top);
-    s += p[threadIdx.x] * f;
-    l += p[D + 1] * f;
+  float m[kMaxCtas / D], l[kMaxCtas / D], top = kNoMax;
+#pragma unroll
+  for (int k = 0; k < kMaxCtas / D; ++k) {
+    const int i = job.z + threadIdx.x + k * D;
+    m[k] = i <= job.w ? part(i)[D] : kNoMax;
+    l[k] = i <= job.w ? part(i)[D + 1] : 0.f;
+    top = fmaxf(top, m[k]);
   }
-  const float y = l == 0.f ? 0.f : s / l;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) top = fmaxf(top, s_top[w]);
+  float ls = 0.f;
+#pragma unroll
+  for (int k = 0; k < kMaxCtas / D; ++k) {
+    const float f = ex2(m[k] - top);
+    s_f[threadIdx.x + k * D] = f;
+    ls += l[k] * f;
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+  if (lane == 0) s_l[warp] = ls;
+  __syncthreads();
+  ls = 0.f;
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) ls += s_l[w];
+  float s = 0.f;
+#pragma unroll 8
+  for (int i = job.z; i <= job.w; ++i) s = fmaf(part(i)[threadIdx.x], s_f[i - job.z], s);
+  const float y = ls == 0.f ? 0.f : s / ls;
   a.out[(((long long)job.x * a.Lq + r_all / a.G) * a.Hq + head * a.G + r_all % a.G) * D + threadIdx.x] = __float2half_rn(y);
 }
 
@@ -714,18 +774,22 @@ cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
   }
-  attn_kv_i4_kernel<D, NT><<<ctas, C::kThreads, C::kSmem, s>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !a.split || ctas == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, C::kRows < a.Lq * a.G ? C::kRows : a.Lq * a.G, 1);
-  cfg.blockDim = dim3(D, 1, 1);
-  cfg.stream = s;
+  // Both launches may start before the kernel ahead of them has ended, and wait for it before they read anything.
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_kv_i4_kernel<D, NT>, a);
+  if (e != cudaSuccess || !a.split || ctas == 1) return e;
+  cfg.gridDim = dim3(ctas, C::kRows < a.Lq * a.G ? C::kRows : a.Lq * a.G, 1);
+  cfg.blockDim = dim3(D, 1, 1);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_kv_i4_join_kernel<D>, a, (int)C::kRows);
 }
 
@@ -765,13 +829,13 @@ cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int 
   // A CTA per unit where they fit the card at once and none can be long (four steps for every warp): one launch and
   // nothing to join across CTAs.  Otherwise an even share of all steps for every SM, but no more CTAs than the longest
   // possible lengths could use, and the joining kernel behind it.
-  const long long units = (long long)B * Hkv * a.RB, most = (a.cap + kStep - 1) / kStep;
+  const long long units = (long long)B * Hkv * a.RB, most = (a.cap + kStep - 1) / kStep + kLead;
   if (units * most > INT_MAX) {
     *err = "more than 2^31 - 1 steps of 32 tokens fit the block table";
     return cudaErrorInvalidValue;
   }
-  a.split = units > sms || most > 4 * 12;
-  const int ctas = (int)(!a.split ? units : units * most < sms ? units * most : sms);
+  a.split = units > sms || most > 4 * 12 + kLead;
+  const int ctas = (int)(!a.split ? units : units * most < sms ? units * most : sms < kMaxCtas ? sms : kMaxCtas);
   if (D == 128) return nt == 1 ? launch<128, 1>(a, ctas, s) : launch<128, 2>(a, ctas, s);
   return nt == 1 ? launch<64, 1>(a, ctas, s) : launch<64, 2>(a, ctas, s);
 }
