@@ -7,8 +7,9 @@
 // CTAs (one per SM), whatever the lengths, and a CTA's steps evenly over its warps, each a run of its own.  One
 // more warp requests the copies: its lane w keeps warp w's ring of steps filled, across unit boundaries, so that no
 // warp waits for another while streaming and a short unit costs no synchronisation.  A warp writes a unit that lies in
-// its run; parts of units that span warps are joined in shared memory at the CTA's end, and those that span CTAs are
-// left in the workspace, where a second, small kernel joins them in a fixed order.
+// its run; parts of units that span warps are joined in shared memory at the CTA's end.  Parts of units that span CTAs
+// go to the workspace; the CTA that finds all the parts of a unit there joins them, in their order, so that no CTA
+// waits for another and the result does not depend on who does it.
 //
 // Mathematics.  Scores: sum_c q_c (code_c s + lo) = s sum_c q_c code_c + lo sum_c q_c, so the matrix product
 // runs on the codes.  Masking a nibble in place makes it an fp16 number without any conversion: a code in
@@ -38,7 +39,6 @@
 namespace wql {
 namespace {
 
-constexpr int kMaxCtas = 256;                   // at most: one per SM
 constexpr int kStep = 32;                       // tokens per step
 constexpr int kLead = 1;                        // steps that stand for a unit's own cost
 constexpr float kNoMax = -1e30f;                // maximum of nothing
@@ -48,7 +48,7 @@ constexpr float kTop = 7.0f, kRaise = 15.0f;
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kWarps = NT == 1 ? 12 : 7;
+  static constexpr int kWarps = NT == 1 ? (D == 64 ? 15 : 11) : (D == 64 ? 11 : 7);  // and one: a multiple of 4
   static constexpr int kThreads = 32 * (kWarps + 1);  // and the warp that requests the copies
   static constexpr int kStepBytes = kStep / kKvBlock * KvI4<D>::kBytes;
   static constexpr int kStages = D == 64 ? 4 : 3;
@@ -56,7 +56,8 @@ struct Cfg {
   static constexpr int kJoinPitch = D + 4;                                  // floats per row of the join buffer
   static constexpr int kOffJoin = kWarps * kStages * kStepBytes;            // [kWarps][kRows][kJoinPitch] fp32: first parts
   static constexpr int kOffMl = kOffJoin + kWarps * kRows * kJoinPitch * 4; // [2][kWarps][kRows] {m, l}: first parts, last parts
-  static constexpr int kOffBar = kOffMl + 2 * kWarps * kRows * 8;              // [2][kWarps][kStages] mbarriers: full, empty
+  static constexpr int kOffFac = kOffMl + 2 * kWarps * kRows * 8;           // [2][kWarps][kRows] {factor, its l, maximum}
+  static constexpr int kOffBar = kOffFac + 2 * kWarps * kRows * 16;              // [2][kWarps][kStages] mbarriers: full, empty
   static_assert(kRows * kJoinPitch * 4 <= kStages * kStepBytes, "a last part takes the warp's ring");
   static constexpr int kSmem = kOffBar + 2 * kWarps * kStages * 8;
 };
@@ -127,6 +128,9 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// A flag with any other value says that the part is not there, so the workspace may hold anything before a call.
+constexpr unsigned long long kThere = 0x9d6b2f81c35ae704ull;
+
 struct Args {
   const __half* q;
   long long q_stride;
@@ -140,8 +144,8 @@ struct Args {
   float scale_log2;
   FastDiv bpp, rb;  // blocks per page, row blocks per head
   __half* out;
-  float* part;  // [gridDim][2][kRows][D + 2]: O, m, l of the units that end (0) and go on (1) behind the CTA's range
-  int4* job;    // [gridDim]: {sequence, head and row block, first CTA, last CTA} of a unit to join; sequence -1: none
+  float* part;  // [gridDim][2][kRows][D + 4]: O, m, l of the units that end (0) and go on (1) behind the CTA's range
+  unsigned long long* flag;  // [gridDim][2]: kThere where that part is complete
   unsigned* err;
 };
 
@@ -204,10 +208,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   float* join = reinterpret_cast<float*>(smem + C::kOffJoin);
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  __shared__ int s_sum[kW + 1];
-  __shared__ int s_total;
-  __shared__ int4 s_start;
-  __shared__ int4 s_first[kW], s_last[kW];  // {sequence, head and row block, ends here / -, exists} of the warps' parts
+  __shared__ int4 s_start[kW];              // the warps' first positions
+  __shared__ int4 s_first[kW], s_last[kW];  // {sequence, head and row block, first step of the unit, kPart | kEnds}
+  __shared__ int s_all;
+  constexpr int kPart = 1, kEnds = 2;       // there is such a part; the unit ends in it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
 
   for (int i = tid; i < 2 * kW * kS; i += C::kThreads) mbar_init(&bars[i], 1);
@@ -217,78 +221,69 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
 
   // ---- this CTA's range [n0, n1) of the order of all steps (of its unit's, where each has a CTA) --------
   const int hr_all = a.Hkv * a.RB;
-  int n0, n1, quota;
+  int n0, n1, quota, incl = 0, mine = 0, b0 = 0, b1 = 0;
   if (!a.split) {
-    const int b = (int)blockIdx.x / hr_all, n = seq_steps(a, b);  // the lead step goes to some warp here too
-    if (tid == 0) {
-      if (a.kv_lens[b] > a.cap) report_error(a.err, kErrBadIndex);
-      s_start = make_int4(b, (int)blockIdx.x - b * hr_all, 0, n);
-    }
-    n0 = 0, n1 = quota = n;
-    if (n == 0) {
+    const int b = (int)blockIdx.x / hr_all;
+    if (tid == 0 && a.kv_lens[b] > a.cap) report_error(a.err, kErrBadIndex);
+    n0 = 0, n1 = quota = seq_steps(a, b);
+    if (n1 == 0) {
       const int head = (int)blockIdx.x % hr_all / a.RB, row0 = (int)blockIdx.x % a.RB * C::kRows;
       zero_rows<D>(a, b, head, row0, C::kRows);
       return;
     }
-    __syncthreads();
-  } else {
-    const int per = (a.B + C::kThreads - 1) / C::kThreads;
-    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    int mine = 0;
+  } else {  // every warp scans the lengths itself
+    const int per = (a.B + 31) / 32;
+    b0 = min(lane * per, a.B), b1 = min(b0 + per, a.B);
     for (int b = b0; b < b1; ++b) {
       if (a.kv_lens[b] > a.cap) report_error(a.err, kErrBadIndex);
       mine += seq_steps(a, b) * hr_all;
     }
-    int incl = mine;
+    incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += o;
     }
-    if (lane == 31) s_sum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += s_sum[w];
-    if (tid == C::kThreads - 1) s_total = incl;
-    __syncthreads();
-    const int total = s_total;
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
     // at least one step for every warp of a CTA: a short batch uses fewer CTAs and has fewer parts to join
     quota = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), kW);
     n0 = (int)min((unsigned)quota * blockIdx.x, (unsigned)total), n1 = min(n0 + quota, total);
-    int first = incl - mine;
-    if (n0 < n1 && first <= n0 && n0 < incl)
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // sequences without any token
+      if (seq_len(a, b) == 0)
+        for (int head = 0; head < a.Hkv; ++head) zero_rows<D>(a, b, head, 0, a.Lq * a.G);
+    if (n0 >= n1) return;
+  }
+  // warp w's run of steps is [run(w), run(w + 1))
+  const int quota_w = (n1 - n0 + kW - 1) / kW, warps = (n1 - n0 + quota_w - 1) / quota_w;  // warps with a run
+  auto run = [&](int w) { return min(n0 + quota_w * w, n1); };
+  if (warp < warps) {
+    const int at = run(warp);
+    if (!a.split) {
+      if (lane == 0) s_start[warp] = make_int4((int)blockIdx.x / hr_all, (int)blockIdx.x % hr_all, at, n1);
+    } else if (int first = incl - mine; first <= at && at < incl) {
       for (int b = b0; b < b1; ++b) {
         const int n = seq_steps(a, b);
-        if (n0 < first + n * hr_all) {
-          s_start = make_int4(b, (n0 - first) / n, (n0 - first) % n, n);
+        if (at < first + n * hr_all) {
+          s_start[warp] = make_int4(b, (at - first) / n, (at - first) % n, n);
           break;
         }
         first += n * hr_all;
       }
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // sequences without any token
-      if (seq_len(a, b) == 0)
-        for (int head = 0; head < a.Hkv; ++head) zero_rows<D>(a, b, head, 0, a.Lq * a.G);
-    if (n0 >= n1) {
-      if (tid == 0) a.job[blockIdx.x] = make_int4(-1, 0, 0, 0);
-      return;
     }
-    __syncthreads();
   }
-
-  // warp w's run of steps is [run(w), run(w + 1))
-  const int quota_w = (n1 - n0 + kW - 1) / kW;
-  auto run = [&](int w) { return min(n0 + quota_w * w, n1); };
+  if (warp < kW && lane == 0) s_first[warp] = s_last[warp] = make_int4(0, 0, 0, 0);
+  __syncthreads();
 
   // ---- the warp that requests: lane w keeps warp w's ring filled ---------------------------------
   if (warp == kW) {
-    if (lane < kW) {
+    if (lane < warps) {
     const int bpp = (int)a.bpp.d;
     const uint32_t ring = smem_u32(smem) + lane * kS * C::kStepBytes;
     uint64_t* full = bars + lane * kS;
     uint64_t* empty = bars + (kW + lane) * kS;
-    Cursor pc{s_start.x, s_start.y, s_start.z, s_start.w};
+    Cursor pc{s_start[lane].x, s_start[lane].y, s_start[lane].z, s_start[lane].w};
     int pn = run(lane);  // next step to request
     const int pn1 = run(lane + 1);
-    if (pn < pn1) advance(a, pc, pn - n0);
     int slot = 0, pg0 = 0, pg1 = 0, blk = 0, col0 = 0, last = 0;
     uint32_t parity = 1;  // the first round finds every stage free
     auto look_up = [&]() {  // the pages of the two blocks of the step at pc
@@ -301,7 +296,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
     };
     auto next = [&](int by) {  // to the next step with tokens
       pn += by;
-      if (pn < pn1) advance(a, pc, by);
+      if (by && pn < pn1) advance(a, pc, by);
       while (pn < pn1 && pc.s < kLead) {
         pn += 1;
         if (pn < pn1) advance(a, pc, 1);
@@ -354,9 +349,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   uint32_t parity = 0;
   bool alive = true;
   const int r0 = run(warp), r1 = run(warp + 1);
-  Cursor u{s_start.x, s_start.y, s_start.z, s_start.w};
-  if (r0 < r1) advance(a, u, r0 - n0);
-  if (lane == 0) s_first[warp] = s_last[warp] = make_int4(0, 0, 0, 0);
+  Cursor u{s_start[warp].x, s_start[warp].y, s_start[warp].z, s_start[warp].w};  // of no meaning without a run
   for (int at = r0; at < r1;) {
     const int end = min(at + (u.n - u.s), r1);  // of this warp's part of the unit
     const int len = seq_len(a, u.b), head = (int)quot(u.hr, a.rb), rb = u.hr - head * a.RB;
@@ -605,7 +598,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
       const bool open_left = u.s > 0, open_right = at + (u.n - u.s) > r1, whole = !open_left && !open_right;
       float* dst = open_left ? join + warp * C::kRows * C::kJoinPitch : const_cast<float*>(reinterpret_cast<const float*>(ring));
       float2* mld = ml + ((open_left ? 0 : kW) + warp) * C::kRows;
-      if (lane == 0 && !whole) (open_left ? s_first : s_last)[warp] = make_int4(u.b, u.hr, !open_right, 1);
+      if (lane == 0 && !whole)
+        (open_left ? s_first : s_last)[warp] = make_int4(u.b, u.hr, at - u.s, open_right ? kPart : kPart | kEnds);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -661,103 +655,131 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   }  // of the warps that compute
 
   // ---- join the parts of the warps -----------------------------------------------------------------
-  // A unit in parts is a first part of the CTA's first warp (its beginning lies in an earlier CTA) or a warp's last
-  // part, and the first parts of the warps behind it, up to one that ends it or the CTA's end.
+  // The parts of a unit are consecutive among first(0), last(0), first(1), last(1) ..: chain c starts with the last part
+  // of warp c - 1 (chain 0 with the first part of warp 0: that unit began in an earlier CTA) and goes on with the first
+  // parts of warps c .. up to one that ends the unit, or to the CTA's end.
   __syncthreads();
-  const int warps = (n1 - n0 + quota_w - 1) / quota_w;  // with a run
-  if (a.split && tid == 0) {  // a unit that spans CTAs is named once, by the second of them
-    int4 j = make_int4(-1, 0, 0, 0);
-    if (s_start.z > 0 && s_start.z <= quota)
-      j = make_int4(s_start.x, s_start.y, (int)blockIdx.x - 1, (n0 + (s_start.w - s_start.z) - 1) / quota);
-    a.job[blockIdx.x] = j;
+  const int4 none = make_int4(0, 0, 0, 0), info_f = lane < warps ? s_first[lane] : none, info_l = lane < warps ? s_last[lane] : none;
+  const unsigned has_f = __ballot_sync(0xffffffffu, info_f.w & kPart), ends_f = __ballot_sync(0xffffffffu, info_f.w & kEnds);
+  const unsigned has_l = __ballot_sync(0xffffffffu, info_l.w & kPart);
+  const unsigned chains = (has_l << 1) | (has_f & 1u);
+  if (chains == 0) return;
+  auto chain_end = [&](int ch) { return ends_f >> ch ? ch + __ffs(ends_f >> ch) - 1 : warps - 1; };  // its last warp
+  float4* fac = reinterpret_cast<float4*>(smem + C::kOffFac);
+  for (int i = tid; i < 2 * kW * C::kRows; i += C::kThreads) {
+    const int p = i / C::kRows, row = i % C::kRows, w = p < kW ? p : p - kW;
+    if (!((p < kW ? has_f : has_l) >> w & 1u)) continue;
+    const int ch = p < kW ? 31 - __clz(chains & ((2u << w) - 1u)) : w + 1, w_end = chain_end(ch);
+    float top = kNoMax;
+    if (ch > 0) top = ml[(kW + ch - 1) * C::kRows + row].x;
+#pragma unroll 4
+    for (int k = ch; k <= w_end; ++k) top = fmaxf(top, ml[k * C::kRows + row].x);
+    const float2 x = ml[i];
+    const float f = ex2(x.x - top);
+    fac[i] = make_float4(f, x.y * f, top, 0.f);
   }
-  for (int chain = -1; chain < warps; ++chain) {  // -1: the first warp's first part, w: warp w's last part
-    const int w0 = max(chain, 0);
-    const int4 head_part = chain < 0 ? s_first[0] : s_last[w0];
-    if (!head_part.w) continue;
-    bool ends = head_part.z;
-    int w_end = w0;  // last warp of the unit
-    while (!ends && w_end + 1 < warps) ends = s_first[++w_end].z;
-    const bool begins = chain >= 0, whole = begins && ends;
-    const int head = (int)quot(head_part.y, a.rb), row0 = (head_part.y - head * a.RB) * C::kRows;
-    float* part = a.part + ((long long)blockIdx.x * 2 + (ends ? 0 : 1)) * C::kRows * (D + 2);
-    for (int i = tid; i < C::kRows * (D / 4); i += C::kThreads) {
-      const int row = i / (D / 4), ch = i % (D / 4) * 4, r_all = row0 + row;
-      if (r_all >= a.Lq * a.G) continue;
-      float top = kNoMax, ls = 0.f;
-      for (int w = w0; w <= w_end; ++w) top = fmaxf(top, ml[((begins && w == w0 ? kW : 0) + w) * C::kRows + row].x);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = w0; w <= w_end; ++w) {
-        const bool last = begins && w == w0;
-        const float2 y = ml[((last ? kW : 0) + w) * C::kRows + row];
-        const float f = ex2(y.x - top);
-        ls = fmaf(y.y, f, ls);
-        const float* src = last ? reinterpret_cast<const float*>(smem + w * kS * C::kStepBytes) : join + w * C::kRows * C::kJoinPitch;
-        const float4 z = *reinterpret_cast<const float4*>(src + row * C::kJoinPitch + ch);
-        x.x = fmaf(z.x, f, x.x), x.y = fmaf(z.y, f, x.y), x.z = fmaf(z.z, f, x.z), x.w = fmaf(z.w, f, x.w);
-      }
-      if (whole) {
-        const float inv = ls == 0.f ? 0.f : 1.f / ls;
-        __half* y = a.out + (((long long)head_part.x * a.Lq + r_all / a.G) * a.Hq + head * a.G + r_all % a.G) * D + ch;
-        *reinterpret_cast<uint2*>(y) = make_uint2(pack_h2(x.x * inv, x.y * inv), pack_h2(x.z * inv, x.w * inv));
-      } else {
-        float* p = part + row * (D + 2);
-        p[ch] = x.x, p[ch + 1] = x.y, p[ch + 2] = x.z, p[ch + 3] = x.w;
-        if (ch == 0) p[D] = top, p[D + 1] = ls;
-      }
+  __syncthreads();
+  constexpr int kPitch = D + 4;  // floats per row of a part in the workspace: O, m, l
+  for (int i = tid; i < __popc(chains) * C::kRows * (D / 4); i += C::kThreads) {
+    const int k = i / (C::kRows * (D / 4)), row = i / (D / 4) % C::kRows, q4 = i % (D / 4) * 4;
+    unsigned rest = chains;
+    for (int x = 0; x < k; ++x) rest &= rest - 1u;
+    const int ch = __ffs(rest) - 1, w_end = chain_end(ch);
+    const bool ends = (ends_f >> ch) != 0, whole = ch > 0 && ends;
+    const int4 info = ch > 0 ? s_last[ch - 1] : s_first[0];
+    const int head = (int)quot(info.y, a.rb), r_all = (info.y - head * a.RB) * C::kRows + row;
+    if (r_all >= a.Lq * a.G) continue;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float ls = 0.f;
+    auto add = [&](const float4& f, const float* src) {
+      const float4 z = *reinterpret_cast<const float4*>(src + row * C::kJoinPitch + q4);
+      x.x = fmaf(z.x, f.x, x.x), x.y = fmaf(z.y, f.x, x.y), x.z = fmaf(z.z, f.x, x.z), x.w = fmaf(z.w, f.x, x.w);
+      ls += f.y;
+    };
+    if (ch > 0) add(fac[(kW + ch - 1) * C::kRows + row], reinterpret_cast<const float*>(smem + (ch - 1) * kS * C::kStepBytes));
+#pragma unroll 4
+    for (int w = ch; w <= w_end; ++w) add(fac[w * C::kRows + row], join + w * C::kRows * C::kJoinPitch);
+    if (whole) {
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      __half* y = a.out + (((long long)info.x * a.Lq + r_all / a.G) * a.Hq + head * a.G + r_all % a.G) * D + q4;
+      *reinterpret_cast<uint2*>(y) = make_uint2(pack_h2(x.x * inv, x.y * inv), pack_h2(x.z * inv, x.w * inv));
+    } else {
+      float* p = a.part + (((long long)blockIdx.x * 2 + (ends ? 0 : 1)) * C::kRows + row) * kPitch;
+      *reinterpret_cast<float4*>(p + q4) = x;
+      if (q4 == 0) *reinterpret_cast<float2*>(p + D) = make_float2(fac[(ch > 0 ? kW + ch - 1 : 0) * C::kRows + row].z, ls);
     }
   }
-}
 
-// Joins the parts of the units that span CTAs, in the CTAs' order: CTA (c, row) handles that row of job c.
-template <int D>
-__global__ void __launch_bounds__(D) attn_kv_i4_join_kernel(const Args a, int rows_per_block) {
-  __shared__ float s_f[kMaxCtas], s_top[D / 32], s_l[D / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  grid_dependents_launch();
-  grid_dependency_wait();
-  const int4 job = a.job[blockIdx.x];
-  if (job.x < 0) return;
-  const int row = blockIdx.y, head = (int)quot(job.y, a.rb), rb = job.y - head * a.RB;
-  const int r_all = rb * rows_per_block + row;
-  if (r_all >= a.Lq * a.G) return;
-  // a CTA leaves its part in slot 1 where the unit goes on in the next CTA, in slot 0 where it ends
-  auto part = [&](int cta) {
-    return a.part + (((long long)cta * 2 + (cta < job.w ? 1 : 0)) * rows_per_block + row) * (D + 2);
-  };
-  float m[kMaxCtas / D], l[kMaxCtas / D], top = kNoMax;
-#pragma unroll
-  for (int k = 0; k < kMaxCtas / D; ++k) {
-    const int i = job.z + threadIdx.x + k * D;
-    m[k] = i <= job.w ? part(i)[D] : kNoMax;
-    l[k] = i <= job.w ? part(i)[D + 1] : 0.f;
-    top = fmaxf(top, m[k]);
-  }
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  if (lane == 0) s_top[warp] = top;
+  // ---- join the parts of the CTAs: whoever finds a unit's parts complete -----------------------------
+  // The one that goes on behind the CTA's range is in the last chain, the one that began before it in chain 0.
+  const bool into = (chains & 1u) != 0;
+  const int last_chain = 31 - __clz(chains);
+  const bool on = (ends_f >> last_chain) == 0;
+  if (!into && !on) return;
+  __threadfence();
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < D / 32; ++w) top = fmaxf(top, s_top[w]);
-  float ls = 0.f;
-#pragma unroll
-  for (int k = 0; k < kMaxCtas / D; ++k) {
-    const float f = ex2(m[k] - top);
-    s_f[threadIdx.x + k * D] = f;
-    ls += l[k] * f;
+  if (tid == 0) {
+    if (into && ends_f) atomicExch(a.flag + 2 * blockIdx.x, kThere);
+    if (on) atomicExch(a.flag + 2 * blockIdx.x + 1, kThere);
   }
+  __threadfence();
+  for (int side = 0; side < 2; ++side) {
+    if (!(side ? on : into && ends_f != 0)) continue;
+    __syncthreads();
+    __threadfence();
+    const int ch = side ? last_chain : 0;
+    const int4 info = ch > 0 ? s_last[ch - 1] : s_first[0];
+    const int n = seq_steps(a, info.x);
+    const int c0 = info.z / quota, c1 = (info.z + n - 1) / quota, parts = c1 - c0 + 1;  // the unit's CTAs
+    bool there = true;
+    for (int i = tid; i < parts; i += C::kThreads)
+      there &= *reinterpret_cast<volatile unsigned long long*>(a.flag + 2 * (c0 + i) + (i < parts - 1 ? 1 : 0)) == kThere;
+    if (tid == 0) s_all = 0;
+    if (!__syncthreads_and(there)) continue;
+    if (tid == 0) s_all = atomicCAS(a.flag + 2 * c0 + 1, kThere, 0ull) == kThere;  // one of those who find them
+    __syncthreads();
+    if (!s_all) continue;
+    __threadfence();
+    for (int i = 1 + tid; i < parts; i += C::kThreads) a.flag[2 * (c0 + i) + (i < parts - 1 ? 1 : 0)] = 0ull;
+    const int head = (int)quot(info.y, a.rb), row0 = (info.y - head * a.RB) * C::kRows;
+    auto part = [&](int i, int row) {
+      return a.part + (((long long)(c0 + i) * 2 + (i < parts - 1 ? 1 : 0)) * C::kRows + row) * kPitch;
+    };
+    float2* fp = reinterpret_cast<float2*>(smem);  // [kRows][parts] {factor, its l}, over the rings
+    for (int row = warp; row < C::kRows; row += kW + 1) {
+      float top = kNoMax;
+      for (int i = lane; i < parts; i += 32) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(part(i, row) + D));
+        fp[row * parts + i] = x;
+        top = fmaxf(top, x.x);
+      }
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
-  if (lane == 0) s_l[warp] = ls;
-  __syncthreads();
-  ls = 0.f;
-#pragma unroll
-  for (int w = 0; w < D / 32; ++w) ls += s_l[w];
-  float s = 0.f;
+      for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      for (int i = lane; i < parts; i += 32) {
+        const float2 x = fp[row * parts + i];
+        const float f = ex2(x.x - top);
+        fp[row * parts + i] = make_float2(f, x.y * f);
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < C::kRows * (D / 4); i += C::kThreads) {
+      const int row = i / (D / 4), q4 = i % (D / 4) * 4, r_all = row0 + row;
+      if (r_all >= a.Lq * a.G) continue;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ls = 0.f;
 #pragma unroll 8
-  for (int i = job.z; i <= job.w; ++i) s = fmaf(part(i)[threadIdx.x], s_f[i - job.z], s);
-  const float y = ls == 0.f ? 0.f : s / ls;
-  a.out[(((long long)job.x * a.Lq + r_all / a.G) * a.Hq + head * a.G + r_all % a.G) * D + threadIdx.x] = __float2half_rn(y);
+      for (int k = 0; k < parts; ++k) {
+        const float2 f = fp[row * parts + k];
+        const float4 z = __ldcg(reinterpret_cast<const float4*>(part(k, row) + q4));
+        x.x = fmaf(z.x, f.x, x.x), x.y = fmaf(z.y, f.x, x.y), x.z = fmaf(z.z, f.x, x.z), x.w = fmaf(z.w, f.x, x.w);
+        ls += f.y;
+      }
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      __half* y = a.out + (((long long)info.x * a.Lq + r_all / a.G) * a.Hq + head * a.G + r_all % a.G) * D + q4;
+      *reinterpret_cast<uint2*>(y) = make_uint2(pack_h2(x.x * inv, x.y * inv), pack_h2(x.z * inv, x.w * inv));
+    }
+    __syncthreads();
+  }
 }
 
 int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
@@ -774,7 +796,7 @@ cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
   }
-  // Both launches may start before the kernel ahead of them has ended, and wait for it before they read anything.
+  // The launch may start before the kernel ahead of it has ended; it waits for it before it reads anything.
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -785,21 +807,16 @@ cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_kv_i4_kernel<D, NT>, a);
-  if (e != cudaSuccess || !a.split || ctas == 1) return e;
-  cfg.gridDim = dim3(ctas, C::kRows < a.Lq * a.G ? C::kRows : a.Lq * a.G, 1);
-  cfg.blockDim = dim3(D, 1, 1);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_kv_i4_join_kernel<D>, a, (int)C::kRows);
+  return cudaLaunchKernelEx(&cfg, attn_kv_i4_kernel<D, NT>, a);
 }
 
 }  // namespace
 
-// Two parts per CTA (a CTA's first and its last unit may span CTAs) and a job word per CTA.
+// Per CTA two parts of units that span CTAs, and their flags.
 size_t attn_kv_i4_workspace_bytes(int B, int Lq, int Hq, int Hkv, int D) {
   const int rows = 8 * row_tiles(Lq * (Hq / Hkv));
   (void)B;
-  return (size_t)num_sms() * (2 * (size_t)rows * (D + 2) * 4 + 16);
+  return (size_t)num_sms() * 2 * ((size_t)rows * (D + 4) * 4 + 8);
 }
 
 cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int Lq, int Hq, int Hkv, int D,
@@ -822,20 +839,21 @@ cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int 
   a.bpp = fast_div(ps / kKvBlock);
   a.rb = fast_div(a.RB);
   a.out = reinterpret_cast<__half*>(out);
-  a.job = static_cast<int4*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 16 * (size_t)sms);
+  a.part = static_cast<float*>(workspace);
+  a.flag = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) +
+                                                 (size_t)sms * 2 * 8 * nt * (D + 4) * sizeof(float));
   a.err = dev_err;
   a.cap = width * ps;
   // A CTA per unit where they fit the card at once and none can be long (four steps for every warp): one launch and
-  // nothing to join across CTAs.  Otherwise an even share of all steps for every SM, but no more CTAs than the longest
-  // possible lengths could use, and the joining kernel behind it.
+  // nothing to join between CTAs.  Otherwise an even share of all steps for every SM, but no more CTAs than the longest
+  // possible lengths could use.
   const long long units = (long long)B * Hkv * a.RB, most = (a.cap + kStep - 1) / kStep + kLead;
   if (units * most > INT_MAX) {
     *err = "more than 2^31 - 1 steps of 32 tokens fit the block table";
     return cudaErrorInvalidValue;
   }
   a.split = units > sms || most > 4 * 12 + kLead;
-  const int ctas = (int)(!a.split ? units : units * most < sms ? units * most : sms < kMaxCtas ? sms : kMaxCtas);
+  const int ctas = (int)(!a.split ? units : units * most < sms ? units * most : sms);
   if (D == 128) return nt == 1 ? launch<128, 1>(a, ctas, s) : launch<128, 2>(a, ctas, s);
   return nt == 1 ? launch<64, 1>(a, ctas, s) : launch<64, 2>(a, ctas, s);
 }
