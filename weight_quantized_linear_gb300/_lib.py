@@ -507,9 +507,22 @@ def kv_dequant_i8(q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | Non
 
 
 # ---- paged KV cache in 4 bits, and attention -----------------------------------------------------
+#
+# A decode step makes these calls once per layer on little data, so their checks are written to cost little: one test
+# per tensor (_is), and the one that names what is wrong (_refuse) only when it fails.
 
-def _rows(t: torch.Tensor, name: str, heads: int | None = None, dim: int | None = None) -> int:
-    """Check an fp16 CUDA tensor [T, heads, D] whose rows [heads, D] are dense (a view of a fused projection's
+def _is(t, dtype: torch.dtype, shape: tuple, dev: torch.device) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous())
+
+
+def _refuse(t, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device) -> None:
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _stride_of(t, name: str, heads: int | None, dim: int | None, tokens: int | None, dev: torch.device | None) -> int:
+    """Check an fp16 CUDA tensor [tokens, heads, D] whose rows [heads, D] are dense (a view of a fused projection's
     output); returns its token stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -517,12 +530,18 @@ def _rows(t: torch.Tensor, name: str, heads: int | None = None, dim: int | None 
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.float16:
         raise TypeError(f"{name} must have dtype {torch.float16}, got {t.dtype}")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
-        raise ValueError(f"{name} must have shape [tokens, {heads or 'heads'}, {dim or 'D'}], got {tuple(t.shape)}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape [tokens, heads, D], got {tuple(t.shape)}")
     T, H, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
-        raise ValueError(f"{name} must be dense within a token (strides [any, {D}, 1], got {tuple(t.stride())})")
-    return t.stride(0) if T > 1 else H * D
+    if (heads is not None and H != heads) or (dim is not None and D != dim) or (tokens is not None and T != tokens):
+        raise ValueError(f"{name} must have shape [{'tokens' if tokens is None else tokens}, "
+                         f"{'heads' if heads is None else heads}, {'D' if dim is None else dim}], got {tuple(t.shape)}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name} must be dense within a token (strides [any, {D}, 1], got {(st, sh, sd)})")
+    return st if T > 1 else H * D
 
 
 def _cache_dims(cache: torch.Tensor):
@@ -531,15 +550,27 @@ def _cache_dims(cache: torch.Tensor):
         raise TypeError("cache must be a torch.Tensor")
     if cache.dim() != 4 or cache.shape[3] % 16 != 0:
         raise ValueError("cache must be [pages, heads, page_size / 16, 16 (D + 8)]; see kv_cache_i4")
-    _need(cache, "cache", torch.uint8, tuple(cache.shape))
+    if not (cache.dtype == torch.uint8 and cache.is_cuda and cache.is_contiguous()):
+        _need(cache, "cache", torch.uint8, tuple(cache.shape))
     pages, H, blocks, nbytes = cache.shape
     return pages, H, 16 * blocks, nbytes // 16 - 8
 
 
-def _same_device(ref: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+# the current stream's handle without a Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(fn: str, dev: torch.device, *args) -> None:
+    """Call fn(*args, stream) with dev current, on dev's current stream."""
+    lib = _lib or load()
+    if torch.cuda.current_device() == dev.index:
+        status = getattr(lib, fn)(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib, fn)(*args, _raw_stream(dev.index))
+    if status != WQL_OK:
+        _check(status, fn)
 
 
 def kv_cache_i4(pages: int, heads: int, head_dim: int, page_size: int, device=None) -> torch.Tensor:
@@ -559,24 +590,20 @@ def kv_plan_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     pages are written in place; free_pages [F] int32 with free_count [1] int32 of them free.  Returns (slots
     [tokens], cu_new [B + 1], kv_lens [B], free_count_out [1]), int32; slots behind the last new token and those of
     refused requests are -1, kv_lens of refused requests 0.  See wql_kv_plan_pages in include/wql.h."""
-    B = ctx_lens.shape[0]
-    _need(ctx_lens, "ctx_lens", torch.int32, (B,))
-    _need(new_lens, "new_lens", torch.int32, (B,))
-    width = block_table.shape[-1]
-    _need(block_table, "block_table", torch.int32, (B, width))
-    F = free_pages.shape[0]
-    _need(free_pages, "free_pages", torch.int32, (F,))
-    _need(free_count, "free_count", torch.int32, (1,))
+    i32, B, width, F = torch.int32, ctx_lens.shape[0], block_table.shape[-1], free_pages.shape[0]
     dev = ctx_lens.device
-    _same_device(ctx_lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages, free_count=free_count)
+    for t, name, shape in ((ctx_lens, "ctx_lens", (B,)), (new_lens, "new_lens", (B,)),
+                           (block_table, "block_table", (B, width)), (free_pages, "free_pages", (F,)),
+                           (free_count, "free_count", (1,))):
+        if not (t.is_cuda and _is(t, i32, shape, dev)):
+            _refuse(t, name, i32, shape, dev)
     # one allocation: slots first (its start is 16-byte aligned), then the small outputs
-    out = torch.empty((tokens + 2 * B + 2,), dtype=torch.int32, device=dev)
-    slots, cu_new = out[:tokens], out[tokens:tokens + B + 1]
-    kv_lens, left = out[tokens + B + 1:tokens + 2 * B + 1], out[tokens + 2 * B + 1:]
-    with torch.cuda.device(dev):
-        _check(load().wql_kv_plan_pages(_ptr(ctx_lens), _ptr(new_lens), B, page_size, _ptr(free_pages), F,
-                                        _ptr(free_count), _ptr(block_table), width, tokens, _ptr(cu_new),
-                                        _ptr(kv_lens), _ptr(slots), _ptr(left), _stream(dev)), "wql_kv_plan_pages")
+    out = torch.empty((tokens + 2 * B + 2,), dtype=i32, device=dev)
+    slots, cu_new, kv_lens, left = out.split((tokens, B + 1, B, 1))
+    p = out.data_ptr()
+    _run("wql_kv_plan_pages", dev, ctx_lens.data_ptr(), new_lens.data_ptr(), B, page_size, free_pages.data_ptr(), F,
+         free_count.data_ptr(), block_table.data_ptr(), width, tokens, p + 4 * tokens, p + 4 * (tokens + B + 1), p,
+         p + 4 * (tokens + 2 * B + 1))
     return slots, cu_new, kv_lens, left
 
 
@@ -584,15 +611,14 @@ def kv_append_i4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: t
     """Quantise rows k, v [T, heads, D] fp16 (views of a fused QKV output are taken as they are) into the 4-bit
     cache at slots [T] int32; negative slots are passed over.  Returns cache."""
     pages, H, ps, D = _cache_dims(cache)
+    dev = cache.device
+    ks = _stride_of(k, "k", H, D, None, dev)
     T = k.shape[0]
-    ks, vs = _rows(k, "k", H, D), _rows(v, "v", H, D)
-    if v.shape[0] != T:
-        raise ValueError(f"v must have {T} tokens, got {v.shape[0]}")
-    _need(slots, "slots", torch.int32, (T,))
-    _same_device(cache, k=k, v=v, slots=slots)
-    with torch.cuda.device(cache.device):
-        _check(load().wql_kv_append_i4(_ptr(k), _ptr(v), ks, vs, T, H, D, _ptr(slots), _ptr(cache), pages, ps,
-                                       _stream(cache.device)), "wql_kv_append_i4")
+    vs = _stride_of(v, "v", H, D, T, dev)
+    if not _is(slots, torch.int32, (T,), dev):
+        _refuse(slots, "slots", torch.int32, (T,), dev)
+    _run("wql_kv_append_i4", dev, k.data_ptr(), v.data_ptr(), ks, vs, T, H, D, slots.data_ptr(), cache.data_ptr(), pages,
+         ps)
     return cache
 
 
@@ -600,18 +626,19 @@ def kv_read_i4(cache: torch.Tensor, slots: torch.Tensor, k: torch.Tensor | None 
                v: torch.Tensor | None = None):
     """(k, v) [T, heads, D] fp16: the values of the 4-bit cache at slots [T] int32; zeros for negative slots."""
     pages, H, ps, D = _cache_dims(cache)
-    T = slots.shape[0]
-    _need(slots, "slots", torch.int32, (T,))
+    dev, T, f16 = cache.device, slots.shape[0], torch.float16
+    shape = (T, H, D)
+    if not _is(slots, torch.int32, (T,), dev):
+        _refuse(slots, "slots", torch.int32, (T,), dev)
     if k is None:
-        k = torch.empty((T, H, D), dtype=torch.float16, device=cache.device)
+        k = torch.empty(shape, dtype=f16, device=dev)
+    elif not _is(k, f16, shape, dev):
+        _refuse(k, "k", f16, shape, dev)
     if v is None:
-        v = torch.empty((T, H, D), dtype=torch.float16, device=cache.device)
-    _need(k, "k", torch.float16, (T, H, D))
-    _need(v, "v", torch.float16, (T, H, D))
-    _same_device(cache, k=k, v=v, slots=slots)
-    with torch.cuda.device(cache.device):
-        _check(load().wql_kv_read_i4(_ptr(cache), pages, ps, H, D, _ptr(slots), T, _ptr(k), _ptr(v),
-                                     _stream(cache.device)), "wql_kv_read_i4")
+        v = torch.empty(shape, dtype=f16, device=dev)
+    elif not _is(v, f16, shape, dev):
+        _refuse(v, "v", f16, shape, dev)
+    _run("wql_kv_read_i4", dev, cache.data_ptr(), pages, ps, H, D, slots.data_ptr(), T, k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -626,31 +653,39 @@ def attention_kv_i4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
 
     q [B, Hq, D] (one token each) or [B, Lq, Hq, D] fp16, its tokens evenly strided; block_table [B, width] and
     kv_lens [B] int32, the queried tokens counted in.  Row r of Lq sees the tokens up to kv_lens - Lq + r; a row that
-    sees none is zero.  scale defaults to D ** -0.5.  Returns out, dense, of q's shape."""
+    sees none is zero.  scale defaults to D ** -0.5.  workspace: uint8, attention_kv_i4_workspace_bytes() of them,
+    allocated here if not given.  Returns out, dense, of q's shape."""
     pages, Hkv, ps, D = _cache_dims(cache)
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be a tensor [B, Hq, D] or [B, Lq, Hq, D]")
-    B, Lq, Hq = q.shape[0], 1 if q.dim() == 3 else q.shape[1], q.shape[-2]
-    if q.dim() == 4 and B > 1 and Lq > 1 and q.stride(0) != Lq * q.stride(1):
-        raise ValueError("the tokens of q must be evenly strided")
-    rows = q if q.dim() == 3 else q[:, 0] if Lq == 1 else q.as_strided((B * Lq, Hq, q.shape[-1]), q.stride()[1:])
-    qs = _rows(rows, "q", None, D)
+    dev, shape = cache.device, q.shape
+    B, Hq = shape[0], shape[-2]
+    if len(shape) == 3:
+        Lq, rows = 1, q
+    else:
+        Lq = shape[1]
+        if B > 1 and Lq > 1 and q.stride(0) != Lq * q.stride(1):
+            raise ValueError("the tokens of q must be evenly strided")
+        rows = q[:, 0] if Lq == 1 else q.as_strided((B * Lq, Hq, shape[3]), q.stride()[1:])
+    qs = _stride_of(rows, "q", None, D, None, dev)
     width = block_table.shape[-1]
-    _need(block_table, "block_table", torch.int32, (B, width))
-    _need(kv_lens, "kv_lens", torch.int32, (B,))
+    if not _is(block_table, torch.int32, (B, width), dev):
+        _refuse(block_table, "block_table", torch.int32, (B, width), dev)
+    if not _is(kv_lens, torch.int32, (B,), dev):
+        _refuse(kv_lens, "kv_lens", torch.int32, (B,), dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
-    _need(out, "out", torch.float16, tuple(q.shape))
-    _same_device(cache, q=q, block_table=block_table, kv_lens=kv_lens, out=out)
-    with torch.cuda.device(cache.device):
-        if workspace is None:
-            workspace = torch.empty((attention_kv_i4_workspace_bytes(B, Lq, Hq, Hkv, D),), dtype=torch.uint8,
-                                    device=q.device)
-        _same_device(cache, workspace=workspace)
-        _check(load().wql_attention_kv_i4(_ptr(q), qs, B, Lq, Hq, Hkv, D, _ptr(cache), pages, ps, _ptr(block_table),
-                                          width, _ptr(kv_lens), D ** -0.5 if scale is None else scale, _ptr(out),
-                                          _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                          _stream(cache.device)), "wql_attention_kv_i4")
+        out = torch.empty(shape, dtype=torch.float16, device=dev)
+    elif not _is(out, torch.float16, shape, dev):
+        _refuse(out, "out", torch.float16, tuple(shape), dev)
+    if workspace is None:
+        with torch.cuda.device(dev):
+            n = attention_kv_i4_workspace_bytes(B, Lq, Hq, Hkv, D)
+        workspace = torch.empty((n,), dtype=torch.uint8, device=dev)
+    elif not _is(workspace, torch.uint8, (workspace.numel(),), dev):
+        _refuse(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    _run("wql_attention_kv_i4", dev, q.data_ptr(), qs, B, Lq, Hq, Hkv, D, cache.data_ptr(), pages, ps,
+         block_table.data_ptr(), width, kv_lens.data_ptr(), D ** -0.5 if scale is None else scale, out.data_ptr(),
+         workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -659,21 +694,19 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     """Causal attention over packed prompts, grouped heads: q [T, Hq, D], k and v [T, Hkv, D] fp16 (views of a fused
     QKV output are taken as they are), cu_seqlens [B + 1] int32.  scale defaults to D ** -0.5.  Returns out
     [T, Hq, D], dense; rows of no sequence are left as they were (undefined when out is not given)."""
-    qs = _rows(q, "q")
-    T, Hq, D = q.shape
-    ks = _rows(k, "k", None, D)
+    qs = _stride_of(q, "q", None, None, None, None)
+    dev, shape = q.device, q.shape
+    T, Hq, D = shape
+    ks = _stride_of(k, "k", None, D, T, dev)
     Hkv = k.shape[1]
-    vs = _rows(v, "v", Hkv, D)
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError(f"k and v must have {T} tokens, got {k.shape[0]} and {v.shape[0]}")
+    vs = _stride_of(v, "v", Hkv, D, T, dev)
     B = cu_seqlens.shape[0] - 1
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    if not _is(cu_seqlens, torch.int32, (B + 1,), dev):
+        _refuse(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.float16, device=q.device)
-    _need(out, "out", torch.float16, (T, Hq, D))
-    _same_device(q, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
-    with torch.cuda.device(q.device):
-        _check(load().wql_attention_prompt(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, T, Hq, Hkv, D, _ptr(cu_seqlens), B,
-                                           D ** -0.5 if scale is None else scale, _ptr(out), _stream(q.device)),
-               "wql_attention_prompt")
+        out = torch.empty(shape, dtype=torch.float16, device=dev)
+    elif not _is(out, torch.float16, shape, dev):
+        _refuse(out, "out", torch.float16, tuple(shape), dev)
+    _run("wql_attention_prompt", dev, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hkv, D,
+         cu_seqlens.data_ptr(), B, D ** -0.5 if scale is None else scale, out.data_ptr())
     return out

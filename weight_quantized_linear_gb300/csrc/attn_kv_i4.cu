@@ -210,7 +210,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   __shared__ int4 s_start[kW];              // the warps' first positions
   __shared__ int4 s_first[kW], s_last[kW];  // {sequence, head and row block, first step of the unit, kPart | kEnds}
-  __shared__ int s_all;
   constexpr int kPart = 1, kEnds = 2;       // there is such a part; the unit ends in it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
 
@@ -716,31 +715,29 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   const int last_chain = 31 - __clz(chains);
   const bool on = (ends_f >> last_chain) == 0;
   if (!into && !on) return;
-  __threadfence();
   __syncthreads();
   if (tid == 0) {
-    if (into && ends_f) atomicExch(a.flag + 2 * blockIdx.x, kThere);
-    if (on) atomicExch(a.flag + 2 * blockIdx.x + 1, kThere);
+    __threadfence();  // what the CTA has written, before its flags
+    if (into && ends_f) a.flag[2 * blockIdx.x] = kThere;
+    if (on) a.flag[2 * blockIdx.x + 1] = kThere;
+    __threadfence();  // its flags, before it looks at others'
   }
-  __threadfence();
   for (int side = 0; side < 2; ++side) {
     if (!(side ? on : into && ends_f != 0)) continue;
     __syncthreads();
-    __threadfence();
     const int ch = side ? last_chain : 0;
     const int4 info = ch > 0 ? s_last[ch - 1] : s_first[0];
     const int n = seq_steps(a, info.x);
     const int c0 = info.z / quota, c1 = (info.z + n - 1) / quota, parts = c1 - c0 + 1;  // the unit's CTAs
     bool there = true;
+    __threadfence();
     for (int i = tid; i < parts; i += C::kThreads)
       there &= *reinterpret_cast<volatile unsigned long long*>(a.flag + 2 * (c0 + i) + (i < parts - 1 ? 1 : 0)) == kThere;
-    if (tid == 0) s_all = 0;
+    // The last CTA to set its flag finds them all.  Others may too, if they look before that one has taken the flags
+    // back; they then write the same values.
     if (!__syncthreads_and(there)) continue;
-    if (tid == 0) s_all = atomicCAS(a.flag + 2 * c0 + 1, kThere, 0ull) == kThere;  // one of those who find them
-    __syncthreads();
-    if (!s_all) continue;
     __threadfence();
-    for (int i = 1 + tid; i < parts; i += C::kThreads) a.flag[2 * (c0 + i) + (i < parts - 1 ? 1 : 0)] = 0ull;
+    for (int i = tid; i < parts; i += C::kThreads) a.flag[2 * (c0 + i) + (i < parts - 1 ? 1 : 0)] = 0ull;
     const int head = (int)quot(info.y, a.rb), row0 = (info.y - head * a.RB) * C::kRows;
     auto part = [&](int i, int row) {
       return a.part + (((long long)(c0 + i) * 2 + (i < parts - 1 ? 1 : 0)) * C::kRows + row) * kPitch;
@@ -767,7 +764,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
       if (r_all >= a.Lq * a.G) continue;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       float ls = 0.f;
-#pragma unroll 8
+#pragma unroll 16
       for (int k = 0; k < parts; ++k) {
         const float2 f = fp[row * parts + k];
         const float4 z = __ldcg(reinterpret_cast<const float4*>(part(k, row) + q4));
