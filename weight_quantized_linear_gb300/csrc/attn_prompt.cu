@@ -9,12 +9,14 @@
 // S = Q K^T into tensor memory (tcgen05, both operands in shared memory), the tile's four softmax warps turn it
 // into weights P -- thread r owns row r, so neither maximum nor sum needs an exchange -- and write them over S as
 // fp16, and the tensor cores add P V to the tile's accumulator, P from tensor memory.  While one tile's softmax runs,
-// the tensor cores work on the other's products; 2 x (S 128 + O 128) columns fill tensor memory.  K and V tiles arrive
-// by TMA in a ring of kSlots 128-row tiles.
+// the tensor cores work on the other's products.  2 x (S 128 + O 128) columns fill tensor memory, so a tile's next S
+// waits for its P to be used, and a step takes a tile's two products plus its softmax's latency.  K and V tiles
+// arrive by TMA in a ring of kSlots 128-row tiles.
 //
-// The accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last time (the weights
-// are then still below 2^15), by the softmax warps themselves: S(j) complete implies P V(j - 1) complete, since
-// both were issued before the commit that signals S(j).
+// That latency is why the weights are computed with the maximum as it was, while the new one is still being found: the
+// accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last time (the weights are
+// then still below 2^15), and only then are the step's weights computed again.  The softmax warps rescale it
+// themselves: S(j) complete implies P V(j - 1) complete, since both were issued before the commit that signals S(j).
 //
 // Rows see nothing behind them: scores above the diagonal are replaced, not added to.  V rows behind a row would meet
 // its zero weights in the product, so in the tiles on the diagonal two warps first replace V values that are not
@@ -33,9 +35,9 @@ constexpr int kThreads = 384;               // warps 0-3, 4-7: softmax of tiles 
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kCheckWarp = 10;
 constexpr float kTop = 7.0f;                // the largest weight after a rescale is 2^7 ...
 constexpr float kRaise = 8.0f;              // ... and before the next at most 2^15
-// registers per thread: launched with 168; the softmax warpgroups take 216, the third gives down to 64
-// (2 x 128 x 216 + 128 x 64 = 63488 <= 384 x 168 = 64512)
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 64;
+// registers per thread: launched with 168; the softmax warpgroups take 208, the third gives down to 80
+// (2 x 128 x 208 + 128 x 80 = 63488 <= 384 x 168 = 64512)
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 
 template <int D>
 struct Cfg {
@@ -68,6 +70,11 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // Two fp32 at once.
 __device__ __forceinline__ void fma2(float& x, float& y, float a, float c) {
   asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n mov.b64 r, {%3, %3};\n"
@@ -80,6 +87,30 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
       " mov.b64 {%0, %1}, p;\n}"
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
+// Shared-memory descriptors whose upper word (8-row groups 1 KB apart, 128-byte swizzle) is the same for all tiles: the
+// lower word is the address / 16 and, for V, the distance of its 64-channel boxes / 16 above it.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(acc)
+      : "memory");
 }
 
 // Start and length of sequence b; an invalid one has no rows.
@@ -109,9 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* sbar = empty + C::kSlots;                               // [2] S complete
   uint64_t* pbar = sbar + 2;                                        // [2] P written (4 warps)
   uint64_t* obar = pbar + 2;                                        // [2] O complete
-  uint64_t* cbar = obar + 2;                                        // [1] V checked (2 warps)
-  uint64_t* vbar = cbar + 1;                                        // [1] V to be checked has landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vbar + 1);
+  uint64_t* cbar = obar + 2;                                        // [2] V(jcheck), V(jcheck + 1) checked (2 warps)
+  uint64_t* vbar = cbar + 2;                                        // [2] V(jcheck), V(jcheck + 1) landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vbar + 2);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // ---- the sequence and row tiles of this CTA, counted from the last one: the longest rows start first ----
@@ -153,8 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(qbar, 1);
     for (int s = 0; s < C::kSlots; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
     for (int x = 0; x < 2; ++x) mbar_init(&sbar[x], 1), mbar_init(&pbar[x], 4), mbar_init(&obar[x], 1);
-    mbar_init(cbar, 2);
-    mbar_init(vbar, 1);
+    for (int x = 0; x < 2; ++x) mbar_init(&cbar[x], 2), mbar_init(&vbar[x], 1);
     fence_mbarrier_init();
   }
   for (int i = tid; i < D; i += kThreads) bad[i] = INT_MAX;
@@ -208,82 +238,96 @@ __global__ void __launch_bounds__(kThreads, 1)
           report_error(a.err, kErrTimeoutDrain);
           break;
         }
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp) {
       // ---------------- the tensor cores' work, issued by one thread ----------------
+      // The whole warp walks through this, so that what the instructions take is uniform and stays in uniform
+      // registers; under a branch on the lane every operand of every product would be moved there first (16384 tokens,
+      // 32 heads: 1.82 ms).
+      const bool leader = elect_one();
       const uint32_t idesc_s = umma_idesc_f16(kTile, kTile, 0, 0) | a.negate;
       constexpr uint32_t idesc_o = umma_idesc_f16(kTile, D, /*A from TMEM*/ 0, /*B MN-major*/ 1);
-      const uint32_t q_smem = smem_u32(smem), ring = smem_u32(smem + C::kOffRing);
+      const uint32_t q_lo = smem_u32(smem) >> 4, ring_lo = smem_u32(smem + C::kOffRing) >> 4;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int phase) {
-        if (ok && !mbar_wait_bounded(bar, phase & 1)) {
-          report_error(a.err, kErrTimeoutMma);
+        if (ok && !mbar_wait_warp(bar, phase & 1)) {
+          if (leader) report_error(a.err, kErrTimeoutMma);
           ok = false;
         }
         return ok;
       };
-      auto qk = [&](int x, int j) {  // S_x = Q_x K(j)^T
-        const uint32_t slot = (uint32_t)(2 * j) % C::kSlots;
-        const uint64_t ad = umma_sdesc_sw128(q_smem + x * C::kTileBytes, 16, 1024);
-        const uint64_t bd = umma_sdesc_sw128(ring + slot * C::kTileBytes, 16, 1024);
+      auto commit = [&](uint64_t* bar) {
+        if (leader) umma_commit(bar);
+      };
+      auto qk = [&](int x, int slot) {  // S_x = Q_x K^T, K in `slot`
+        const uint32_t ad = (1u << 16) + q_lo + x * (C::kTileBytes >> 4), bd = (1u << 16) + ring_lo + slot * (C::kTileBytes >> 4);
+        if (leader) {
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint64_t off = (uint64_t)(((s >> 2) * C::kBox + (s & 3) * 32) >> 4);
-          umma_f16(tmem + x * kTile, ad + off, bd + off, idesc_s, s > 0);
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = ((s >> 2) * C::kBox + (s & 3) * 32) >> 4;
+            mma_ss(tmem + x * kTile, ad + off, bd + off, idesc_s, s > 0);
+          }
         }
       };
-      auto pv = [&](int x, int j) {  // O_x += P_x V(j)
-        const uint32_t slot = (uint32_t)(2 * j + 1) % C::kSlots;
-        const uint64_t bd = umma_sdesc_sw128(ring + slot * C::kTileBytes, C::kBox, 1024);
+      auto pv = [&](int x, int slot, uint32_t acc) {  // O_x (+)= P_x V, V in `slot`
+        const uint32_t bd = ((uint32_t)(C::kBox >> 4) << 16) + ring_lo + slot * (C::kTileBytes >> 4);
+        if (leader) {
 #pragma unroll
-        for (int s = 0; s < kTile / 16; ++s)
-          umma_f16_ta(tmem + 2 * kTile + x * D, tmem + x * kTile + s * 8, bd + (uint64_t)((s * 2048) >> 4), idesc_o,
-                      j > 0 || s > 0);
+          for (int s = 0; s < kTile / 16; ++s)
+            mma_ts(tmem + 2 * kTile + x * D, tmem + x * kTile + s * 8, bd + ((s * 2048) >> 4), idesc_o, s > 0 ? 1u : acc);
+        }
       };
       wait(qbar, 0);
       wait(&full[0], 0);
       if (ok) {
         tc_fence_after_sync();
         qk(0, 0);
-        umma_commit(&sbar[0]);
+        commit(&sbar[0]);
         if (n1 > 0) {
           qk(1, 0);
-          umma_commit(&sbar[1]);
+          commit(&sbar[1]);
         }
-        if (C::kSlots < 2 * nmax) umma_commit(&empty[0]);
+        if (C::kSlots < 2 * nmax) commit(&empty[0]);
       }
+      if (jcheck == 0 && wait(&full[1], 0) && leader) mbar_arrive(&vbar[0]);
+      int sv = 1, pv_phase = 0, sk = 2, k_phase = 0;  // slots and phases of V(j) and K(j + 1)
       for (int j = 0; j < nmax && ok; ++j) {
         const int iv = 2 * j + 1, ik = 2 * j + 2;  // ring items V(j) and K(j + 1)
-        wait(&full[iv % C::kSlots], iv / C::kSlots);
-        if (j >= jcheck && ok) mbar_arrive(vbar);
-        if (j + 1 < nmax) wait(&full[ik % C::kSlots], ik / C::kSlots);
+        wait(&full[sv], pv_phase);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int n = x ? n1 : n0;
           if (j >= n || !wait(&pbar[x], j)) continue;
-          if (j >= jcheck && !wait(cbar, j - jcheck)) continue;
+          if (j >= jcheck && !wait(&cbar[j - jcheck], 0)) continue;
           tc_fence_after_sync();
-          pv(x, j);
-          if (j + 1 < n) {
-            qk(x, j + 1);
-            umma_commit(&sbar[x]);
-          } else {
-            umma_commit(&obar[x]);
+          pv(x, sv, j > 0);
+          if (j + 1 < n && wait(&full[sk], k_phase)) {
+            tc_fence_after_sync();
+            qk(x, sk);
+            commit(&sbar[x]);
+          } else if (ok) {
+            commit(&obar[x]);
           }
         }
-        if (ok && iv + C::kSlots < 2 * nmax) umma_commit(&empty[iv % C::kSlots]);
-        if (ok && ik + C::kSlots < 2 * nmax) umma_commit(&empty[ik % C::kSlots]);
+        if (ok && iv + C::kSlots < 2 * nmax) commit(&empty[sv]);
+        if (ok && ik + C::kSlots < 2 * nmax) commit(&empty[sk]);
+        sv += 2;
+        if (sv >= C::kSlots) sv -= C::kSlots, pv_phase ^= 1;
+        sk += 2;
+        if (sk >= C::kSlots) sk -= C::kSlots, k_phase ^= 1;
+        // the next V is checked while its step's softmax runs
+        if (j + 1 >= jcheck && j + 1 < nmax && wait(&full[sv], pv_phase) && leader) mbar_arrive(&vbar[j + 1 - jcheck]);
       }
     } else if (warp >= kCheckWarp) {
       // ---------------- V tiles on a diagonal: values that are not finite ----------------
       for (int j = jcheck; j < nmax; ++j) {
         const int i = 2 * j + 1;
         // not on the ring's own barrier, which goes through phases that these warps do not follow
-        if (!mbar_wait_warp(vbar, (j - jcheck) & 1)) {
+        if (!mbar_wait_warp(&vbar[j - jcheck], 0)) {
           if (lane == 0) report_error(a.err, kErrTimeoutFull);
           break;
         }
         uint4* v = reinterpret_cast<uint4*>(smem + C::kOffRing + (i % C::kSlots) * C::kTileBytes);
-        constexpr int kBatch = 8;
+        constexpr int kBatch = 4;
         for (int at = tid - kCheckWarp * 32; at < C::kTileBytes / 16; at += 64 * kBatch) {
           uint4 x[kBatch];
 #pragma unroll
@@ -314,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(cbar);
+        if (lane == 0) mbar_arrive(&cbar[j - jcheck]);
       }
     }
   } else {
@@ -345,11 +389,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int i = 0; i < 128; i += 2)
-        top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1])));
-      const float up = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c - kTop;
-      if (j == 0) {
-        m = up;
-      } else if (__any_sync(0xffffffffu, up > m + kRaise)) {
+        top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
+      const float up = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c - kTop;
+      if (j == 0) m = up;
+      float a0, a1;  // this step's sums
+      auto weights = [&]() {
+        a0 = a1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float u = __uint_as_float(s[i][2 * e]), v = __uint_as_float(s[i][2 * e + 1]);
+            fma2(u, v, c, -m);
+            u = ex2(u), v = ex2(v);
+            add2(a0, a1, u, v);
+            p[e] = pack_h2(u, v);
+          }
+          tmem_st_32x32b_x16(ts + 16 * i, p);
+        }
+      };
+      weights();
+      if (__any_sync(0xffffffffu, up > m + kRaise)) {
         const float now = fmaxf(m, up), f = ex2(m - now);
         m = now;
         l0 *= f, l1 *= f;
@@ -362,20 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
           tmem_st_32x32b_x32(to + i, o);
         }
+        weights();
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t p[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float u = __uint_as_float(s[i][2 * e]), v = __uint_as_float(s[i][2 * e + 1]);
-          fma2(u, v, c, -m);
-          u = ex2(u), v = ex2(v);
-          add2(l0, l1, u, v);
-          p[e] = pack_h2(u, v);
-        }
-        tmem_st_32x32b_x16(ts + 16 * i, p);
-      }
+      l0 += a0, l1 += a1;
       tmem_st_wait();
       tc_fence_before_sync();
       __syncwarp();
@@ -385,13 +435,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait_warp(&obar[x], 0)) {
         if (lane == 0) report_error(a.err, kErrTimeoutMma);
       } else {
-        mbar_wait_warp(cbar, (nmax - 1 - jcheck) & 1);  // complete already where this tile used it
+        mbar_wait_warp(&cbar[nmax - 1 - jcheck], 0);  // complete already where this tile used it
         tc_fence_after_sync();
         const int r = (x ? r1 : q0) + row;
         const float inv = 1.f / (l0 + l1);
-        __half* dst = a.out + ((long long)(start + r) * a.Hq + (x ? h1 : h0)) * D;
         const bool poison = any_bad != 0;
-#pragma unroll 1
+        // through the tile's Q rows, which are not needed any more, so that whole lines are written
+        constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+        uint4* stage = reinterpret_cast<uint4*>(smem + x * C::kTileBytes) + (warp & 3) * 32 * kChunks;
+#pragma unroll
         for (int i = 0; i < D; i += 32) {
           uint32_t o[32];
           tmem_ld_32x32b_x32(to + i, o);
@@ -401,15 +453,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (r >= bad[i + e]) o[e] = 0x7fc00000u;
           }
-          if (r >= len) continue;
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint32_t h[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               h[k] = pack_h2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-            *reinterpret_cast<uint4*>(dst + i + e) = make_uint4(h[0], h[1], h[2], h[3]);
+            stage[lane * kChunks + (((i + e) >> 3) ^ (lane & (kChunks - 1)))] = make_uint4(h[0], h[1], h[2], h[3]);
           }
+        }
+        __syncwarp();
+        const int rw = (x ? r1 : q0) + (warp & 3) * 32;  // the warp's first row
+        __half* dst = a.out + ((long long)(start + rw) * a.Hq + (x ? h1 : h0)) * D;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int at = i * 32 + lane, rr = at / kChunks, ch = at % kChunks;
+          if (rw + rr < len)
+            *reinterpret_cast<uint4*>(dst + (long long)rr * a.Hq * D + 8 * ch) = stage[rr * kChunks + (ch ^ (rr & (kChunks - 1)))];
         }
       }
     }
