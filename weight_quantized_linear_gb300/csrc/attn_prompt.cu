@@ -4,14 +4,19 @@
 //   o[r] = sum_{j <= r} softmax_j(scale q[r] . k[j]) v[j],  k and v those of head h / (Hq / Hkv)
 // One pass over the keys with the running maximum and sum of the softmax in fp32.
 //
-// A CTA takes two tiles of 128 query rows that read the same keys: the same rows of two heads of a group where
-// the group is even, else two consecutive row tiles of one head.  Per key tile of 128, the tensor cores compute
+// A CTA takes two tiles of 128 query rows that read the same keys at a time: the same rows of two heads of a group
+// where the group is even, else two consecutive row tiles of one head.  Per key tile of 128, the tensor cores compute
 // S = Q K^T into tensor memory (tcgen05, both operands in shared memory), the tile's four softmax warps turn it
 // into weights P -- thread r owns row r, so neither maximum nor sum needs an exchange -- and write them over S as
 // fp16, and the tensor cores add P V to the tile's accumulator, P from tensor memory.  While one tile's softmax runs,
 // the tensor cores work on the other's products.  2 x (S 128 + O 128) columns fill tensor memory, so a tile's next S
 // waits for its P to be used, and a step takes a tile's two products plus its softmax's latency.  K and V tiles
 // arrive by TMA in a ring of kSlots 128-row tiles.
+//
+// One CTA per SM walks through the pairs of tiles, those with the most keys first and every second round in the
+// opposite order, which evens out what the CTAs get.  One warp finds the next pair while the current one is worked on,
+// and loads and products of the next begin before the outputs of this one are written: a CTA per pair spends about
+// 8 us per pair outside the loop over its keys (nine packed prompts of 412 to 3700 tokens, 32 heads: 404 us).
 //
 // That latency is why the weights are computed with the maximum as it was, while the new one is still being found: the
 // accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last time (the weights are
@@ -31,13 +36,15 @@ namespace wql {
 namespace {
 
 constexpr int kTile = 128;                  // query rows and keys of a tile
-constexpr int kThreads = 384;               // warps 0-3, 4-7: softmax of tiles 0, 1; 8: TMA; 9: MMA; 10, 11: V check
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kCheckWarp = 10;
+// warps 0-3, 4-7: softmax of tiles 0, 1; 8: TMA; 9, 10: products of tiles 0, 1; 11: V check; 12: next pair; 13-15: none
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kCheckWarp = 11, kNextWarp = 12;
+constexpr int kSorted = 128;                // up to so many sequences, the pairs are sorted by their keys
 constexpr float kTop = 7.0f;                // the largest weight after a rescale is 2^7 ...
 constexpr float kRaise = 8.0f;              // ... and before the next at most 2^15
-// registers per thread: launched with 168; the softmax warpgroups take 208, the third gives down to 80
-// (2 x 128 x 208 + 128 x 80 = 63488 <= 384 x 168 = 64512)
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+// registers per thread: launched with 128; the softmax warpgroups take 208, the others give down to 48
+// (256 x 208 + 256 x 48 = 65536 = 512 x 128)
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 48;
 
 template <int D>
 struct Cfg {
@@ -46,8 +53,7 @@ struct Cfg {
   static constexpr int kTileBytes = kBoxes * kBox;    // a Q, K or V tile
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kOffRing = 2 * kTileBytes;
-  static constexpr int kOffBar = kOffRing + kSlots * kTileBytes;
-  static constexpr int kSmem = kOffBar + 1024 + 1024;  // barriers, and alignment of the start
+  static constexpr int kSmem = kOffRing + kSlots * kTileBytes + 1024;  // and alignment of the start
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -113,6 +119,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
       : "memory");
 }
 
+// 32 bytes, a whole sector, per thread.
+__device__ __forceinline__ void st_global_32(void* dst, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(dst)), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // Start and length of sequence b; an invalid one has no rows.
 __device__ __forceinline__ int2 sequence(const Args& a, int b) {
   const int s = a.cu[b], e = a.cu[b + 1];
@@ -123,130 +136,137 @@ __device__ __forceinline__ int2 sequence(const Args& a, int b) {
   return make_int2(s, e - s);
 }
 
+// Slot and phase of a ring.
+template <int N>
+struct Ring {
+  int slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, phase ^= 1;
+  }
+};
+
+// A pair of tiles: rows r0 .. + 127 of head h0 and r1 .. + 127 of head h1 of a sequence, with n0 and n1 key tiles (n1 = 0:
+// there is no second one).  V tiles from jcheck on lie on a diagonal.
+struct Pair {
+  int start, len, r0, r1, h0, h1, n0, n1, nmax, jcheck;
+  __device__ __forceinline__ Pair(const Args& a, const int4& v) {  // {start, length (-1: no more pairs), first row, head}
+    start = v.x, len = v.y, r0 = v.z;
+    h0 = a.pair ? 2 * v.w : v.w, h1 = a.pair ? h0 + 1 : h0;
+    r1 = a.pair ? r0 : r0 + kTile;
+    n0 = r0 / kTile + 1, n1 = r1 < len ? r1 / kTile + 1 : 0;
+    nmax = max(n0, n1);
+    jcheck = (n1 > 0 ? min(n0, n1) : n0) - 1;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const Args a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int bad[D];  // first key (in the sequence) whose V value of this channel is not finite
-  __shared__ int any_bad;
-  __shared__ int s_sum[kThreads / 32];
-  __shared__ int3 s_tile;
+  // [parity of the pair]: first key (in the sequence) whose V value of this channel is not finite, and whether any is
+  __shared__ int bad[2][D], any_bad[2];
+  __shared__ int4 s_pair[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ uint64_t qbar, qfree;             // Q tiles landed; not read any more
+  __shared__ uint64_t full[C::kSlots], empty[C::kSlots];
+  __shared__ uint64_t sbar[2], pbar[2];        // [tile] S complete; P written (4 warps)
+  __shared__ uint64_t obar[2], ofree[2];       // [tile] O complete; O read (4 warps)
+  __shared__ uint64_t vbar[2][2], cbar[2][2];  // [parity of the pair][first, second V tile on a diagonal] landed; checked
+  __shared__ uint64_t pair_full[2], pair_empty[2];
+  __shared__ uint64_t turn[2];                 // [tile] its products may be queued
+  __shared__ uint64_t done;                    // every product (both tiles)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t* qbar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [1] Q tiles
-  uint64_t* full = qbar + 1;                                        // [kSlots]
-  uint64_t* empty = full + C::kSlots;                               // [kSlots]
-  uint64_t* sbar = empty + C::kSlots;                               // [2] S complete
-  uint64_t* pbar = sbar + 2;                                        // [2] P written (4 warps)
-  uint64_t* obar = pbar + 2;                                        // [2] O complete
-  uint64_t* cbar = obar + 2;                                        // [2] V(jcheck), V(jcheck + 1) checked (2 warps)
-  uint64_t* vbar = cbar + 2;                                        // [2] V(jcheck), V(jcheck + 1) landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vbar + 2);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  // ---- the sequence and row tiles of this CTA, counted from the last one: the longest rows start first ----
-  const int rows_per = a.pair ? kTile : 2 * kTile;
-  const int nh = a.pair ? a.Hq / 2 : a.Hq, tile_index = blockIdx.x / nh, hx = blockIdx.x - tile_index * nh;
-  {
-    const int per = (a.B + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (sequence(a, b).y + rows_per - 1) / rows_per;
-    int incl = mine;
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    if (lane == 31) s_sum[warp] = incl;
-    __syncthreads();
-    int total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) incl += s_sum[w];
-      total += s_sum[w];
-    }
-    const int want = total - 1 - tile_index;
-    if (want < 0) return;
-    int first = incl - mine;
-    if (first <= want && want < incl)
-      for (int b = b0; b < b1; ++b) {
-        const int2 s = sequence(a, b);
-        const int n = (s.y + rows_per - 1) / rows_per;
-        if (want < first + n) {
-          s_tile = make_int3(s.x, s.y, (want - first) * rows_per);
-          break;
-        }
-        first += n;
-      }
-  }
   if (tid == 0) {
-    any_bad = 0;
-    mbar_init(qbar, 1);
-    for (int s = 0; s < C::kSlots; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-    for (int x = 0; x < 2; ++x) mbar_init(&sbar[x], 1), mbar_init(&pbar[x], 4), mbar_init(&obar[x], 1);
-    for (int x = 0; x < 2; ++x) mbar_init(&cbar[x], 2), mbar_init(&vbar[x], 1);
+    mbar_init(&qbar, 1), mbar_init(&qfree, 2), mbar_init(&done, 2);
+    for (int s = 0; s < C::kSlots; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 2);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&turn[x], 1), mbar_init(&sbar[x], 1), mbar_init(&pbar[x], 4), mbar_init(&obar[x], 1), mbar_init(&ofree[x], 4);
+      for (int k = 0; k < 2; ++k) mbar_init(&vbar[x][k], 1), mbar_init(&cbar[x][k], 1);
+      mbar_init(&pair_full[x], 1), mbar_init(&pair_empty[x], 4 + 8);  // TMA, product, check and softmax warps
+      any_bad[x] = 0;
+    }
     fence_mbarrier_init();
+    mbar_arrive(&turn[0]);
   }
-  for (int i = tid; i < D; i += kThreads) bad[i] = INT_MAX;
+  for (int i = tid; i < 2 * D; i += kThreads) bad[i / D][i % D] = INT_MAX;
   if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
-  const int start = s_tile.x, len = s_tile.y, q0 = s_tile.z;
-  // tile x: head h[x], rows r0[x] .. + 127 of the sequence, n[x] key tiles (0: no such tile)
-  const int h0 = a.pair ? 2 * hx : hx, h1 = a.pair ? h0 + 1 : h0;
-  const int r1 = a.pair ? q0 : q0 + kTile;
-  const int n0 = q0 / kTile + 1, n1 = r1 < len ? r1 / kTile + 1 : 0;
-  const int nmax = max(n0, n1), kvh = h0 / a.G;
-  const int jcheck = (n1 > 0 ? min(n0, n1) : n0) - 1;  // key tiles from here on are on a diagonal
+  const uint32_t tmem = tmem_slot;
+  grid_dependency_wait();  // everything before this line overlaps the end of the preceding kernel
+  grid_dependents_launch();
 
-  if (warp >= 8) {
+  if (warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp && lane == 0) {
       // ---------------- Q, then K(0), V(0), K(1), V(1) .. into the ring ----------------
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      mbar_arrive_expect_tx(qbar, (n1 > 0 ? 2 : 1) * C::kTileBytes);
-      for (int b = 0; b < C::kBoxes; ++b) tma_load_3d(smem + b * C::kBox, &tm_q, qbar, 64 * b, h0, start + q0);
+      Ring<C::kSlots> ring;
       int issued = 0;
       bool ok = true;
-      for (int i = 0; i < 2 * nmax && ok; ++i) {
-        const int slot = i % C::kSlots;
-        if (!mbar_wait_bounded(&empty[slot], ((i / C::kSlots) & 1) ^ 1)) {
+      auto wait = [&](uint64_t* bar, int phase) {
+        if (ok && !mbar_wait_bounded(bar, phase & 1)) {
           report_error(a.err, kErrTimeoutEmpty);
           ok = false;
-          break;
         }
-        uint8_t* dst = smem + C::kOffRing + slot * C::kTileBytes;
-        mbar_arrive_expect_tx(&full[slot], C::kTileBytes);
-        for (int b = 0; b < C::kBoxes; ++b)
-          tma_load_3d(dst + b * C::kBox, i & 1 ? &tm_v : &tm_k, &full[slot], 64 * b, kvh, start + (i >> 1) * kTile);
-        if (i == 0 && n1 > 0)  // the second Q tile behind the first K tile
+        return ok;
+      };
+      auto load_q = [&](int x, int h, int row) {
+        for (int b = 0; b < C::kBoxes; ++b) tma_load_3d(smem + x * C::kTileBytes + b * C::kBox, &tm_q, &qbar, 64 * b, h, row);
+      };
+      for (int it = 0; wait(&pair_full[it & 1], it >> 1); ++it) {
+        const int4 v = s_pair[it & 1];
+        mbar_arrive(&pair_empty[it & 1]);
+        if (v.y < 0) break;
+        const Pair p(a, v);
+        const int kvh = p.h0 / a.G;
+        if (!wait(&qfree, (it & 1) ^ 1)) break;
+        mbar_arrive_expect_tx(&qbar, (p.n1 > 0 ? 2 : 1) * C::kTileBytes);
+        load_q(0, p.h0, p.start + p.r0);
+        for (int i = 0; i < 2 * p.nmax && wait(&empty[ring.slot], ring.phase ^ 1); ++i) {
+          uint8_t* dst = smem + C::kOffRing + ring.slot * C::kTileBytes;
+          mbar_arrive_expect_tx(&full[ring.slot], C::kTileBytes);
           for (int b = 0; b < C::kBoxes; ++b)
-            tma_load_3d(smem + C::kTileBytes + b * C::kBox, &tm_q, qbar, 64 * b, h1, start + r1);
-        ++issued;
+            tma_load_3d(dst + b * C::kBox, i & 1 ? &tm_v : &tm_k, &full[ring.slot], 64 * b, kvh, p.start + (i >> 1) * kTile);
+          if (i == 0 && p.n1 > 0) load_q(1, p.h1, p.start + p.r1);  // the second Q tile behind the first K tile
+          ring.next();
+          ++issued;
+        }
       }
       // copies that may still be in flight land before the kernel ends
-      if (!mbar_wait_bounded(qbar, 0)) report_error(a.err, kErrTimeoutDrain);
-      for (int i = max(0, issued - C::kSlots); i < issued; ++i)
-        if (!mbar_wait_bounded(&full[i % C::kSlots], (i / C::kSlots) & 1)) {
+      for (int i = 0; i < C::kSlots && i < issued; ++i) {
+        if (ring.slot == 0) ring.phase ^= 1;
+        ring.slot = ring.slot == 0 ? C::kSlots - 1 : ring.slot - 1;
+        if (!mbar_wait_bounded(&full[ring.slot], ring.phase)) {
           report_error(a.err, kErrTimeoutDrain);
           break;
         }
-    } else if (warp == kMmaWarp) {
-      // ---------------- the tensor cores' work, issued by one thread ----------------
-      // The whole warp walks through this, so that what the instructions take is uniform and stays in uniform
-      // registers; under a branch on the lane every operand of every product would be moved there first (16384 tokens,
-      // 32 heads: 1.82 ms).
+      }
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      // ---------------- the tensor cores' work: a warp per tile ----------------
+      // Products are queued only a few deep, so what one warp spent on waits and commits between them was time in which
+      // the tensor cores had nothing to do (16384 tokens, 32 heads: 1.69 ms).  Each warp now waits for what its next
+      // products need while the other's are queued, and they take turns in queueing them: left to themselves, the two
+      // tiles fall into step, and both softmaxes run while the tensor cores wait (1.73 ms).  A whole warp walks through
+      // this, so that what the instructions take is uniform and stays in uniform registers; under a branch on the lane
+      // every operand of every product would be moved there first.
+      const int x = warp - kMmaWarp;
       const bool leader = elect_one();
       const uint32_t idesc_s = umma_idesc_f16(kTile, kTile, 0, 0) | a.negate;
       constexpr uint32_t idesc_o = umma_idesc_f16(kTile, D, /*A from TMEM*/ 0, /*B MN-major*/ 1);
-      const uint32_t q_lo = smem_u32(smem) >> 4, ring_lo = smem_u32(smem + C::kOffRing) >> 4;
+      const uint32_t ring_lo = smem_u32(smem + C::kOffRing) >> 4;
+      const uint32_t q_desc = (1u << 16) + ((smem_u32(smem) + x * C::kTileBytes) >> 4);
+      const uint32_t ts = tmem + x * kTile, to = tmem + 2 * kTile + x * D;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int phase) {
         if (ok && !mbar_wait_warp(bar, phase & 1)) {
@@ -255,223 +275,358 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return ok;
       };
-      auto commit = [&](uint64_t* bar) {
-        if (leader) umma_commit(bar);
+      auto release = [&](uint64_t* bar, bool used) {  // when the products queued so far are complete; at once without any
+        if (!leader) return;
+        if (used)
+          umma_commit(bar);
+        else
+          mbar_arrive(bar);
       };
-      auto qk = [&](int x, int slot) {  // S_x = Q_x K^T, K in `slot`
-        const uint32_t ad = (1u << 16) + q_lo + x * (C::kTileBytes >> 4), bd = (1u << 16) + ring_lo + slot * (C::kTileBytes >> 4);
+      auto qk = [&](int slot) {  // S = Q K^T, K in `slot`
+        const uint32_t bd = (1u << 16) + ring_lo + slot * (C::kTileBytes >> 4);
         if (leader) {
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
             const uint32_t off = ((s >> 2) * C::kBox + (s & 3) * 32) >> 4;
-            mma_ss(tmem + x * kTile, ad + off, bd + off, idesc_s, s > 0);
+            mma_ss(ts, q_desc + off, bd + off, idesc_s, s > 0);
           }
+          umma_commit(&sbar[x]);
         }
       };
-      auto pv = [&](int x, int slot, uint32_t acc) {  // O_x (+)= P_x V, V in `slot`
+      auto pv = [&](int slot, uint32_t acc) {  // O (+)= P V, V in `slot`
         const uint32_t bd = ((uint32_t)(C::kBox >> 4) << 16) + ring_lo + slot * (C::kTileBytes >> 4);
         if (leader) {
 #pragma unroll
-          for (int s = 0; s < kTile / 16; ++s)
-            mma_ts(tmem + 2 * kTile + x * D, tmem + x * kTile + s * 8, bd + ((s * 2048) >> 4), idesc_o, s > 0 ? 1u : acc);
+          for (int s = 0; s < kTile / 16; ++s) mma_ts(to, ts + s * 8, bd + ((s * 2048) >> 4), idesc_o, s > 0 ? 1u : acc);
         }
       };
-      wait(qbar, 0);
-      wait(&full[0], 0);
-      if (ok) {
+      Ring<C::kSlots> rk, rv;                 // K(j + 1), V(j)
+      int pcount = 0, ocount = 0, turns = 0;  // phases of pbar, of obar / ofree, and of turn
+      auto pass = [&]() {
+        if (leader) mbar_arrive(&turn[x ^ 1]);
+      };
+      for (int it = 0; wait(&pair_full[it & 1], it >> 1); ++it) {
+        const int4 v = s_pair[it & 1];
+        __syncwarp();
+        if (leader) mbar_arrive(&pair_empty[it & 1]);
+        if (v.y < 0) break;
+        const Pair p(a, v);
+        const int n = x ? p.n1 : p.n0;
+        const bool signals = x == (p.n1 > 0);  // this warp tells the check warp about V tiles
+        // S of the first key tile; the S columns are free, since the products that read their last P come before.  A
+        // tile that does not exist, or has fewer keys, follows the ring all the same.
+        if (!wait(&qbar, it) || !wait(&full[rk.slot], rk.phase) || !wait(&turn[x], turns++)) break;
         tc_fence_after_sync();
-        qk(0, 0);
-        commit(&sbar[0]);
-        if (n1 > 0) {
-          qk(1, 0);
-          commit(&sbar[1]);
+        if (n > 0) qk(rk.slot);
+        pass();
+        release(&empty[rk.slot], n > 0);
+        if (n <= 1) release(&qfree, n > 0);
+        rv = rk;
+        rv.next();
+        rk = rv;
+        rk.next();
+        if (signals) {
+          if (p.jcheck == 0 && wait(&full[rv.slot], rv.phase) && leader) mbar_arrive(&vbar[it & 1][0]);
+          if (p.nmax - 1 == p.jcheck && leader) mbar_arrive(&vbar[it & 1][1]);  // there is no second one
         }
-        if (C::kSlots < 2 * nmax) commit(&empty[0]);
-      }
-      if (jcheck == 0 && wait(&full[1], 0) && leader) mbar_arrive(&vbar[0]);
-      int sv = 1, pv_phase = 0, sk = 2, k_phase = 0;  // slots and phases of V(j) and K(j + 1)
-      for (int j = 0; j < nmax && ok; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2;  // ring items V(j) and K(j + 1)
-        wait(&full[sv], pv_phase);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int n = x ? n1 : n0;
-          if (j >= n || !wait(&pbar[x], j)) continue;
-          if (j >= jcheck && !wait(&cbar[j - jcheck], 0)) continue;
+        for (int j = 0; j < p.nmax && wait(&full[rv.slot], rv.phase); ++j) {
+          if (j + 1 < p.nmax && !wait(&full[rk.slot], rk.phase)) break;
+          if (j < n) {
+            if (!wait(&pbar[x], pcount++)) break;
+            // the accumulator is taken over when the softmax warps have read that of the pair before
+            if (j == 0 && ocount > 0 && !wait(&ofree[x], ocount - 1)) break;
+            if (j >= p.jcheck && !wait(&cbar[it & 1][j - p.jcheck], it >> 1)) break;
+          }
+          if (!wait(&turn[x], turns++)) break;
           tc_fence_after_sync();
-          pv(x, sv, j > 0);
-          if (j + 1 < n && wait(&full[sk], k_phase)) {
-            tc_fence_after_sync();
-            qk(x, sk);
-            commit(&sbar[x]);
-          } else if (ok) {
-            commit(&obar[x]);
+          if (j < n) {
+            pv(rv.slot, j > 0);
+            if (j + 1 == n) {
+              release(&obar[x], true);
+              ++ocount;
+            }
+          }
+          if (j + 1 < n) qk(rk.slot);
+          pass();
+          if (j + 1 < p.nmax) {
+            release(&empty[rv.slot], j < n);
+            release(&empty[rk.slot], j + 1 < n);
+            if (j + 2 == n) release(&qfree, true);
+            rv = rk;
+            rv.next();
+            rk = rv;
+            rk.next();
+            // the next V is checked while its step's softmax runs
+            if (signals && j + 1 >= p.jcheck && wait(&full[rv.slot], rv.phase) && leader)
+              mbar_arrive(&vbar[it & 1][j + 1 - p.jcheck]);
+          } else {
+            release(&empty[rv.slot], j < n);  // rk is at K(0) of the next pair
           }
         }
-        if (ok && iv + C::kSlots < 2 * nmax) commit(&empty[sv]);
-        if (ok && ik + C::kSlots < 2 * nmax) commit(&empty[sk]);
-        sv += 2;
-        if (sv >= C::kSlots) sv -= C::kSlots, pv_phase ^= 1;
-        sk += 2;
-        if (sk >= C::kSlots) sk -= C::kSlots, k_phase ^= 1;
-        // the next V is checked while its step's softmax runs
-        if (j + 1 >= jcheck && j + 1 < nmax && wait(&full[sv], pv_phase) && leader) mbar_arrive(&vbar[j + 1 - jcheck]);
       }
-    } else if (warp >= kCheckWarp) {
+      if (ok) {
+        release(&done, true);
+        wait(&done, 0);
+      }
+    } else if (warp == kCheckWarp) {
       // ---------------- V tiles on a diagonal: values that are not finite ----------------
-      for (int j = jcheck; j < nmax; ++j) {
-        const int i = 2 * j + 1;
-        // not on the ring's own barrier, which goes through phases that these warps do not follow
-        if (!mbar_wait_warp(&vbar[j - jcheck], 0)) {
+      int base = 0;  // slot of K(0)
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int phase) {
+        if (ok && !mbar_wait_warp(bar, phase & 1)) {
           if (lane == 0) report_error(a.err, kErrTimeoutFull);
-          break;
+          ok = false;
         }
-        uint4* v = reinterpret_cast<uint4*>(smem + C::kOffRing + (i % C::kSlots) * C::kTileBytes);
-        constexpr int kBatch = 4;
-        for (int at = tid - kCheckWarp * 32; at < C::kTileBytes / 16; at += 64 * kBatch) {
-          uint4 x[kBatch];
+        return ok;
+      };
+      for (int it = 0; wait(&pair_full[it & 1], it >> 1); ++it) {
+        const int4 v4 = s_pair[it & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pair_empty[it & 1]);
+        if (v4.y < 0) break;
+        const Pair p(a, v4);
+        int* first_bad = bad[it & 1];
+        if (any_bad[it & 1]) {  // of the pair before the last, whose outputs are written
+          for (int i = lane; i < D; i += 32) first_bad[i] = INT_MAX;
+          __syncwarp();
+          if (lane == 0) any_bad[it & 1] = 0;
+          __syncwarp();
+        }
+        for (int k = 0; k < 2; ++k) {
+          // not on the ring's own barrier, which goes through phases that this warp does not follow
+          if (!wait(&vbar[it & 1][k], it >> 1)) break;
+          const int j = p.jcheck + k;
+          if (j >= p.nmax) {
+            if (lane == 0) mbar_arrive(&cbar[it & 1][k]);
+            continue;
+          }
+          uint4* v = reinterpret_cast<uint4*>(smem + C::kOffRing + (base + 2 * j + 1) % C::kSlots * C::kTileBytes);
+          constexpr int kBatch = 4;
+          for (int at = lane; at < C::kTileBytes / 16; at += 32 * kBatch) {
+            uint4 x[kBatch];
 #pragma unroll
-          for (int u = 0; u < kBatch; ++u) x[u] = v[at + 64 * u];
+            for (int u = 0; u < kBatch; ++u) x[u] = v[at + 32 * u];
+            uint32_t hits = 0;
 #pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-            bool hit = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)  // an exponent of all ones survives the carry into the bit above it
-              hit |= (((w[e] & 0x7c007c00u) + 0x04000400u) & 0x80008000u) != 0;
-            if (!hit) continue;
-            // chunk c of row r (16-byte units, 8 per 128-byte row) holds channels 8 (c ^ r % 8) of the box
-            const int p = at + 64 * u, row = (p >> 3) & (kTile - 1), box = p / (kTile * 8);
-            const int ch = 64 * box + 8 * ((p ^ row) & 7), key = j * kTile + row;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t m = 0x7c00u << (16 * (e & 1));
-              if ((w[e >> 1] & m) != m) continue;
-              w[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
-              if (key < len) {
-                atomicMin(&bad[ch + e], key);
-                any_bad = 1;
+            for (int u = 0; u < kBatch; ++u) {
+              // an exponent of all ones carries into the bit above it
+              const uint32_t h = ((x[u].x & 0x7c007c00u) + 0x04000400u) | ((x[u].y & 0x7c007c00u) + 0x04000400u) |
+                                 ((x[u].z & 0x7c007c00u) + 0x04000400u) | ((x[u].w & 0x7c007c00u) + 0x04000400u);
+              hits |= (h & 0x80008000u) ? 1u << u : 0u;
+            }
+            for (; hits; hits &= hits - 1) {  // rare
+              // chunk c of row r (16-byte units, 8 per 128-byte row) holds channels 8 (c ^ r % 8) of the box
+              const int pos = at + 32 * (__ffs(hits) - 1), row = (pos >> 3) & (kTile - 1), box = pos / (kTile * 8);
+              const int ch = 64 * box + 8 * ((pos ^ row) & 7), key = j * kTile + row;
+              uint16_t* h = reinterpret_cast<uint16_t*>(v + pos);
+              for (int e = 0; e < 8; ++e) {
+                if ((h[e] & 0x7c00u) != 0x7c00u) continue;
+                h[e] = 0;
+                if (key < p.len) {
+                  atomicMin(&first_bad[ch + e], key);
+                  any_bad[it & 1] = 1;
+                }
               }
             }
-            v[p] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&cbar[it & 1][k]);
+        }
+        base = (base + 2 * p.nmax) % C::kSlots;
+      }
+    } else if (warp == kNextWarp) {
+      // ---------------- the pairs of this CTA ----------------
+      const int rows_per = a.pair ? kTile : 2 * kTile, nh = a.pair ? a.Hq / 2 : a.Hq;
+      auto tiles_of = [&](int len) { return (len + rows_per - 1) / rows_per; };
+      constexpr int kPer = kSorted / 32;
+      int2 seq[kPer];  // sequences 32 k + lane
+      int most = 0, all = 0;
+      if (a.B <= kSorted) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          seq[k] = 32 * k + lane < a.B ? sequence(a, 32 * k + lane) : make_int2(0, 0);
+          most = max(most, tiles_of(seq[k].y));
+          all += tiles_of(seq[k].y);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        all = __reduce_add_sync(0xffffffffu, all);
+      }
+      auto beyond = [&](int t) {  // row tiles number t and later, of all sequences
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) n += max(tiles_of(seq[k].y) - t, 0);
+        return (int)__reduce_add_sync(0xffffffffu, n);
+      };
+      int chunk = 0, before = 0;  // more sequences: 32 at a time, with the tiles of those before
+      for (int it = 0;; ++it) {
+        const long long at = (long long)it * gridDim.x + (it & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const long long y = at / nh;  // row tile, in order
+        int4 out = make_int4(0, -1, 0, (int)(at - y * nh));
+        if (a.B <= kSorted) {
+          if (y < all) {
+            int lo = 0, hi = most;  // beyond(lo) > y >= beyond(hi)
+            while (hi - lo > 1) {
+              const int mid = (lo + hi) >> 1;
+              (beyond(mid) > (int)y ? lo : hi) = mid;
+            }
+            int r = (int)y - beyond(lo + 1);  // among the sequences that have a tile lo
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+              const unsigned has = __ballot_sync(0xffffffffu, tiles_of(seq[k].y) > lo);
+              const int cnt = __popc(has);
+              if (out.y < 0 && r < cnt) {
+                const int src = __fns(has, 0, r + 1);
+                out.x = __shfl_sync(0xffffffffu, seq[k].x, src);
+                out.y = __shfl_sync(0xffffffffu, seq[k].y, src);
+                out.z = lo * rows_per;
+              }
+              r -= cnt;
+            }
+          }
+        } else {
+          while (chunk < a.B) {
+            const int2 q = chunk + lane < a.B ? sequence(a, chunk + lane) : make_int2(0, 0);
+            const int n = tiles_of(q.y);
+            int incl = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+              const int o = __shfl_up_sync(0xffffffffu, incl, d);
+              if (lane >= d) incl += o;
+            }
+            const int sum = __shfl_sync(0xffffffffu, incl, 31);
+            if (y >= (long long)before + sum) {
+              before += sum;
+              chunk += 32;
+              continue;
+            }
+            const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > (int)y)) - 1;
+            out.x = __shfl_sync(0xffffffffu, q.x, src);
+            out.y = __shfl_sync(0xffffffffu, q.y, src);
+            out.z = __shfl_sync(0xffffffffu, before + incl - 1, src);  // the longest rows first
+            out.z = (out.z - (int)y) * rows_per;
+            break;
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&cbar[j - jcheck]);
+        if (!mbar_wait_warp(&pair_empty[it & 1], ((it >> 1) & 1) ^ 1)) {
+          if (lane == 0) report_error(a.err, kErrTimeoutEmpty);
+          break;
+        }
+        if (lane == 0) {
+          s_pair[it & 1] = out;
+          mbar_arrive(&pair_full[it & 1]);
+        }
+        if (out.y < 0) break;
       }
     }
   } else {
     // ---------------- softmax and output of tile x: thread r owns row r ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int x = warp >> 2, n = x ? n1 : n0, row = tid & 127;
+    const int x = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + x * kTile + lanes, to = tmem + 2 * kTile + x * D + lanes;
     const float c = a.scale_log2;
-    float m = 0.f, l0 = 0.f, l1 = 0.f;  // m: what is subtracted from the scaled scores
+    int scount = 0, ocount = 0;  // phases of sbar and obar
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (!mbar_wait_warp(&sbar[x], j & 1)) {
+    auto wait = [&](uint64_t* bar, int phase) {
+      if (ok && !mbar_wait_warp(bar, phase & 1)) {
         if (lane == 0) report_error(a.err, kErrTimeoutMma);
         ok = false;
-        break;
       }
-      tc_fence_after_sync();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
-      tmem_ld_wait();
-      if (j == n - 1) {  // the diagonal tile
-#pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (i > row) s[i >> 5][i & 31] = 0xff800000u;
-      }
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < 128; i += 2)
-        top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
-      const float up = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c - kTop;
-      if (j == 0) m = up;
-      float a0, a1;  // this step's sums
-      auto weights = [&]() {
-        a0 = a1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float u = __uint_as_float(s[i][2 * e]), v = __uint_as_float(s[i][2 * e + 1]);
-            fma2(u, v, c, -m);
-            u = ex2(u), v = ex2(v);
-            add2(a0, a1, u, v);
-            p[e] = pack_h2(u, v);
-          }
-          tmem_st_32x32b_x16(ts + 16 * i, p);
-        }
-      };
-      weights();
-      if (__any_sync(0xffffffffu, up > m + kRaise)) {
-        const float now = fmaxf(m, up), f = ex2(m - now);
-        m = now;
-        l0 *= f, l1 *= f;
-#pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(to + i, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tmem_st_32x32b_x32(to + i, o);
-        }
-        weights();
-      }
-      l0 += a0, l1 += a1;
-      tmem_st_wait();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pbar[x]);
-    }
-    if (n > 0 && ok) {
-      if (!mbar_wait_warp(&obar[x], 0)) {
-        if (lane == 0) report_error(a.err, kErrTimeoutMma);
-      } else {
-        mbar_wait_warp(&cbar[nmax - 1 - jcheck], 0);  // complete already where this tile used it
+      return ok;
+    };
+    for (int it = 0; wait(&pair_full[it & 1], it >> 1); ++it) {
+      const int4 v4 = s_pair[it & 1];
+      if (v4.y < 0) break;
+      const Pair p(a, v4);
+      const int n = x ? p.n1 : p.n0;
+      float m = 0.f, l0 = 0.f, l1 = 0.f;  // m: what is subtracted from the scaled scores
+      for (int j = 0; j < n && wait(&sbar[x], scount++); ++j) {
         tc_fence_after_sync();
-        const int r = (x ? r1 : q0) + row;
-        const float inv = 1.f / (l0 + l1);
-        const bool poison = any_bad != 0;
-        // through the tile's Q rows, which are not needed any more, so that whole lines are written
-        constexpr int kChunks = D / 8;  // 16-byte chunks of a row
-        uint4* stage = reinterpret_cast<uint4*>(smem + x * C::kTileBytes) + (warp & 3) * 32 * kChunks;
+        uint32_t s[4][32];
 #pragma unroll
-        for (int i = 0; i < D; i += 32) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(to + i, o);
-          tmem_ld_wait();
-          if (poison) {
+        for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
+        tmem_ld_wait();
+        if (j == n - 1) {  // the diagonal tile
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (r >= bad[i + e]) o[e] = 0x7fc00000u;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              h[k] = pack_h2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-            stage[lane * kChunks + (((i + e) >> 3) ^ (lane & (kChunks - 1)))] = make_uint4(h[0], h[1], h[2], h[3]);
-          }
+          for (int i = 0; i < 128; ++i)
+            if (i > row) s[i >> 5][i & 31] = 0xff800000u;
         }
-        __syncwarp();
-        const int rw = (x ? r1 : q0) + (warp & 3) * 32;  // the warp's first row
-        __half* dst = a.out + ((long long)(start + rw) * a.Hq + (x ? h1 : h0)) * D;
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const int at = i * 32 + lane, rr = at / kChunks, ch = at % kChunks;
-          if (rw + rr < len)
-            *reinterpret_cast<uint4*>(dst + (long long)rr * a.Hq * D + 8 * ch) = stage[rr * kChunks + (ch ^ (rr & (kChunks - 1)))];
+        for (int i = 0; i < 128; i += 2)
+          top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
+        const float up = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c - kTop;
+        if (j == 0) m = up;
+        float a0, a1;  // this step's sums
+        auto weights = [&]() {
+          a0 = a1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float u = __uint_as_float(s[i][2 * e]), v = __uint_as_float(s[i][2 * e + 1]);
+              fma2(u, v, c, -m);
+              u = ex2(u), v = ex2(v);
+              add2(a0, a1, u, v);
+              w[e] = pack_h2(u, v);
+            }
+            tmem_st_32x32b_x16(ts + 16 * i, w);
+          }
+        };
+        weights();
+        if (__any_sync(0xffffffffu, up > m + kRaise)) {
+          const float now = fmaxf(m, up), f = ex2(m - now);
+          m = now;
+          l0 *= f, l1 *= f;
+#pragma unroll 1
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + i, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st_32x32b_x32(to + i, o);
+          }
+          weights();
+        }
+        l0 += a0, l1 += a1;
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pbar[x]);
+      }
+      if (n > 0 && wait(&obar[x], ocount++)) {
+        tc_fence_after_sync();
+        uint32_t o[D / 32][32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) tmem_ld_32x32b_x32(to + 32 * i, o[i]);
+        tmem_ld_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ofree[x]);
+        const int r = (x ? p.r1 : p.r0) + row;
+        const float inv = 1.f / (l0 + l1);
+        if (any_bad[it & 1]) {
+#pragma unroll
+          for (int i = 0; i < D; ++i)
+            if (r >= bad[it & 1][i]) o[i >> 5][i & 31] = 0x7fc00000u;
+        }
+        if (r < p.len) {
+          __half* dst = a.out + ((long long)(p.start + r) * a.Hq + (x ? p.h1 : p.h0)) * D;
+#pragma unroll
+          for (int i = 0; i < D; i += 16) {
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              h[e] = pack_h2(__uint_as_float(o[i >> 5][(i & 31) + 2 * e]) * inv, __uint_as_float(o[i >> 5][(i & 31) + 2 * e + 1]) * inv);
+            st_global_32(dst + i, h);
+          }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pair_empty[it & 1]);
     }
   }
   tc_fence_before_sync();
@@ -485,7 +640,7 @@ bool tensor_map(CUtensorMap* m, const uint16_t* p, int D, int heads, int T, long
 }
 
 template <int D>
-cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const Args& a, dim3 grid, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const Args& a, int ctas, cudaStream_t s) {
   using C = Cfg<D>;
   static std::atomic<bool> ready[64];  // per device; racing first calls set the same attribute
   int dev = 0;
@@ -496,8 +651,17 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
   }
-  attn_prompt_kernel<D><<<grid, kThreads, C::kSmem, s>>>(q, k, v, a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_prompt_kernel<D>, q, k, v, a);
 }
 
 }  // namespace
@@ -514,16 +678,10 @@ cudaError_t launch_attn_prompt(const uint16_t* q, long long q_stride, const uint
   const float mag = scale < 0.f ? -scale : scale;
   Args a{cu, B, T, Hq, G, pair, (mag < 1e-30f ? 1e-30f : mag) * 1.4426950408889634f, scale < 0.f ? 1u << 13 : 0u,
          reinterpret_cast<__half*>(out), dev_err};
-  // every sequence may end in a ragged tile
-  const int rows_per = pair ? kTile : 2 * kTile;
-  const long long tiles = (long long)T / rows_per + (B < T ? B : T);
-  const long long ctas = tiles * (pair ? Hq / 2 : Hq);
-  if (ctas > INT_MAX) {
-    *err = "too many row tiles and heads";
-    return cudaErrorInvalidConfiguration;
-  }
-  const dim3 grid((unsigned)ctas);
-  return D == 128 ? launch<128>(tq, tk, tv, a, grid, s) : launch<64>(tq, tk, tv, a, grid, s);
+  // at most this many pairs: every sequence may end in a ragged tile
+  const long long pairs = ((long long)T / (pair ? kTile : 2 * kTile) + (B < T ? B : T)) * (pair ? Hq / 2 : Hq);
+  const int ctas = (int)(pairs < num_sms() ? pairs : num_sms());
+  return D == 128 ? launch<128>(tq, tk, tv, a, ctas, s) : launch<64>(tq, tk, tv, a, ctas, s);
 }
 
 }  // namespace wql
