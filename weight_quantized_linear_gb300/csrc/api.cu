@@ -510,6 +510,7 @@ wql_status wql_kv_append_i4(const uint16_t* k, const uint16_t* v, int64_t k_stri
   WQL_REQUIRE(T >= 0, "T must be >= 0");
   WQL_REQUIRE(H >= 1, "H must be >= 1");
   WQL_REQUIRE_CACHE();
+  if ((int64_t)T * H > INT_MAX) return fail(WQL_EUNSUPPORTED, "T * H must be below 2^31");
   if (T == 0) {
     g_last_error.clear();
     return WQL_OK;
@@ -532,6 +533,7 @@ wql_status wql_kv_read_i4(const uint8_t* cache, int64_t pages, int page_size, in
   WQL_REQUIRE(T >= 0, "T must be >= 0");
   WQL_REQUIRE(H >= 1, "H must be >= 1");
   WQL_REQUIRE_CACHE();
+  if ((int64_t)T * H > INT_MAX) return fail(WQL_EUNSUPPORTED, "T * H must be below 2^31");
   if (T == 0) {
     g_last_error.clear();
     return WQL_OK;

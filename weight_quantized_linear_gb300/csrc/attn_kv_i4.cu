@@ -98,17 +98,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Division by a number known at launch: n / d for 0 <= n < 2^31 (Granlund and Montgomery's multiplier with l = ceil(log2 d)).
-struct FastDiv {
-  uint32_t d, m, l;
-};
-FastDiv fast_div(uint32_t d) {
-  uint32_t l = 0;
-  while ((1ull << l) < d) ++l;
-  return {d, (uint32_t)((((1ull << l) - d) << 32) / d + 1), l};
-}
-__device__ __forceinline__ uint32_t quot(uint32_t n, const FastDiv& f) { return (__umulhi(n, f.m) + n) >> f.l; }
-
 __device__ __forceinline__ float2 h2f2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 
 // Copy of `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.

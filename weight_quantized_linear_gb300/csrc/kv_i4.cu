@@ -21,79 +21,86 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanSlots = 4 * kPlanThreads;  // slots per CTA
 
-// Inclusive scan over the CTA of one 64-bit value per thread.
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += o;
-  }
-  __syncthreads();  // warp_sums may still be read from the scan before
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) v += warp_sums[w];
-  return v;
-}
+// Every CTA scans the requests' lengths itself (new tokens and new pages of at most kPlanPer requests per thread, all
+// loaded before any is used) and then fills its own slots, so that nothing has to be passed between CTAs and one launch
+// does it all.  The table entries read here (pages held already) and those written (new pages) are different ones.
+// Latency is what it takes: a launch, the loads of the lengths, two barriers, and the loads of a page number.
+constexpr int kPlanPer = kPlanMaxB / kPlanThreads;
 
-// Every CTA scans the requests' lengths itself (two values per request, at most 16 requests per thread)
-// and then fills its own slots, so that nothing has to be passed between CTAs and one launch does it all.
-// The table entries read here (pages held already) and those written (new pages) are different ones.
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(
-    const int* __restrict__ ctx_lens, const int* __restrict__ new_lens, int B, int ps, const int* __restrict__ free_pages,
-    int free_cap, const int* __restrict__ free_count, int* table, int width, int T, int* __restrict__ cu_new,
-    int* __restrict__ kv_lens, int* __restrict__ slots, int* __restrict__ free_count_out) {
+    const int* __restrict__ ctx_lens, const int* __restrict__ new_lens, int B, int ps, FastDiv by_ps,
+    const int* __restrict__ free_pages, int free_cap, const int* __restrict__ free_count, int* table, int width, int T,
+    int* __restrict__ cu_new, int* __restrict__ kv_lens, int* __restrict__ slots, int* __restrict__ free_count_out) {
   __shared__ int cu[kPlanMaxB + 1];   // first new token of each request
   __shared__ int off[kPlanMaxB + 1];  // new pages of the requests before it; -1: refused
-  __shared__ long long sums[kPlanThreads / 32];
-  const int tid = threadIdx.x;
+  __shared__ long long sum_t[kPlanThreads / 32], sum_p[kPlanThreads / 32];
+  __shared__ int taken[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  grid_dependency_wait();  // the lengths may come from the preceding kernel
+  grid_dependents_launch();
   const int nfree = min(max(free_count[0], 0), free_cap);
   const int per = (B + kPlanThreads - 1) / kPlanThreads;
-  const int r0 = min(tid * per, B), r1 = min(r0 + per, B);
-  // pages a request needs beyond those it holds; -1 if its table row is too short
-  auto pages_of = [&](int c, int n) -> long long {
-    const long long total = ((long long)c + n + ps - 1) / ps;
-    return total > width ? -1 : total - (c + (ps - 1LL)) / ps;
+  const int r0 = min(tid * per, B), cnt = min(per, B - r0);
+  auto pages = [&](int n) {  // ceil(n / ps)
+    const int q = (int)quot((uint32_t)n, by_ps);
+    return q + (q * ps != n);
   };
+  int c[kPlanPer], n[kPlanPer], need[kPlanPer];  // need: pages beyond those held; -1 if the table row is too short
   long long tok = 0, pg = 0;
-  for (int r = r0; r < r1; ++r) {
-    const int c = max(ctx_lens[r], 0), n = max(new_lens[r], 0);
-    tok += n;
-    pg += max(pages_of(c, n), 0LL);
+#pragma unroll
+  for (int k = 0; k < kPlanPer; ++k) {
+    c[k] = k < cnt ? max(ctx_lens[r0 + k], 0) : 0;
+    n[k] = k < cnt ? max(new_lens[r0 + k], 0) : 0;
   }
-  const long long tok_incl = block_scan(tok, sums);
-  const long long pg_incl = block_scan(pg, sums);
-  long long t = tok_incl - tok, p = pg_incl - pg;
-  long long taken = 0;
-  for (int r = r0; r < r1; ++r) {
-    const int c = max(ctx_lens[r], 0), n = max(new_lens[r], 0);
-    const long long need = pages_of(c, n);
-    const bool ok = need == 0 || (need > 0 && p + need <= nfree);
+#pragma unroll
+  for (int k = 0; k < kPlanPer; ++k) {
+    const long long most = (long long)width * ps;  // below 2^31
+    need[k] = (long long)c[k] + n[k] > most ? -1 : pages(c[k] + n[k]) - pages(c[k]);
+    tok += n[k];
+    pg += max(need[k], 0);
+  }
+  long long t = tok, p = pg;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long ot = __shfl_up_sync(0xffffffffu, t, d), op = __shfl_up_sync(0xffffffffu, p, d);
+    if (lane >= d) t += ot, p += op;
+  }
+  if (lane == 31) sum_t[wid] = t, sum_p[wid] = p;
+  __syncthreads();
+  for (int w = 0; w < wid; ++w) t += sum_t[w], p += sum_p[w];
+  t -= tok, p -= pg;
+  int used = 0;  // those who are served take a run of the list from its end: its length is the furthest one's
+#pragma unroll
+  for (int k = 0; k < kPlanPer; ++k) {
+    if (k >= cnt) break;
+    const int r = r0 + k;
+    const bool ok = need[k] == 0 || (need[k] > 0 && p + need[k] <= nfree);
     cu[r] = (int)min(t, (long long)INT_MAX);
     off[r] = ok ? (int)min(p, (long long)INT_MAX) : -1;
     if (blockIdx.x == 0) {
       cu_new[r] = cu[r];
-      kv_lens[r] = ok ? c + n : 0;
+      kv_lens[r] = ok ? c[k] + n[k] : 0;
     }
-    if (ok) taken += need;
-    t += n;
-    p += max(need, 0LL);
+    if (ok && need[k] > 0) used = (int)p + need[k];
+    t += n[k];
+    p += max(need[k], 0);
   }
-  if (B == 0 && tid == 0) cu[0] = 0;
-  if (r1 == B && r0 < B) cu[B] = (int)min(t, (long long)INT_MAX);
-  const long long taken_incl = block_scan(taken, sums);
-  if (blockIdx.x == 0 && tid == kPlanThreads - 1) *free_count_out = nfree - (int)taken_incl;
+  if (tid == 0 && B == 0) cu[0] = 0;
+  if (r0 < B && r0 + cnt == B) cu[B] = (int)min(t, (long long)INT_MAX);
+  used = __reduce_max_sync(0xffffffffu, used);
+  if (lane == 0) taken[wid] = used;
   __syncthreads();
-  if (blockIdx.x == 0 && tid == 0) cu_new[B] = cu[B];
+  if (blockIdx.x == 0 && tid == 0) {
+    for (int w = 1; w < kPlanThreads / 32; ++w) used = max(used, taken[w]);
+    *free_count_out = nfree - used;
+    cu_new[B] = cu[B];
+  }
 
   // the requests' new pages: a warp per request
-  const int lane = tid & 31, warp = blockIdx.x * (kPlanThreads / 32) + (tid >> 5);
-  for (int r = warp; r < B; r += gridDim.x * (kPlanThreads / 32)) {
-    const int c = max(ctx_lens[r], 0), n = max(new_lens[r], 0);
+  for (int r = blockIdx.x * (kPlanThreads / 32) + wid; r < B; r += gridDim.x * (kPlanThreads / 32)) {
     if (off[r] < 0) continue;
-    const int held = (int)((c + (ps - 1LL)) / ps), need = (int)pages_of(c, n);
-    for (int k = lane; k < need; k += 32)
-      table[(size_t)r * width + held + k] = free_pages[nfree - 1 - off[r] - k];
+    const int len = max(ctx_lens[r], 0), held = pages(len), more = pages(len + max(new_lens[r], 0)) - held;
+    for (int k = lane; k < more; k += 32) table[(size_t)r * width + held + k] = free_pages[nfree - 1 - off[r] - k];
   }
 
   // the slots of tokens t0 .. t0 + 3
@@ -111,8 +118,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(
     while (lo + 1 < B && cu[lo + 1] <= tt) ++lo;
     out[j] = -1;
     if (tt < cu[B] && off[lo] >= 0) {
-      const int c = max(ctx_lens[lo], 0);
-      const int pos = c + (tt - cu[lo]), k = pos / ps, held = (int)((c + (ps - 1LL)) / ps);
+      const int len = max(ctx_lens[lo], 0);
+      const int pos = len + (tt - cu[lo]), k = (int)quot((uint32_t)pos, by_ps), held = pages(len);
       const int page = k < held ? table[(size_t)lo * width + k] : free_pages[nfree - 1 - off[lo] - (k - held)];
       if (page >= 0) out[j] = page * ps + (pos - k * ps);
     }
@@ -149,25 +156,72 @@ __device__ __forceinline__ __half kv_scale(float d, float e) {
   return __half_as_ushort(h) == 0 ? __ushort_as_half(0x3c00) : h;
 }
 
-// clamp(round_half_even((x - lo) / s), 0, 15) of the real quotient.  t = fl(fl(x - lo) * fl(1 / s)) is off by
-// at most 3 * 2^-24 * 16 < 3e-6, so it decides unless it is that close to a half; then the sign of
-// ((x - lo) - (c + 1/2) s) does, computed exactly: x - lo = d + e, (c + 1/2) s has 16 bits, and d minus it
-// is exact because the two are close.
-__device__ __forceinline__ int kv_code(float x, float lo, float s, float inv) {
-  const float d = __fsub_rn(x, lo);
-  const float t = __fmul_rn(d, inv);
-  const float rt = rintf(t);
-  int c = (int)rt;
-  if (fabsf(__fsub_rn(t, rt)) > 0.49999f) {
-    const float fl = floorf(t);
-    // x - lo = d + e (Knuth's two-sum of x and -lo)
-    const float bb = __fsub_rn(d, x);
-    const float e = __fadd_rn(__fsub_rn(x, __fsub_rn(d, bb)), __fsub_rn(-lo, bb));
-    const float r = __fadd_rn(__fsub_rn(d, __fmul_rn(fl + 0.5f, s)), e);
-    c = (int)fl;
-    if (r > 0.f || (r == 0.f && (c & 1))) ++c;
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ float2 kv_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 kv_add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// round_half_even((x - lo) / s) of the real quotient, where fl(x - lo) * fl(1 / s) comes within 1e-5 of the middle
+// between c and c + 1: the sign of ((x - lo) - (c + 1/2) s) decides, computed exactly: x - lo = d + e, (c + 1/2) s has
+// 16 bits, and d minus it is exact because the two are close.
+__device__ __forceinline__ float kv_code_near_tie(float x, float lo, float s, float inv) {
+  const float d = __fsub_rn(x, lo), fl = floorf(__fmul_rn(d, inv));
+  const float bb = __fsub_rn(d, x);  // Knuth's two-sum of x and -lo
+  const float e = __fadd_rn(__fsub_rn(x, __fsub_rn(d, bb)), __fsub_rn(-lo, bb));
+  const float r = __fadd_rn(__fsub_rn(d, __fmul_rn(fl + 0.5f, s)), e);
+  return fl + (r > 0.f || (r == 0.f && ((int)fl & 1)) ? 1.0f : 0.0f);
+}
+
+// The codes clamp(round_half_even((x - lo) / s), 0, 15) of eight values, the first in the lowest bits.
+// y = fl(d * inv + 1.5 * 2^23) with d = fl(x - lo), inv = fl(1 / s) is that magic number plus the integer nearest to
+// d * inv, which is off the quotient by at most 2^-23 * 16 < 2e-6, so that integer is the code unless the rest
+// d * inv - integer (exact up to one rounding) comes within 1e-5 of a half; then kv_code_near_tie decides.  x >= lo, and
+// d * inv <= 15.01 unless s has lost bits below 2^-14, where the codes are clamped.  The bits of y are those of the magic
+// number plus the code, and the multiples of the former that eight products with powers of 16 add up are one constant.
+__device__ __forceinline__ uint32_t kv_codes(const float2 (&x)[4], float lo, float s, float inv) {
+  constexpr float kMagic = 12582912.f;  // 0x4b400000
+  const float2 nlo = make_float2(-lo, -lo), i2 = make_float2(inv, inv), mg = make_float2(kMagic, kMagic),
+               minus = make_float2(-1.f, -1.f);
+  float2 y[4];
+  float rest = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 d = kv_add2(x[j], nlo);
+    y[j] = kv_fma2(d, i2, mg);
+    const float2 f = kv_fma2(d, i2, kv_fma2(y[j], minus, mg));
+    rest = fmaxf(rest, fmaxf(fabsf(f.x), fabsf(f.y)));
   }
-  return min(max(c, 0), 15);
+  if (rest > 0.49999f || s < 6.103515625e-05f) {  // rare
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float& v = k ? y[j].y : y[j].x;
+        const float xx = k ? x[j].y : x[j].x, c = v - kMagic;
+        const float f = __fmaf_rn(__fsub_rn(xx, lo), inv, -c);
+        const float best = fabsf(f) > 0.49999f ? kv_code_near_tie(xx, lo, s, inv) : c;
+        v = fminf(best, 15.f) + kMagic;
+      }
+    }
+  }
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    word += __float_as_uint(y[j].x) * (1u << (8 * j)) + __float_as_uint(y[j].y) * (1u << (8 * j + 4));
+  return word - 0x4b400000u * 0x11111111u;
 }
 
 // A warp takes kAppendTokens consecutive tokens of one head, of K or of V; a row is held by D / 8 lanes, 8
@@ -175,15 +229,18 @@ __device__ __forceinline__ int kv_code(float x, float lo, float s, float inv) {
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_i4_kernel(
     const __half* __restrict__ k, const __half* __restrict__ v, long long k_stride, long long v_stride, int T, int H,
-    const int* __restrict__ slots, uint8_t* __restrict__ cache, long long pages, int ps, unsigned* err) {
+    const int* __restrict__ slots, uint8_t* __restrict__ cache, int pages, int ps, FastDiv by_ps, FastDiv by_h,
+    unsigned* err) {
   using L = KvI4<D>;
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIter = kAppendTokens / kRows;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, rl = lane / kLanes;
-  const long long unit = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
-  const long long ntb = (T + kAppendTokens - 1) / kAppendTokens;
-  if (unit >= ntb * 2 * H) return;
-  const int is_v = (int)(unit & 1), h = (int)((unit >> 1) % H);
-  const long long t0 = (unit >> 1) / H * kAppendTokens;
+  grid_dependency_wait();  // k and v may come from the preceding kernel
+  grid_dependents_launch();
+  const uint32_t unit = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);  // (8 tokens, head, K or V)
+  const uint32_t tb = quot(unit >> 1, by_h);
+  const int is_v = (int)(unit & 1), h = (int)((unit >> 1) - tb * H);
+  const long long t0 = (long long)tb * kAppendTokens;
+  if (t0 >= T) return;
   const __half* src = is_v ? v : k;
   const long long stride = is_v ? v_stride : k_stride;
   const int bpp = ps / kKvBlock;
@@ -207,21 +264,16 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_i4_kernel(
     for (int o = kLanes / 2; o >= 1; o >>= 1) mm = __hmin2_nan(mm, __shfl_xor_sync(0xffffffffu, mm, o));
     const float lo = __low2float(mm), hi = -__high2float(mm);
     const float d = __fsub_rn(hi, lo);
-    uint32_t word = 0, par = 0x7fff7fffu;
-    if (isfinite(lo) && isfinite(hi)) {
-      const float bb = __fsub_rn(d, hi);
-      const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(d, bb)), __fsub_rn(-lo, bb));
-      const __half sh = kv_scale(d, e);
-      const float s = __half2float(sh), inv = __fdiv_rn(1.0f, s);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        word |= (uint32_t)kv_code(__low2float(x2[j]), lo, s, inv) << (8 * j);
-        word |= (uint32_t)kv_code(__high2float(x2[j]), lo, s, inv) << (8 * j + 4);
-      }
-      par = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(__low2half(mm)) << 16);
-    }
+    const float bb = __fsub_rn(d, hi);
+    const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(d, bb)), __fsub_rn(-lo, bb));
+    const __half sh = kv_scale(d, e);
+    const float s = __half2float(sh), inv = __fdiv_rn(1.0f, s);
+    const float2 x[4] = {__half22float2(x2[0]), __half22float2(x2[1]), __half22float2(x2[2]), __half22float2(x2[3])};
+    uint32_t word = kv_codes(x, lo, s, inv);
+    uint32_t par = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(__low2half(mm)) << 16);
+    if (!isfinite(lo) || !isfinite(hi)) word = 0, par = 0x7fff7fffu;
     if (slot[i] < 0) continue;
-    const int page = slot[i] / ps, at = slot[i] - page * ps;
+    const int page = (int)quot((uint32_t)slot[i], by_ps), at = slot[i] - page * ps;
     if (page >= pages) {
       if (sub == 0) report_error(err, kErrBadIndex);
       continue;
@@ -242,29 +294,31 @@ constexpr int kReadThreads = 256;
 // A thread reads 8 channels (4 bytes of codes) of one row of K and of V and writes 16 bytes to each output; rows of
 // negative slots read as zeros.
 template <int D>
-__global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const uint8_t* __restrict__ cache, long long pages,
-                                                                  int ps, int H, const int* __restrict__ slots, int T,
+__global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const uint8_t* cache, int pages, int ps, FastDiv by_ps,
+                                                                  int H, FastDiv by_h, const int* __restrict__ slots, int T,
                                                                   __half* __restrict__ k, __half* __restrict__ v,
                                                                   unsigned* err) {
   using L = KvI4<D>;
   constexpr int kLanes = D / 8;
   const long long n = (long long)T * H * kLanes;
   const int bpp = ps / kKvBlock;
+  grid_dependency_wait();  // the cache may come from the preceding kernel
+  grid_dependents_launch();
   for (long long i = (long long)blockIdx.x * kReadThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kReadThreads) {
     const int sub = (int)(i % kLanes);
-    const long long th = i / kLanes;
-    const int h = (int)(th % H), slot = __ldg(slots + th / H);
+    const uint32_t th = (uint32_t)(i / kLanes), t = quot(th, by_h);  // T * H is below 2^31
+    const int h = (int)(th - t * H), slot = __ldg(slots + t);
     __align__(16) __half2 o[2][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j >> 2][j & 3] = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
-    const int page = slot / ps, at = slot - page * ps;
+    const int page = slot < 0 ? -1 : (int)quot((uint32_t)slot, by_ps), at = slot - page * ps;
     if (slot >= 0 && page >= pages) report_error(err, kErrBadIndex);
     if (slot >= 0 && page < pages) {
       const uint8_t* blk = cache + (((long long)page * H + h) * bpp + at / kKvBlock) * L::kBytes;
       const int row = at % kKvBlock;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(blk + (s ? L::kV : 0) + row * L::kRow + 4 * sub));
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + (s ? L::kV : 0) + row * L::kRow + 4 * sub);
         const __half2 par = *reinterpret_cast<const __half2*>(blk + (s ? L::kVp : L::kKp) + 4 * row);
         const __half2 sc = __low2half2(par), lo = __high2half2(par);
 #pragma unroll
@@ -276,10 +330,25 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const uint8_t*
         }
       }
     }
-    const long long at8 = th * kLanes + sub;
+    const long long at8 = (long long)th * kLanes + sub;
     __stcs(reinterpret_cast<uint4*>(k) + at8, *reinterpret_cast<const uint4*>(o[0]));
     __stcs(reinterpret_cast<uint4*>(v) + at8, *reinterpret_cast<const uint4*>(o[1]));
   }
+}
+
+// A launch that may start before the kernel ahead of it has ended; the kernels wait for it before they read anything.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), int grid, int threads, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 }  // namespace
@@ -287,10 +356,11 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const uint8_t*
 cudaError_t launch_kv_plan(const int* ctx_lens, const int* new_lens, int B, int ps, const int* free_pages, int free_cap,
                            const int* free_count, int* table, int width, int T, int* cu_new, int* kv_lens, int* slots,
                            int* free_count_out, cudaStream_t s) {
-  const int grid = T > 0 ? (T + kPlanSlots - 1) / kPlanSlots : 1;
-  kv_plan_kernel<<<grid, kPlanThreads, 0, s>>>(ctx_lens, new_lens, B, ps, free_pages, free_cap, free_count, table, width,
-                                               T, cu_new, kv_lens, slots, free_count_out);
-  return cudaGetLastError();
+  // a CTA for every kPlanSlots slots, and enough for four requests' tables per warp
+  const int for_slots = (T + kPlanSlots - 1) / kPlanSlots, for_pages = (B + 31) / 32;
+  const int grid = for_slots > for_pages ? for_slots : for_pages > 0 ? for_pages : 1;
+  return launch_early(kv_plan_kernel, grid, kPlanThreads, s, ctx_lens, new_lens, B, ps, fast_div(ps), free_pages, free_cap,
+                      free_count, table, width, T, cu_new, kv_lens, slots, free_count_out);
 }
 
 cudaError_t launch_kv_append_i4(const uint16_t* k, const uint16_t* v, long long k_stride, long long v_stride, int T,
@@ -299,9 +369,9 @@ cudaError_t launch_kv_append_i4(const uint16_t* k, const uint16_t* v, long long 
   const long long units = (long long)((T + kAppendTokens - 1) / kAppendTokens) * 2 * H;
   const long long per = kAppendThreads / 32, grid = (units + per - 1) / per;
   auto* kernel = D == 128 ? kv_append_i4_kernel<128> : kv_append_i4_kernel<64>;
-  kernel<<<(unsigned)grid, kAppendThreads, 0, s>>>(reinterpret_cast<const __half*>(k), reinterpret_cast<const __half*>(v),
-                                                   k_stride, v_stride, T, H, slots, cache, pages, ps, dev_err);
-  return cudaGetLastError();
+  return launch_early(kernel, (int)grid, kAppendThreads, s, reinterpret_cast<const __half*>(k),
+                      reinterpret_cast<const __half*>(v), k_stride, v_stride, T, H, slots, cache, (int)pages, ps,
+                      fast_div(ps), fast_div(H), dev_err);
 }
 
 cudaError_t launch_kv_read_i4(const uint8_t* cache, long long pages, int ps, int H, int D, const int* slots, int T,
@@ -309,9 +379,8 @@ cudaError_t launch_kv_read_i4(const uint8_t* cache, long long pages, int ps, int
   const long long n = (long long)T * H * (D / 8), want = (n + kReadThreads - 1) / kReadThreads;
   const long long cap = 8LL * num_sms();
   auto* kernel = D == 128 ? kv_read_i4_kernel<128> : kv_read_i4_kernel<64>;
-  kernel<<<(unsigned)(want < cap ? want : cap), kReadThreads, 0, s>>>(
-      cache, pages, ps, H, slots, T, reinterpret_cast<__half*>(k), reinterpret_cast<__half*>(v), dev_err);
-  return cudaGetLastError();
+  return launch_early(kernel, (int)(want < cap ? want : cap), kReadThreads, s, cache, (int)pages, ps, fast_div(ps), H, fast_div(H),
+                      slots, T, reinterpret_cast<__half*>(k), reinterpret_cast<__half*>(v), dev_err);
 }
 
 }  // namespace wql

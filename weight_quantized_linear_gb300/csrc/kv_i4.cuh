@@ -24,4 +24,15 @@ struct KvI4 {
   static constexpr int kBytes = kKvBlock * (D + 8);     // a block
 };
 
+// Division by a number known at launch: n / d for 0 <= n < 2^31 (Granlund and Montgomery's multiplier with l = ceil(log2 d)).
+struct FastDiv {
+  uint32_t d, m, l;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return {d, (uint32_t)((((1ull << l) - d) << 32) / d + 1), l};
+}
+__device__ __forceinline__ uint32_t quot(uint32_t n, const FastDiv& f) { return (__umulhi(n, f.m) + n) >> f.l; }
+
 }  // namespace wql
