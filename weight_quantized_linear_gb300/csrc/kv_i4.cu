@@ -139,12 +139,12 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 8;  // tokens per warp, of one head and one of K and V
 
 // fp16((max - lo) / 15) of the real quotient, from d + e = max - lo (d the fp32 difference, e its exact
-// remainder).  fl(d / 15) is within 2 fp32 ulps of the real quotient, so only when it comes within 4 ulps
+// remainder).  fl(d * fl(1 / 15)) is within 2 fp32 ulps of the real quotient, so only when it comes within 4 ulps
 // of the middle between two fp16 numbers can its rounding differ from the real quotient's; there the sign of
 // (d - 15 tie) + e decides, whose first difference is exact (both are close, 15 tie has 16 bits).  Below
 // 2^-14 (fp16 subnormals) x is a small multiple of 2^-24, d is exact, and n / 15 is never a tie.
 __device__ __forceinline__ __half kv_scale(float d, float e) {
-  const float q = __fdiv_rn(d, 15.0f);
+  const float q = __fmul_rn(d, 1.0f / 15.0f);
   const unsigned b = __float_as_uint(q), low = b & 0x1fffu;
   float r = q;
   if (q >= 6.103515625e-05f && low - 0xffcu <= 8u) {
@@ -186,8 +186,8 @@ __device__ __forceinline__ float kv_code_near_tie(float x, float lo, float s, fl
 }
 
 // The codes clamp(round_half_even((x - lo) / s), 0, 15) of eight values, the first in the lowest bits.
-// y = fl(d * inv + 1.5 * 2^23) with d = fl(x - lo), inv = fl(1 / s) is that magic number plus the integer nearest to
-// d * inv, which is off the quotient by at most 2^-23 * 16 < 2e-6, so that integer is the code unless the rest
+// y = fl(d * inv + 1.5 * 2^23) with d = fl(x - lo), inv within 2^-23 of 1 / s is that magic number plus the integer nearest
+// to d * inv, which is off the quotient by at most 2^-22 * 16 < 4e-6, so that integer is the code unless the rest
 // d * inv - integer (exact up to one rounding) comes within 1e-5 of a half; then kv_code_near_tie decides.  x >= lo, and
 // d * inv <= 15.01 unless s has lost bits below 2^-14, where the codes are clamped.  The bits of y are those of the magic
 // number plus the code, and the multiples of the former that eight products with powers of 16 add up are one constant.
@@ -202,20 +202,21 @@ __device__ __forceinline__ uint32_t kv_codes(const float2 (&x)[4], float lo, flo
     const float2 d = kv_add2(x[j], nlo);
     y[j] = kv_fma2(d, i2, mg);
     const float2 f = kv_fma2(d, i2, kv_fma2(y[j], minus, mg));
-    rest = fmaxf(rest, fmaxf(fabsf(f.x), fabsf(f.y)));
+    asm("max.f32 %0, %0, %1, %2;" : "+f"(rest) : "f"(fabsf(f.x)), "f"(fabsf(f.y)));
   }
-  if (rest > 0.49999f || s < 6.103515625e-05f) {  // rare
+  if (rest > 0.49999f) {  // one lane in a hundred
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float& v = k ? y[j].y : y[j].x;
-        const float xx = k ? x[j].y : x[j].x, c = v - kMagic;
-        const float f = __fmaf_rn(__fsub_rn(xx, lo), inv, -c);
-        const float best = fabsf(f) > 0.49999f ? kv_code_near_tie(xx, lo, s, inv) : c;
-        v = fminf(best, 15.f) + kMagic;
+        const float xx = k ? x[j].y : x[j].x;
+        if (fabsf(__fmaf_rn(__fsub_rn(xx, lo), inv, kMagic - v)) > 0.49999f) v = kMagic + kv_code_near_tie(xx, lo, s, inv);
       }
-    }
+  }
+  if (s < 6.103515625e-05f) {  // 2^-14
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = make_float2(fminf(y[j].x, kMagic + 15.f), fminf(y[j].y, kMagic + 15.f));
   }
   uint32_t word = 0;
 #pragma unroll
@@ -267,11 +268,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_i4_kernel(
     const float bb = __fsub_rn(d, hi);
     const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(d, bb)), __fsub_rn(-lo, bb));
     const __half sh = kv_scale(d, e);
-    const float s = __half2float(sh), inv = __fdiv_rn(1.0f, s);
+    const float s = __half2float(sh);
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
     const float2 x[4] = {__half22float2(x2[0]), __half22float2(x2[1]), __half22float2(x2[2]), __half22float2(x2[3])};
     uint32_t word = kv_codes(x, lo, s, inv);
     uint32_t par = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(__low2half(mm)) << 16);
-    if (!isfinite(lo) || !isfinite(hi)) word = 0, par = 0x7fff7fffu;
+    if (!(d <= 131008.f)) word = 0, par = 0x7fff7fffu;  // some value is not finite
     if (slot[i] < 0) continue;
     const int page = (int)quot((uint32_t)slot[i], by_ps), at = slot[i] - page * ps;
     if (page >= pages) {
