@@ -40,7 +40,7 @@ namespace wql {
 namespace {
 
 constexpr int kStep = 32;                       // tokens per step
-constexpr int kLead = 1;                        // steps that stand for a unit's own cost
+constexpr int kLead = 3;                        // steps that stand for a unit's own cost
 constexpr float kNoMax = -1e30f;                // maximum of nothing
 // Weights are kept below 2^15: at each raise of m the largest becomes 2^7, so that those down to 2^-21 of it are normal
 // fp16 numbers.
@@ -140,7 +140,8 @@ struct Args {
 
 __device__ __forceinline__ int seq_len(const Args& a, int b) { return min(max(a.kv_lens[b], 0), a.cap); }
 // Steps of a unit of sequence b.  Its first kLead steps are no tokens: they stand for what a unit costs beside them (its
-// queries, reductions and output), so that the warps that meet many short units get fewer tokens.
+// queries, reductions and output), so that the warps that meet many short units get fewer tokens (64 ragged contexts:
+// 62 us without, 61, 60 and 59 us with one, two and three lead steps).
 __device__ __forceinline__ int seq_steps(const Args& a, int b) {
   const int n = (seq_len(a, b) + kStep - 1) / kStep;
   return n > 0 ? n + kLead : 0;
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   if (!a.split) {
     const int b = (int)blockIdx.x / hr_all;
     if (tid == 0 && a.kv_lens[b] > a.cap) report_error(a.err, kErrBadIndex);
-    n0 = 0, n1 = quota = seq_steps(a, b);
+    n0 = kLead, n1 = quota = seq_steps(a, b);  // nothing to even out: no lead steps
     if (n1 == 0) {
       const int head = (int)blockIdx.x % hr_all / a.RB, row0 = (int)blockIdx.x % a.RB * C::kRows;
       zero_rows<D>(a, b, head, row0, C::kRows);
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
       }
 
       // ---- the unit's result, or this warp's part of it --------------------------------------------
-      const bool open_left = u.s > 0, open_right = at + (u.n - u.s) > r1, whole = !open_left && !open_right;
+      const bool open_left = u.s > (a.split ? 0 : kLead), open_right = at + (u.n - u.s) > r1, whole = !open_left && !open_right;
       float* dst = open_left ? join + warp * C::kRows * C::kJoinPitch : const_cast<float*>(reinterpret_cast<const float*>(ring));
       float2* mld = ml + ((open_left ? 0 : kW) + warp) * C::kRows;
       if (lane == 0 && !whole)
@@ -728,43 +729,42 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
     __threadfence();
     for (int i = tid; i < parts; i += C::kThreads) a.flag[2 * (c0 + i) + (i < parts - 1 ? 1 : 0)] = 0ull;
     const int head = (int)quot(info.y, a.rb), row0 = (info.y - head * a.RB) * C::kRows;
-    auto part = [&](int i, int row) {
-      return a.part + (((long long)(c0 + i) * 2 + (i < parts - 1 ? 1 : 0)) * C::kRows + row) * kPitch;
-    };
-    float2* fp = reinterpret_cast<float2*>(smem);  // [kRows][parts] {factor, its l}, over the rings
-    for (int row = warp; row < C::kRows; row += kW + 1) {
-      float top = kNoMax;
-      for (int i = lane; i < parts; i += 32) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(part(i, row) + D));
-        fp[row * parts + i] = x;
-        top = fmaxf(top, x.x);
-      }
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      for (int i = lane; i < parts; i += 32) {
-        const float2 x = fp[row * parts + i];
-        const float f = ex2(x.x - top);
-        fp[row * parts + i] = make_float2(f, x.y * f);
-      }
-    }
-    __syncthreads();
+    // one pass over the parts, kAhead of them in flight at a time: one more trip to the L2 cache for the maxima costs 1 us
+    constexpr int kAhead = D == 128 ? 20 : 10;
     for (int i = tid; i < C::kRows * (D / 4); i += C::kThreads) {
       const int row = i / (D / 4), q4 = i % (D / 4) * 4, r_all = row0 + row;
       if (r_all >= a.Lq * a.G) continue;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      float ls = 0.f;
-#pragma unroll 16
-      for (int k = 0; k < parts; ++k) {
-        const float2 f = fp[row * parts + k];
-        const float4 z = __ldcg(reinterpret_cast<const float4*>(part(k, row) + q4));
-        x.x = fmaf(z.x, f.x, x.x), x.y = fmaf(z.y, f.x, x.y), x.z = fmaf(z.z, f.x, x.z), x.w = fmaf(z.w, f.x, x.w);
-        ls += f.y;
+      float ls = 0.f, top = kNoMax;
+      // slot 1 of the CTAs in which the unit goes on, slot 0 of the last
+      const float* first = a.part + (((long long)c0 * 2 + 1) * C::kRows + row) * kPitch;
+      for (int k0 = 0; k0 < parts; k0 += kAhead) {
+        float2 ml2[kAhead];
+        float4 z[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int n = k0 + k;
+          const float* src = first + (n * 2 - (n == parts - 1 ? 1 : 0)) * (C::kRows * kPitch);
+          ml2[k] = n < parts ? __ldcg(reinterpret_cast<const float2*>(src + D)) : make_float2(kNoMax, 0.f);
+          z[k] = n < parts ? __ldcg(reinterpret_cast<const float4*>(src + q4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float now = top;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) now = fmaxf(now, ml2[k].x);
+        const float old = ex2(top - now);
+        top = now;
+        x.x *= old, x.y *= old, x.z *= old, x.w *= old, ls *= old;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float f = ex2(ml2[k].x - top);
+          x.x = fmaf(z[k].x, f, x.x), x.y = fmaf(z[k].y, f, x.y), x.z = fmaf(z[k].z, f, x.z), x.w = fmaf(z[k].w, f, x.w);
+          ls = fmaf(ml2[k].y, f, ls);
+        }
       }
       const float inv = ls == 0.f ? 0.f : 1.f / ls;
       __half* y = a.out + (((long long)info.x * a.Lq + r_all / a.G) * a.Hq + head * a.G + r_all % a.G) * D + q4;
       *reinterpret_cast<uint2*>(y) = make_uint2(pack_h2(x.x * inv, x.y * inv), pack_h2(x.z * inv, x.w * inv));
     }
-    __syncthreads();
   }
 }
 
