@@ -18,10 +18,12 @@
 // and loads and products of the next begin before the outputs of this one are written: a CTA per pair spends about
 // 8 us per pair outside the loop over its keys (nine packed prompts of 412 to 3700 tokens, 32 heads: 404 us).
 //
-// That latency is why the weights are computed with the maximum as it was, while the new one is still being found: the
-// accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last time (the weights are
-// then still below 2^15), and only then are the step's weights computed again.  The softmax warps rescale it
-// themselves: S(j) complete implies P V(j - 1) complete, since both were issued before the commit that signals S(j).
+// That latency is why a step's weights are computed with the maximum as it was, without looking for the new one: as
+// long as they add up to less than 2^15, none of them is too large for fp16, and the sum is needed anyway.  Only a step
+// with more looks for its maximum, rescales the accumulator and computes its weights again (with the maximum found
+// in every step, and an exponent's growth of 8 as the sign to rescale, 16384 tokens of 32 heads take 1.44 ms).  The softmax
+// warps rescale it themselves: S(j) complete implies P V(j - 1) complete, since both were issued before the commit that
+// signals S(j).
 //
 // Rows see nothing behind them: scores above the diagonal are replaced, not added to.  V rows behind a row would meet
 // its zero weights in the product, so in the tiles on the diagonal two warps first replace V values that are not
@@ -40,8 +42,8 @@ constexpr int kTile = 128;                  // query rows and keys of a tile
 constexpr int kThreads = 512;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kCheckWarp = 11, kNextWarp = 12;
 constexpr int kSorted = 128;                // up to so many sequences, the pairs are sorted by their keys
-constexpr float kTop = 7.0f;                // the largest weight after a rescale is 2^7 ...
-constexpr float kRaise = 8.0f;              // ... and before the next at most 2^15
+constexpr float kTop = 7.0f;                // the largest weight after a rescale is 2^7, the 128 of a step at most 2^14
+constexpr float kMost = 32768.f;            // and a step whose weights come to more than 2^15 asks for the next
 // registers per thread: launched with 128; the softmax warpgroups take 208, the others give down to 48
 // (256 x 208 + 256 x 48 = 65536 = 512 x 128)
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 48;
@@ -552,12 +554,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 128; ++i)
             if (i > row) s[i >> 5][i & 31] = 0xff800000u;
         }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto row_max = [&]() {  // of the scaled scores, less kTop
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 128; i += 2)
-          top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
-        const float up = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c - kTop;
-        if (j == 0) m = up;
+          for (int i = 0; i < 128; i += 2)
+            top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
+          return fmaxf(max3(top[0], top[1], top[2]), top[3]) * c - kTop;
+        };
+        if (j == 0) m = row_max();
         float a0, a1;  // this step's sums
         auto weights = [&]() {
           a0 = a1 = 0.f;
@@ -576,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         weights();
-        if (__any_sync(0xffffffffu, up > m + kRaise)) {
-          const float now = fmaxf(m, up), f = ex2(m - now);
+        if (__any_sync(0xffffffffu, a0 + a1 > kMost)) {
+          const float now = fmaxf(m, row_max()), f = ex2(m - now);
           m = now;
           l0 *= f, l1 *= f;
 #pragma unroll 1
