@@ -565,6 +565,10 @@ wql_status wql_attention_kv_i4(const uint16_t* q, int64_t q_stride, int B, int L
               "table_width * page_size must be between 16 and 2^31 - 1");
   WQL_REQUIRE((int64_t)Lq * Hq <= INT_MAX / 256, "Lq * Hq is too large");
   WQL_REQUIRE(std::isfinite(scale), "scale must be finite");
+  // the kernel counts 32-token steps (and a few per K/V head beside them) in 32 bits
+  const int64_t row_blocks = ((int64_t)Lq * (Hq / Hkv) + 7) / 8, steps = ((int64_t)table_width * page_size + 31) / 32 + 4;
+  if ((double)B * Hkv * (double)row_blocks * (double)steps > (double)INT_MAX)
+    return fail(WQL_EUNSUPPORTED, "B * Hkv * row blocks * (table_width * page_size / 32 + 4) must be below 2^31");
   if (B == 0 || Lq == 0) {
     g_last_error.clear();
     return WQL_OK;
@@ -580,10 +584,6 @@ wql_status wql_attention_kv_i4(const uint16_t* q, int64_t q_stride, int B, int L
               "workspace is smaller than wql_attention_kv_i4_workspace_bytes");
   unsigned* dev_err = device_error_word();
   if (!dev_err) return fail(WQL_ECUDA, "wql_attention_kv_i4: cannot locate the device error word");
-  // 32-bit counts of 32-token steps in the kernel
-  const int64_t rows = ((int64_t)Lq * (Hq / Hkv) + 7) / 8, steps = ((int64_t)table_width * page_size + 31) / 32;
-  if ((double)B * Hkv * (double)rows * (double)steps > (double)INT_MAX)
-    return fail(WQL_EUNSUPPORTED, "B * Hkv * row blocks * table_width * page_size / 32 must be below 2^31");
   std::string err;
   const cudaError_t e = wql::launch_attn_kv_i4(q, q_stride, B, Lq, Hq, Hkv, D, cache, pages, page_size, block_table,
                                                table_width, kv_lens, scale, out, workspace, dev_err,

@@ -55,9 +55,9 @@ struct Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kJoinPitch = D + 4;                                  // floats per row of the join buffer
   static constexpr int kOffJoin = kWarps * kStages * kStepBytes;            // [kWarps][kRows][kJoinPitch] fp32: first parts
-  static constexpr int kOffMl = kOffJoin + kWarps * kRows * kJoinPitch * 4; // [2][kWarps][kRows] {m, l}: first parts, last parts
+  static constexpr int kOffMl = kOffJoin + kWarps * kRows * kJoinPitch * 4; // [first, last part][kWarps][kRows] {m, l}
   static constexpr int kOffFac = kOffMl + 2 * kWarps * kRows * 8;           // [2][kWarps][kRows] {factor, its l, maximum}
-  static constexpr int kOffBar = kOffFac + 2 * kWarps * kRows * 16;              // [2][kWarps][kStages] mbarriers: full, empty
+  static constexpr int kOffBar = kOffFac + 2 * kWarps * kRows * 16;         // [full, empty][kWarps][kStages] mbarriers
   static_assert(kRows * kJoinPitch * 4 <= kStages * kStepBytes, "a last part takes the warp's ring");
   static constexpr int kSmem = kOffBar + 2 * kWarps * kStages * 8;
 };
@@ -266,84 +266,83 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   // ---- the warp that requests: lane w keeps warp w's ring filled ---------------------------------
   if (warp == kW) {
     if (lane < warps) {
-    const int bpp = (int)a.bpp.d;
-    const uint32_t ring = smem_u32(smem) + lane * kS * C::kStepBytes;
-    uint64_t* full = bars + lane * kS;
-    uint64_t* empty = bars + (kW + lane) * kS;
-    Cursor pc{s_start[lane].x, s_start[lane].y, s_start[lane].z, s_start[lane].w};
-    int pn = run(lane);  // next step to request
-    const int pn1 = run(lane + 1);
-    int slot = 0, pg0 = 0, pg1 = 0, blk = 0, col0 = 0, last = 0;
-    uint32_t parity = 1;  // the first round finds every stage free
-    auto look_up = [&]() {  // the pages of the two blocks of the step at pc
-      blk = (pc.s - kLead) * (kStep / kKvBlock);
-      last = (seq_len(a, pc.b) - 1) / kKvBlock;
-      col0 = (int)quot(blk, a.bpp);
-      const int* row = a.table + (long long)pc.b * a.width;
-      pg0 = row[col0];
-      pg1 = blk < last ? row[quot(blk + 1, a.bpp)] : pg0;
-    };
-    auto next = [&](int by) {  // to the next step with tokens
-      pn += by;
-      if (by && pn < pn1) advance(a, pc, by);
-      while (pn < pn1 && pc.s < kLead) {
-        pn += 1;
-        if (pn < pn1) advance(a, pc, 1);
-      }
-      if (pn < pn1) look_up();
-    };
-    next(0);
-    unsigned long long since = globaltimer_ns();
-    while (pn < pn1) {
-      // a test, not a wait: a lane whose stage is in use must not hold up the others
-      if (!mbar_test_wait(&empty[slot], parity)) {
-        if (globaltimer_ns() - since > kWaitLimitNs) {
-          report_error(a.err, kErrTimeoutEmpty);
-          break;
+      const int bpp = (int)a.bpp.d;
+      const uint32_t ring = smem_u32(smem) + lane * kS * C::kStepBytes;
+      uint64_t* full = bars + lane * kS;
+      uint64_t* empty = bars + (kW + lane) * kS;
+      Cursor pc{s_start[lane].x, s_start[lane].y, s_start[lane].z, s_start[lane].w};
+      int pn = run(lane);  // next step to request
+      const int pn1 = run(lane + 1);
+      int slot = 0, pg0 = 0, pg1 = 0, blk = 0, col0 = 0, last = 0;
+      uint32_t parity = 1;  // the first round finds every stage free
+      auto look_up = [&]() {  // the pages of the two blocks of the step at pc
+        blk = (pc.s - kLead) * (kStep / kKvBlock);
+        last = (seq_len(a, pc.b) - 1) / kKvBlock;
+        col0 = (int)quot(blk, a.bpp);
+        const int* row = a.table + (long long)pc.b * a.width;
+        pg0 = row[col0];
+        pg1 = blk < last ? row[quot(blk + 1, a.bpp)] : pg0;
+      };
+      auto next = [&](int by) {  // to the next step with tokens
+        pn += by;
+        if (by && pn < pn1) advance(a, pc, by);
+        while (pn < pn1 && pc.s < kLead) {
+          pn += 1;
+          if (pn < pn1) advance(a, pc, 1);
         }
-        __nanosleep(40);
-        continue;
+        if (pn < pn1) look_up();
+      };
+      next(0);
+      unsigned long long since = globaltimer_ns();
+      while (pn < pn1) {
+        // a test, not a wait: a lane whose stage is in use must not hold up the others
+        if (!mbar_test_wait(&empty[slot], parity)) {
+          if (globaltimer_ns() - since > kWaitLimitNs) {
+            report_error(a.err, kErrTimeoutEmpty);
+            break;
+          }
+          __nanosleep(40);
+          continue;
+        }
+        if ((unsigned)pg0 >= (unsigned)a.pages || (unsigned)pg1 >= (unsigned)a.pages) {
+          report_error(a.err, kErrBadIndex);
+          if ((unsigned)pg0 >= (unsigned)a.pages) pg0 = 0;
+          if ((unsigned)pg1 >= (unsigned)a.pages) pg1 = 0;
+        }
+        const int head = (int)quot(pc.hr, a.rb), in0 = blk - col0 * bpp, in1 = in0 + 1 < bpp ? in0 + 1 : 0;
+        const bool two = blk < last;
+        const uint32_t dst = ring + slot * C::kStepBytes;
+        const uint8_t* s0 = a.cache + (((long long)pg0 * a.Hkv + head) * bpp + in0) * L::kBytes;
+        mbar_arrive_expect_tx(&full[slot], two ? 2 * L::kBytes : L::kBytes);
+        if (two && in1 > 0) {
+          bulk_load(dst, s0, 2 * L::kBytes, &full[slot]);
+        } else {
+          bulk_load(dst, s0, L::kBytes, &full[slot]);
+          if (two)
+            bulk_load(dst + L::kBytes, a.cache + (((long long)pg1 * a.Hkv + head) * bpp + in1) * L::kBytes, L::kBytes,
+                      &full[slot]);
+        }
+        slot = slot + 1 == kS ? 0 : slot + 1;
+        parity ^= slot == 0;
+        next(1);
+        since = globaltimer_ns();
       }
-      if ((unsigned)pg0 >= (unsigned)a.pages || (unsigned)pg1 >= (unsigned)a.pages) {
-        report_error(a.err, kErrBadIndex);
-        if ((unsigned)pg0 >= (unsigned)a.pages) pg0 = 0;
-        if ((unsigned)pg1 >= (unsigned)a.pages) pg1 = 0;
-      }
-      const int head = (int)quot(pc.hr, a.rb), in0 = blk - col0 * bpp, in1 = in0 + 1 < bpp ? in0 + 1 : 0;
-      const bool two = blk < last;
-      const uint32_t dst = ring + slot * C::kStepBytes;
-      const uint8_t* s0 = a.cache + (((long long)pg0 * a.Hkv + head) * bpp + in0) * L::kBytes;
-      mbar_arrive_expect_tx(&full[slot], two ? 2 * L::kBytes : L::kBytes);
-      if (two && in1 > 0) {
-        bulk_load(dst, s0, 2 * L::kBytes, &full[slot]);
-      } else {
-        bulk_load(dst, s0, L::kBytes, &full[slot]);
-        if (two)
-          bulk_load(dst + L::kBytes, a.cache + (((long long)pg1 * a.Hkv + head) * bpp + in1) * L::kBytes, L::kBytes,
-                    &full[slot]);
-      }
-      slot = slot + 1 == kS ? 0 : slot + 1;
-      parity ^= slot == 0;
-      next(1);
-      since = globaltimer_ns();
-    }
     }
   } else {
 
-  // ---- the units of a warp's run ---------------------------------------------------------------
-  const uint8_t* ring = smem + warp * kS * C::kStepBytes;
-  uint64_t* full = bars + warp * kS;
-  uint64_t* empty = bars + (kW + warp) * kS;
-  int slot = 0;
-  uint32_t parity = 0;
-  bool alive = true;
-  const int r0 = run(warp), r1 = run(warp + 1);
-  Cursor u{s_start[warp].x, s_start[warp].y, s_start[warp].z, s_start[warp].w};  // of no meaning without a run
-  for (int at = r0; at < r1;) {
-    const int end = min(at + (u.n - u.s), r1);  // of this warp's part of the unit
-    const int len = seq_len(a, u.b), head = (int)quot(u.hr, a.rb), rb = u.hr - head * a.RB;
-    const int rows = a.Lq * a.G, row0 = rb * C::kRows;
-    {
+    // ---- the units of a warp's run ---------------------------------------------------------------
+    const uint8_t* ring = smem + warp * kS * C::kStepBytes;
+    uint64_t* full = bars + warp * kS;
+    uint64_t* empty = bars + (kW + warp) * kS;
+    int slot = 0;
+    uint32_t parity = 0;
+    bool alive = true;
+    const int r0 = run(warp), r1 = run(warp + 1);
+    Cursor u{s_start[warp].x, s_start[warp].y, s_start[warp].z, s_start[warp].w};  // of no meaning without a run
+    for (int at = r0; at < r1;) {
+      const int end = min(at + (u.n - u.s), r1);  // of this warp's part of the unit
+      const int len = seq_len(a, u.b), head = (int)quot(u.hr, a.rb), rb = u.hr - head * a.RB;
+      const int rows = a.Lq * a.G, row0 = rb * C::kRows;
       // Q fragments: thread (g, c) holds row g's channels of its K words, paired as the codes will be
       uint32_t qf[NT][kKw][4];
       float2 qsum[NT];  // of rows 2c and 2c + 1, scaled
@@ -634,13 +633,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
           }
         }
       }
+      at = end;
+      if (at < r1) {
+        u.s = u.n - 1;
+        advance(a, u, 1);
+      }
     }
-    at = end;
-    if (at < r1) {
-      u.s = u.n - 1;
-      advance(a, u, 1);
-    }
-  }
   }  // of the warps that compute
 
   // ---- join the parts of the warps -----------------------------------------------------------------
@@ -648,7 +646,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   // of warp c - 1 (chain 0 with the first part of warp 0: that unit began in an earlier CTA) and goes on with the first
   // parts of warps c .. up to one that ends the unit, or to the CTA's end.
   __syncthreads();
-  const int4 none = make_int4(0, 0, 0, 0), info_f = lane < warps ? s_first[lane] : none, info_l = lane < warps ? s_last[lane] : none;
+  const int4 none = make_int4(0, 0, 0, 0);
+  const int4 info_f = lane < warps ? s_first[lane] : none, info_l = lane < warps ? s_last[lane] : none;
   const unsigned has_f = __ballot_sync(0xffffffffu, info_f.w & kPart), ends_f = __ballot_sync(0xffffffffu, info_f.w & kEnds);
   const unsigned has_l = __ballot_sync(0xffffffffu, info_l.w & kPart);
   const unsigned chains = (has_l << 1) | (has_f & 1u);
