@@ -392,7 +392,8 @@ wql_status wql_kv_plan_pages(const int32_t* ctx_lens, const int32_t* new_lens, i
  * Differences and quotients are the real ones, rounded once, so the cache is bit-exact with this
  * definition.  A row that holds an infinity or a NaN gets s = lo = NaN and reads back as NaN.
  * Negative slots are passed over (padding); slots behind the last page are left out and recorded.
- * No slot may occur twice in a call: what such a slot then holds is unspecified.
+ * No slot may occur twice in a call: what such a slot then holds is unspecified.  T * H < 2^31
+ * (WQL_EUNSUPPORTED above), here and in kv_read_i4.
  * kv_read_i4: k, v [T, H, D] fp16 (dense) = fp16(code * s + lo) of the rows at slots, one rounding;
  * zeros for negative slots and slots out of range.  A slot may occur any number of times.
  * ---------------------------------------------------------------------------------------- */
@@ -418,6 +419,8 @@ wql_status wql_kv_read_i4(const uint8_t* cache, int64_t pages, int page_size, in
  * workspace: device scratch of at least wql_attention_kv_i4_workspace_bytes(B, Lq, Hq, Hkv, D)
  * bytes (the current device's), with no contents to keep; calls that may run at the same time
  * need one each.  out must overlap no input.  Calls and results are deterministic.
+ * Requires B * Hkv * ceil(Lq * Hq / Hkv / 8) * (table_width * page_size / 32 + 5) < 2^31
+ * (WQL_EUNSUPPORTED above).
  * ---------------------------------------------------------------------------------------- */
 size_t wql_attention_kv_i4_workspace_bytes(int B, int Lq, int Hq, int Hkv, int D);
 wql_status wql_attention_kv_i4(const uint16_t* q, int64_t q_stride, int B, int Lq, int Hq, int Hkv,

@@ -511,17 +511,17 @@ def kv_dequant_i8(q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | Non
 # A decode step makes these calls once per layer on little data, so their checks are written to cost little: one test
 # per tensor (_is), and the one that names what is wrong (_refuse) only when it fails.
 
-def _is(t, dtype: torch.dtype, shape: tuple, dev: torch.device) -> bool:
-    return (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == dev
+def _is(t, dtype: torch.dtype, shape: tuple, index: int) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape
             and t.is_contiguous())
 
 
-def _refuse(t, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device) -> None:
-    _need(t, name, dtype, shape)
-    raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _refuse(t, name: str, dtype: torch.dtype, shape: tuple, index: int) -> None:
+    _need(t, name, dtype, tuple(shape))
+    raise ValueError(f"{name} is on {t.device}, expected device {index}")
 
 
-def _stride_of(t, name: str, heads: int | None, dim: int | None, tokens: int | None, dev: torch.device | None) -> int:
+def _stride_of(t, name: str, heads: int | None, dim: int | None, tokens: int | None, index: int | None) -> int:
     """Check an fp16 CUDA tensor [tokens, heads, D] whose rows [heads, D] are dense (a view of a fused projection's
     output); returns its token stride."""
     if not isinstance(t, torch.Tensor):
@@ -536,8 +536,8 @@ def _stride_of(t, name: str, heads: int | None, dim: int | None, tokens: int | N
     if (heads is not None and H != heads) or (dim is not None and D != dim) or (tokens is not None and T != tokens):
         raise ValueError(f"{name} must have shape [{'tokens' if tokens is None else tokens}, "
                          f"{'heads' if heads is None else heads}, {'D' if dim is None else dim}], got {tuple(t.shape)}")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected device {index}")
     st, sh, sd = t.stride()
     if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"{name} must be dense within a token (strides [any, {D}, 1], got {(st, sh, sd)})")
@@ -561,14 +561,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _run(fn: str, dev: torch.device, *args) -> None:
-    """Call fn(*args, stream) with dev current, on dev's current stream."""
+def _run(fn: str, index: int, *args) -> None:
+    """Call fn(*args, stream) with device `index` current, on its current stream."""
     lib = _lib or load()
-    if torch.cuda.current_device() == dev.index:
-        status = getattr(lib, fn)(*args, _raw_stream(dev.index))
+    if torch.cuda.current_device() == index:
+        status = getattr(lib, fn)(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            status = getattr(lib, fn)(*args, _raw_stream(dev.index))
+        with torch.cuda.device(index):
+            status = getattr(lib, fn)(*args, _raw_stream(index))
     if status != WQL_OK:
         _check(status, fn)
 
@@ -591,17 +591,20 @@ def kv_plan_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     [tokens], cu_new [B + 1], kv_lens [B], free_count_out [1]), int32; slots behind the last new token and those of
     refused requests are -1, kv_lens of refused requests 0.  See wql_kv_plan_pages in include/wql.h."""
     i32, B, width, F = torch.int32, ctx_lens.shape[0], block_table.shape[-1], free_pages.shape[0]
-    dev = ctx_lens.device
-    for t, name, shape in ((ctx_lens, "ctx_lens", (B,)), (new_lens, "new_lens", (B,)),
-                           (block_table, "block_table", (B, width)), (free_pages, "free_pages", (F,)),
-                           (free_count, "free_count", (1,))):
-        if not (t.is_cuda and _is(t, i32, shape, dev)):
-            _refuse(t, name, i32, shape, dev)
+    index = ctx_lens.get_device()
+    if not (index >= 0 and _is(ctx_lens, i32, (B,), index) and _is(new_lens, i32, (B,), index)
+            and _is(block_table, i32, (B, width), index) and _is(free_pages, i32, (F,), index)
+            and _is(free_count, i32, (1,), index)):
+        for t, name, shape in ((ctx_lens, "ctx_lens", (B,)), (new_lens, "new_lens", (B,)),
+                               (block_table, "block_table", (B, width)), (free_pages, "free_pages", (F,)),
+                               (free_count, "free_count", (1,))):
+            if index < 0 or not _is(t, i32, shape, index):
+                _refuse(t, name, i32, shape, index)
     # one allocation: slots first (its start is 16-byte aligned), then the small outputs
-    out = torch.empty((tokens + 2 * B + 2,), dtype=i32, device=dev)
-    slots, cu_new, kv_lens, left = out.split((tokens, B + 1, B, 1))
+    out = torch.empty((tokens + 2 * B + 2,), dtype=i32, device=ctx_lens.device)
+    slots, cu_new, kv_lens, left = torch.unsafe_split_with_sizes(out, (tokens, B + 1, B, 1))
     p = out.data_ptr()
-    _run("wql_kv_plan_pages", dev, ctx_lens.data_ptr(), new_lens.data_ptr(), B, page_size, free_pages.data_ptr(), F,
+    _run("wql_kv_plan_pages", index, ctx_lens.data_ptr(), new_lens.data_ptr(), B, page_size, free_pages.data_ptr(), F,
          free_count.data_ptr(), block_table.data_ptr(), width, tokens, p + 4 * tokens, p + 4 * (tokens + B + 1), p,
          p + 4 * (tokens + 2 * B + 1))
     return slots, cu_new, kv_lens, left
@@ -611,13 +614,13 @@ def kv_append_i4(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: t
     """Quantise rows k, v [T, heads, D] fp16 (views of a fused QKV output are taken as they are) into the 4-bit
     cache at slots [T] int32; negative slots are passed over.  Returns cache."""
     pages, H, ps, D = _cache_dims(cache)
-    dev = cache.device
-    ks = _stride_of(k, "k", H, D, None, dev)
+    index = cache.get_device()
+    ks = _stride_of(k, "k", H, D, None, index)
     T = k.shape[0]
-    vs = _stride_of(v, "v", H, D, T, dev)
-    if not _is(slots, torch.int32, (T,), dev):
-        _refuse(slots, "slots", torch.int32, (T,), dev)
-    _run("wql_kv_append_i4", dev, k.data_ptr(), v.data_ptr(), ks, vs, T, H, D, slots.data_ptr(), cache.data_ptr(), pages,
+    vs = _stride_of(v, "v", H, D, T, index)
+    if not _is(slots, torch.int32, (T,), index):
+        _refuse(slots, "slots", torch.int32, (T,), index)
+    _run("wql_kv_append_i4", index, k.data_ptr(), v.data_ptr(), ks, vs, T, H, D, slots.data_ptr(), cache.data_ptr(), pages,
          ps)
     return cache
 
@@ -626,19 +629,18 @@ def kv_read_i4(cache: torch.Tensor, slots: torch.Tensor, k: torch.Tensor | None 
                v: torch.Tensor | None = None):
     """(k, v) [T, heads, D] fp16: the values of the 4-bit cache at slots [T] int32; zeros for negative slots."""
     pages, H, ps, D = _cache_dims(cache)
-    dev, T, f16 = cache.device, slots.shape[0], torch.float16
-    shape = (T, H, D)
-    if not _is(slots, torch.int32, (T,), dev):
-        _refuse(slots, "slots", torch.int32, (T,), dev)
+    dev, index, T, f16, shape = cache.device, cache.get_device(), slots.shape[0], torch.float16, (slots.shape[0], H, D)
+    if not _is(slots, torch.int32, (T,), index):
+        _refuse(slots, "slots", torch.int32, (T,), index)
     if k is None:
         k = torch.empty(shape, dtype=f16, device=dev)
-    elif not _is(k, f16, shape, dev):
-        _refuse(k, "k", f16, shape, dev)
+    elif not _is(k, f16, shape, index):
+        _refuse(k, "k", f16, shape, index)
     if v is None:
         v = torch.empty(shape, dtype=f16, device=dev)
-    elif not _is(v, f16, shape, dev):
-        _refuse(v, "v", f16, shape, dev)
-    _run("wql_kv_read_i4", dev, cache.data_ptr(), pages, ps, H, D, slots.data_ptr(), T, k.data_ptr(), v.data_ptr())
+    elif not _is(v, f16, shape, index):
+        _refuse(v, "v", f16, shape, index)
+    _run("wql_kv_read_i4", index, cache.data_ptr(), pages, ps, H, D, slots.data_ptr(), T, k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -658,7 +660,7 @@ def attention_kv_i4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
     pages, Hkv, ps, D = _cache_dims(cache)
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be a tensor [B, Hq, D] or [B, Lq, Hq, D]")
-    dev, shape = cache.device, q.shape
+    dev, index, shape = cache.device, cache.get_device(), q.shape
     B, Hq = shape[0], shape[-2]
     if len(shape) == 3:
         Lq, rows = 1, q
@@ -667,23 +669,23 @@ def attention_kv_i4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
         if B > 1 and Lq > 1 and q.stride(0) != Lq * q.stride(1):
             raise ValueError("the tokens of q must be evenly strided")
         rows = q[:, 0] if Lq == 1 else q.as_strided((B * Lq, Hq, shape[3]), q.stride()[1:])
-    qs = _stride_of(rows, "q", None, D, None, dev)
+    qs = _stride_of(rows, "q", None, D, None, index)
     width = block_table.shape[-1]
-    if not _is(block_table, torch.int32, (B, width), dev):
-        _refuse(block_table, "block_table", torch.int32, (B, width), dev)
-    if not _is(kv_lens, torch.int32, (B,), dev):
-        _refuse(kv_lens, "kv_lens", torch.int32, (B,), dev)
+    if not _is(block_table, torch.int32, (B, width), index):
+        _refuse(block_table, "block_table", torch.int32, (B, width), index)
+    if not _is(kv_lens, torch.int32, (B,), index):
+        _refuse(kv_lens, "kv_lens", torch.int32, (B,), index)
     if out is None:
         out = torch.empty(shape, dtype=torch.float16, device=dev)
-    elif not _is(out, torch.float16, shape, dev):
-        _refuse(out, "out", torch.float16, tuple(shape), dev)
+    elif not _is(out, torch.float16, shape, index):
+        _refuse(out, "out", torch.float16, shape, index)
     if workspace is None:
         with torch.cuda.device(dev):
             n = attention_kv_i4_workspace_bytes(B, Lq, Hq, Hkv, D)
         workspace = torch.empty((n,), dtype=torch.uint8, device=dev)
-    elif not _is(workspace, torch.uint8, (workspace.numel(),), dev):
-        _refuse(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
-    _run("wql_attention_kv_i4", dev, q.data_ptr(), qs, B, Lq, Hq, Hkv, D, cache.data_ptr(), pages, ps,
+    elif not _is(workspace, torch.uint8, (workspace.numel(),), index):
+        _refuse(workspace, "workspace", torch.uint8, (workspace.numel(),), index)
+    _run("wql_attention_kv_i4", index, q.data_ptr(), qs, B, Lq, Hq, Hkv, D, cache.data_ptr(), pages, ps,
          block_table.data_ptr(), width, kv_lens.data_ptr(), D ** -0.5 if scale is None else scale, out.data_ptr(),
          workspace.data_ptr(), workspace.numel())
     return out
@@ -695,18 +697,18 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     QKV output are taken as they are), cu_seqlens [B + 1] int32.  scale defaults to D ** -0.5.  Returns out
     [T, Hq, D], dense; rows of no sequence are left as they were (undefined when out is not given)."""
     qs = _stride_of(q, "q", None, None, None, None)
-    dev, shape = q.device, q.shape
+    dev, index, shape = q.device, q.get_device(), q.shape
     T, Hq, D = shape
-    ks = _stride_of(k, "k", None, D, T, dev)
+    ks = _stride_of(k, "k", None, D, T, index)
     Hkv = k.shape[1]
-    vs = _stride_of(v, "v", Hkv, D, T, dev)
+    vs = _stride_of(v, "v", Hkv, D, T, index)
     B = cu_seqlens.shape[0] - 1
-    if not _is(cu_seqlens, torch.int32, (B + 1,), dev):
-        _refuse(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    if not _is(cu_seqlens, torch.int32, (B + 1,), index):
+        _refuse(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), index)
     if out is None:
         out = torch.empty(shape, dtype=torch.float16, device=dev)
-    elif not _is(out, torch.float16, shape, dev):
-        _refuse(out, "out", torch.float16, tuple(shape), dev)
-    _run("wql_attention_prompt", dev, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hkv, D,
+    elif not _is(out, torch.float16, shape, index):
+        _refuse(out, "out", torch.float16, shape, index)
+    _run("wql_attention_prompt", index, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hkv, D,
          cu_seqlens.data_ptr(), B, D ** -0.5 if scale is None else scale, out.data_ptr())
     return out
