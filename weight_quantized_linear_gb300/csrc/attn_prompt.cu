@@ -54,6 +54,11 @@ struct Cfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kBoxes * kBox;    // a Q, K or V tile
   static constexpr int kSlots = D == 128 ? 5 : 8;
+  // D = 64 leaves room in tensor memory for P beside S, so that the next S is computed while this one's softmax runs.  The
+  // products are then half of the softmax's work at most, and the tiles need not take turns.
+  static constexpr bool kBeside = D == 64;
+  static constexpr int kColO = 2 * kTile, kColP = kBeside ? kColO + 2 * D : 0;  // tensor memory columns; S from 0
+  static constexpr int kStrideP = kBeside ? kTile / 2 : kTile;                    // between the tiles' P
   static constexpr int kOffRing = 2 * kTileBytes;
   static constexpr int kSmem = kOffRing + kSlots * kTileBytes + 1024;  // and alignment of the start
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -175,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t full[C::kSlots], empty[C::kSlots];
   __shared__ uint64_t sbar[2], pbar[2];        // [tile] S complete; P written (4 warps)
   __shared__ uint64_t obar[2], ofree[2];       // [tile] O complete; O read (4 warps)
+  __shared__ uint64_t sfree[2], pfree[2];      // [tile] P beside S: S read (4 warps); P used
   __shared__ uint64_t vbar[2][2], cbar[2][2];  // [parity of the pair][first, second V tile on a diagonal] landed; checked
   __shared__ uint64_t pair_full[2], pair_empty[2];
   __shared__ uint64_t turn[2];                 // [tile] its products may be queued
@@ -187,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::kSlots; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 2);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&turn[x], 1), mbar_init(&sbar[x], 1), mbar_init(&pbar[x], 4), mbar_init(&obar[x], 1), mbar_init(&ofree[x], 4);
+      mbar_init(&sfree[x], 4), mbar_init(&pfree[x], 1);
       for (int k = 0; k < 2; ++k) mbar_init(&vbar[x][k], 1), mbar_init(&cbar[x][k], 1);
       mbar_init(&pair_full[x], 1), mbar_init(&pair_empty[x], 4 + 8);  // TMA, product, check and softmax warps
       any_bad[x] = 0;
@@ -268,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_o = umma_idesc_f16(kTile, D, /*A from TMEM*/ 0, /*B MN-major*/ 1);
       const uint32_t ring_lo = smem_u32(smem + C::kOffRing) >> 4;
       const uint32_t q_desc = (1u << 16) + ((smem_u32(smem) + x * C::kTileBytes) >> 4);
-      const uint32_t ts = tmem + x * kTile, to = tmem + 2 * kTile + x * D;
+      const uint32_t ts = tmem + x * kTile, to = tmem + C::kColO + x * D, tp = tmem + C::kColP + x * C::kStrideP;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int phase) {
         if (ok && !mbar_wait_warp(bar, phase & 1)) {
@@ -299,13 +306,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bd = ((uint32_t)(C::kBox >> 4) << 16) + ring_lo + slot * (C::kTileBytes >> 4);
         if (leader) {
 #pragma unroll
-          for (int s = 0; s < kTile / 16; ++s) mma_ts(to, ts + s * 8, bd + ((s * 2048) >> 4), idesc_o, s > 0 ? 1u : acc);
+          for (int s = 0; s < kTile / 16; ++s) mma_ts(to, tp + s * 8, bd + ((s * 2048) >> 4), idesc_o, s > 0 ? 1u : acc);
         }
       };
       Ring<C::kSlots> rk, rv;                 // K(j + 1), V(j)
       int pcount = 0, ocount = 0, turns = 0;  // phases of pbar, of obar / ofree, and of turn
+      int scount = 0;                         // S so far
+      auto my_turn = [&]() { return C::kBeside || wait(&turn[x], turns++); };
       auto pass = [&]() {
-        if (leader) mbar_arrive(&turn[x ^ 1]);
+        if (!C::kBeside && leader) mbar_arrive(&turn[x ^ 1]);
+      };
+      auto s_free = [&]() {  // S may be written: its softmax has read it, where P does not say so
+        const bool r = !C::kBeside || scount == 0 || wait(&sfree[x], scount - 1);
+        ++scount;
+        return r;
       };
       for (int it = 0; wait(&pair_full[it & 1], it >> 1); ++it) {
         const int4 v = s_pair[it & 1];
@@ -317,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool signals = x == (p.n1 > 0);  // this warp tells the check warp about V tiles
         // S of the first key tile; the S columns are free, since the products that read their last P come before.  A
         // tile that does not exist, or has fewer keys, follows the ring all the same.
-        if (!wait(&qbar, it) || !wait(&full[rk.slot], rk.phase) || !wait(&turn[x], turns++)) break;
+        if (!wait(&qbar, it) || !wait(&full[rk.slot], rk.phase) || !my_turn()) break;
+        if (n > 0 && !s_free()) break;
         tc_fence_after_sync();
         if (n > 0) qk(rk.slot);
         pass();
@@ -333,22 +348,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int j = 0; j < p.nmax && wait(&full[rv.slot], rv.phase); ++j) {
           if (j + 1 < p.nmax && !wait(&full[rk.slot], rk.phase)) break;
+          if (C::kBeside && j + 1 < n) {
+            if (!s_free()) break;
+            tc_fence_after_sync();
+            qk(rk.slot);
+          }
           if (j < n) {
             if (!wait(&pbar[x], pcount++)) break;
             // the accumulator is taken over when the softmax warps have read that of the pair before
             if (j == 0 && ocount > 0 && !wait(&ofree[x], ocount - 1)) break;
             if (j >= p.jcheck && !wait(&cbar[it & 1][j - p.jcheck], it >> 1)) break;
           }
-          if (!wait(&turn[x], turns++)) break;
+          if (!my_turn()) break;
           tc_fence_after_sync();
           if (j < n) {
             pv(rv.slot, j > 0);
+            if (C::kBeside) release(&pfree[x], true);
             if (j + 1 == n) {
               release(&obar[x], true);
               ++ocount;
             }
           }
-          if (j + 1 < n) qk(rk.slot);
+          if (!C::kBeside && j + 1 < n) qk(rk.slot);
           pass();
           if (j + 1 < p.nmax) {
             release(&empty[rv.slot], j < n);
@@ -526,9 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int x = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + x * kTile + lanes, to = tmem + 2 * kTile + x * D + lanes;
+    const uint32_t ts = tmem + x * kTile + lanes, to = tmem + C::kColO + x * D + lanes;
+    const uint32_t tp = tmem + C::kColP + x * C::kStrideP + lanes;
     const float c = a.scale_log2;
-    int scount = 0, ocount = 0;  // phases of sbar and obar
+    int scount = 0, ocount = 0, pcount = 0;  // phases of sbar and obar; P so far
     bool ok = true;
     auto wait = [&](uint64_t* bar, int phase) {
       if (ok && !mbar_wait_warp(bar, phase & 1)) {
@@ -549,6 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
         tmem_ld_wait();
+        if constexpr (C::kBeside) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[x]);
+        }
         if (j == n - 1) {  // the diagonal tile
 #pragma unroll
           for (int i = 0; i < 128; ++i)
@@ -563,23 +590,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (j == 0) m = row_max();
         float a0, a1;  // this step's sums
+        uint32_t w[C::kBeside ? 4 : 1][16];
         auto weights = [&]() {
           a0 = a1 = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t w[16];
+            uint32_t (&wi)[16] = w[C::kBeside ? i : 0];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float u = __uint_as_float(s[i][2 * e]), v = __uint_as_float(s[i][2 * e + 1]);
               fma2(u, v, c, -m);
               u = ex2(u), v = ex2(v);
               add2(a0, a1, u, v);
-              w[e] = pack_h2(u, v);
+              wi[e] = pack_h2(u, v);
             }
-            tmem_st_32x32b_x16(ts + 16 * i, w);
+            if constexpr (!C::kBeside) tmem_st_32x32b_x16(tp + 16 * i, wi);
           }
         };
         weights();
+        if constexpr (C::kBeside) {  // the last P has been used, and O is that of the steps before
+          if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;
+          ++pcount;
+          tc_fence_after_sync();
+        }
         if (__any_sync(0xffffffffu, a0 + a1 > kMost)) {
           const float now = fmaxf(m, row_max()), f = ex2(m - now);
           m = now;
@@ -594,6 +627,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_32x32b_x32(to + i, o);
           }
           weights();
+        }
+        if constexpr (C::kBeside) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_st_32x32b_x16(tp + 16 * i, w[i]);
         }
         l0 += a0, l1 += a1;
         tmem_st_wait();
