@@ -24,6 +24,10 @@
 // the product as 15 - code with the weight -w, so that the accumulators stay small; and with w' the rounded, signed
 // weights, 7.5 sum_t w'_t is taken off at the end (one more product, with a matrix of ones, gives that sum where it is
 // needed) while p_t (lo_t + 7.5 s_t) goes to the fp32 sum: a weight's rounding then meets code - 7.5.
+// Up to four rows leave half of the products' eight columns free: there the same rows stand a second time (kTwin), with
+// what the rounding of their weights left as weights.  The output is then off by its own rounding alone
+// (2.0e-4 of its norm instead of 2.9e-4).  64 contexts with 4 rows: 59.2 -> 59.9 us; a second set of products instead,
+// which more rows would need, 59 -> 67 us, so those keep rounded weights.
 //
 // mma.sync, not tcgen05: operands come out of registers after the unpacking, 8 rows (the query heads of a K/V
 // head) are the narrow side, and a 16-token block needs 16 products of 16 x 8 x 16, which the SM does in a
@@ -192,8 +196,9 @@ __device__ __forceinline__ int token_of(int r) {
   return 2 * c + (e ^ (D == 128 ? (c & 1) : (c >> 1)));
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kTwin>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(const Args a) {
+  static_assert(!kTwin || NT == 1, "rows 0-3 of one tile, twice");
   using C = Cfg<D, NT>;
   using L = KvI4<D>;
   constexpr int kW = C::kWarps, kS = C::kStages;
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
       int lim[NT][2];   // last visible token of those rows
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int row = row0 + 8 * t + g;
+        const int row = row0 + 8 * t + (kTwin ? g & 3 : g);
         float sum = 0.f;
         uint4 raw[kKw];
 #pragma unroll
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
         qsum[t].y = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int row_e = row0 + 8 * t + 2 * c + e;
+          const int row_e = row0 + 8 * t + (kTwin ? (2 * c + e) & 3 : 2 * c + e);
           lim[t][e] = row_e < rows ? len - a.Lq + row_e / a.G : -1;
         }
       }
@@ -525,7 +530,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
                 }
                 (e ? l[t].y : l[t].x) += p;
               }
-              wb[t][hh] = movmatrix_trans(pack_h2(w[0], w[1]));
+              uint32_t wr = pack_h2(w[0], w[1]);
+              if constexpr (kTwin) {
+                const float2 back = h2f2(wr);
+                if (c >= 2) wr = pack_h2(w[0] - back.x, w[1] - back.y);
+              }
+              wb[t][hh] = movmatrix_trans(wr);
             }
           // codes: words 2g and 2g + 1 (D = 64: word g) of four tokens, paired by token
           uint32_t xv[2][2][2];  // [tile rows g / g + 8][token half][low / high 16 bits of the word]
@@ -618,7 +628,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
 #pragma unroll
             for (int i = 0; i < kMt; ++i) {
               const float k = (i & 1) ? 1048576.f : 16777216.f;
-              v[i] = fmaf(fmaf(wsum, -7.5f / k, o[t][i][e + 2 * hi]), k, add);
+              v[i] = fmaf(wsum, -7.5f / k, o[t][i][e + 2 * hi]) * k;
+              if constexpr (kTwin) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 2);  // both halves of a weight
+              v[i] += add;
             }
             const int ch = (2 * g + hi) * kMt;
             if (!whole) {
@@ -774,7 +786,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
 
 int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
 
-template <int D, int NT>
+template <int D, int NT, bool kTwin>
 cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
   using C = Cfg<D, NT>;
   static std::atomic<bool> ready[64];  // per device; racing first calls set the same attribute
@@ -782,7 +794,7 @@ cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(attn_kv_i4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(attn_kv_i4_kernel<D, NT, kTwin>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
   }
@@ -797,7 +809,7 @@ cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_kv_i4_kernel<D, NT>, a);
+  return cudaLaunchKernelEx(&cfg, attn_kv_i4_kernel<D, NT, kTwin>, a);
 }
 
 }  // namespace
@@ -844,8 +856,13 @@ cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int 
   }
   a.split = units > sms || most > 4 * 12 + kLead;
   const int ctas = (int)(!a.split ? units : units * most < sms ? units * most : sms);
-  if (D == 128) return nt == 1 ? launch<128, 1>(a, ctas, s) : launch<128, 2>(a, ctas, s);
-  return nt == 1 ? launch<64, 1>(a, ctas, s) : launch<64, 2>(a, ctas, s);
+  const bool twin = Lq * G <= 4;  // free columns for the rounding's rest: at the top
+  if (D == 128) {
+    if (twin) return launch<128, 1, true>(a, ctas, s);
+    return nt == 1 ? launch<128, 1, false>(a, ctas, s) : launch<128, 2, false>(a, ctas, s);
+  }
+  if (twin) return launch<64, 1, true>(a, ctas, s);
+  return nt == 1 ? launch<64, 1, false>(a, ctas, s) : launch<64, 2, false>(a, ctas, s);
 }
 
 }  // namespace wql
