@@ -214,6 +214,52 @@ def test_prompt_attention(wql, lens, Hq, Hkv, D):
     assert torch.equal(y.view(torch.int16), z.view(torch.int16))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_attention_tensors_on_16_byte_boundaries(wql, D):
+    # every tensor a view that begins 16 bytes behind a 32-byte boundary
+    q, k, v, cu = _prompt([150], 4, 2, D, seed=3)
+    cu = i32(cu)
+    y = wql.attention_prompt(q, k, v, cu)
+
+    def shifted(x):
+        z = torch.zeros(x.numel() + 16, dtype=x.dtype, device="cuda")[8:8 + x.numel()].view(x.shape)
+        assert z.data_ptr() % 32 == 16
+        return z.copy_(x)
+
+    out = shifted(torch.zeros_like(q))
+    assert wql.attention_prompt(shifted(q), shifted(k), shifted(v), cu, out=out) is out
+    wql.device_status()
+    assert torch.equal(out.view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_kv_i4_tensors_on_16_byte_boundaries(wql, D):
+    q, cache, table, lens = ref.paged_case(3, [40, 700, 9], 2, 8, 2, D, 32, seed=4)
+    y = wql.attention_kv_i4(q, cache, table, lens)
+
+    def shifted(x):
+        n = 16 // x.element_size()
+        z = torch.zeros(x.numel() + 2 * n, dtype=x.dtype, device="cuda")[n:n + x.numel()].view(x.shape)
+        assert z.data_ptr() % 32 == 16
+        return z.copy_(x)
+
+    work = torch.zeros(wql.attention_kv_i4_workspace_bytes(3, 2, 8, 2, D), dtype=torch.uint8, device="cuda")
+    out = wql.attention_kv_i4(shifted(q), shifted(cache), shifted(table), shifted(torch.nn.functional.pad(lens, (0, 1)))[:3],
+                              out=shifted(torch.zeros_like(q)), workspace=shifted(work))
+    wql.device_status()
+    assert torch.equal(out.view(torch.int16), y.view(torch.int16))
+    slots = torch.arange(96, dtype=torch.int32, device="cuda")
+    k, v = wql.kv_read_i4(cache, slots)
+    k2, v2 = wql.kv_read_i4(shifted(cache), shifted(slots), shifted(torch.zeros_like(k)), shifted(torch.zeros_like(v)))
+    assert torch.equal(k.view(torch.int16), k2.view(torch.int16)) and torch.equal(v.view(torch.int16), v2.view(torch.int16))
+    k, v = torch.randn_like(k), torch.randn_like(v)
+    a, b = torch.zeros_like(cache), shifted(torch.zeros_like(cache))
+    wql.kv_append_i4(k, v, slots, a)
+    wql.kv_append_i4(shifted(k), shifted(v), shifted(slots), b)
+    wql.device_status()
+    assert torch.equal(a, b)
+
+
 def test_prompt_attention_rows_of_no_sequence_stay(wql):
     q, k, v, cu = _prompt([100, 70], 4, 2, 128, 1, behind=90)
     out = torch.full(q.shape, 3.0, dtype=torch.float16, device="cuda")

@@ -131,8 +131,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
       : "memory");
 }
 
-// 32 bytes, a whole sector, per thread.
-__device__ __forceinline__ void st_global_32(void* dst, const uint32_t (&v)[8]) {
+// 32 bytes, a whole sector, per thread, where out begins at such a boundary.
+__device__ __forceinline__ void st_global_32(void* dst, const uint32_t (&v)[8], bool whole) {
+  if (!whole) {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    return;
+  }
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(dst)), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
@@ -555,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + x * kTile + lanes, to = tmem + C::kColO + x * D + lanes;
     const uint32_t tp = tmem + C::kColP + x * C::kStrideP + lanes;
     const float c = a.scale_log2;
+    const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     int scount = 0, ocount = 0, pcount = 0;  // phases of sbar and obar; P so far
     bool ok = true;
     auto wait = [&](uint64_t* bar, int phase) {
@@ -667,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               h[e] = pack_h2(__uint_as_float(o[i >> 5][(i & 31) + 2 * e]) * inv, __uint_as_float(o[i >> 5][(i & 31) + 2 * e + 1]) * inv);
-            st_global_32(dst + i, h);
+            st_global_32(dst + i, h, sectors);
           }
         }
       }
