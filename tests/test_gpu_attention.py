@@ -316,6 +316,23 @@ def test_prompt_attention_scales_and_large_scores(wql):
     within(y, o, bound)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 128), (3, 3, 128), (4, 1, 64)])
+def test_prompt_attention_rows_do_not_depend_on_later_ones(wql, Hq, Hkv, D):
+    # to the last bit, although rows from 300 on see scores that grow by thousands
+    T, n = 700, 300
+    q, k, v, cu = _prompt([T], Hq, Hkv, D, seed=11)
+    y = wql.attention_prompt(q, k, v, i32(cu))
+    q, k, v = q.clone(), k.clone(), v.clone()
+    q[n:] *= 64
+    k[n:] *= torch.linspace(1, 64, T - n, device="cuda").half()[:, None, None]
+    v[n:] *= -100
+    z = wql.attention_prompt(q, k, v, i32(cu))
+    short = wql.attention_prompt(q[:n].clone(), k[:n].clone(), v[:n].clone(), i32([0, n]))
+    wql.device_status()
+    assert torch.equal(y[:n].view(torch.int16), z[:n].view(torch.int16))
+    assert torch.equal(y[:n].view(torch.int16), short.view(torch.int16))
+
+
 def test_prompt_attention_bad_sequences_are_left_out_and_recorded(wql):
     q, k, v, cu = _prompt([50, 60, 70], 2, 1, 64, 6)
     good = wql.attention_prompt(q, k, v, i32(cu))

@@ -625,7 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after_sync();
         }
         if (__any_sync(0xffffffffu, a0 + a1 > kMost)) {
-          const float now = fmaxf(m, row_max()), f = ex2(m - now);
+          // only the rows that need it, so that a row's roundings do not depend on its neighbours
+          const float now = a0 + a1 > kMost ? fmaxf(m, row_max()) : m, f = ex2(m - now);
           m = now;
           l0 *= f, l1 *= f;
 #pragma unroll 1
