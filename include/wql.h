@@ -373,7 +373,8 @@ wql_status wql_kv_dequant_i8(const int8_t* q, const float* scales, int64_t rows,
  *     kv_lens [B]      ctx_lens + new_lens; 0 for a refused request
  *     slots [T]        slot of each new token, in the packed order of cu_new; -1 for tokens of
  *                      refused requests and behind the last token (T may exceed cu_new[B]; tokens
- *                      from T on get no slot)
+ *                      from T on get no slot), and where the page number is negative or so large
+ *                      that the slot would pass 2^31 - 1
  *     free_count_out   [1]: pages left, which are free_pages[0 .. free_count_out - 1]
  * Only the entries of new pages are written in block_table.  free_capacity is free_pages' size, and
  * free_count is taken as at most that.  Repeating a call gives the same result.

@@ -86,6 +86,16 @@ def test_plan_fewer_slots_than_tokens_and_empty(wql):
     assert slots.tolist() == [9 * 16, 9 * 16 + 1, -1] and lens.tolist() == [2, 3] and int(left) == 1
 
 
+def test_plan_pages_beyond_every_slot(wql):
+    # 16 * 2^30 = 0 in 32 bits: such a page must not stand for page 0
+    table = i32([[2 ** 30], [2 ** 27 - 1], [-3], [-1]])
+    slots, cu, lens, left = wql.kv_plan_pages(i32([4, 15, 2, 0]), i32([1, 1, 1, 2]), table, i32([2 ** 31 - 1]), i32([1]), 16, 6)
+    assert slots.tolist() == [-1, 2 ** 31 - 1, -1, -1, -1, -1]
+    assert cu.tolist() == [0, 1, 2, 3, 5] and lens.tolist() == [5, 16, 3, 2] and int(left) == 0
+    assert int(table[3, 0]) == 2 ** 31 - 1
+    wql.device_status()
+
+
 # ---- append and read ---------------------------------------------------------------------------
 
 def _kv(T, H, D, seed, fused):

@@ -122,13 +122,14 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(
       const int len = max(ctx_lens[lo], 0);
       const int pos = len + (tt - cu[lo]), k = (int)quot((uint32_t)pos, by_ps), held = pages(len);
       const int page = k < held ? table[(size_t)lo * width + k] : free_pages[nfree - 1 - off[lo] - (k - held)];
-      if (page >= 0) out[j] = page * ps + (pos - k * ps);
+      const long long slot = (long long)page * ps + (pos - k * ps);
+      if (page >= 0 && slot <= INT_MAX) out[j] = (int)slot;
     }
   }
-  if (t0 + 4 <= T) {
+  if (t0 <= T - 4) {
     *reinterpret_cast<int4*>(slots + t0) = make_int4(out[0], out[1], out[2], out[3]);
   } else {
-    for (int j = 0; t0 + j < T; ++j) slots[t0 + j] = out[j];
+    for (int j = 0; j < T - t0; ++j) slots[t0 + j] = out[j];
   }
 }
 
@@ -363,7 +364,7 @@ cudaError_t launch_kv_plan(const int* ctx_lens, const int* new_lens, int B, int 
                            const int* free_count, int* table, int width, int T, int* cu_new, int* kv_lens, int* slots,
                            int* free_count_out, cudaStream_t s) {
   // a CTA for every kPlanSlots slots, and enough for four requests' tables per warp
-  const int for_slots = (T + kPlanSlots - 1) / kPlanSlots, for_pages = (B + 31) / 32;
+  const int for_slots = (int)(((long long)T + kPlanSlots - 1) / kPlanSlots), for_pages = (B + 31) / 32;
   const int grid = for_slots > for_pages ? for_slots : for_pages > 0 ? for_pages : 1;
   return launch_early(kv_plan_kernel, grid, kPlanThreads, s, ctx_lens, new_lens, B, ps, fast_div(ps), free_pages, free_cap,
                       free_count, table, width, T, cu_new, kv_lens, slots, free_count_out);
@@ -372,7 +373,7 @@ cudaError_t launch_kv_plan(const int* ctx_lens, const int* new_lens, int B, int 
 cudaError_t launch_kv_append_i4(const uint16_t* k, const uint16_t* v, long long k_stride, long long v_stride, int T,
                                 int H, int D, const int* slots, uint8_t* cache, long long pages, int ps,
                                 unsigned* dev_err, cudaStream_t s) {
-  const long long units = (long long)((T + kAppendTokens - 1) / kAppendTokens) * 2 * H;
+  const long long units = ((long long)T + kAppendTokens - 1) / kAppendTokens * 2 * H;
   const long long per = kAppendThreads / 32, grid = (units + per - 1) / per;
   auto* kernel = D == 128 ? kv_append_i4_kernel<128> : kv_append_i4_kernel<64>;
   return launch_early(kernel, (int)grid, kAppendThreads, s, reinterpret_cast<const __half*>(k),
