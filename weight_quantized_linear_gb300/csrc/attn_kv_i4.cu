@@ -152,8 +152,8 @@ __device__ __forceinline__ int seq_len(const Args& a, int b) { return min(max(a.
 // queries, reductions and output), so that the warps that meet many short units get fewer tokens (64 ragged contexts:
 // 62 us without, 61, 60 and 59 us with one, two and three lead steps).
 __device__ __forceinline__ int seq_steps(const Args& a, int b) {
-  const int n = (seq_len(a, b) + kStep - 1) / kStep;
-  return n > 0 ? n + kLead : 0;
+  const int len = seq_len(a, b);  // may be up to 2^31 - 1
+  return len > 0 ? (len - 1) / kStep + 1 + kLead : 0;
 }
 
 // Position in the order of all steps: unit (b, hr = head * RB + row block), step s of `n` of that unit.
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
     const int total = __shfl_sync(0xffffffffu, incl, 31);
     // at least one step for every warp of a CTA: a short batch uses fewer CTAs and has fewer parts to join
     quota = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), kW);
-    n0 = (int)min((unsigned)quota * blockIdx.x, (unsigned)total), n1 = min(n0 + quota, total);
+    n0 = (int)min((unsigned)quota * blockIdx.x, (unsigned)total), n1 = (int)min((unsigned)n0 + quota, (unsigned)total);
     for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // sequences without any token
       if (seq_len(a, b) == 0)
         for (int head = 0; head < a.Hkv; ++head) zero_rows<D>(a, b, head, 0, a.Lq * a.G);
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   }
   // warp w's run of steps is [run(w), run(w + 1))
   const int quota_w = (n1 - n0 + kW - 1) / kW, warps = (n1 - n0 + quota_w - 1) / quota_w;  // warps with a run
-  auto run = [&](int w) { return min(n0 + quota_w * w, n1); };
+  auto run = [&](int w) { return (int)min((unsigned)n0 + (unsigned)quota_w * w, (unsigned)n1); };
   if (warp < warps) {
     const int at = run(warp);
     if (!a.split) {
@@ -849,7 +849,7 @@ cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int 
   // A CTA per unit where they fit the card at once and none can be long (four steps for every warp): one launch and
   // nothing to join between CTAs.  Otherwise an even share of all steps for every SM, but no more CTAs than the longest
   // possible lengths could use.
-  const long long units = (long long)B * Hkv * a.RB, most = (a.cap + kStep - 1) / kStep + kLead;
+  const long long units = (long long)B * Hkv * a.RB, most = ((long long)a.cap + kStep - 1) / kStep + kLead;
   if (units * most > INT_MAX) {
     *err = "more than 2^31 - 1 steps of 32 tokens fit the block table";
     return cudaErrorInvalidValue;
