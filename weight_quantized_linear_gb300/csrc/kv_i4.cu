@@ -140,18 +140,23 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 8;  // tokens per warp, of one head and one of K and V
 
-// fp16((max - lo) / 15) of the real quotient, from d + e = max - lo (d the fp32 difference, e its exact
-// remainder).  fl(d * fl(1 / 15)) is within 2 fp32 ulps of the real quotient, so only when it comes within 4 ulps
+// The exact remainder of d = fl(x - y): x - y = d + remainder (Knuth's two-sum of x and -y).
+__device__ __forceinline__ float kv_rest(float x, float y, float d) {
+  const float b = __fsub_rn(d, x);
+  return __fadd_rn(__fsub_rn(x, __fsub_rn(d, b)), __fsub_rn(-y, b));
+}
+
+// fp16((max - lo) / 15) of the real quotient, from d = fl(max - lo) and its remainder e.  fl(d * fl(1 / 15)) is within 2 fp32 ulps of the real quotient, so only when it comes within 4 ulps
 // of the middle between two fp16 numbers can its rounding differ from the real quotient's; there the sign of
 // (d - 15 tie) + e decides, whose first difference is exact (both are close, 15 tie has 16 bits).  Below
 // 2^-14 (fp16 subnormals) x is a small multiple of 2^-24, d is exact, and n / 15 is never a tie.
-__device__ __forceinline__ __half kv_scale(float d, float e) {
+__device__ __forceinline__ __half kv_scale(float hi, float lo, float d) {
   const float q = __fmul_rn(d, 1.0f / 15.0f);
   const unsigned b = __float_as_uint(q), low = b & 0x1fffu;
   float r = q;
   if (q >= 6.103515625e-05f && low - 0xffcu <= 8u) {
     const float tie = __uint_as_float((b & ~0x1fffu) | 0x1000u);
-    const float s = __fadd_rn(__fsub_rn(d, __fmul_rn(15.0f, tie)), e);
+    const float s = __fadd_rn(__fsub_rn(d, __fmul_rn(15.0f, tie)), kv_rest(hi, lo, d));
     r = s > 0.f ? __uint_as_float(__float_as_uint(tie) + 1) : s < 0.f ? __uint_as_float(__float_as_uint(tie) - 1) : tie;
   }
   const __half h = __float2half_rn(r);
@@ -181,9 +186,7 @@ __device__ __forceinline__ float2 kv_add2(float2 a, float2 b) {
 // 16 bits, and d minus it is exact because the two are close.
 __device__ __forceinline__ float kv_code_near_tie(float x, float lo, float s, float inv) {
   const float d = __fsub_rn(x, lo), fl = floorf(__fmul_rn(d, inv));
-  const float bb = __fsub_rn(d, x);  // Knuth's two-sum of x and -lo
-  const float e = __fadd_rn(__fsub_rn(x, __fsub_rn(d, bb)), __fsub_rn(-lo, bb));
-  const float r = __fadd_rn(__fsub_rn(d, __fmul_rn(fl + 0.5f, s)), e);
+  const float r = __fadd_rn(__fsub_rn(d, __fmul_rn(fl + 0.5f, s)), kv_rest(x, lo, d));
   return fl + (r > 0.f || (r == 0.f && ((int)fl & 1)) ? 1.0f : 0.0f);
 }
 
@@ -191,40 +194,44 @@ __device__ __forceinline__ float kv_code_near_tie(float x, float lo, float s, fl
 // y = fl(d * inv + 1.5 * 2^23) with d = fl(x - lo), inv within 2^-23 of 1 / s is that magic number plus the integer nearest
 // to d * inv, which is off the quotient by at most 2^-22 * 16 < 4e-6, so that integer is the code unless the rest
 // d * inv - integer (exact up to one rounding) comes within 1e-5 of a half; then kv_code_near_tie decides.  x >= lo, and
-// d * inv <= 15.01 unless s has lost bits below 2^-14, where the codes are clamped.  The bits of y are those of the magic
-// number plus the code, and the multiples of the former that eight products with powers of 16 add up are one constant.
-__device__ __forceinline__ uint32_t kv_codes(const float2 (&x)[4], float lo, float s, float inv) {
-  constexpr float kMagic = 12582912.f;  // 0x4b400000
+// d * inv <= 15.01 unless s has lost bits below 2^-14, where the codes are clamped.  Four codes are added up, times powers
+// of 16, in fp32 (below 2^16 and exact); their sum stands in the low bits of 2^23 plus it.  Ties are not rare (differences
+// and scales have 11 bits): one lane in a hundred has one, one warp in four, so they are taken one at a time.
+__device__ __forceinline__ uint32_t kv_codes(const uint4& raw, float lo, float s, float inv) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+  const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
   const float2 nlo = make_float2(-lo, -lo), i2 = make_float2(inv, inv), mg = make_float2(kMagic, kMagic),
                minus = make_float2(-1.f, -1.f);
-  float2 y[4];
+  float2 f[4], n[4];  // what rounding left, minus the codes
   float rest = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 d = kv_add2(x[j], nlo);
-    y[j] = kv_fma2(d, i2, mg);
-    const float2 f = kv_fma2(d, i2, kv_fma2(y[j], minus, mg));
-    asm("max.f32 %0, %0, %1, %2;" : "+f"(rest) : "f"(fabsf(f.x)), "f"(fabsf(f.y)));
-  }
-  if (rest > 0.49999f) {  // one lane in a hundred
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float& v = k ? y[j].y : y[j].x;
-        const float xx = k ? x[j].y : x[j].x;
-        if (fabsf(__fmaf_rn(__fsub_rn(xx, lo), inv, kMagic - v)) > 0.49999f) v = kMagic + kv_code_near_tie(xx, lo, s, inv);
-      }
+    const float2 d = kv_add2(__half22float2(*reinterpret_cast<const __half2*>(&r[j])), nlo);
+    n[j] = kv_fma2(kv_fma2(d, i2, mg), minus, mg);
+    f[j] = kv_fma2(d, i2, n[j]);
+    asm("max.f32 %0, %0, %1, %2;" : "+f"(rest) : "f"(fabsf(f[j].x)), "f"(fabsf(f[j].y)));
   }
   if (s < 6.103515625e-05f) {  // 2^-14
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = make_float2(fminf(y[j].x, kMagic + 15.f), fminf(y[j].y, kMagic + 15.f));
+    for (int j = 0; j < 4; ++j) n[j] = make_float2(fmaxf(n[j].x, -15.f), fmaxf(n[j].y, -15.f));
   }
-  uint32_t word = 0;
+  const float2 p256 = make_float2(256.f, 256.f), a = kv_fma2(n[1], p256, n[0]), b = kv_fma2(n[3], p256, n[2]);
+  const uint32_t low = __float_as_uint(fmaf(a.y, -16.f, 8388608.f - a.x)), high = __float_as_uint(fmaf(b.y, -16.f, 8388608.f - b.x));
+  uint32_t word = __byte_perm(low, high, 0x5410);
+  if (rest > 0.49999f) {
+    uint32_t hits = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    word += __float_as_uint(y[j].x) * (1u << (8 * j)) + __float_as_uint(y[j].y) * (1u << (8 * j + 4));
-  return word - 0x4b400000u * 0x11111111u;
+    for (int j = 0; j < 4; ++j) hits |= (fabsf(f[j].x) > 0.49999f ? 1u << (2 * j) : 0u) | (fabsf(f[j].y) > 0.49999f ? 2u << (2 * j) : 0u);
+    do {
+      const int k = __ffs(hits) - 1;
+      const uint32_t pair = k & 4 ? (k & 2 ? r[3] : r[2]) : (k & 2 ? r[1] : r[0]);
+      const float x = __half2float(__ushort_as_half((unsigned short)(k & 1 ? pair >> 16 : pair)));
+      const uint32_t code = min((int)kv_code_near_tie(x, lo, s, inv), 15);
+      word = (word & ~(15u << (4 * k))) | (code << (4 * k));
+      hits &= hits - 1;
+    } while (hits);
+  }
+  return word;
 }
 
 // A warp takes kAppendTokens consecutive tokens of one head, of K or of V; a row is held by D / 8 lanes, 8
@@ -248,15 +255,23 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_i4_kernel(
   if (t0 >= T) return;
   const __half* src = is_v ? v : k;
   const long long stride = is_v ? v_stride : k_stride;
-  const int bpp = ps / kKvBlock;
   uint4 raw[kIter];
-  int slot[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     const long long t = t0 + i * kRows + rl;
-    slot[i] = t < T ? __ldg(slots + t) : -1;
     raw[i] = t < T ? __ldcs(reinterpret_cast<const uint4*>(src + t * stride + (long long)h * D) + sub)
                    : make_uint4(0u, 0u, 0u, 0u);
+  }
+  // lane t % 8: where token t goes, its block's offset (a multiple of 128) plus its row there; -1: nowhere
+  long long to = -1;
+  if (const long long t = t0 + lane % kAppendTokens; t < T) {
+    if (const int slot = __ldg(slots + t); slot >= 0) {
+      const int page = (int)quot((uint32_t)slot, by_ps), at = slot - page * ps;
+      if (page < pages)
+        to = (((long long)page * H + h) * (ps / kKvBlock) + at / kKvBlock) * L::kBytes + at % kKvBlock;
+      else if (lane < kAppendTokens)
+        report_error(err, kErrBadIndex);
+    }
   }
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
@@ -269,24 +284,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_i4_kernel(
     for (int o = kLanes / 2; o >= 1; o >>= 1) mm = __hmin2_nan(mm, __shfl_xor_sync(0xffffffffu, mm, o));
     const float lo = __low2float(mm), hi = -__high2float(mm);
     const float d = __fsub_rn(hi, lo);
-    const float bb = __fsub_rn(d, hi);
-    const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(d, bb)), __fsub_rn(-lo, bb));
-    const __half sh = kv_scale(d, e);
+    const __half sh = kv_scale(hi, lo, d);
     const float s = __half2float(sh);
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-    const float2 x[4] = {__half22float2(x2[0]), __half22float2(x2[1]), __half22float2(x2[2]), __half22float2(x2[3])};
-    uint32_t word = kv_codes(x, lo, s, inv);
+    uint32_t word = kv_codes(raw[i], lo, s, inv);
     uint32_t par = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(__low2half(mm)) << 16);
     if (!(d <= 131008.f)) word = 0, par = 0x7fff7fffu;  // some value is not finite
-    if (slot[i] < 0) continue;
-    const int page = (int)quot((uint32_t)slot[i], by_ps), at = slot[i] - page * ps;
-    if (page >= pages) {
-      if (sub == 0) report_error(err, kErrBadIndex);
-      continue;
-    }
-    uint8_t* blk = cache + (((long long)page * H + h) * bpp + at / kKvBlock) * L::kBytes;
-    const int row = at % kKvBlock;
+    const long long dst = __shfl_sync(0xffffffffu, to, i * kRows + rl);
+    if (dst < 0) continue;
+    const int row = (int)dst & (kKvBlock - 1);
+    uint8_t* blk = cache + (dst - row);
     *reinterpret_cast<uint32_t*>(blk + (is_v ? L::kV : 0) + row * L::kRow + 4 * sub) = word;
     if (sub == 0) *reinterpret_cast<uint32_t*>(blk + (is_v ? L::kVp : L::kKp) + 4 * row) = par;
   }
