@@ -137,6 +137,20 @@ def test_append_and_read_bit_exact(wql, T, H, D, ps, fused):
     wql.device_status()
 
 
+@pytest.mark.parametrize("T,H,D", [(8191, 9, 64), (8191, 9, 128), (4001, 40, 64), (5, 700, 128), (17, 400, 64)])
+def test_append_many_rows_bit_exact(wql, T, H, D):
+    # both numbers of tokens that a warp may take, with a ragged end
+    k, v = _kv(T, H, D, T, True)
+    pages = -(-T // 32) + 1
+    slots = torch.randperm(pages * 32, generator=torch.Generator().manual_seed(H))[:T].to(torch.int32).cuda()
+    slots[T // 3] = -1
+    cache, want = wql.kv_cache_i4(pages, H, D, 32), wql.kv_cache_i4(pages, H, D, 32)
+    ref.write(want, slots, k, v)
+    wql.kv_append_i4(k, v, slots, cache)
+    assert torch.equal(cache, want)
+    wql.device_status()
+
+
 def test_append_ties_constant_rows_and_non_finite(wql):
     D, T = 128, 9
     x = torch.zeros((T, 1, D), dtype=torch.float64)

@@ -137,8 +137,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(
 // Quantise and append
 // ---------------------------------------------------------------------------------------------
 
-constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 8;  // tokens per warp, of one head and one of K and V
+constexpr int kAppendThreads = 128;
 
 // The exact remainder of d = fl(x - y): x - y = d + remainder (Knuth's two-sum of x and -y).
 __device__ __forceinline__ float kv_rest(float x, float y, float d) {
@@ -234,51 +233,58 @@ __device__ __forceinline__ uint32_t kv_codes(const uint4& raw, float lo, float s
   return word;
 }
 
-// A warp takes kAppendTokens consecutive tokens of one head, of K or of V; a row is held by D / 8 lanes, 8
-// channels (one 16-byte load) each, and its codes are one 4-byte store per lane.
-// Bound by the arithmetic of the codes: 8190 tokens of 32 heads of 128 take 53 us (170 MB, 3.2 TB/s; 34.5 us with the
-// codes left out).  16 tokens per warp take 62 us, 4 tokens 54.5.
-template <int D>
+// A warp takes kTokens consecutive tokens of one head, of K or of V; a row is held by four lanes, each with D / 32 chunks
+// of 8 channels (one 16-byte load, one 4-byte store of codes).  More lanes per row spend more on the row's minimum,
+// maximum and scale, which all its lanes work out: 8190 tokens of 32 heads of 128 take 42.4 us with 16 lanes, 33.7 with
+// 8, 28.1 with 4, 30.9 with 2; 27.3 in blocks of four warps instead of eight (170 MB, 6.2 TB/s, what reading back takes).
+template <int D, int kTokens>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_i4_kernel(
     const __half* __restrict__ k, const __half* __restrict__ v, long long k_stride, long long v_stride, int T, int H,
     const int* __restrict__ slots, uint8_t* __restrict__ cache, int pages, int ps, FastDiv by_ps, FastDiv by_h,
     unsigned* err) {
   using L = KvI4<D>;
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIter = kAppendTokens / kRows;
+  constexpr int kLanes = 4, kChunks = D / (8 * kLanes), kRows = 32 / kLanes, kIter = kTokens / kRows;
   const int lane = threadIdx.x & 31, sub = lane % kLanes, rl = lane / kLanes;
   grid_dependency_wait();  // k and v may come from the preceding kernel
   grid_dependents_launch();
-  const uint32_t unit = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);  // (8 tokens, head, K or V)
+  const uint32_t unit = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);  // (tokens, head, K or V)
   const uint32_t tb = quot(unit >> 1, by_h);
   const int is_v = (int)(unit & 1), h = (int)((unit >> 1) - tb * H);
-  const long long t0 = (long long)tb * kAppendTokens;
+  const long long t0 = (long long)tb * kTokens;
   if (t0 >= T) return;
   const __half* src = is_v ? v : k;
   const long long stride = is_v ? v_stride : k_stride;
-  uint4 raw[kIter];
+  uint4 raw[kIter][kChunks];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     const long long t = t0 + i * kRows + rl;
-    raw[i] = t < T ? __ldcs(reinterpret_cast<const uint4*>(src + t * stride + (long long)h * D) + sub)
-                   : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int m = 0; m < kChunks; ++m)
+      raw[i][m] = t < T ? __ldcs(reinterpret_cast<const uint4*>(src + t * stride + (long long)h * D) + sub + m * kLanes)
+                        : make_uint4(0u, 0u, 0u, 0u);
   }
-  // lane t % 8: where token t goes, its block's offset (a multiple of 128) plus its row there; -1: nowhere
+  // lane t % kTokens: where token t goes, its block's offset (a multiple of 128) plus its row there; -1: nowhere
   long long to = -1;
-  if (const long long t = t0 + lane % kAppendTokens; t < T) {
+  if (const long long t = t0 + lane % kTokens; t < T) {
     if (const int slot = __ldg(slots + t); slot >= 0) {
       const int page = (int)quot((uint32_t)slot, by_ps), at = slot - page * ps;
       if (page < pages)
         to = (((long long)page * H + h) * (ps / kKvBlock) + at / kKvBlock) * L::kBytes + at % kKvBlock;
-      else if (lane < kAppendTokens)
+      else if (lane < kTokens)
         report_error(err, kErrBadIndex);
     }
   }
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    const __half2* x2 = reinterpret_cast<const __half2*>(&raw[i]);
     // the row's minimum and maximum, NaN if it holds one: (min, -max) travel as one pair
-    const __half2 a = __hmin2_nan(__hmin2_nan(x2[0], x2[1]), __hmin2_nan(x2[2], x2[3]));
-    const __half2 b = __hmax2_nan(__hmax2_nan(x2[0], x2[1]), __hmax2_nan(x2[2], x2[3]));
+    __half2 a, b;
+#pragma unroll
+    for (int m = 0; m < kChunks; ++m) {
+      const __half2* x2 = reinterpret_cast<const __half2*>(&raw[i][m]);
+      const __half2 a1 = __hmin2_nan(__hmin2_nan(x2[0], x2[1]), __hmin2_nan(x2[2], x2[3]));
+      const __half2 b1 = __hmax2_nan(__hmax2_nan(x2[0], x2[1]), __hmax2_nan(x2[2], x2[3]));
+      a = m ? __hmin2_nan(a, a1) : a1, b = m ? __hmax2_nan(b, b1) : b1;
+    }
     __half2 mm = __halves2half2(__hmin_nan(__low2half(a), __high2half(a)), __hneg(__hmax_nan(__low2half(b), __high2half(b))));
 #pragma unroll
     for (int o = kLanes / 2; o >= 1; o >>= 1) mm = __hmin2_nan(mm, __shfl_xor_sync(0xffffffffu, mm, o));
@@ -288,14 +294,22 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_i4_kernel(
     const float s = __half2float(sh);
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-    uint32_t word = kv_codes(raw[i], lo, s, inv);
+    uint32_t word[kChunks];
+#pragma unroll
+    for (int m = 0; m < kChunks; ++m) word[m] = kv_codes(raw[i][m], lo, s, inv);
     uint32_t par = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(__low2half(mm)) << 16);
-    if (!(d <= 131008.f)) word = 0, par = 0x7fff7fffu;  // some value is not finite
+    if (!(d <= 131008.f)) {  // some value is not finite
+      par = 0x7fff7fffu;
+#pragma unroll
+      for (int m = 0; m < kChunks; ++m) word[m] = 0;
+    }
     const long long dst = __shfl_sync(0xffffffffu, to, i * kRows + rl);
     if (dst < 0) continue;
     const int row = (int)dst & (kKvBlock - 1);
     uint8_t* blk = cache + (dst - row);
-    *reinterpret_cast<uint32_t*>(blk + (is_v ? L::kV : 0) + row * L::kRow + 4 * sub) = word;
+#pragma unroll
+    for (int m = 0; m < kChunks; ++m)
+      *reinterpret_cast<uint32_t*>(blk + (is_v ? L::kV : 0) + row * L::kRow + 4 * (sub + m * kLanes)) = word[m];
     if (sub == 0) *reinterpret_cast<uint32_t*>(blk + (is_v ? L::kVp : L::kKp) + 4 * row) = par;
   }
 }
@@ -381,9 +395,13 @@ cudaError_t launch_kv_plan(const int* ctx_lens, const int* new_lens, int B, int 
 cudaError_t launch_kv_append_i4(const uint16_t* k, const uint16_t* v, long long k_stride, long long v_stride, int T,
                                 int H, int D, const int* slots, uint8_t* cache, long long pages, int ps,
                                 unsigned* dev_err, cudaStream_t s) {
-  const long long units = ((long long)T + kAppendTokens - 1) / kAppendTokens * 2 * H;
-  const long long per = kAppendThreads / 32, grid = (units + per - 1) / per;
-  auto* kernel = D == 128 ? kv_append_i4_kernel<128> : kv_append_i4_kernel<64>;
+  // 16 tokens per warp where that still gives every SM 40 warps (of 64 that fit), else 8: 4099 tokens of 8 heads of 64
+  // (27 warps of 16) take 3.7 us with 8 and 4.4 with 16, 8190 of them (54) 6.1 and 5.7, 8190 of 32 heads of 128 30.3 and 27.8
+  const long long warps = ((long long)T + 15) / 16 * 2 * H, per = kAppendThreads / 32;
+  const bool many = warps >= 40LL * num_sms();
+  const long long units = many ? warps : ((long long)T + 7) / 8 * 2 * H, grid = (units + per - 1) / per;
+  auto* kernel = D == 128 ? (many ? kv_append_i4_kernel<128, 16> : kv_append_i4_kernel<128, 8>)
+                          : (many ? kv_append_i4_kernel<64, 16> : kv_append_i4_kernel<64, 8>);
   return launch_early(kernel, (int)grid, kAppendThreads, s, reinterpret_cast<const __half*>(k),
                       reinterpret_cast<const __half*>(v), k_stride, v_stride, T, H, slots, cache, (int)pages, ps,
                       fast_div(ps), fast_div(H), dev_err);
