@@ -33,9 +33,10 @@
 // head) are the narrow side, and a 16-token block needs 16 products of 16 x 8 x 16, which the SM does in a
 // third of the time in which HBM delivers the block.
 //
-// Measured on GB300: 64 ragged contexts up to 8192 tokens, 8 K/V heads of 128 (290 MB) 59 us, of which 47 stream the
+// Measured on GB300: 64 ragged contexts up to 8192 tokens, 8 K/V heads of 128 (290 MB) 60 us, of which 47 stream the
 // cache at 6.2 TB/s and the rest is finding the range, joining and the launch; one context of 120001 tokens (131 MB) 31 us;
-// 16 rows per K/V head with heads of 64 (48 MB) 28 us, bound by instruction issue; 700 tokens, 32 K/V heads 7.4 us, bound
+// 16 rows per K/V head with heads of 64 (48 MB) 28 us, half of it the unit's own cost and joins, the rest bound by the
+// steps' instructions and their latency (14 us more per 48 MB; issue slots 48 % used by the 12 warps that fit); 700 tokens, 32 K/V heads 7.4 us, bound
 // by its chain of latencies.
 #include <atomic>
 #include <climits>
@@ -57,6 +58,8 @@ constexpr float kTop = 7.0f, kRaise = 15.0f;
 
 template <int D, int NT>
 struct Cfg {
+  // as many as registers allow.  More with fewer registers: heads of 64, 8 rows with 19 warps 23.4 us for 23.2 (190 MB:
+  // 57 for 59), 16 rows with 15 warps spill and take 37 us for 28.
   static constexpr int kWarps = NT == 1 ? (D == 64 ? 15 : 11) : (D == 64 ? 11 : 7);  // and one: a multiple of 4
   static constexpr int kThreads = 32 * (kWarps + 1);  // and the warp that requests the copies
   static constexpr int kStepBytes = kStep / kKvBlock * KvI4<D>::kBytes;
