@@ -413,8 +413,11 @@ wql_status wql_kv_read_i4(const uint8_t* cache, int64_t pages, int page_size, in
  * and zeros where no t is visible (kv_lens[b] = 0, or fewer tokens than rows).  q is [B * Lq, Hq,
  * D] fp16 with q_stride, out [B, Lq, Hq, D] fp16, dense.  Lq = 1 is the decode step; more rows verify
  * drafted tokens or run a chunk of a prompt over its cached beginning.
- * Score and value sums are fp32; a weight times its token's s is rounded to fp16 for the product
- * with the codes.  The result does not depend on what lies behind a sequence's last token.
+ * Score and value sums are fp32.  From five rows (Lq * Hq / Hkv) on, a weight times its token's s is
+ * rounded to fp16 for the product with code - 7.5, so that the rounding adds at most 2^-11 p s |code -
+ * 7.5| of a token with the weight p; a token whose v is constant adds exactly p v.  With fewer rows
+ * what the rounding leaves is added too.  The result does not depend on what lies behind a
+ * sequence's last token.
  * A length beyond table_width * page_size is cut there and recorded; a page number out of range
  * among the pages in use is recorded, and the outputs of that sequence are then unspecified.
  * workspace: device scratch of at least wql_attention_kv_i4_workspace_bytes(B, Lq, Hq, Hkv, D)
