@@ -49,6 +49,9 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kCheckWarp = 11, kNextWarp = 12;
 constexpr int kSorted = 128;                // up to so many sequences, the pairs are sorted by their keys
 constexpr float kTop = 7.0f;                // the largest weight after a rescale is 2^7, the 128 of a step at most 2^14
 constexpr float kMost = 32768.f;            // and a step whose weights come to more than 2^15 asks for the next
+// The maximum of keys whose scores are all minus infinity.  Their weights are zero by it, and the first finite score that
+// follows has an infinite one, which makes its step ask for the maximum.
+constexpr float kNoMax = -3e38f;
 // registers per thread: launched with 128; the softmax warpgroups take 208, the others give down to 48
 // (256 x 208 + 256 x 48 = 65536 = 512 x 128)
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 48;
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
           return fmaxf(max3(top[0], top[1], top[2]), top[3]) * c - kTop;
         };
-        if (j == 0) m = row_max();
+        if (j == 0) m = fmaxf(row_max(), kNoMax);
         float a0, a1;  // this step's sums
         uint32_t w[C::kBeside ? 4 : 1][16];
         auto weights = [&]() {
