@@ -140,6 +140,18 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // A flag with any other value says that the part is not there, so the workspace may hold anything before a call.
 constexpr unsigned long long kThere = 0x9d6b2f81c35ae704ull;
 
+// The flags are the only words that CTAs write and read at the same time, by operations that are strong at the GPU's scope.
+// The fences around them order the parts before the flags and the flags before the parts that are read; release and acquire
+// on top of those cost 0.5 us (64 contexts) to 1.3 us (four drafted tokens x 32).
+__device__ __forceinline__ void set_flag(unsigned long long* f, unsigned long long v) {
+  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(__cvta_generic_to_global(f)), "l"(v) : "memory");
+}
+__device__ __forceinline__ bool flag_set(const unsigned long long* f) {
+  unsigned long long v;
+  asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(__cvta_generic_to_global(f)) : "memory");
+  return v == kThere;
+}
+
 struct Args {
   const __half* q;
   long long q_stride;
@@ -762,9 +774,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
   __syncthreads();
   if (tid == 0) {
     __threadfence();  // what the CTA has written, before its flags
-    if (into && ends_f) a.flag[2 * blockIdx.x] = kThere;
-    if (on) a.flag[2 * blockIdx.x + 1] = kThere;
-    __threadfence();  // its flags, before it looks at others'
+    if (into && ends_f) set_flag(a.flag + 2 * blockIdx.x, kThere);
+    if (on) set_flag(a.flag + 2 * blockIdx.x + 1, kThere);
+    __threadfence();  // its flags, before it looks at others': of two CTAs at least one sees the other's
   }
   for (int side = 0; side < 2; ++side) {
     if (!(side ? on : into && ends_f != 0)) continue;
@@ -776,12 +788,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
     bool there = true;
     __threadfence();
     for (int i = tid; i < parts; i += C::kThreads)
-      there &= *reinterpret_cast<volatile unsigned long long*>(a.flag + 2 * (c0 + i) + (i < parts - 1 ? 1 : 0)) == kThere;
+      there &= flag_set(a.flag + 2 * (c0 + i) + (i < parts - 1 ? 1 : 0));
     // The last CTA to set its flag finds them all.  Others may too, if they look before that one has taken the flags
     // back; they then write the same values.
     if (!__syncthreads_and(there)) continue;
     __threadfence();
-    for (int i = tid; i < parts; i += C::kThreads) a.flag[2 * (c0 + i) + (i < parts - 1 ? 1 : 0)] = 0ull;
+    for (int i = tid; i < parts; i += C::kThreads) set_flag(a.flag + 2 * (c0 + i) + (i < parts - 1 ? 1 : 0), 0ull);
     const int head = (int)quot(info.y, a.rb), row0 = (info.y - head * a.RB) * C::kRows;
     // one pass over the parts, kAhead of them in flight at a time: one more trip to the L2 cache for the maxima costs 1 us
     constexpr int kAhead = D == 128 ? 20 : 10;
