@@ -392,6 +392,10 @@ wql_status wql_kv_plan_pages(const int32_t* ctx_lens, const int32_t* new_lens, i
  *     code = clamp(round_half_even((x - lo) / s), 0, 15)
  * Differences and quotients are the real ones, rounded once, so the cache is bit-exact with this
  * definition.  A row that holds an infinity or a NaN gets s = lo = NaN and reads back as NaN.
+ * s may be rounded up, so that code * s + lo passes the row's maximum by up to 2^-11 of max x - lo
+ * (15 * 2^-25 where s is below 2^-14): a finite row with values near 65504 can hold more than fp16 does
+ * (0 .. 65504: 15 * 4368 = 65520), which kv_read_i4 rounds to infinity and attention_kv_i4, whose sums
+ * are fp32, takes as it is.
  * Negative slots are passed over (padding); slots behind the last page are left out and recorded.
  * No slot may occur twice in a call: what such a slot then holds is unspecified.  T * H < 2^31
  * (WQL_EUNSUPPORTED above), here and in kv_read_i4.
