@@ -37,14 +37,18 @@
 // which more rows would need, 59 -> 67 us, so those keep rounded weights.
 //
 // mma.sync, not tcgen05: operands come out of registers after the unpacking, 8 rows (the query heads of a K/V
-// head) are the narrow side, and a 16-token block needs 16 products of 16 x 8 x 16, which the SM does in a
-// third of the time in which HBM delivers the block.
+// head) are the narrow side, and a 16-token block with heads of 128 needs 17 products of 16 x 8 x 16 for 8 rows (8 for the
+// scores, 8 for the values, one for the weights' sum; 9 with heads of 64), which the SM does in a third of the time in
+// which HBM delivers the block.  That holds for decode steps and drafted tokens.  A chunk of a prompt has many more rows, and
+// every 16 of them read the cache again: 512 tokens behind 8192 cached ones take 314 us (128 tokens 87, 16 tokens 25; 32
+// query and 8 K/V heads of 128), where tiles of 128 rows would read it an eighth as often.
 //
 // Measured on GB300: 64 ragged contexts up to 8192 tokens, 8 K/V heads of 128 (290 MB) 60 us, of which 47 stream the
 // cache at 6.2 TB/s and the rest is finding the range, joining and the launch; one context of 120001 tokens (131 MB) 31 us;
 // 16 rows per K/V head with heads of 64 (48 MB) 28 us, half of it the unit's own cost and joins, the rest bound by the
-// steps' instructions and their latency (14 us more per 48 MB; issue slots 48 % used by the 12 warps that fit); 700 tokens, 32 K/V heads 7.4 us, bound
-// by its chain of latencies.
+// steps' instructions and their latency (14 us more per 48 MB; issue slots 48 % used by the 12 warps that fit); heads of 64
+// with 4 rows, 64 contexts (154 MB) 49 us, one of 120001 tokens (69 MB) 26 us; 700 tokens, 32 K/V heads 7.5 us, bound by its
+// chain of latencies.
 #include <atomic>
 #include <climits>
 #include <type_traits>
@@ -58,6 +62,7 @@ namespace {
 
 constexpr int kStep = 32;                       // tokens per step
 constexpr int kLead = 3;                        // steps that stand for a unit's own cost
+constexpr int kOwnSteps = 48;                   // steps (1536 tokens) up to which a unit may have a CTA of its own
 constexpr float kNoMax = -1e30f;                // maximum of nothing
 constexpr float kLeast = 5.9604644775390625e-8f, kLeastLog2 = -24.f;  // the least s above zero, 2^-24
 // Weights are kept below 2^15: at each raise of m the largest becomes 2^7, so that those down to 2^-21 of it are normal
@@ -157,7 +162,7 @@ struct Args {
   long long q_stride;
   int B, Lq, Hq, Hkv, G, RB;  // RB: row blocks per K/V head
   const uint8_t* cache;
-  int pages, ps;
+  int pages;
   const int* table;
   int width, cap;  // pages of a row of the table, and their tokens
   int split;       // 0: a CTA per unit; 1: the steps of all units evenly over the CTAs
@@ -883,7 +888,6 @@ cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int 
   a.RB = (Lq * G + 8 * nt - 1) / (8 * nt);
   a.cache = cache;
   a.pages = (int)pages;
-  a.ps = ps;
   a.table = table;
   a.width = width;
   a.kv_lens = kv_lens;
@@ -896,15 +900,23 @@ cudaError_t launch_attn_kv_i4(const uint16_t* q, long long q_stride, int B, int 
                                                  (size_t)sms * 2 * 8 * nt * (D + 4) * sizeof(float));
   a.err = dev_err;
   a.cap = width * ps;
-  // A CTA per unit where they fit the card at once and none can be long (four steps for every warp): one launch and
-  // nothing to join between CTAs.  Otherwise an even share of all steps for every SM, but no more CTAs than the longest
-  // possible lengths could use.
+  // A CTA per unit where they fit the card at once and none can be long, as far as the table's width tells: nothing to join
+  // between CTAs.  Otherwise an even share of all steps for every SM, but no more CTAs than the longest possible lengths
+  // could use.  With a CTA per unit the longest one decides, with even shares the joins do; by the tokens of every context
+  // (us, a CTA per unit / even shares):
+  //                                   512        1024       1536       2048       4096       8192
+  //     8 units, 8 rows, D = 128    6.2/10.8   7.9/10.7   9.9/11.0   11.1/11.1  17.4/11.3  29.8/11.9
+  //   128 units, 8 rows, D = 128    6.5/13.3   8.4/14.4  10.5/15.2   11.6/17.9  18.2/22.7  31.7/34.5
+  //     8 units, 16 rows, D = 128   8.9/12.9  11.3/11.7  13.5/13.2   16.8/13.4  26.6/14.0  46.4/19.2
+  //     8 units, 16 rows, D = 64    7.0/10.8   8.6/11.1  10.7/11.3   11.9/11.4  18.5/12.0  31.7/13.9
+  // Up to 1536 tokens it is the better plan for all of them but the third, which loses 2 % there.  Wider tables take the
+  // shares: their lengths are not known here, and one long unit would cost more than the joins do.
   const long long units = (long long)B * Hkv * a.RB, most = ((long long)a.cap + kStep - 1) / kStep + kLead;
   if (units * most > INT_MAX) {
     *err = "more than 2^31 - 1 steps of 32 tokens fit the block table";
     return cudaErrorInvalidValue;
   }
-  a.split = units > sms || most > 4 * 12 + kLead;
+  a.split = units > sms || most > kOwnSteps + kLead;
   const int ctas = (int)(!a.split ? units : units * most < sms ? units * most : sms);
   const bool twin = Lq * G <= 4;  // free columns for the rounding's rest: at the top
   if (D == 128) {

@@ -12,23 +12,29 @@
 // the tensor cores work on the other's products.  K and V tiles arrive by TMA in a ring of kSlots 128-row tiles.
 //
 // What bounds it: with heads of 128, 2 x (S 128 + O 128) columns fill tensor memory, so a tile's next S waits for its P
-// to be used, and a tile's step takes its softmax (1000 cycles), its turn at the tensor cores and its two products (400
-// cycles for P V, 650 for Q K^T, which reads shared memory at its full bandwidth): 3000 cycles for the 2048 that the two
-// tiles' products take by themselves.  With heads of 64, P has columns of its own and S does not wait for it; then the
-// two softmaxes, which run at the same time, take 2300 cycles a step.
+// to be used, and a tile's step takes its softmax (1000 cycles), its turn at the tensor cores and its two products (at least
+// 512 cycles each; the queue takes P V in 400 and Q K^T, which reads shared memory at its full bandwidth, in 650): 3000
+// cycles for the 2048 that the two tiles' products take by themselves.  With heads of 64, P has columns of its own and S does
+// not wait for it; then the two softmaxes, which run at the same time, take 2300 cycles a step.
 //
 // The softmax's latency is why a step's weights are computed with the maximum as it was, without looking for the new
 // one: as long as they add up to less than 2^15, none of them is too large for fp16, and the sum is needed anyway.
 // Only a step with more looks for its maximum, rescales the accumulator and computes its weights again (with the
 // maximum found in every step, and its growth by 2^8 as the sign to rescale, 16384 tokens of 32 heads take 1.44 ms
-// instead of 1.37 to 1.41).  The softmax warps rescale the accumulator themselves, when the product that was added to
-// it last is complete: S(j) complete implies that where P is written over S, since P V(j - 1) was queued before it.
+// instead of 1.38 to 1.41, in bursts of 20 to 50 calls; over seconds, with the card at its power limit, 1.46 to 1.50).  The
+// softmax warps rescale the accumulator themselves, when the product that was added to it last is complete: S(j) complete
+// implies that where P is written over S, since P V(j - 1) was queued before it.
 //
 // One CTA per SM walks through the pairs of tiles, those with the most keys first and every second round in the
 // opposite order, which evens out what the CTAs get.  One warp finds the next pair while the current one is worked on,
 // and loads and products of the next begin before the outputs of this one are written: a CTA per pair spent about
 // 8 us per pair outside the loop over its keys (nine packed prompts of 412 to 3700 tokens, 32 heads: 404 us instead of
 // 371).
+//
+// The weights are rounded to fp16, which the product with fp16 values asks for; their sums are not.  That is off by 2.3e-4 to
+// 2.7e-4 of the output's norm, of which 2.0e-4 is the output's own rounding.  A second product with what the rounding leaves
+// would make three of a tile's two products per step, half as much tensor work again (16384 tokens: a floor of 1.72 ms instead
+// of 1.15): not taken.
 //
 // Rows see nothing behind them: scores above the diagonal are replaced, not added to.  V rows behind a row would meet
 // its zero weights in the product, so in the tiles on the diagonal one warp first replaces V values that are not

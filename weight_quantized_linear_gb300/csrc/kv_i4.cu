@@ -25,7 +25,7 @@ constexpr int kPlanSlots = 4 * kPlanThreads;  // slots per CTA
 // loaded before any is used) and then fills its own slots, so that nothing has to be passed between CTAs and one launch
 // does it all.  The table entries read here (pages held already) and those written (new pages) are different ones.
 // Latency is what it takes: a launch, the loads of the lengths, two barriers, and the loads of a page number (8 requests
-// 4.6 us, 256 with 98680 new tokens 5.0 us, 4096 requests 11.5 us).
+// 4.3 us, 256 with 97005 new tokens 4.9 us, 4096 requests 11.5 to 12.8 us).
 constexpr int kPlanPer = kPlanMaxB / kPlanThreads;
 
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(
