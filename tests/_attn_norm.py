@@ -4,7 +4,7 @@ roundings can come to when their signs are independent.  Works on CPU and CUDA t
 Token t enters a row's output with its weight p_t, whose rounding (u = 2^-11 relative, half a step of fp16) meets
 s_t (code_t - 7.5), and whose score's error (d relative, the worst case of tests/_attn_ref.py) meets v_t - o.  So its
 vector of errors is no longer than
-    a_t = p_t (u s_t |code_t - 7.5| + d |v_t - o|) + w 2^-32 |code_t - 7.5|,   w the largest p s of the row:
+    a_t = p_t (u |s_t| |code_t - 7.5| + d |v_t - o|) + w 2^-32 |code_t - 7.5|,   w the largest p |s| of the row:
 a weight below 2^-14, fp16's normal numbers, is off by 2^-25 where the largest one is at least 2^7.  A constant row of V
 (all codes 0, whatever its s) adds its value exactly.  n vectors with independent signs add up to
 3 sqrt(sum a_t^2) with room to spare (a rounding's error is 0.41 u on average, so that this is seven standard deviations;
@@ -23,7 +23,7 @@ U16 = 2.0 ** -11
 
 
 def rows(q, k, v, dev, smax, kmag, unseen, scale, drop=None):
-    """One K/V head: q [R, D], k, v, kmag [n, D], dev = s (code - 7.5) [n, D], smax [n] = s, float64; keys t < unseen[r]
+    """One K/V head: q [R, D], k, v, kmag [n, D], dev = s (code - 7.5) [n, D], smax [n] = |s|, float64; keys t < unseen[r]
     visible, but for token `drop`.  Returns (o [R, D], tolerance [R])."""
     D, n = q.shape[1], k.shape[0]
     see = torch.arange(n, device=q.device)[None] < unseen[:, None]
@@ -58,7 +58,7 @@ def kv_i4(q, cache, table, lens, scale=None, drop=None):
         (kc, ks, klo), (vc, vs, vlo) = ref.read_parts(cache, table[b].long()[t // ps] * ps + t % ps)
         some = vc.any(-1, keepdim=True)
         k, v, dev = kc * ks + klo, vc * vs + vlo, torch.where(some, vs * (vc - 7.5), 0.0)
-        smax, kmag = torch.where(some, vs, 0.0)[..., 0], kc * ks + klo.abs()
+        smax, kmag = torch.where(some, vs.abs(), 0.0)[..., 0], kc * ks.abs() + klo.abs()
         unseen = (n - Lq + 1 + torch.arange(Lq, device=q.device)).repeat_interleave(G)
         for h in range(Hkv):
             qh = q[b, :, h * G:(h + 1) * G].reshape(Lq * G, D).double()

@@ -17,8 +17,9 @@
 // kinds are kept in two accumulators (or, for V, in different output rows) and scaled apart at the end.
 // Values: sum_t p_t (s_t code_t + lo_t) = sum_t (p_t s_t) code_t + sum_t p_t lo_t, with w_t = p_t s_t as the
 // fp16 weight of the second matrix product and the last sum in fp32.  The running maximum m is that of
-// score + log2 s, i.e. of w itself, so the weights use fp16's range however the scales differ between
-// tokens; m is raised only when a weight would pass 2^15 (the rescaling is skipped while it is idle).
+// score + log2 |s|, i.e. of w itself, so the weights use fp16's range however the scales differ between
+// tokens; m is raised only when a weight would pass 2^15 (the rescaling is skipped while it is idle).  An s of zero,
+// which the format allows, counts as 2^-24 for m.
 // What all the codes of a token share is kept out of the sums, which would otherwise grow to hundreds of times the
 // result of a long context and carry their truncation and that of the weights with them.  Every second token enters
 // the product as 15 - code with the weight -w, so that the accumulators stay small; and with w' the rounded, signed
@@ -26,7 +27,7 @@
 // needed) while p_t (lo_t + 7.5 s_t) goes to the fp32 sum: a weight's rounding then meets code - 7.5.
 // A constant row of V has codes 0 and, by the format, s = 1, whatever the size of its value.  Taken as it stands its weight's
 // rounding would meet 7.5 instead of 0, and its s would set the maximum that the other tokens' weights are held against.
-// So a token with s = 1 whose codes are all zero counts as one with s = 2^-24, the least there is: its value stays lo, and
+// So a token with |s| = 1 whose codes are all zero counts as one with s = 2^-24, the least there is: its value stays lo, and
 // what its weight's rounding adds vanishes (64 tokens of size 0.05, four of them zero, 16 rows with heads of 128: error
 // 4.8e-3 -> 2.6e-4 of the norm, 1.8e-2 -> 3.1e-4 in the worst row).  The codes are looked at only in steps that hold an s of
 // 1, on the path that raises the maximum (64 contexts: no change in time, four drafted tokens x 32: 27.9 -> 28.3 us; a vote
@@ -482,10 +483,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_kv_i4_kernel(con
             float2 kp = h2f2(*reinterpret_cast<const uint32_t*>(b16 + L::kKp + 4 * (tok + 8 * hh)));
             vp[b][hh] = h2f2(*reinterpret_cast<const uint32_t*>(b16 + L::kVp + 4 * (tok + 8 * hh)));
             if (kEdge && t0 + b * kKvBlock + tok + 8 * hh >= len) kp = make_float2(1.f, 0.f), vp[b][hh] = make_float2(kLeast, 0.f);
-            raise |= vp[b][hh].x == 1.f;
+            raise |= fabsf(vp[b][hh].x) == 1.f;
             vp[b][hh].y = fmaf(7.5f, vp[b][hh].x, vp[b][hh].y);
             kx[hh] = kp.x * c_lo, ky[hh] = kp.y;
-            lv[b][hh] = lg2(vp[b][hh].x);
+            lv[b][hh] = lg2(fmaxf(fabsf(vp[b][hh].x), kLeast));
             vp[b][hh].x = __uint_as_float(__float_as_uint(vp[b][hh].x) ^ sign);
             lmax = fmaxf(lmax, lv[b][hh]);
           }
