@@ -414,7 +414,8 @@ wql_status wql_kv_read_i4(const uint8_t* cache, int64_t pages, int page_size, in
  * block_table [B, table_width].  For row r < Lq and query head h, with k and v of K/V head
  * h / (Hq / Hkv):
  *     out[b, r, h] = sum_t softmax_t(scale * q[b, r, h] . k[t]) v[t],   t <= kv_lens[b] - Lq + r
- * and zeros where no t is visible (kv_lens[b] = 0, or fewer tokens than rows).  q is [B * Lq, Hq,
+ * and zeros where no t is visible (kv_lens[b] = 0, or fewer tokens than rows).  |scale| <= 2^64, here
+ * and in attention_prompt: scores of any fp16 rows are then finite.  q is [B * Lq, Hq,
  * D] fp16 with q_stride, out [B, Lq, Hq, D] fp16, dense.  Lq = 1 is the decode step; more rows verify
  * drafted tokens or run a chunk of a prompt over its cached beginning.
  * Score and value sums are fp32.  From five rows (Lq * Hq / Hkv) on, a weight times its token's s is

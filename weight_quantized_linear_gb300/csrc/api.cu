@@ -462,6 +462,9 @@ namespace {
 
 bool kv_head_dim(int D) { return D == 64 || D == 128; }
 
+// Scores of fp16 rows stay below 2^(64 + 39), far inside fp32's range, and the kernels' factors beside the scale too.
+bool valid_scale(float scale) { return std::fabs(scale) <= 18446744073709551616.f; }
+
 // Rows [T, H, D] with `stride` elements between tokens, loaded 16 bytes at a time.
 bool valid_stride(int64_t stride, int H, int D) { return stride >= (int64_t)H * D && stride % 8 == 0; }
 
@@ -564,7 +567,7 @@ wql_status wql_attention_kv_i4(const uint16_t* q, int64_t q_stride, int B, int L
   WQL_REQUIRE(table_width >= 1 && (int64_t)table_width * page_size <= INT_MAX,
               "table_width * page_size must be between 16 and 2^31 - 1");
   WQL_REQUIRE((int64_t)Lq * Hq <= INT_MAX / 256, "Lq * Hq is too large");
-  WQL_REQUIRE(std::isfinite(scale), "scale must be finite");
+  WQL_REQUIRE(valid_scale(scale), "scale must be finite and at most 2^64 in magnitude");
   // the kernel counts 32-token steps (and a few per K/V head beside them) in 32 bits
   const int64_t row_blocks = ((int64_t)Lq * (Hq / Hkv) + 7) / 8, steps = ((int64_t)table_width * page_size + 31) / 32 + 4;
   if ((double)B * Hkv * (double)row_blocks * (double)steps > (double)INT_MAX)
@@ -598,7 +601,7 @@ wql_status wql_attention_prompt(const uint16_t* q, int64_t q_stride, const uint1
   WQL_REQUIRE(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0, "Hq must be a positive multiple of Hkv");
   if (!kv_head_dim(D)) return fail(WQL_EUNSUPPORTED, "D must be 64 or 128");
   if (Hq > 65535) return fail(WQL_EUNSUPPORTED, "Hq must be at most 65535");
-  WQL_REQUIRE(std::isfinite(scale), "scale must be finite");
+  WQL_REQUIRE(valid_scale(scale), "scale must be finite and at most 2^64 in magnitude");
   if (T == 0 || B == 0) {
     g_last_error.clear();
     return WQL_OK;

@@ -64,7 +64,7 @@ namespace {
 constexpr int kStep = 32;                       // tokens per step
 constexpr int kLead = 3;                        // steps that stand for a unit's own cost
 constexpr int kOwnSteps = 48;                   // steps (1536 tokens) up to which a unit may have a CTA of its own
-constexpr float kNoMax = -1e30f;                // maximum of nothing
+constexpr float kNoMax = -3e38f;                // maximum of nothing, below every score
 constexpr float kLeast = 5.9604644775390625e-8f, kLeastLog2 = -24.f;  // the least s above zero, 2^-24
 // Weights are kept below 2^15: at each raise of m the largest becomes 2^7, so that those down to 2^-21 of it are normal
 // fp16 numbers.
