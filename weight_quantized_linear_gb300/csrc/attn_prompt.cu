@@ -55,6 +55,10 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kCheckWarp = 11, kNextWarp = 12;
 constexpr int kSorted = 128;                // up to so many sequences, the pairs are sorted by their keys
 constexpr float kTop = 7.0f;                // the largest weight after a rescale is 2^7, the 128 of a step at most 2^14
 constexpr float kMost = 32768.f;            // and a step whose weights come to more than 2^15 asks for the next
+// Scores are scaled and the maximum subtracted in one instruction, which does not round the product, while the maximum is a
+// rounded number: they differ by up to 2^-24 of it, a factor that all the weights of a row share.  Where it may count, every
+// step looks for the maximum and rounds the products first, as the maximum was.
+constexpr float kLarge = 1048576.f;
 // The maximum of keys whose scores are all minus infinity.  Their weights are zero by it, and the first finite score that
 // follows has an infinite one, which makes its step ask for the maximum.
 constexpr float kNoMax = -3e38f;
@@ -606,12 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 128; i += 2)
             top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
-          return fmaxf(max3(top[0], top[1], top[2]), top[3]) * c - kTop;
+          return __fsub_rn(__fmul_rn(fmaxf(max3(top[0], top[1], top[2]), top[3]), c), kTop);
         };
         if (j == 0) m = fmaxf(row_max(), kNoMax);
         float a0, a1;  // this step's sums
         uint32_t w[C::kBeside ? 4 : 1][16];
-        auto weights = [&]() {
+        auto weights = [&](float mul) {
           a0 = a1 = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float u = __uint_as_float(s[i][2 * e]), v = __uint_as_float(s[i][2 * e + 1]);
-              fma2(u, v, c, -m);
+              fma2(u, v, mul, -m);
               u = ex2(u), v = ex2(v);
               add2(a0, a1, u, v);
               wi[e] = pack_h2(u, v);
@@ -627,16 +631,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (!C::kBeside) tmem_st_32x32b_x16(tp + 16 * i, wi);
           }
         };
-        weights();
+        weights(c);
         if constexpr (C::kBeside) {  // the last P has been used, and O is that of the steps before
           if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;
           ++pcount;
           tc_fence_after_sync();
         }
-        if (__any_sync(0xffffffffu, a0 + a1 > kMost)) {
+        const bool more = a0 + a1 > kMost || fabsf(m) > kLarge;
+        if (__any_sync(0xffffffffu, more)) {
           // only the rows that need it, so that a row's roundings do not depend on its neighbours
-          const float now = a0 + a1 > kMost ? fmaxf(m, row_max()) : m, f = ex2(m - now);
+          const float now = more ? fmaxf(m, row_max()) : m, f = ex2(m - now);
           m = now;
+          const bool large = fabsf(m) > kLarge;
+          if (__any_sync(0xffffffffu, large)) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              s[i >> 5][i & 31] = __float_as_uint(__fmul_rn(__uint_as_float(s[i >> 5][i & 31]), large ? c : 1.f));
+          }
           l0 *= f, l1 *= f;
 #pragma unroll 1
           for (int i = 0; i < D; i += 32) {
@@ -647,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
             tmem_st_32x32b_x32(to + i, o);
           }
-          weights();
+          weights(large ? 1.f : c);
         }
         if constexpr (C::kBeside) {
 #pragma unroll
