@@ -419,9 +419,10 @@ wql_status wql_kv_read_i4(const uint8_t* cache, int64_t pages, int page_size, in
  * D] fp16 with q_stride, out [B, Lq, Hq, D] fp16, dense.  Lq = 1 is the decode step; more rows verify
  * drafted tokens or run a chunk of a prompt over its cached beginning.
  * Score and value sums are fp32.  From five rows (Lq * Hq / Hkv) on, a weight times its token's s is
- * rounded to fp16 for the product with code - 7.5, so that the rounding adds at most 2^-11 p s |code -
- * 7.5| of a token with the weight p; a token whose v is constant adds exactly p v.  With fewer rows
- * what the rounding leaves is added too.  The result does not depend on what lies behind a
+ * rounded to fp16 for the product with code - 7.5, so that the rounding adds at most 2^-11 p |s| |code -
+ * 7.5| of a token with the weight p (2^-32 of the row's largest p |s| where p |s| is below 2^-21 of
+ * that); a constant row, as kv_append_i4 stores it, adds exactly p v.  With fewer rows what the
+ * rounding leaves is added too.  The result does not depend on what lies behind a
  * sequence's last token.
  * A length beyond table_width * page_size is cut there and recorded; a page number out of range
  * among the pages in use is recorded, and the outputs of that sequence are then unspecified.
@@ -444,7 +445,8 @@ wql_status wql_attention_kv_i4(const uint16_t* q, int64_t q_stride, int B, int L
  * query head h, with k and v of K/V head h / (Hq / Hkv):
  *     out[r, h] = sum_{j <= r} softmax_j(scale * q[r, h] . k[j]) v[j]
  * out [T, Hq, D] fp16, dense; rows of no sequence are left as they were.  cu_seqlens [B + 1]: a
- * sequence with a negative start, a negative length or an end beyond T is left out and recorded.
+ * sequence with a negative start, a negative length or an end beyond T is left out and recorded;
+ * rows that two of the others then share are written by both, in no order.
  * Sums are fp32, weights fp16.  A row depends on nothing but the rows up to it of its sequence: an
  * infinity or a NaN elsewhere does not reach it; one in v that it does see makes that channel of
  * it infinite or NaN.  No workspace.  Requires Hq <= 65535; out must overlap no input.
