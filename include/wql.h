@@ -456,6 +456,75 @@ wql_status wql_attention_prompt(const uint16_t* q, int64_t q_stride, const uint1
                                 int Hkv, int D, const int32_t* cu_seqlens, int B, float scale,
                                 uint16_t* out, void* stream);
 
+/* ----------------------------------------------------------------------------------------
+ * attention_chunks_kv_i4: attention of packed chunks of new tokens over the cache, as a step of continuous
+ * batching (chunked prefill, whole prompts, single tokens, all in one call) has them after kv_plan_pages and
+ * kv_append_i4.  Sequence b's chunk is rows cu_new[b] .. cu_new[b + 1] - 1 of q [T, Hq, D] (fp16, strided), the
+ * last n of the kv_lens[b] tokens that the pages of row b of block_table [B, table_width] hold.  For its row r < n
+ * and query head h, with k and v of K/V head h / (Hq / Hkv):
+ *     out[cu_new[b] + r, h] = sum_t softmax_t(scale * q . k[t]) v[t],   t <= kv_lens[b] - n + r
+ *     lse[cu_new[b] + r, h] = ln(sum_t exp(scale * q . k[t]))
+ * and zeros with lse = minus infinity where no t is visible (kv_lens[b] = 0, as kv_plan_pages gives a refused
+ * request, or fewer tokens than rows).  out [T, Hq, D] fp16 and lse [T, Hq] fp32 are dense; lse may be NULL.  Rows of
+ * no sequence are left as they were.
+ * k and v are code * s + lo rounded to fp16, as kv_read_i4 gives them, but never infinite: what rounds to infinity is
+ * taken as 65504.  A row of V whose parameters are not finite makes the rows that see it NaN.  Sums are fp32, weights
+ * fp16: a weight is off by 2^-11 of itself (2^-32 of the row's largest one where it is below 2^-21 of that).  A row
+ * depends on nothing behind the last token that it sees.  |scale| <= 2^64.
+ * A sequence with a negative start, a negative length or an end beyond T is left out and recorded; a length beyond
+ * table_width * page_size is cut there and recorded; a page number out of range among the pages in use is recorded, and
+ * the outputs of that sequence are then unspecified.  Rows that two sequences share are written by both, in no order.
+ * workspace: device scratch of at least wql_attention_chunks_kv_i4_workspace_bytes(T, B, Hq, Hkv, D) bytes (the
+ * current device's), with no contents to keep; calls that may run at the same time need one each.  out and lse must
+ * overlap no input and not each other.  Results are deterministic.
+ * Requires B <= 4096, Hq <= 65535, Hq / Hkv <= 128 (WQL_EUNSUPPORTED above).
+ * ---------------------------------------------------------------------------------------- */
+size_t wql_attention_chunks_kv_i4_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
+wql_status wql_attention_chunks_kv_i4(const uint16_t* q, int64_t q_stride, int T, int Hq, int Hkv, int D,
+                                      const uint8_t* cache, int64_t pages, int page_size,
+                                      const int32_t* block_table, int table_width, const int32_t* cu_new,
+                                      const int32_t* kv_lens, int B, float scale, uint16_t* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------------------------------------------------
+ * kv_weights_i4: the attention weight that every cached token gets from the rows of packed chunks, added to
+ * running sums.  q, cu_new, kv_lens, block_table, scale as in attention_chunks_kv_i4, whose lse [T, Hq] it takes:
+ *     weights[b, kvh, t] += sum_{r, h} exp(scale * q[cu_new[b] + r, h] . k[t] - lse[cu_new[b] + r, h])
+ * over the rows r of sequence b that see t and the query heads h of kvh's group.  weights is fp32
+ * [B, Hkv, table_width * page_size], dense; entries from kv_lens[b] on, and those of sequences without rows, are left
+ * as they were.  Each sum is formed in fp32 and added once.  k is what attention_chunks_kv_i4 takes; a row of K whose
+ * parameters are not finite makes the sums that it belongs to NaN, and so does a row r whose lse is NaN.
+ * Sequences, lengths and pages out of range: as there; the sums of a sequence with a bad page are unspecified.
+ * weights must overlap no input.  Results are deterministic.  Requires B <= 4096, Hq <= 65535, Hq / Hkv <= 128
+ * (WQL_EUNSUPPORTED above).
+ * ---------------------------------------------------------------------------------------- */
+wql_status wql_kv_weights_i4(const uint16_t* q, int64_t q_stride, int T, int Hq, int Hkv, int D,
+                             const uint8_t* cache, int64_t pages, int page_size, const int32_t* block_table,
+                             int table_width, const int32_t* cu_new, const int32_t* kv_lens, int B, float scale,
+                             const float* lse, float* weights, void* stream);
+
+/* ----------------------------------------------------------------------------------------
+ * kv_evict_i4: leave the least attended tokens behind.  Of the n = kv_lens[b] tokens of sequence b each K/V head
+ * keeps n' = min(n, budget): the last min(recent, budget) ones and, of the others, those with the greatest
+ * weights[b, h, t] (of equal ones the first; a NaN counts as greater than any number).  They go, in their order, into
+ * the pages of row b of new_table [B, new_width], which kv_plan_pages may have planned for n' tokens:
+ *     kept [B, H, budget]     the kept tokens' numbers, ascending; -1 from n' on
+ *     new_weights [B, H, new_width * page_size]   their weights; 0 from n' on
+ *     new_lens [B]            n'
+ * and rows 0 .. n' - 1 of the new pages are the kept rows' codes and parameters as they are.  Heads keep tokens of their
+ * own choice, so a slot then holds different tokens' rows in different heads; nothing that reads the cache minds.
+ * weights is fp32 [B, H, table_width * page_size], dense.  No page of new_table in use may be in use in block_table or
+ * twice in new_table: what such a page then holds is unspecified.  Pages that sequences share may be read by all of them.
+ * The old pages stay as they are.  A length beyond table_width * page_size is cut there and recorded; rows whose old or
+ * new page number is out of range are not moved and recorded.  Nothing may overlap but the cache with itself.
+ * Requires B <= 4096, 1 <= budget <= new_width * page_size, recent >= 0, B * H * ceil(budget / 16) < 2^31
+ * (WQL_EUNSUPPORTED above).
+ * ---------------------------------------------------------------------------------------- */
+wql_status wql_kv_evict_i4(const float* weights, uint8_t* cache, int64_t pages, int page_size, int H, int D,
+                           const int32_t* block_table, int table_width, const int32_t* kv_lens, int B,
+                           const int32_t* new_table, int new_width, int budget, int recent, int32_t* kept,
+                           float* new_weights, int32_t* new_lens, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -58,6 +58,10 @@ SIGNATURES = {
     "wql_kv_read_i4": (_I, [_P, _I64, _I, _I, _I, _P, _I, _P, _P, _P]),
     "wql_attention_kv_i4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "wql_attention_kv_i4": (_I, [_P, _I64, _I, _I, _I, _I, _I, _P, _I64, _I, _P, _I, _P, _F, _P, _P, _SZ, _P]),
+    "wql_attention_chunks_kv_i4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "wql_attention_chunks_kv_i4": (_I, [_P, _I64, _I, _I, _I, _I, _P, _I64, _I, _P, _I, _P, _P, _I, _F, _P, _P, _P, _SZ, _P]),
+    "wql_kv_weights_i4": (_I, [_P, _I64, _I, _I, _I, _I, _P, _I64, _I, _P, _I, _P, _P, _I, _F, _P, _P, _P]),
+    "wql_kv_evict_i4": (_I, [_P, _P, _I64, _I, _I, _I, _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P]),
     "wql_attention_prompt": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I, _F, _P, _P]),
 }
 
@@ -712,3 +716,113 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     _run("wql_attention_prompt", index, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hkv, D,
          cu_seqlens.data_ptr(), B, D ** -0.5 if scale is None else scale, out.data_ptr())
     return out
+
+
+def _chunk_args(q, cache, block_table, cu_new, kv_lens):
+    """Check what attention over chunks and their weights share; returns (pages, K/V heads, page size, device index, q's
+    stride, B, width)."""
+    pages, Hkv, ps, D = _cache_dims(cache)
+    index = cache.get_device()
+    qs = _stride_of(q, "q", None, D, None, index)
+    B, width = kv_lens.shape[0], block_table.shape[-1]
+    if not _is(block_table, torch.int32, (B, width), index):
+        _refuse(block_table, "block_table", torch.int32, (B, width), index)
+    if not _is(cu_new, torch.int32, (B + 1,), index):
+        _refuse(cu_new, "cu_new", torch.int32, (B + 1,), index)
+    if not _is(kv_lens, torch.int32, (B,), index):
+        _refuse(kv_lens, "kv_lens", torch.int32, (B,), index)
+    return pages, Hkv, ps, index, qs, B, width
+
+
+def attention_chunks_kv_i4_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load().wql_attention_chunks_kv_i4_workspace_bytes(T, B, Hq, Hkv, D))
+
+
+def attention_chunks_kv_i4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, cu_new: torch.Tensor,
+                           kv_lens: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None,
+                           lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of packed chunks of new tokens over the paged 4-bit cache, grouped heads.
+
+    q [T, Hq, D] fp16 (a view of a fused QKV output is taken as it is); sequence b's chunk is rows cu_new[b] ..
+    cu_new[b + 1] - 1 of it, the last of its kv_lens[b] tokens in the pages of block_table[b] (cu_new [B + 1] and
+    kv_lens [B] int32 are what kv_plan_pages returns).  A row sees the tokens up to itself; one that sees none is zero.
+    scale defaults to D ** -0.5.  lse: fp32 [T, Hq], filled with the logarithm of each row's sum of exponentials.
+    workspace: uint8, attention_chunks_kv_i4_workspace_bytes() of them, allocated here if not given.  Returns out
+    [T, Hq, D], dense; rows of no sequence are left as they were (undefined when out is not given)."""
+    pages, Hkv, ps, index, qs, B, width = _chunk_args(q, cache, block_table, cu_new, kv_lens)
+    dev, shape = cache.device, q.shape
+    T, Hq, D = shape
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float16, device=dev)
+    elif not _is(out, torch.float16, shape, index):
+        _refuse(out, "out", torch.float16, shape, index)
+    if lse is not None and not _is(lse, torch.float32, (T, Hq), index):
+        _refuse(lse, "lse", torch.float32, (T, Hq), index)
+    if workspace is None:
+        with torch.cuda.device(dev):
+            n = attention_chunks_kv_i4_workspace_bytes(T, B, Hq, Hkv, D)
+        workspace = torch.empty((n,), dtype=torch.uint8, device=dev)
+    elif not _is(workspace, torch.uint8, (workspace.numel(),), index):
+        _refuse(workspace, "workspace", torch.uint8, (workspace.numel(),), index)
+    _run("wql_attention_chunks_kv_i4", index, q.data_ptr(), qs, T, Hq, Hkv, D, cache.data_ptr(), pages, ps,
+         block_table.data_ptr(), width, cu_new.data_ptr(), kv_lens.data_ptr(), B, D ** -0.5 if scale is None else scale,
+         out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def kv_weights_i4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, cu_new: torch.Tensor,
+                  kv_lens: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor,
+                  scale: float | None = None) -> torch.Tensor:
+    """Add the attention weight that every cached token gets from packed chunks of rows to weights, fp32
+    [B, K/V heads, block_table width * page size]; entries from kv_lens on stay as they are.
+
+    q, cu_new, kv_lens, block_table and scale as in attention_chunks_kv_i4, whose lse [T, Hq] it takes (the rows may be
+    any last ones of the sequences, such as a window at a prompt's end).  Returns weights."""
+    pages, Hkv, ps, index, qs, B, width = _chunk_args(q, cache, block_table, cu_new, kv_lens)
+    T, Hq, D = q.shape
+    if not _is(lse, torch.float32, (T, Hq), index):
+        _refuse(lse, "lse", torch.float32, (T, Hq), index)
+    if not _is(weights, torch.float32, (B, Hkv, width * ps), index):
+        _refuse(weights, "weights", torch.float32, (B, Hkv, width * ps), index)
+    _run("wql_kv_weights_i4", index, q.data_ptr(), qs, T, Hq, Hkv, D, cache.data_ptr(), pages, ps, block_table.data_ptr(),
+         width, cu_new.data_ptr(), kv_lens.data_ptr(), B, D ** -0.5 if scale is None else scale, lse.data_ptr(),
+         weights.data_ptr())
+    return weights
+
+
+def kv_evict_i4(weights: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                new_table: torch.Tensor, budget: int, recent: int = 0, kept: torch.Tensor | None = None,
+                new_weights: torch.Tensor | None = None, new_lens: torch.Tensor | None = None):
+    """Leave the least attended tokens of the paged 4-bit cache behind.
+
+    Each K/V head of sequence b keeps min(kv_lens[b], budget) tokens: the last min(recent, budget) and, of the others,
+    those with the greatest weights [B, heads, block_table width * page size] fp32 (of equal ones the first).  Their rows
+    go, in their order, into the pages of new_table [B, new width] int32, none of which may be in use in block_table.
+    Returns (kept [B, heads, budget] int32: their numbers, then -1; new_weights [B, heads, new width * page size] fp32:
+    their weights, then zeros; new_lens [B] int32)."""
+    pages, H, ps, D = _cache_dims(cache)
+    dev, index, i32, f32 = cache.device, cache.get_device(), torch.int32, torch.float32
+    B, width, new_width = kv_lens.shape[0], block_table.shape[-1], new_table.shape[-1]
+    for t, name, dtype, shape in ((block_table, "block_table", i32, (B, width)), (kv_lens, "kv_lens", i32, (B,)),
+                                  (new_table, "new_table", i32, (B, new_width)),
+                                  (weights, "weights", f32, (B, H, width * ps))):
+        if not _is(t, dtype, shape, index):
+            _refuse(t, name, dtype, shape, index)
+    if budget < 1 or budget > new_width * ps:
+        raise ValueError(f"budget must be between 1 and new_table's width * page size, {new_width * ps}")
+    if kept is None:
+        kept = torch.empty((B, H, budget), dtype=i32, device=dev)
+    elif not _is(kept, i32, (B, H, budget), index):
+        _refuse(kept, "kept", i32, (B, H, budget), index)
+    if new_weights is None:
+        new_weights = torch.empty((B, H, new_width * ps), dtype=f32, device=dev)
+    elif not _is(new_weights, f32, (B, H, new_width * ps), index):
+        _refuse(new_weights, "new_weights", f32, (B, H, new_width * ps), index)
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=i32, device=dev)
+    elif not _is(new_lens, i32, (B,), index):
+        _refuse(new_lens, "new_lens", i32, (B,), index)
+    _run("wql_kv_evict_i4", index, weights.data_ptr(), cache.data_ptr(), pages, ps, H, D, block_table.data_ptr(), width,
+         kv_lens.data_ptr(), B, new_table.data_ptr(), new_width, budget, recent, kept.data_ptr(), new_weights.data_ptr(),
+         new_lens.data_ptr())
+    return kept, new_weights, new_lens

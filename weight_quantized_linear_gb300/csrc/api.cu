@@ -621,6 +621,119 @@ wql_status wql_attention_prompt(const uint16_t* q, int64_t q_stride, const uint1
   return cuda_status(e, "wql_attention_prompt", err);
 }
 
+namespace {
+
+// What attention_chunks_kv_i4 and kv_weights_i4 ask of the arguments that they share; *empty: there is nothing to do.
+wql_status check_chunks(const uint16_t* q, int64_t q_stride, int T, int Hq, int Hkv, int D, const uint8_t* cache,
+                        int64_t pages, int page_size, const int32_t* block_table, int table_width, const int32_t* cu_new,
+                        const int32_t* kv_lens, int B, float scale, bool* empty) {
+  *empty = false;
+  WQL_REQUIRE(T >= 0 && B >= 0, "T and B must be >= 0");
+  WQL_REQUIRE(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0, "Hq must be a positive multiple of Hkv");
+  WQL_REQUIRE_CACHE();
+  if (B > wql::kPlanMaxB) return fail(WQL_EUNSUPPORTED, "B must be at most 4096");
+  if (Hq > 65535 || Hq / Hkv > 128) return fail(WQL_EUNSUPPORTED, "Hq must be at most 65535 and Hq / Hkv at most 128");
+  WQL_REQUIRE(table_width >= 1 && (int64_t)table_width * page_size <= INT_MAX,
+              "table_width * page_size must be between 16 and 2^31 - 1");
+  WQL_REQUIRE(valid_scale(scale), "scale must be finite and at most 2^64 in magnitude");
+  if (T == 0 || B == 0) {
+    *empty = true;
+    g_last_error.clear();
+    return WQL_OK;
+  }
+  WQL_REQUIRE_PTR(q);
+  WQL_REQUIRE(valid_stride(q_stride, Hq, D), "the token stride of q must be a multiple of 8 and at least Hq * D");
+  WQL_REQUIRE_PTR(cache);
+  WQL_REQUIRE_PTR4(block_table);
+  WQL_REQUIRE_PTR4(cu_new);
+  WQL_REQUIRE_PTR4(kv_lens);
+  return WQL_OK;
+}
+
+}  // namespace
+
+size_t wql_attention_chunks_kv_i4_workspace_bytes(int T, int B, int Hq, int Hkv, int D) {
+  if (T < 1 || B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 128 || !kv_head_dim(D)) return 0;
+  return wql::attn_chunks_i4_workspace_bytes(T, B, Hq, Hkv, D);
+}
+
+wql_status wql_attention_chunks_kv_i4(const uint16_t* q, int64_t q_stride, int T, int Hq, int Hkv, int D,
+                                      const uint8_t* cache, int64_t pages, int page_size, const int32_t* block_table,
+                                      int table_width, const int32_t* cu_new, const int32_t* kv_lens, int B, float scale,
+                                      uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  bool empty;
+  const wql_status st = check_chunks(q, q_stride, T, Hq, Hkv, D, cache, pages, page_size, block_table, table_width, cu_new,
+                                     kv_lens, B, scale, &empty);
+  if (st != WQL_OK || empty) return st;
+  WQL_REQUIRE_PTR(out);
+  WQL_REQUIRE((reinterpret_cast<uintptr_t>(lse) & 3u) == 0, "lse must be null or 4-byte aligned");
+  WQL_REQUIRE_PTR(workspace);
+  WQL_REQUIRE(workspace_bytes >= wql::attn_chunks_i4_workspace_bytes(T, B, Hq, Hkv, D),
+              "workspace is smaller than wql_attention_chunks_kv_i4_workspace_bytes");
+  unsigned* dev_err = device_error_word();
+  if (!dev_err) return fail(WQL_ECUDA, "wql_attention_chunks_kv_i4: cannot locate the device error word");
+  std::string err;
+  const cudaError_t e = wql::launch_attn_chunks_i4(q, q_stride, T, Hq, Hkv, D, cache, pages, page_size, block_table,
+                                                   table_width, cu_new, kv_lens, B, scale, out, lse, workspace, dev_err,
+                                                   static_cast<cudaStream_t>(stream), &err);
+  return cuda_status(e, "wql_attention_chunks_kv_i4", err);
+}
+
+wql_status wql_kv_weights_i4(const uint16_t* q, int64_t q_stride, int T, int Hq, int Hkv, int D, const uint8_t* cache,
+                             int64_t pages, int page_size, const int32_t* block_table, int table_width,
+                             const int32_t* cu_new, const int32_t* kv_lens, int B, float scale, const float* lse,
+                             float* weights, void* stream) {
+  bool empty;
+  const wql_status st = check_chunks(q, q_stride, T, Hq, Hkv, D, cache, pages, page_size, block_table, table_width, cu_new,
+                                     kv_lens, B, scale, &empty);
+  if (st != WQL_OK || empty) return st;
+  WQL_REQUIRE_PTR4(lse);
+  WQL_REQUIRE_PTR(weights);
+  unsigned* dev_err = device_error_word();
+  if (!dev_err) return fail(WQL_ECUDA, "wql_kv_weights_i4: cannot locate the device error word");
+  std::string err;
+  const cudaError_t e = wql::launch_kv_weights_i4(q, q_stride, T, Hq, Hkv, D, cache, pages, page_size, block_table,
+                                                  table_width, cu_new, kv_lens, B, scale, lse, weights, dev_err,
+                                                  static_cast<cudaStream_t>(stream), &err);
+  return cuda_status(e, "wql_kv_weights_i4", err);
+}
+
+wql_status wql_kv_evict_i4(const float* weights, uint8_t* cache, int64_t pages, int page_size, int H, int D,
+                           const int32_t* block_table, int table_width, const int32_t* kv_lens, int B,
+                           const int32_t* new_table, int new_width, int budget, int recent, int32_t* kept,
+                           float* new_weights, int32_t* new_lens, void* stream) {
+  WQL_REQUIRE(B >= 0, "B must be >= 0");
+  WQL_REQUIRE(H >= 1, "H must be >= 1");
+  WQL_REQUIRE_CACHE();
+  if (B > wql::kPlanMaxB) return fail(WQL_EUNSUPPORTED, "B must be at most 4096");
+  WQL_REQUIRE(table_width >= 1 && (int64_t)table_width * page_size <= INT_MAX,
+              "table_width * page_size must be between 16 and 2^31 - 1");
+  WQL_REQUIRE(new_width >= 1 && (int64_t)new_width * page_size <= INT_MAX,
+              "new_width * page_size must be between 16 and 2^31 - 1");
+  WQL_REQUIRE(budget >= 1 && budget <= (int64_t)new_width * page_size, "budget must be between 1 and new_width * page_size");
+  WQL_REQUIRE(recent >= 0, "recent must be >= 0");
+  if ((int64_t)B * H > INT_MAX / (((int64_t)budget + 15) / 16))
+    return fail(WQL_EUNSUPPORTED, "B * H * ceil(budget / 16) must be below 2^31");
+  if (B == 0) {
+    g_last_error.clear();
+    return WQL_OK;
+  }
+  WQL_REQUIRE_PTR(weights);
+  WQL_REQUIRE_PTR(cache);
+  WQL_REQUIRE_PTR4(block_table);
+  WQL_REQUIRE_PTR4(kv_lens);
+  WQL_REQUIRE_PTR4(new_table);
+  WQL_REQUIRE_PTR4(kept);
+  WQL_REQUIRE_PTR(new_weights);
+  WQL_REQUIRE_PTR4(new_lens);
+  unsigned* dev_err = device_error_word();
+  if (!dev_err) return fail(WQL_ECUDA, "wql_kv_evict_i4: cannot locate the device error word");
+  return cuda_status(wql::launch_kv_evict_i4(weights, cache, pages, page_size, H, D, block_table, table_width, kv_lens, B,
+                                             new_table, new_width, budget, recent, kept, new_weights, new_lens, dev_err,
+                                             static_cast<cudaStream_t>(stream)),
+                     "wql_kv_evict_i4");
+}
+
 wql_status wql_diag_expire_wait(void* stream) {
   unsigned* dev_err = device_error_word();
   if (!dev_err) return fail(WQL_ECUDA, "wql_diag_expire_wait: cannot locate the device error word");

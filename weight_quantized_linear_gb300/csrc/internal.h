@@ -145,6 +145,20 @@ cudaError_t launch_attn_prompt(const uint16_t* q, long long q_stride, const uint
                                const uint16_t* v, long long v_stride, int T, int Hq, int Hkv, int D, const int* cu, int B,
                                float scale, uint16_t* out, unsigned* dev_err, cudaStream_t s, std::string* err);
 
+// Chunks over the cache, the weights its tokens get, and leaving the least attended ones behind.
+size_t attn_chunks_i4_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
+cudaError_t launch_attn_chunks_i4(const uint16_t* q, long long q_stride, int T, int Hq, int Hkv, int D, const uint8_t* cache,
+                                  long long pages, int ps, const int* table, int width, const int* cu, const int* kv_lens,
+                                  int B, float scale, uint16_t* out, float* lse, void* workspace, unsigned* dev_err,
+                                  cudaStream_t s, std::string* err);
+cudaError_t launch_kv_weights_i4(const uint16_t* q, long long q_stride, int T, int Hq, int Hkv, int D, const uint8_t* cache,
+                                 long long pages, int ps, const int* table, int width, const int* cu, const int* kv_lens, int B,
+                                 float scale, const float* lse, float* weights, unsigned* dev_err, cudaStream_t s,
+                                 std::string* err);
+cudaError_t launch_kv_evict_i4(const float* weights, uint8_t* cache, long long pages, int ps, int H, int D, const int* table,
+                               int width, const int* kv_lens, int B, const int* new_table, int new_width, int budget,
+                               int recent, int* kept, float* new_weights, int* new_lens, unsigned* dev_err, cudaStream_t s);
+
 #ifdef WQL_PHASE_TRACE
 // Phase-trace builds only: register the stamp buffer with the traced kernels of each source file.
 struct TraceDesc;

@@ -24,6 +24,48 @@ struct KvI4 {
   static constexpr int kBytes = kKvBlock * (D + 8);     // a block
 };
 
+// Eight codes of a row as fp16 values code * s + lo, each rounded once (what kv_read_i4 gives), in the order of their
+// nibbles: channels (0, 4), (1, 5), (2, 6), (3, 7).  A code in the low bits of an fp16 number between 1024 and 2048 is that
+// code or 16 times it above 1024, so one masked merge and one exact operation make it a number.
+__device__ __forceinline__ void kv_values8(uint32_t w, uint32_t s2, uint32_t lo2, uint32_t (&v)[4]) {
+  const uint32_t w8 = w >> 8;
+  v[0] = hfma2_u32(hadd2_u32(and_or(w, 0x000f000fu, 0x64006400u), 0xE400E400u), s2, lo2);
+  v[1] = hfma2_u32(hfma2_u32(and_or(w, 0x00f000f0u, 0x64006400u), 0x2C002C00u, 0xD400D400u), s2, lo2);
+  v[2] = hfma2_u32(hadd2_u32(and_or(w8, 0x000f000fu, 0x64006400u), 0xE400E400u), s2, lo2);
+  v[3] = hfma2_u32(hfma2_u32(and_or(w8, 0x00f000f0u, 0x64006400u), 0x2C002C00u, 0xD400D400u), s2, lo2);
+}
+// A finite row may hold values that round to infinity (its s may have been rounded up); attention over fp16 values takes
+// the largest finite number for them.  What of a row's parameters says that.
+__device__ __forceinline__ bool kv_finite(uint32_t par) { return ((par & 0x7c007c00u) + 0x04000400u & 0x80008000u) == 0; }
+__device__ __forceinline__ bool kv_overflows(uint32_t par) {  // for finite parameters
+  const float s = __half2float(__ushort_as_half((unsigned short)par)), lo = __half2float(__ushort_as_half((unsigned short)(par >> 16)));
+  return fabsf(fmaf(15.f, s, lo)) >= 65520.f;
+}
+__device__ __forceinline__ uint32_t kv_clamp2(uint32_t v) {
+  const __half2 x = *reinterpret_cast<const __half2*>(&v), m = __half2half2(__ushort_as_half(0x7bff));
+  const __half2 y = __hmax2_nan(__hmin2_nan(x, m), __hneg2(m));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// A sequence of packed chunks: rows start .. start + rows - 1 of q are the last `rows` of its `len` tokens; row r sees the
+// tokens up to first + r, first = len - rows.  Out of range: no rows, or the length that the table holds.
+struct KvChunk {
+  int start, rows, len, first;
+};
+__device__ __forceinline__ KvChunk kv_chunk(const int* cu, const int* kv_lens, int b, int T, int cap, unsigned* err) {
+  const int s = cu[b], e = cu[b + 1];
+  int len = max(kv_lens[b], 0);
+  if (len > cap) {
+    report_error(err, kErrBadIndex);
+    len = cap;
+  }
+  if (s < 0 || e < s || e > T) {
+    report_error(err, kErrBadIndex);
+    return {0, 0, len, len};
+  }
+  return {s, e - s, len, len - (e - s)};
+}
+
 // Division by a number known at launch: n / d for 0 <= n < 2^31 (Granlund and Montgomery's multiplier with l = ceil(log2 d)).
 struct FastDiv {
   uint32_t d, m, l;
