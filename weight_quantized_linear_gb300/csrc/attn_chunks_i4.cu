@@ -3,151 +3,887 @@
 // Sequence b's chunk is rows cu[b] .. cu[b + 1] - 1 of q, the last ones of its kv_lens[b] tokens, all of which are in the
 // cache.  For row r of n and query head h:
 //   out = sum_t softmax_t(scale q . k[t]) v[t],   lse = ln sum_t exp(scale q . k[t]),   t <= kv_len - n + r
-// with k and v of K/V head h / (Hq / Hkv): code * s + lo, rounded to fp16.
+// with k and v of K/V head h / (Hq / Hkv): code * s + lo, rounded to fp16, which is what the matrix product takes.
 //
-// A CTA takes kRows (token, query head) rows of a K/V head and walks through the keys in tiles of kKeys, dequantised to
-// shared memory; a warp owns two rows, a lane two keys of a tile and then D / 32 channels of the output.
+// A tile is 128 / G tokens of one K/V head, each with its G query heads: up to 128 rows, all of which read the same keys.
+// A CTA works on two tiles of consecutive tokens at a time.  Per 128 keys, the tensor cores compute S = Q K^T into tensor
+// memory, the tile's four softmax warps turn it into weights P (thread r owns row r), written over S as fp16, and the tensor
+// cores add P V to the tile's accumulator.  Where a sequence's last tokens fill one tile only, as in a decode step, both
+// halves of the CTA work on that tile, one on the even and one on the odd key tiles, and are joined in tensor memory.
+//
+// K and V reach the tensor cores by way of four warps that make fp16 numbers of the codes: bulk copies bring the blocks of 16
+// tokens into a small ring, a thread takes one key's row there, and writes it as a row of a swizzled operand tile.  That is
+// 3.5 instructions per pair of values, done once for the 256 rows of a pair of tiles.
+//
+// The rounds (one key tile, or two where both halves share a tile) of all items, one behind the other, are divided evenly
+// over the CTAs, whatever the lengths.  What a CTA computes of an item that it shares with others goes to the workspace as
+// (O, m, l), and a second kernel joins the parts in their order.
+#include <atomic>
+#include <climits>
+
+#include "attn.cuh"
 #include "internal.h"
 #include "kv_i4.cuh"
 
 namespace wql {
 namespace {
 
-constexpr int kRows = 16, kKeys = 64, kThreads = 256;
+constexpr int kTile = 128;  // keys of a tile, and rows at most
+// warps 0-3, 4-7: softmax of tiles 0, 1; 8: copies; 9, 10: products of tiles 0, 1; 11: next item; 12-15: K and V to fp16
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kNextWarp = 11, kConvWarp = 12;
+constexpr int kLead = 1;          // rounds that stand for an item's own cost
+constexpr float kTop = 7.0f;      // the largest weight after a rescale is 2^7, the 128 of a step at most 2^14
+constexpr float kMost = 32768.f;  // and a step whose weights come to more than 2^15 asks for the next
+constexpr float kLarge = 1048576.f;  // from here on scores are rounded before the maximum is subtracted, as it was
+constexpr float kNoMax = -3e38f;     // the maximum of keys whose scores are all minus infinity
+// registers per thread: launched with 128; the softmax warpgroups take 208, the others give down to 48
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 48;
+
+template <int D>
+struct Cfg {
+  static constexpr int kBox = kTile * 128;          // 128 rows of 64 fp16, 128-byte swizzle
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kBoxes * kBox;  // a Q, K or V tile
+  static constexpr int kSlots = D == 128 ? 4 : 8;   // of K and V tiles
+  static constexpr int kRawCodes = kTile * KvI4<D>::kRow;
+  static constexpr int kRawBytes = kRawCodes + kTile * 4;  // K's or V's codes and parameters of 128 tokens
+  static constexpr int kRaw = D == 128 ? 3 : 6;
+  // D = 64 leaves room in tensor memory for P beside S, so that the next S is computed while this one's softmax runs
+  static constexpr bool kBeside = D == 64;
+  static constexpr int kColO = 2 * kTile, kColP = kBeside ? kColO + 2 * D : 0;  // tensor memory columns; S from 0
+  static constexpr int kStrideP = kBeside ? kTile / 2 : kTile;                  // between the tiles' P
+  static constexpr int kOffRing = 2 * kTileBytes;
+  static constexpr int kOffRaw = kOffRing + kSlots * kTileBytes;
+  static constexpr int kSmem = kOffRaw + kRaw * kRawBytes + 1024;  // and alignment of the start
+  static_assert(kSmem <= 223 * 1024, "shared memory, 4 KB of it static");
+};
 
 struct Args {
-  const __half* q;
-  long long q_stride;
-  int T, Hq, Hkv, G;
+  const int *cu, *kv_lens;
+  int B, T, Hq, Hkv, G, tokens;  // tokens of a tile
   const uint8_t* cache;
-  int pages, ps;
-  FastDiv by_ps;
+  int pages, bpp;  // bpp: blocks of a page
+  FastDiv by_bpp;
   const int* table;
   int width, cap;
-  const int *cu, *kv_lens;
-  float scale;
+  float scale_log2;
+  uint32_t negate;  // bit of the instruction descriptor that negates Q, for a negative scale
   __half* out;
   float* lse;
+  // the workspace: what each CTA leaves unfinished, [CTA]; (m, l) and O of up to `part_rows` rows, [CTA][0, 1]
+  int4* begun;   // {row of q, tokens, tokens that the first row sees, K/V head} of the item that it began; no tokens: none
+  int* went_on;  // of the item that it found begun: 0: none, 1: it goes on, 2: it ends here
+  float2* ml;
+  float* part;
+  int part_rows;
   unsigned* err;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) attn_chunks_i4_kernel(const Args a) {
-  using L = KvI4<D>;
-  constexpr int kPitch = D + 8;  // halves
-  __shared__ __align__(16) __half kv[2][kKeys][kPitch];
-  __shared__ float qs[kRows][D], ps[kRows][kKeys];
-  __shared__ bool bad[kKeys];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const int b = blockIdx.z, kvh = blockIdx.y;
-  const KvChunk c = kv_chunk(a.cu, a.kv_lens, b, a.T, a.cap, a.err);
-  const long long rows = (long long)c.rows * a.G;
-  for (long long r0 = (long long)blockIdx.x * kRows; r0 < rows; r0 += (long long)gridDim.x * kRows) {
-    __syncthreads();
-    for (int i = tid; i < kRows * D; i += kThreads) {
-      const long long r = r0 + i / D;
-      float v = 0.f;
-      if (r < rows) {
-        const int tok = (int)(r / a.G), h = kvh * a.G + (int)(r % a.G);
-        v = __half2float(a.q[(c.start + tok) * a.q_stride + (long long)h * D + i % D]);
-      }
-      qs[i / D][i % D] = v;
+// Rounds of an item and what is before it in its sequence.  Tokens [A p, A p + A) of a chunk of n are item p, A = 2 a.tokens;
+// its last row sees first + A p + (its tokens) keys.
+struct Shape {
+  int first, n, A, items;
+  __device__ __forceinline__ Shape(const Args& a, const KvChunk& c)
+      : first(c.first), n(c.rows), A(2 * a.tokens), items(c.rows > 0 ? (c.rows - 1) / (2 * a.tokens) + 1 : 0) {}
+  __device__ __forceinline__ int count(int p) const { return min(n - p * A, A); }
+  __device__ __forceinline__ int tiles(int p) const { return max(first + p * A + count(p) - 1, 0) / kTile + 1; }  // of keys
+  __device__ __forceinline__ bool twin(int p) const { return 2 * count(p) <= A; }
+  __device__ __forceinline__ int rounds(int p) const { return twin(p) ? (tiles(p) + 1) / 2 : tiles(p); }
+  // Rounds (kLead more for each) of items 0 .. p - 1, all of them whole, p < items: sum over i of max(1, ceil(x / 128)) with x
+  // = first + A (i + 1).  The sum of floors by Euclid's steps on (A, 128).
+  __device__ long long before(int p) const {
+    const long long one = min(max(floor_div((long long)kTile - first, A), 0LL), (long long)p);  // items with a single round
+    long long sum = (long long)p * kLead + one, n_ = p - one, m = kTile, x = A, y = A * one + (long long)first + A + kTile - 1;
+    while (n_ > 0) {
+      if (x >= m) sum += n_ * (n_ - 1) / 2 * (x / m), x %= m;
+      if (y >= m) sum += n_ * (y / m), y %= m;
+      const long long top = x * n_ + y;
+      if (top < m) break;
+      n_ = top / m, y = top % m;
+      const long long t = m;
+      m = x, x = t;
     }
-    const long long last_row = min(r0 + kRows, rows) - 1;
-    const int keys = min(c.len, c.first + (int)(last_row / a.G) + 1);
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][D / 32] = {};
-    for (int t0 = 0; t0 < keys; t0 += kKeys) {
-      __syncthreads();
-      for (int i = tid; i < 2 * kKeys * (D / 8); i += kThreads) {
-        const int is_v = i / (kKeys * (D / 8)), row = i / (D / 8) % kKeys, ch = i % (D / 8), t = t0 + row;
-        uint32_t v[4] = {0u, 0u, 0u, 0u};
-        bool nan = false;
-        if (t < keys) {
-          const int pg = (int)quot((uint32_t)t, a.by_ps), at = t - pg * a.ps, page = a.table[(long long)b * a.width + pg];
-          if (page < 0 || page >= a.pages) {
+    return sum;
+  }
+  __device__ long long all() const { return items ? before(items - 1) + rounds(items - 1) + kLead : 0; }
+  static __device__ __forceinline__ long long floor_div(long long a, long long b) { return a >= 0 ? a / b : -1; }
+};
+
+// What a CTA does of an item: key tiles j0 .. j1 - 1 of `tiles` for the tokens from row0 on.
+struct Item {
+  int row0, tokens;  // row of q of the first token, tokens (none: there is no item)
+  int seen;          // tokens that it sees, less one; may be negative
+  int len, kvh, b;
+  int j0, j1;
+  int n0, n1;  // key tiles of tiles 0 and 1 (both those of tile 0 where they share it)
+  int twin;
+  int slot;  // -1: the whole item; 0: begun by others, 1: begun here and unfinished
+};
+// Steps of tile x: key tiles step(0) .. step(count - 1); rounds: turns of both tiles.
+struct Steps {
+  int x, j0, count, rounds, keys, stride, offset;
+  __device__ __forceinline__ Steps(const Item& t, int x_) : x(x_), j0(t.j0) {
+    keys = t.j1 - t.j0;
+    stride = t.twin ? 2 : 1, offset = t.twin ? x : 0;
+    rounds = t.twin ? (keys + 1) / 2 : keys;
+    count = t.twin ? (keys + 1 - x) / 2 : max(min((x ? t.n1 : t.n0) - t.j0, keys), 0);
+  }
+  __device__ __forceinline__ int at(int r) const { return stride * r + offset; }  // key tile, less j0
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __grid_constant__ CUtensorMap tm_q, const Args a) {
+  using C = Cfg<D>;
+  using L = KvI4<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Item s_item[2];
+  __shared__ int s_bad[2];             // [parity of the item] first key whose V row is not finite
+  __shared__ float2 s_ml[2][kTile];    // [parity of the item] (m, l) of tile 1's half of a shared tile
+  __shared__ long long s_sum[kThreads / 32], s_off;
+  __shared__ int s_b;
+  __shared__ uint32_t tmem_slot;
+  __shared__ uint64_t qbar, qfree;                              // Q tiles landed; not read any more
+  __shared__ uint64_t raw_full[C::kRaw], raw_empty[C::kRaw];    // codes landed; read (4 warps)
+  __shared__ uint64_t full[C::kSlots], empty[C::kSlots];        // K or V tile written (4 warps); used (both tiles)
+  __shared__ uint64_t sbar[2], pbar[2];                         // [tile] S complete; P written (4 warps)
+  __shared__ uint64_t obar[2], ofree[2];                        // [tile] O complete; O read (4 warps)
+  __shared__ uint64_t sfree[2], pfree[2];                       // [tile] P beside S: S read (4 warps); P used
+  __shared__ uint64_t half;                                     // tile 1's half of a shared tile is complete (4 warps)
+  __shared__ uint64_t item_full[2], item_empty[2];
+  __shared__ uint64_t turn[2];                                  // [tile] its products may be queued
+  __shared__ uint64_t done;                                     // every product (both tiles)
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    mbar_init(&qbar, 1), mbar_init(&qfree, 2), mbar_init(&done, 2), mbar_init(&half, 4);
+    for (int s = 0; s < C::kRaw; ++s) mbar_init(&raw_full[s], 1), mbar_init(&raw_empty[s], 4);
+    for (int s = 0; s < C::kSlots; ++s) mbar_init(&full[s], 4), mbar_init(&empty[s], 2);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&turn[x], 1), mbar_init(&sbar[x], 1), mbar_init(&pbar[x], 4), mbar_init(&obar[x], 1), mbar_init(&ofree[x], 4);
+      mbar_init(&sfree[x], 4), mbar_init(&pfree[x], 1);
+      mbar_init(&item_full[x], 1), mbar_init(&item_empty[x], 3 + 4 + 8);  // copy, product, conversion and softmax warps
+    }
+    fence_mbarrier_init();
+    mbar_arrive(&turn[0]);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();  // everything before this line overlaps the end of the preceding kernel
+  grid_dependents_launch();
+
+  // ---- this CTA's range [w0, w1) of the rounds of all items, in the order of sequences, their items, K/V heads ----
+  long long total, w0, w1;
+  {
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b)
+      mine += Shape(a, kv_chunk(a.cu, a.kv_lens, b, a.T, a.cap, blockIdx.x == 0 ? a.err : nullptr)).all() * a.Hkv;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) incl += s_sum[w];
+      total += s_sum[w];
+    }
+    const long long quota = (total + gridDim.x - 1) / gridDim.x;
+    w0 = min(quota * blockIdx.x, total), w1 = min(w0 + quota, total);
+    long long at = incl - mine;
+    if (at <= w0 && w0 < incl)
+      for (int b = b0; b < b1; ++b) {
+        const long long n = Shape(a, kv_chunk(a.cu, a.kv_lens, b, a.T, a.cap, nullptr)).all() * a.Hkv;
+        if (w0 < at + n) {
+          s_b = b, s_off = w0 - at;
+          break;
+        }
+        at += n;
+      }
+    __syncthreads();
+  }
+  const uint32_t tmem = tmem_slot;
+
+  if (warp >= kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp) {
+      // ---------------- Q, and the codes and parameters of K(0), V(0), K(1), V(1) .. ----------------
+      if (lane == 0) tma_prefetch_desc(&tm_q);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int phase) {
+        if (ok && !mbar_wait_warp(bar, phase & 1)) {
+          if (lane == 0) report_error(a.err, kErrTimeoutEmpty);
+          ok = false;
+        }
+        return ok;
+      };
+      const int blk = lane & 7, part = lane >> 3;  // lanes 0-7: codes of block `lane` of a tile, 8-15: its parameters
+      const uint32_t bytes = part ? 4 * kKvBlock : kKvBlock * L::kRow;
+      const uint32_t dst = part ? C::kRawCodes + blk * 4 * kKvBlock : blk * kKvBlock * L::kRow;
+      uint32_t n = 0, rs = 0, rp = 0;  // raw tiles so far, the next one's slot and round
+      int items = 0;
+      for (int it = 0; wait(&item_full[it & 1], it >> 1); ++it) {
+        const Item t = s_item[it & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[it & 1]);
+        if (t.tokens == 0) break;
+        if (!wait(&qfree, (it & 1) ^ 1)) break;
+        ++items;
+        if (lane == 0) {
+          const bool two = !t.twin;
+          const int rows = a.tokens * a.G;
+          mbar_arrive_expect_tx(&qbar, (two ? 2 : 1) * rows * D * 2);
+          for (int x = 0; x < (two ? 2 : 1); ++x)
+            for (int b = 0; b < C::kBoxes; ++b)
+              tma_load_3d(smem + x * C::kTileBytes + b * C::kBox, &tm_q, &qbar, 64 * b, t.kvh * a.G, t.row0 + x * a.tokens);
+        }
+        auto page_of = [&](int j) {  // the block's page; -1: nothing to copy
+          const int gb = j * 8 + blk;
+          return part < 2 && j < t.j1 && (long long)gb * kKvBlock < t.len
+                     ? a.table[(long long)t.b * a.width + quot((uint32_t)gb, a.by_bpp)]
+                     : -1;
+        };
+        int page = page_of(t.j0);
+        for (int j = t.j0; j < t.j1 && ok; ++j) {
+          const int next = page_of(j + 1), gb = j * 8 + blk;
+          bool there = part < 2 && (long long)gb * kKvBlock < t.len;
+          if (there && (page < 0 || page >= a.pages)) {
             report_error(a.err, kErrBadIndex);
-          } else {
-            const uint8_t* blk = a.cache + (((long long)page * a.Hkv + kvh) * (a.ps / kKvBlock) + at / kKvBlock) * L::kBytes;
-            const int rr = at % kKvBlock;
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + (is_v ? L::kV : 0) + rr * L::kRow + 4 * ch);
-            const uint32_t par = *reinterpret_cast<const uint32_t*>(blk + (is_v ? L::kVp : L::kKp) + 4 * rr);
-            nan = !kv_finite(par);
-            kv_values8(w, prmt(par, 0, 0x1010), prmt(par, 0, 0x3232), v);
-            if (!nan && kv_overflows(par))
-              for (int j = 0; j < 4; ++j) v[j] = kv_clamp2(v[j]);
-            if (nan)
-              for (int j = 0; j < 4; ++j) v[j] = is_v ? 0u : 0x7fff7fffu;
+            there = false;
+          }
+          const uint8_t* src = nullptr;
+          if (there) {
+            const int in = gb - (int)quot((uint32_t)gb, a.by_bpp) * a.bpp;
+            src = a.cache + (((long long)page * a.Hkv + t.kvh) * a.bpp + in) * L::kBytes;
+          }
+          const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, there) & 0xffu);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            if (!wait(&raw_empty[rs], (rp & 1) ^ 1)) break;
+            if (lane == 0) {
+              if (blocks)
+                mbar_arrive_expect_tx(&raw_full[rs], blocks * kKvBlock * (L::kRow + 4));
+              else
+                mbar_arrive(&raw_full[rs]);
+            }
+            __syncwarp();
+            if (there)
+              bulk_load(smem_u32(smem + C::kOffRaw + rs * C::kRawBytes) + dst,
+                        src + (v ? (part ? L::kVp : L::kV) : (part ? L::kKp : 0)), bytes, &raw_full[rs]);
+            ++n;
+            if (++rs == C::kRaw) rs = 0, ++rp;
+          }
+          page = next;
+        }
+      }
+      // copies that may still be in flight land before the kernel ends
+      bool landed = true;
+      for (int i = 0; i < C::kRaw && i < (int)n && landed; ++i) {
+        if (rs == 0) rs = C::kRaw, --rp;
+        --rs;
+        landed = mbar_wait_warp(&raw_full[rs], rp & 1);
+      }
+      if (items > 0 && landed) landed = mbar_wait_warp(&qbar, (items - 1) & 1);
+      if (!landed && lane == 0) report_error(a.err, kErrTimeoutDrain);
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      // ---------------- the tensor cores' work: a warp per tile, taking turns ----------------
+      const int x = warp - kMmaWarp;
+      const bool leader = elect_one();
+      const uint32_t idesc_s = umma_idesc_f16(kTile, kTile, 0, 0) | a.negate;
+      constexpr uint32_t idesc_o = umma_idesc_f16(kTile, D, /*A from TMEM*/ 0, /*B MN-major*/ 1);
+      const uint32_t ring_lo = smem_u32(smem + C::kOffRing) >> 4;
+      const uint32_t ts = tmem + x * kTile, to = tmem + C::kColO + x * D, tp = tmem + C::kColP + x * C::kStrideP;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int phase) {
+        if (ok && !mbar_wait_warp(bar, phase & 1)) {
+          if (leader) report_error(a.err, kErrTimeoutMma);
+          ok = false;
+        }
+        return ok;
+      };
+      auto release = [&](uint64_t* bar, bool used) {  // when the products queued so far are complete; at once without any
+        if (!leader) return;
+        if (used)
+          umma_commit(bar);
+        else
+          mbar_arrive(bar);
+      };
+      // K and V tiles are numbered through all items: K of key tile j0 + s of this one is base + 2 s, V the next
+      uint32_t base = 0;
+      auto slot = [&](uint32_t n) { return n % C::kSlots; };
+      auto wait_full = [&](uint32_t n) { return wait(&full[slot(n)], (int)(n / C::kSlots)); };
+      auto qk = [&](uint32_t q_desc, uint32_t n) {  // S = Q K^T
+        const uint32_t bd = (1u << 16) + ring_lo + slot(n) * (C::kTileBytes >> 4);
+        if (leader) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = ((s >> 2) * C::kBox + (s & 3) * 32) >> 4;
+            mma_ss(ts, q_desc + off, bd + off, idesc_s, s > 0);
+          }
+          umma_commit(&sbar[x]);
+        }
+      };
+      auto pv = [&](uint32_t n, uint32_t acc) {  // O (+)= P V
+        const uint32_t bd = ((uint32_t)(C::kBox >> 4) << 16) + ring_lo + slot(n) * (C::kTileBytes >> 4);
+        if (leader) {
+#pragma unroll
+          for (int s = 0; s < kTile / 16; ++s) mma_ts(to, tp + s * 8, bd + ((s * 2048) >> 4), idesc_o, s > 0 ? 1u : acc);
+        }
+      };
+      int pcount = 0, ocount = 0, turns = 0, scount = 0;  // phases of pbar, of obar / ofree, of turn; S so far
+      auto my_turn = [&]() { return C::kBeside || wait(&turn[x], turns++); };
+      auto pass = [&]() {
+        if (!C::kBeside && leader) mbar_arrive(&turn[x ^ 1]);
+      };
+      auto s_free = [&]() {  // S may be written: its softmax has read it, where P does not say so
+        const bool r = !C::kBeside || scount == 0 || wait(&sfree[x], scount - 1);
+        ++scount;
+        return r;
+      };
+      for (int it = 0; wait(&item_full[it & 1], it >> 1); ++it) {
+        const Item t = s_item[it & 1];
+        __syncwarp();
+        if (leader) mbar_arrive(&item_empty[it & 1]);
+        if (t.tokens == 0) break;
+        const Steps st(t, x);
+        const uint32_t end = base + 2 * st.keys;
+        const uint32_t q_desc = (1u << 16) + ((smem_u32(smem) + (t.twin ? 0 : x) * C::kTileBytes) >> 4);
+        uint32_t to_free = base;  // K and V tiles before this one are released
+        // Release the tiles up to that of K of step r: those of V of the step before and of K are in use, the others of the
+        // other half of the CTA.
+        auto release_to = [&](int r, bool used_v, bool used_k) {
+          const uint32_t k = base + 2 * st.at(r), stop = min(k + 1, end);
+          const uint32_t v = r > 0 ? base + 2 * st.at(r - 1) + 1 : 0xffffffffu;
+          for (; to_free < stop; ++to_free) {
+            const bool used = (used_v && to_free == v) || (used_k && to_free == k);
+            if (!used && !wait_full(to_free)) return;
+            release(&empty[slot(to_free)], used);
+          }
+        };
+        // S of the first step; the S columns are free, since the products that read their last P come before
+        bool next = st.count > 0;
+        if (!wait(&qbar, it) || (next && !wait_full(base + 2 * st.at(0))) || !my_turn() || (next && !s_free())) break;
+        tc_fence_after_sync();
+        if (next) qk(q_desc, base + 2 * st.at(0));
+        pass();
+        release_to(0, false, next);
+        if (st.count <= 1) release(&qfree, next);
+        for (int r = 0; r < st.rounds && ok; ++r) {
+          const bool now = r < st.count;
+          next = r + 1 < st.count;
+          const uint32_t v = base + 2 * st.at(r) + 1, k = base + 2 * st.at(r + 1);
+          if (now && !wait_full(v)) break;
+          if (next && !wait_full(k)) break;
+          if (C::kBeside && next) {
+            if (!s_free()) break;
+            tc_fence_after_sync();
+            qk(q_desc, k);
+          }
+          if (now) {
+            if (!wait(&pbar[x], pcount++)) break;
+            // the accumulator is taken over when the softmax warps have read that of the item before
+            if (r == 0 && ocount > 0 && !wait(&ofree[x], ocount - 1)) break;
+          }
+          if (!my_turn()) break;
+          tc_fence_after_sync();
+          if (now) {
+            pv(v, r > 0);
+            if (C::kBeside) release(&pfree[x], true);
+            if (!next) {
+              release(&obar[x], true);
+              ++ocount;
+            }
+          }
+          if (!C::kBeside && next) qk(q_desc, k);
+          pass();
+          release_to(r + 1, now, next);
+          if (r + 2 == st.count) release(&qfree, true);
+        }
+        base = end;
+      }
+      if (ok) {
+        release(&done, true);
+        wait(&done, 0);
+      }
+    } else if (warp == kNextWarp) {
+      // ---------------- the items of this CTA ----------------
+      int4 begun = make_int4(0, 0, 0, 0);
+      int went_on = 0, it = 0;
+      bool ok = true;
+      auto put = [&](const Item& t) {
+        if (!mbar_wait_warp(&item_empty[it & 1], ((it >> 1) & 1) ^ 1)) {
+          if (lane == 0) report_error(a.err, kErrTimeoutEmpty);
+          ok = false;
+          return;
+        }
+        if (lane == 0) {
+          s_item[it & 1] = t;
+          mbar_arrive(&item_full[it & 1]);
+        }
+        ++it;
+      };
+      if (w0 < w1) {
+        int b = s_b, p, kvh, s;
+        KvChunk c = kv_chunk(a.cu, a.kv_lens, b, a.T, a.cap, nullptr);
+        Shape sh(a, c);
+        {  // the last item that begins at s_off or before: 32 guesses at a time
+          int lo = 0, hi = sh.items - 1;
+          while (lo < hi) {
+            const int g = lo + (int)(((long long)(hi - lo) * (lane + 1) + 31) / 32);
+            const unsigned yes = __ballot_sync(0xffffffffu, sh.before(g) * a.Hkv <= s_off);
+            const int cnt = __popc(yes);  // of ascending guesses, the first ones
+            const int below = __shfl_sync(0xffffffffu, g, max(cnt - 1, 0)), above = __shfl_sync(0xffffffffu, g, min(cnt, 31));
+            if (cnt < 32) hi = above - 1;
+            if (cnt > 0) lo = below;
+          }
+          p = lo;
+          const long long rest = s_off - sh.before(p) * a.Hkv;
+          const int cost = sh.rounds(p) + kLead;
+          kvh = (int)(rest / cost), s = (int)(rest % cost);
+        }
+        long long left = w1 - w0;
+        while (left > 0 && ok) {
+          const int rounds = sh.rounds(p), cost = rounds + kLead;
+          const int take = (int)min((long long)(cost - s), left);
+          const int r0 = max(s - kLead, 0), r1 = s + take - kLead;
+          if (r1 > r0) {
+            Item t;
+            t.row0 = c.start + p * sh.A, t.tokens = sh.count(p), t.seen = c.first + p * sh.A, t.len = c.len, t.kvh = kvh, t.b = b;
+            const int tiles = sh.tiles(p), k = sh.twin(p) ? 2 : 1;
+            t.twin = sh.twin(p);
+            t.j0 = r0 * k, t.j1 = min(r1 * k, tiles);
+            t.n0 = t.twin ? tiles : max(t.seen + a.tokens - 1, 0) / kTile + 1, t.n1 = tiles;
+            t.slot = r0 > 0 ? 0 : r1 < rounds ? 1 : -1;
+            if (t.slot == 0) went_on = r1 == rounds ? 2 : 1;
+            if (t.slot == 1) begun = make_int4(t.row0, t.tokens, t.seen, kvh);
+            put(t);
+          }
+          left -= take, s = 0;
+          if (++kvh == a.Hkv && left > 0) {
+            kvh = 0;
+            if (++p == sh.items) {
+              p = 0;
+              do {
+                c = kv_chunk(a.cu, a.kv_lens, ++b, a.T, a.cap, nullptr);
+              } while (c.rows == 0);
+              sh = Shape(a, c);
+            }
           }
         }
-        if (is_v && ch == 0) bad[row] = nan;
-        *reinterpret_cast<uint4*>(&kv[is_v][row][8 * ch]) =
-            make_uint4(prmt(v[0], v[1], 0x5410), prmt(v[2], v[3], 0x5410), prmt(v[0], v[1], 0x7632), prmt(v[2], v[3], 0x7632));
       }
-      __syncthreads();
-      for (int k = 0; k < 2; ++k) {
-        const int row = 2 * warp + k;
-        const long long r = r0 + row;
-        const int last = c.first + (int)(min(r, rows - 1) / a.G);
-        float s[2] = {0.f, 0.f};
-        for (int d = 0; d < D; ++d) {
-          s[0] = fmaf(qs[row][d], __half2float(kv[0][lane][d]), s[0]);
-          s[1] = fmaf(qs[row][d], __half2float(kv[0][lane + 32][d]), s[1]);
+      if (lane == 0) a.begun[blockIdx.x] = begun, a.went_on[blockIdx.x] = went_on;
+      if (ok) {
+        Item t = {};
+        put(t);
+      }
+    } else {
+      // ---------------- codes to fp16: a thread takes one key's row ----------------
+      const int row = tid - kConvWarp * 32;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int phase) {
+        if (ok && !mbar_wait_warp(bar, phase & 1)) {
+          if (lane == 0) report_error(a.err, kErrTimeoutFull);
+          ok = false;
         }
-        bool nan = false;
-        for (int j = 0; j < 2; ++j) {
-          const int t = t0 + lane + 32 * j;
-          s[j] = t <= last ? s[j] * a.scale : -INFINITY;
-          nan |= t <= last && bad[lane + 32 * j];
-        }
-        float top = fmaxf(m[k], fmaxf(s[0], s[1]));
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float base = top == -INFINITY ? 0.f : top;
-        const float f = __expf(m[k] - base), p0 = __expf(s[0] - base), p1 = __expf(s[1] - base);
-        m[k] = top;
-        float sum = p0 + p1;
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        l[k] = l[k] * f + sum;
-        ps[row][lane] = p0, ps[row][lane + 32] = p1;
-        const bool any = __any_sync(0xffffffffu, nan);
+        return ok;
+      };
+      uint32_t n = 0, rs = 0, rp = 0;
+      for (int it = 0; wait(&item_full[it & 1], it >> 1); ++it) {
+        const int2 keys = make_int2(s_item[it & 1].j0, s_item[it & 1].j1);
+        const int len = s_item[it & 1].len, tokens = s_item[it & 1].tokens;
+        if (row == 0) s_bad[it & 1] = INT_MAX;
         __syncwarp();
-        for (int i = 0; i < D / 32; ++i) {
-          float x = o[k][i] * f;
-          for (int t = 0; t < kKeys; ++t) x = fmaf(ps[row][t], __half2float(kv[1][t][lane + 32 * i]), x);
-          o[k][i] = any ? NAN : x;
+        if (lane == 0) mbar_arrive(&item_empty[it & 1]);
+        if (tokens == 0) break;
+        named_barrier_sync(1, 128);  // s_bad is reset
+        for (int j = keys.x; j < keys.y && ok; ++j) {
+          const int key = j * kTile + row;
+          const bool inside = key < len && key >= 0;
+#pragma unroll 1
+          for (int v = 0; v < 2; ++v) {
+            const uint32_t slot = n % C::kSlots;
+            if (!wait(&raw_full[rs], (int)rp) || !wait(&empty[slot], (int)(n / C::kSlots) ^ 1)) break;
+            const uint8_t* raw = smem + C::kOffRaw + rs * C::kRawBytes;
+            const uint32_t src = smem_u32(raw) + row * L::kRow;
+            const uint32_t dst = smem_u32(smem + C::kOffRing + slot * C::kTileBytes) + row * 128;
+            uint32_t par = inside ? *reinterpret_cast<const uint32_t*>(raw + C::kRawCodes + 4 * row) : 0u;
+            if (!kv_finite(par)) {
+              if (v) atomicMin(&s_bad[it & 1], key);
+              par = v ? 0u : 0x7fff7fffu;
+            }
+            const bool over = kv_overflows(par);  // of a NaN: no
+            const uint32_t s2 = prmt(par, 0, 0x1010), lo2 = prmt(par, 0, 0x3232);
+#pragma unroll
+            for (int i = 0; i < L::kRow / 16; ++i) {
+              // eight lanes read eight different 16-byte columns of the banks, and write eight
+              const int c = D == 128 ? (i + (row >> 1)) & 3 : i;
+              const uint4 w4 = lds_u128(src + 16 * c);
+              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t h[4];
+                kv_values8(w[e], s2, lo2, h);
+                if (over) {
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) h[u] = kv_clamp2(h[u]);
+                }
+                const uint32_t to = dst + (c >> 1) * C::kBox + ((((c & 1) * 4 + e) ^ (row & 7)) << 4);
+                // V's channels stay in the order (0, 4), (1, 5), (2, 6), (3, 7): the output is put right at the end
+                const uint4 o = v ? make_uint4(h[0], h[1], h[2], h[3])
+                                  : make_uint4(prmt(h[0], h[1], 0x5410), prmt(h[2], h[3], 0x5410), prmt(h[0], h[1], 0x7632),
+                                               prmt(h[2], h[3], 0x7632));
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
+                             : "memory");
+              }
+            }
+            fence_proxy_async_smem();  // the tile for the products, and the codes' reads before the next copy
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[slot]), mbar_arrive(&raw_empty[rs]);
+            ++n;
+            if (++rs == C::kRaw) rs = 0, ++rp;
+          }
         }
       }
     }
-    for (int k = 0; k < 2; ++k) {
-      const long long r = r0 + 2 * warp + k;
-      if (r >= rows) continue;
-      const int tok = (int)(r / a.G), h = kvh * a.G + (int)(r % a.G);
-      const bool none = c.first + tok < 0;  // sees nothing
-      const long long at = (long long)(c.start + tok) * a.Hq + h;
-      for (int i = 0; i < D / 32; ++i) a.out[at * D + lane + 32 * i] = __float2half_rn(none ? 0.f : o[k][i] / l[k]);
-      if (a.lse && lane == 0) a.lse[at] = none ? -INFINITY : m[k] + logf(l[k]);
+  } else {
+    // ---------------- softmax and output of tile x: thread r owns row r ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int x = warp >> 2, row = tid & 127, tok = row / a.G, g = row - tok * a.G;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + x * kTile + lanes, to = tmem + C::kColO + x * D + lanes;
+    const uint32_t tp = tmem + C::kColP + x * C::kStrideP + lanes;
+    const float c = a.scale_log2;
+    const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+    int scount = 0, ocount = 0, pcount = 0, hcount = 0;  // phases of sbar, obar, half; P so far
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase) {
+      if (ok && !mbar_wait_warp(bar, phase & 1)) {
+        if (lane == 0) report_error(a.err, kErrTimeoutMma);
+        ok = false;
+      }
+      return ok;
+    };
+    for (int it = 0; wait(&item_full[it & 1], it >> 1); ++it) {
+      const Item& t = s_item[it & 1];
+      if (t.tokens == 0) break;
+      const Steps st(t, x);
+      const bool twin = t.twin;
+      const int seen = t.seen + (twin ? 0 : x * a.tokens);  // last key that the tile's first token sees
+      float m = kNoMax, l0 = 0.f, l1 = 0.f;                 // m: what is subtracted from the scaled scores
+      for (int r = 0; r < st.count && wait(&sbar[x], scount++); ++r) {
+        tc_fence_after_sync();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
+        tmem_ld_wait();
+        if constexpr (C::kBeside) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[x]);
+        }
+        const int key0 = (st.j0 + st.at(r)) * kTile;
+        if (seen - key0 < kTile - 1) {  // some row sees less than the whole tile
+          const int last = seen + tok - key0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > last) s[i >> 5][i & 31] = 0xff800000u;
+        }
+        auto row_max = [&]() {  // of the scaled scores, less kTop
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 128; i += 2)
+            top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
+          return __fsub_rn(__fmul_rn(fmaxf(max3(top[0], top[1], top[2]), top[3]), c), kTop);
+        };
+        if (r == 0) m = fmaxf(row_max(), kNoMax);
+        float a0, a1;  // this step's sums
+        uint32_t w[C::kBeside ? 4 : 1][16];
+        auto weights = [&](float mul) {
+          a0 = a1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t (&wi)[16] = w[C::kBeside ? i : 0];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float u = __uint_as_float(s[i][2 * e]), v = __uint_as_float(s[i][2 * e + 1]);
+              fma2(u, v, mul, -m);
+              u = ex2(u), v = ex2(v);
+              add2(a0, a1, u, v);
+              wi[e] = pack_h2(u, v);
+            }
+            if constexpr (!C::kBeside) tmem_st_32x32b_x16(tp + 16 * i, wi);
+          }
+        };
+        weights(c);
+        if constexpr (C::kBeside) {  // the last P has been used, and O is that of the steps before
+          if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;
+          ++pcount;
+          tc_fence_after_sync();
+        }
+        const bool more = a0 + a1 > kMost || fabsf(m) > kLarge;
+        if (__any_sync(0xffffffffu, more)) {
+          // only the rows that need it, so that a row's roundings do not depend on its neighbours
+          const float now = more ? fmaxf(m, row_max()) : m, f = ex2(m - now);
+          m = now;
+          const bool large = fabsf(m) > kLarge;
+          if (__any_sync(0xffffffffu, large)) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              s[i >> 5][i & 31] = __float_as_uint(__fmul_rn(__uint_as_float(s[i >> 5][i & 31]), large ? c : 1.f));
+          }
+          l0 *= f, l1 *= f;
+          if (r > 0) {
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(to + i, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x32(to + i, o);
+            }
+          }
+          weights(large ? 1.f : c);
+        }
+        if constexpr (C::kBeside) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_st_32x32b_x16(tp + 16 * i, w[i]);
+        }
+        l0 += a0, l1 += a1;
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pbar[x]);
+      }
+      float l = l0 + l1;
+      if (st.count > 0 && !wait(&obar[x], ocount++)) break;
+      tc_fence_after_sync();
+      const bool shared = twin && st.keys > 1;  // both halves have steps
+      if (twin && x) {
+        if (shared) {
+          s_ml[it & 1][row] = make_float2(m, l);
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&half);
+        }
+      } else {
+        uint32_t o[D / 32][32];
+        if (st.count > 0) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) tmem_ld_32x32b_x32(to + 32 * i, o[i]);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < D; ++i) o[i >> 5][i & 31] = 0u;
+        }
+        if (shared) {
+          if (!wait(&half, hcount++)) break;
+          tc_fence_after_sync();
+          const float2 ml = s_ml[it & 1][row];
+          const float now = fmaxf(m, ml.x), f0 = ex2(m - now), f1 = ex2(ml.x - now);
+          m = now, l = l * f0 + ml.y * f1;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o1[32];
+            tmem_ld_32x32b_x32(to + D + 32 * i, o1);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[i][e] = __float_as_uint(__uint_as_float(o[i][e]) * f0 + __uint_as_float(o1[e]) * f1);
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (st.count > 0) mbar_arrive(&ofree[x]);
+          if (shared) mbar_arrive(&ofree[1]);
+        }
+        const int mine = (twin ? 0 : x * a.tokens) + tok;  // token of the item
+        if (tok < a.tokens && mine < t.tokens) {
+          const int last = seen + tok;
+          if (last >= s_bad[it & 1]) {
+#pragma unroll
+            for (int i = 0; i < D; ++i) o[i >> 5][i & 31] = 0x7fc00000u;
+          }
+          // channel k of eight stands in column 2 k of theirs (k < 4) or 2 k - 7
+          auto at = [&](int ch) { return (ch & ~7) + ((ch & 7) < 4 ? 2 * (ch & 7) : 2 * (ch & 7) - 7); };
+          if (t.slot < 0) {
+            const long long to_row = (long long)(t.row0 + mine) * a.Hq + t.kvh * a.G + g;
+            const float inv = last < 0 ? 0.f : 1.f / l;
+            __half* dst = a.out + to_row * D;
+#pragma unroll
+            for (int i = 0; i < D; i += 16) {
+              uint32_t h[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int u = at(i + 2 * e), v = at(i + 2 * e + 1);
+                h[e] = pack_h2(__uint_as_float(o[u >> 5][u & 31]) * inv, __uint_as_float(o[v >> 5][v & 31]) * inv);
+              }
+              st_global_32(dst + i, h, sectors);
+            }
+            if (a.lse) {
+              float lg;
+              asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(l));
+              a.lse[to_row] = last < 0 ? -INFINITY : (m + lg) * 0.6931471805599453f;
+            }
+          } else {
+            const long long to_row = ((long long)blockIdx.x * 2 + t.slot) * a.part_rows + mine * a.G + g;
+            a.ml[to_row] = make_float2(m, l);
+            float* dst = a.part + to_row * D;
+#pragma unroll
+            for (int i = 0; i < D; i += 8) {
+              uint32_t h[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) h[e] = o[at(i + e) >> 5][at(i + e) & 31];
+              st_global_32(dst + i, h, true);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[it & 1]);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of items that CTAs shared, in their order: a warp per row of an item that CTA blockIdx.x began.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_chunks_join_kernel(const Args a, int ctas) {
+  constexpr int kPer = D / 32;  // channels per lane
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int4 it = a.begun[c];
+  const int rows = it.y * a.G;
+  int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  int n = 1;  // parts: slot 1 of CTA c, slot 0 of those behind it
+  for (int k0 = c + 1; k0 < ctas; k0 += 32) {
+    const int v = k0 + lane < ctas ? a.went_on[k0 + lane] : 2;
+    const unsigned stop = __ballot_sync(0xffffffffu, v != 1);
+    if (stop) {
+      n += __ffs(stop);
+      break;
+    }
+    n += 32;
+  }
+  for (; r < rows; r += gridDim.y * kJoinWarps) {
+    auto place = [&](int i) { return ((long long)(c + i) * 2 + (i == 0)) * a.part_rows + r; };
+    float m = kNoMax;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, a.ml[place(i)].x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float l = 0.f, o[kPer] = {};
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float2 ml = a.ml[place(i)];
+      const float f = ex2(ml.x - m);
+      l += ml.y * f;
+      const float* src = a.part + place(i) * D + kPer * lane;
+      float v[kPer];
+      if constexpr (kPer == 4)
+        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+      else
+        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] += v[e] * f;
+    }
+    const int tok = r / a.G;
+    const bool none = it.z + tok < 0;  // sees nothing
+    const float inv = none ? 0.f : 1.f / l;
+    const long long to = (long long)(it.x + tok) * a.Hq + it.w * a.G + (r - tok * a.G);
+    uint32_t h[kPer / 2];
+#pragma unroll
+    for (int e = 0; e < kPer / 2; ++e) h[e] = pack_h2(o[2 * e] * inv, o[2 * e + 1] * inv);
+    if constexpr (kPer == 4)
+      reinterpret_cast<uint2*>(a.out + to * D)[lane] = make_uint2(h[0], h[1]);
+    else
+      reinterpret_cast<uint32_t*>(a.out + to * D)[lane] = h[0];
+    if (a.lse && lane == 0) {
+      float lg;
+      asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(l));
+      a.lse[to] = none ? -INFINITY : (m + lg) * 0.6931471805599453f;
     }
   }
 }
 
+int part_rows(int T, int G) {
+  const long long rows = (long long)T * G, most = 2 * (kTile / G) * G;
+  return (int)(rows < most ? rows : most);
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& q, const Args& a, int ctas, cudaStream_t s) {
+  using C = Cfg<D>;
+  static std::atomic<bool> ready[64];  // per device; racing first calls set the same attribute
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(attn_chunks_i4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_chunks_i4_kernel<D>, q, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(ctas, a.part_rows < 8 * kJoinWarps ? (a.part_rows + kJoinWarps - 1) / kJoinWarps : 8, 1);
+  cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, attn_chunks_join_kernel<D>, a, ctas);
+}
+
 }  // namespace
 
-size_t attn_chunks_i4_workspace_bytes(int, int, int, int, int) { return 16; }
+size_t attn_chunks_i4_workspace_bytes(int T, int, int Hq, int Hkv, int D) {
+  const size_t ctas = num_sms(), rows = 2 * ctas * part_rows(T, Hq / Hkv);
+  return ctas * 32 + rows * (8 + 4 * (size_t)D) + 32;
+}
 
 cudaError_t launch_attn_chunks_i4(const uint16_t* q, long long q_stride, int T, int Hq, int Hkv, int D, const uint8_t* cache,
                                   long long pages, int ps, const int* table, int width, const int* cu, const int* kv_lens,
-                                  int B, float scale, uint16_t* out, float* lse, void*, unsigned* dev_err, cudaStream_t s,
-                                  std::string*) {
-  Args a{reinterpret_cast<const __half*>(q), q_stride, T, Hq, Hkv, Hq / Hkv, cache, (int)pages, ps, fast_div(ps), table,
-         width, width * ps, cu, kv_lens, scale, reinterpret_cast<__half*>(out), lse, dev_err};
-  const long long tiles = ((long long)T * a.G + kRows - 1) / kRows;
-  const dim3 grid((unsigned)(tiles < 256 ? tiles : 256), Hkv, B);
-  if (D == 128)
-    attn_chunks_i4_kernel<128><<<grid, kThreads, 0, s>>>(a);
-  else
-    attn_chunks_i4_kernel<64><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+                                  int B, float scale, uint16_t* out, float* lse, void* workspace, unsigned* dev_err,
+                                  cudaStream_t s, std::string* err) {
+  const int G = Hq / Hkv, tokens = kTile / G, ctas = num_sms();
+  CUtensorMap tq;
+  if (!make_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, D, Hq, T, (uint64_t)D * 2, (uint64_t)q_stride * 2, 64, G, tokens,
+                    CU_TENSOR_MAP_SWIZZLE_128B, err))
+    return cudaErrorInvalidValue;
+  // O first, at a 32-byte boundary, then (m, l), then what the CTAs say
+  uint8_t* w = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~(uintptr_t)31);
+  const int rows = part_rows(T, G);
+  float* part = reinterpret_cast<float*>(w);
+  float2* ml = reinterpret_cast<float2*>(part + 2LL * ctas * rows * D);
+  int4* begun = reinterpret_cast<int4*>(ml + 2LL * ctas * rows);
+  // a scale of zero keeps a trace of itself, so that masked scores stay minus infinity
+  const float mag = scale < 0.f ? -scale : scale;
+  Args a{cu, kv_lens, B, T, Hq, Hkv, G, tokens, cache, (int)pages, ps / kKvBlock, fast_div(ps / kKvBlock), table, width,
+         width * ps, (mag < 1e-30f ? 1e-30f : mag) * 1.4426950408889634f, scale < 0.f ? 1u << 13 : 0u,
+         reinterpret_cast<__half*>(out), lse, begun, reinterpret_cast<int*>(begun + ctas), ml, part, rows, dev_err};
+  return D == 128 ? launch<128>(tq, a, ctas, s) : launch<64>(tq, a, ctas, s);
 }
 
 }  // namespace wql
