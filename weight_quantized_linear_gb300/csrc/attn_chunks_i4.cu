@@ -11,8 +11,8 @@
 // cores add P V to the tile's accumulator.  Where a sequence's last tokens fill one tile only, as in a decode step, both
 // halves of the CTA work on that tile, one on the even and one on the odd key tiles, and are joined in tensor memory.
 //
-// K and V reach the tensor cores by way of four warps that make fp16 numbers of the codes: bulk copies bring the blocks of 16
-// tokens into a small ring, a thread takes one key's row there, and writes it as a row of a swizzled operand tile.  That is
+// K and V reach the tensor cores by way of eight warps that make fp16 numbers of the codes: bulk copies bring the blocks of
+// 64 tokens into a small ring, a thread takes one key's row there, and writes it as a row of a swizzled operand tile.  That is
 // 3.5 instructions per pair of values, done once for the 256 rows of a pair of tiles.
 //
 // The rounds (one key tile, or two where both halves share a tile) of all items, one behind the other, are divided evenly
@@ -28,17 +28,18 @@
 namespace wql {
 namespace {
 
-constexpr int kTile = 128;  // keys of a tile, and rows at most
-// warps 0-3, 4-7: softmax of tiles 0, 1; 8: copies; 9, 10: products of tiles 0, 1; 11: next item; 12-15: K and V to fp16
-constexpr int kThreads = 512;
+constexpr int kTile = 128, kHalf = 64;  // keys of a tile, and rows at most; keys of a step of the copies
+// warps 0-3, 4-7: softmax of tiles 0, 1; 8: copies; 9, 10: products of tiles 0, 1; 11: next item; 12-19: K and V to fp16
+constexpr int kThreads = 640;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kNextWarp = 11, kConvWarp = 12;
 constexpr int kLead = 1;          // rounds that stand for an item's own cost
 constexpr float kTop = 7.0f;      // the largest weight after a rescale is 2^7, the 128 of a step at most 2^14
 constexpr float kMost = 32768.f;  // and a step whose weights come to more than 2^15 asks for the next
 constexpr float kLarge = 1048576.f;  // from here on scores are rounded before the maximum is subtracted, as it was
 constexpr float kNoMax = -3e38f;     // the maximum of keys whose scores are all minus infinity
-// registers per thread: launched with 128; the softmax warpgroups take 208, the others give down to 48
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 48;
+// registers per thread: launched with 96; two warpgroups for the softmax, two convert, one does the rest
+constexpr int kSoftmaxRegs = 168, kConvRegs = 48, kOtherRegs = 48;
+static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kOtherRegs <= 5 * 96, "of what the block was launched with");
 
 template <int D>
 struct Cfg {
@@ -46,8 +47,7 @@ struct Cfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kBoxes * kBox;  // a Q, K or V tile
   static constexpr int kSlots = D == 128 ? 4 : 8;   // of K and V tiles
-  static constexpr int kRawCodes = kTile * KvI4<D>::kRow;
-  static constexpr int kRawBytes = kRawCodes + kTile * 4;  // K's or V's codes and parameters of 128 tokens
+  static constexpr int kRawBytes = kHalf / kKvBlock * KvI4<D>::kBytes;  // blocks as they are, of half a tile of keys
   static constexpr int kRaw = D == 128 ? 3 : 6;
   // D = 64 leaves room in tensor memory for P beside S, so that the next S is computed while this one's softmax runs
   static constexpr bool kBeside = D == 64;
@@ -132,6 +132,39 @@ struct Steps {
   __device__ __forceinline__ int at(int r) const { return stride * r + offset; }  // key tile, less j0
 };
 
+__device__ __forceinline__ void sts_u128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// The codes of a key's row at `src` to fp16 numbers code * s + lo in row `row` of an operand tile, whose first box has it at
+// `dst`.  Eight lanes read eight different 16-byte columns of the banks, and write eight.  V's channels stay in the order (0,
+// 4), (1, 5), (2, 6), (3, 7) of kv_values8: the output is put right at the end.
+template <int D, bool kV>
+__device__ __forceinline__ void convert_row(uint32_t src, uint32_t dst, int row, uint32_t s2, uint32_t lo2) {
+  constexpr int kN = KvI4<D>::kRow / 16;
+  const int turn = D == 128 ? row >> 1 : 0;
+  const uint32_t x = (row & 7) << 4;
+  uint4 next = lds_u128(src + 16 * (turn & (kN - 1)));
+  // rolled up: this runs between others' long stretches of code and would be fetched anew each time
+#pragma unroll 1
+  for (int i = 0; i < kN; ++i) {
+    const int c = (i + turn) & (kN - 1);
+    const uint32_t to = dst + (c >> 1) * Cfg<D>::kBox, xc = x ^ ((c & 1) << 6);
+    const uint32_t w[4] = {next.x, next.y, next.z, next.w};
+    next = lds_u128(src + 16 * ((i + 1 + turn) & (kN - 1)));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t h[4];
+      kv_values8(w[e], s2, lo2, h);
+      if constexpr (kV)
+        sts_u128(to + (xc ^ (e << 4)), h[0], h[1], h[2], h[3]);
+      else
+        sts_u128(to + (xc ^ (e << 4)), prmt(h[0], h[1], 0x5410), prmt(h[2], h[3], 0x5410), prmt(h[0], h[1], 0x7632),
+                 prmt(h[2], h[3], 0x7632));
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __grid_constant__ CUtensorMap tm_q, const Args a) {
   using C = Cfg<D>;
@@ -144,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
   __shared__ int s_b;
   __shared__ uint32_t tmem_slot;
   __shared__ uint64_t qbar, qfree;                              // Q tiles landed; not read any more
-  __shared__ uint64_t raw_full[C::kRaw], raw_empty[C::kRaw];    // codes landed; read (4 warps)
+  __shared__ uint64_t raw_full[C::kRaw], raw_empty[C::kRaw];    // blocks landed; read (4 warps)
   __shared__ uint64_t full[C::kSlots], empty[C::kSlots];        // K or V tile written (4 warps); used (both tiles)
   __shared__ uint64_t sbar[2], pbar[2];                         // [tile] S complete; P written (4 warps)
   __shared__ uint64_t obar[2], ofree[2];                        // [tile] O complete; O read (4 warps)
@@ -163,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
     for (int x = 0; x < 2; ++x) {
       mbar_init(&turn[x], 1), mbar_init(&sbar[x], 1), mbar_init(&pbar[x], 4), mbar_init(&obar[x], 1), mbar_init(&ofree[x], 4);
       mbar_init(&sfree[x], 4), mbar_init(&pfree[x], 1);
-      mbar_init(&item_full[x], 1), mbar_init(&item_empty[x], 3 + 4 + 8);  // copy, product, conversion and softmax warps
+      mbar_init(&item_full[x], 1), mbar_init(&item_empty[x], 3 + 8 + 8);  // copy, product, conversion and softmax warps
     }
     fence_mbarrier_init();
     mbar_arrive(&turn[0]);
@@ -214,7 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
   const uint32_t tmem = tmem_slot;
 
   if (warp >= kLoadWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp >= kConvWarp)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
       // ---------------- Q, and the codes and parameters of K(0), V(0), K(1), V(1) .. ----------------
       if (lane == 0) tma_prefetch_desc(&tm_q);
@@ -226,10 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
         }
         return ok;
       };
-      const int blk = lane & 7, part = lane >> 3;  // lanes 0-7: codes of block `lane` of a tile, 8-15: its parameters
-      const uint32_t bytes = part ? 4 * kKvBlock : kKvBlock * L::kRow;
-      const uint32_t dst = part ? C::kRawCodes + blk * 4 * kKvBlock : blk * kKvBlock * L::kRow;
-      uint32_t n = 0, rs = 0, rp = 0;  // raw tiles so far, the next one's slot and round
+      uint32_t n = 0, rs = 0, rp = 0;  // half tiles so far, the next one's slot and round
       int items = 0;
       for (int it = 0; wait(&item_full[it & 1], it >> 1); ++it) {
         const Item t = s_item[it & 1];
@@ -246,42 +279,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
             for (int b = 0; b < C::kBoxes; ++b)
               tma_load_3d(smem + x * C::kTileBytes + b * C::kBox, &tm_q, &qbar, 64 * b, t.kvh * a.G, t.row0 + x * a.tokens);
         }
-        auto page_of = [&](int j) {  // the block's page; -1: nothing to copy
-          const int gb = j * 8 + blk;
-          return part < 2 && j < t.j1 && (long long)gb * kKvBlock < t.len
-                     ? a.table[(long long)t.b * a.width + quot((uint32_t)gb, a.by_bpp)]
-                     : -1;
+        // Lane i looks after block i of half a tile: where it is the first one of a page, or of the half, it copies what
+        // follows of that page.  A block is 16 tokens' K and V; small copies cost as much as large ones, so they go together.
+        const int blocks = (t.len - 1) / kKvBlock + 1;  // of a sequence without tokens, one that is not copied
+        auto starts = [&](int h) {                      // blocks to copy from here on
+          const int gb = h * (kHalf / kKvBlock) + lane, in = gb - (int)quot((uint32_t)gb, a.by_bpp) * a.bpp;
+          return lane < kHalf / kKvBlock && h < 2 * t.j1 && gb < blocks && t.len > 0 && (lane == 0 || in == 0)
+                     ? min(min(kHalf / kKvBlock - lane, a.bpp - in), blocks - gb)
+                     : 0;
         };
-        int page = page_of(t.j0);
-        for (int j = t.j0; j < t.j1 && ok; ++j) {
-          const int next = page_of(j + 1), gb = j * 8 + blk;
-          bool there = part < 2 && (long long)gb * kKvBlock < t.len;
-          if (there && (page < 0 || page >= a.pages)) {
+        auto page_of = [&](int h) {
+          const int gb = h * (kHalf / kKvBlock) + lane;
+          return starts(h) ? a.table[(long long)t.b * a.width + quot((uint32_t)gb, a.by_bpp)] : 0;
+        };
+        int page = page_of(2 * t.j0);
+        for (int h = 2 * t.j0; h < 2 * t.j1; ++h) {
+          const int next = page_of(h + 1), gb = h * (kHalf / kKvBlock) + lane;
+          int run = starts(h);
+          if (run && (page < 0 || page >= a.pages)) {
             report_error(a.err, kErrBadIndex);
-            there = false;
+            run = 0;
           }
-          const uint8_t* src = nullptr;
-          if (there) {
+          const uint32_t bytes = run * L::kBytes, all = __reduce_add_sync(0xffffffffu, bytes);
+          if (!wait(&raw_empty[rs], (rp & 1) ^ 1)) break;
+          if (lane == 0) {
+            if (all)
+              mbar_arrive_expect_tx(&raw_full[rs], all);
+            else
+              mbar_arrive(&raw_full[rs]);
+          }
+          __syncwarp();
+          if (run) {
             const int in = gb - (int)quot((uint32_t)gb, a.by_bpp) * a.bpp;
-            src = a.cache + (((long long)page * a.Hkv + t.kvh) * a.bpp + in) * L::kBytes;
+            bulk_load(smem_u32(smem + C::kOffRaw + rs * C::kRawBytes) + lane * L::kBytes,
+                      a.cache + (((long long)page * a.Hkv + t.kvh) * a.bpp + in) * L::kBytes, bytes, &raw_full[rs]);
           }
-          const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, there) & 0xffu);
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            if (!wait(&raw_empty[rs], (rp & 1) ^ 1)) break;
-            if (lane == 0) {
-              if (blocks)
-                mbar_arrive_expect_tx(&raw_full[rs], blocks * kKvBlock * (L::kRow + 4));
-              else
-                mbar_arrive(&raw_full[rs]);
-            }
-            __syncwarp();
-            if (there)
-              bulk_load(smem_u32(smem + C::kOffRaw + rs * C::kRawBytes) + dst,
-                        src + (v ? (part ? L::kVp : L::kV) : (part ? L::kKp : 0)), bytes, &raw_full[rs]);
-            ++n;
-            if (++rs == C::kRaw) rs = 0, ++rp;
-          }
+          ++n;
+          if (++rs == C::kRaw) rs = 0, ++rp;
           page = next;
         }
       }
@@ -340,9 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
         }
       };
       int pcount = 0, ocount = 0, turns = 0, scount = 0;  // phases of pbar, of obar / ofree, of turn; S so far
-      auto my_turn = [&]() { return C::kBeside || wait(&turn[x], turns++); };
+      bool take_turns = false;  // both tiles read the same keys, and P is written over S
+      auto my_turn = [&]() { return !take_turns || wait(&turn[x], turns++); };
       auto pass = [&]() {
-        if (!C::kBeside && leader) mbar_arrive(&turn[x ^ 1]);
+        if (take_turns && leader) mbar_arrive(&turn[x ^ 1]);
       };
       auto s_free = [&]() {  // S may be written: its softmax has read it, where P does not say so
         const bool r = !C::kBeside || scount == 0 || wait(&sfree[x], scount - 1);
@@ -357,37 +392,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
         const Steps st(t, x);
         const uint32_t end = base + 2 * st.keys;
         const uint32_t q_desc = (1u << 16) + ((smem_u32(smem) + (t.twin ? 0 : x) * C::kTileBytes) >> 4);
-        uint32_t to_free = base;  // K and V tiles before this one are released
-        // Release the tiles up to that of K of step r: those of V of the step before and of K are in use, the others of the
-        // other half of the CTA.
-        auto release_to = [&](int r, bool used_v, bool used_k) {
-          const uint32_t k = base + 2 * st.at(r), stop = min(k + 1, end);
-          const uint32_t v = r > 0 ? base + 2 * st.at(r - 1) + 1 : 0xffffffffu;
-          for (; to_free < stop; ++to_free) {
-            const bool used = (used_v && to_free == v) || (used_k && to_free == k);
-            if (!used && !wait_full(to_free)) return;
-            release(&empty[slot(to_free)], used);
-          }
+        const bool twin = t.twin;
+        take_turns = !C::kBeside && !twin;
+        // K or V tile n is not needed any more; where each half of the CTA has key tiles of its own, for both
+        auto free_tile = [&](uint32_t n, bool used) {
+          release(&empty[slot(n)], used);
+          if (twin) release(&empty[slot(n)], used);
         };
         // S of the first step; the S columns are free, since the products that read their last P come before
         bool next = st.count > 0;
-        if (!wait(&qbar, it) || (next && !wait_full(base + 2 * st.at(0))) || !my_turn() || (next && !s_free())) break;
-        tc_fence_after_sync();
-        if (next) qk(q_desc, base + 2 * st.at(0));
+        if (!wait(&qbar, it) || !my_turn() || (next && !s_free())) break;
+        if (next || !twin) {
+          const uint32_t k = base + 2 * st.at(0);
+          if (!wait_full(k)) break;
+          tc_fence_after_sync();
+          if (next) qk(q_desc, k);
+          free_tile(k, next);
+        }
         pass();
-        release_to(0, false, next);
         if (st.count <= 1) release(&qfree, next);
         for (int r = 0; r < st.rounds && ok; ++r) {
-          const bool now = r < st.count;
+          const bool now = r < st.count, some = now || !twin;  // a tile with fewer steps releases what the other has
           next = r + 1 < st.count;
+          const bool some_next = next || (!twin && r + 1 < st.rounds);
           const uint32_t v = base + 2 * st.at(r) + 1, k = base + 2 * st.at(r + 1);
-          if (now && !wait_full(v)) break;
-          if (next && !wait_full(k)) break;
-          if (C::kBeside && next) {
-            if (!s_free()) break;
+          if (C::kBeside && some_next) {
+            if (!wait_full(k) || (next && !s_free())) break;
             tc_fence_after_sync();
-            qk(q_desc, k);
+            if (next) qk(q_desc, k);
+            free_tile(k, next);
           }
+          if (some && !wait_full(v)) break;
           if (now) {
             if (!wait(&pbar[x], pcount++)) break;
             // the accumulator is taken over when the softmax warps have read that of the item before
@@ -403,9 +438,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
               ++ocount;
             }
           }
-          if (!C::kBeside && next) qk(q_desc, k);
+          if (some) free_tile(v, now);
+          if (!C::kBeside && some_next) {
+            if (!wait_full(k)) break;
+            tc_fence_after_sync();
+            if (next) qk(q_desc, k);
+            free_tile(k, next);
+          }
           pass();
-          release_to(r + 1, now, next);
           if (r + 2 == st.count) release(&qfree, true);
         }
         base = end;
@@ -486,8 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
         put(t);
       }
     } else {
-      // ---------------- codes to fp16: a thread takes one key's row ----------------
-      const int row = tid - kConvWarp * 32;
+      // ---------------- codes to fp16: two warps K, two V of every other half tile, a thread one key's row ----------------
+      const int group = (warp - kConvWarp) >> 2, v = (warp & 3) >= 2, key_in = tid & (kHalf - 1);
       bool ok = true;
       auto wait = [&](uint64_t* bar, int phase) {
         if (ok && !mbar_wait_warp(bar, phase & 1)) {
@@ -496,61 +536,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
         }
         return ok;
       };
-      uint32_t n = 0, rs = 0, rp = 0;
+      uint32_t n = 0;  // tiles so far
       for (int it = 0; wait(&item_full[it & 1], it >> 1); ++it) {
-        const int2 keys = make_int2(s_item[it & 1].j0, s_item[it & 1].j1);
-        const int len = s_item[it & 1].len, tokens = s_item[it & 1].tokens;
-        if (row == 0) s_bad[it & 1] = INT_MAX;
+        const int j0 = s_item[it & 1].j0, j1 = s_item[it & 1].j1, len = s_item[it & 1].len, tokens = s_item[it & 1].tokens;
+        if (tid == kConvWarp * 32) s_bad[it & 1] = INT_MAX;
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[it & 1]);
         if (tokens == 0) break;
-        named_barrier_sync(1, 128);  // s_bad is reset
-        for (int j = keys.x; j < keys.y && ok; ++j) {
-          const int key = j * kTile + row;
-          const bool inside = key < len && key >= 0;
-#pragma unroll 1
-          for (int v = 0; v < 2; ++v) {
-            const uint32_t slot = n % C::kSlots;
-            if (!wait(&raw_full[rs], (int)rp) || !wait(&empty[slot], (int)(n / C::kSlots) ^ 1)) break;
-            const uint8_t* raw = smem + C::kOffRaw + rs * C::kRawBytes;
-            const uint32_t src = smem_u32(raw) + row * L::kRow;
-            const uint32_t dst = smem_u32(smem + C::kOffRing + slot * C::kTileBytes) + row * 128;
-            uint32_t par = inside ? *reinterpret_cast<const uint32_t*>(raw + C::kRawCodes + 4 * row) : 0u;
-            if (!kv_finite(par)) {
-              if (v) atomicMin(&s_bad[it & 1], key);
-              par = v ? 0u : 0x7fff7fffu;
-            }
-            const bool over = kv_overflows(par);  // of a NaN: no
-            const uint32_t s2 = prmt(par, 0, 0x1010), lo2 = prmt(par, 0, 0x3232);
-#pragma unroll
-            for (int i = 0; i < L::kRow / 16; ++i) {
-              // eight lanes read eight different 16-byte columns of the banks, and write eight
-              const int c = D == 128 ? (i + (row >> 1)) & 3 : i;
-              const uint4 w4 = lds_u128(src + 16 * c);
-              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t h[4];
-                kv_values8(w[e], s2, lo2, h);
-                if (over) {
-#pragma unroll
-                  for (int u = 0; u < 4; ++u) h[u] = kv_clamp2(h[u]);
-                }
-                const uint32_t to = dst + (c >> 1) * C::kBox + ((((c & 1) * 4 + e) ^ (row & 7)) << 4);
-                // V's channels stay in the order (0, 4), (1, 5), (2, 6), (3, 7): the output is put right at the end
-                const uint4 o = v ? make_uint4(h[0], h[1], h[2], h[3])
-                                  : make_uint4(prmt(h[0], h[1], 0x5410), prmt(h[2], h[3], 0x5410), prmt(h[0], h[1], 0x7632),
-                                               prmt(h[2], h[3], 0x7632));
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w)
-                             : "memory");
-              }
-            }
-            fence_proxy_async_smem();  // the tile for the products, and the codes' reads before the next copy
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[slot]), mbar_arrive(&raw_empty[rs]);
-            ++n;
-            if (++rs == C::kRaw) rs = 0, ++rp;
+        named_barrier_sync(1, 256);  // s_bad is reset
+        for (int j = j0; j < j1; ++j, ++n) {
+          const int row = group * kHalf + key_in, key = j * kTile + row;
+          const uint32_t tile = 2 * n + v, slot = tile % C::kSlots, half_n = 2 * n + group, rs = half_n % C::kRaw;
+          if (!wait(&raw_full[rs], (int)(half_n / C::kRaw)) || !wait(&empty[slot], (int)(tile / C::kSlots) ^ 1)) break;
+          const uint8_t* raw = smem + C::kOffRaw + rs * C::kRawBytes + key_in / kKvBlock * L::kBytes;
+          const uint32_t src = smem_u32(raw) + (v ? L::kV : 0) + key_in % kKvBlock * L::kRow;
+          const uint32_t dst = smem_u32(smem + C::kOffRing + slot * C::kTileBytes) + row * 128;
+          uint32_t par = key < len ? *reinterpret_cast<const uint32_t*>(raw + (v ? L::kVp : L::kKp) + 4 * (key_in % kKvBlock)) : 0u;
+          if (!kv_finite(par)) {
+            if (v) atomicMin(&s_bad[it & 1], key);
+            par = v ? 0u : 0x7fff7fffu;
           }
+          const uint32_t s2 = prmt(par, 0, 0x1010), lo2 = prmt(par, 0, 0x3232);
+          if (v)
+            convert_row<D, true>(src, dst, row, s2, lo2);
+          else
+            convert_row<D, false>(src, dst, row, s2, lo2);
+          if (kv_overflows(par)) {  // rare; of a NaN: no
+            for (int i = 0; i < D / 8; ++i) {
+              const uint32_t at = dst + (i >> 3) * C::kBox + (((i & 7) ^ (row & 7)) << 4);
+              const uint4 x = lds_u128(at);
+              sts_u128(at, kv_clamp2(x.x), kv_clamp2(x.y), kv_clamp2(x.z), kv_clamp2(x.w));
+            }
+          }
+          fence_proxy_async_smem();  // the tile for the products, and the codes' reads before the next copy
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[slot]), mbar_arrive(&raw_empty[rs]);
         }
       }
     }
