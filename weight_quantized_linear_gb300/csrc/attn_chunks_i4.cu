@@ -33,12 +33,12 @@ constexpr int kTile = 128, kHalf = 64;  // keys of a tile, and rows at most; key
 constexpr int kThreads = 640;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kNextWarp = 11, kConvWarp = 12;
 constexpr int kLead = 1;          // rounds that stand for an item's own cost
-constexpr float kTop = 7.0f;      // the largest weight after a rescale is 2^7, the 128 of a step at most 2^14
-constexpr float kMost = 32768.f;  // and a step whose weights come to more than 2^15 asks for the next
+constexpr float kTop = 7.0f;         // the largest weight after a rescale is 2^7
+constexpr float kGrown = 15.0f;      // and the next rescale comes when one would pass 2^15, as fp16 asks
 constexpr float kLarge = 1048576.f;  // from here on scores are rounded before the maximum is subtracted, as it was
 constexpr float kNoMax = -3e38f;     // the maximum of keys whose scores are all minus infinity
 // registers per thread: launched with 96; two warpgroups for the softmax, two convert, one does the rest
-constexpr int kSoftmaxRegs = 168, kConvRegs = 48, kOtherRegs = 48;
+constexpr int kSoftmaxRegs = 136, kConvRegs = 72, kOtherRegs = 56;
 static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kOtherRegs <= 5 * 96, "of what the block was launched with");
 
 template <int D>
@@ -132,6 +132,11 @@ struct Steps {
   __device__ __forceinline__ int at(int r) const { return stride * r + offset; }  // key tile, less j0
 };
 
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ void sts_u128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -601,84 +606,110 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
       float m = kNoMax, l0 = 0.f, l1 = 0.f;                 // m: what is subtracted from the scaled scores
       for (int r = 0; r < st.count && wait(&sbar[x], scount++); ++r) {
         tc_fence_after_sync();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
-        tmem_ld_wait();
-        if constexpr (C::kBeside) {
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sfree[x]);
-        }
         const int key0 = (st.j0 + st.at(r)) * kTile;
         if (seen - key0 < kTile - 1) {  // some row sees less than the whole tile
           const int last = seen + tok - key0;
+#pragma unroll 1
+          for (int i = 0; i < kTile; i += 32) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(ts + i, v);
+            tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i > last) s[i >> 5][i & 31] = 0xff800000u;
-        }
-        auto row_max = [&]() {  // of the scaled scores, less kTop
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 128; i += 2)
-            top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
-          return __fsub_rn(__fmul_rn(fmaxf(max3(top[0], top[1], top[2]), top[3]), c), kTop);
-        };
-        if (r == 0) m = fmaxf(row_max(), kNoMax);
-        float a0, a1;  // this step's sums
-        uint32_t w[C::kBeside ? 4 : 1][16];
-        auto weights = [&](float mul) {
-          a0 = a1 = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t (&wi)[16] = w[C::kBeside ? i : 0];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float u = __uint_as_float(s[i][2 * e]), v = __uint_as_float(s[i][2 * e + 1]);
-              fma2(u, v, mul, -m);
-              u = ex2(u), v = ex2(v);
-              add2(a0, a1, u, v);
-              wi[e] = pack_h2(u, v);
-            }
-            if constexpr (!C::kBeside) tmem_st_32x32b_x16(tp + 16 * i, wi);
+            for (int e = 0; e < 32; ++e)
+              if (i + e > last) v[e] = 0xff800000u;
+            tmem_st_32x32b_x32(ts + i, v);
           }
-        };
-        weights(c);
+          tmem_st_wait();
+        }
+        // The scores are read twice, 32 at a time and the next ones while the last are worked on: first for the maximum, then
+        // for the weights.  Rolled up, since the eight converting warps' code and this have to stay near their schedulers.
+        uint32_t va[32], vb[32];
+        tmem_ld_32x32b_x32(ts, va);
+        float top0 = -INFINITY, top1 = -INFINITY;
+        tmem_ld_wait();
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          tmem_ld_32x32b_x32(ts + 64 * i + 32, vb);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            top0 = max3(top0, __uint_as_float(va[e]), __uint_as_float(va[e + 1]));
+            top1 = max3(top1, __uint_as_float(va[e + 2]), __uint_as_float(va[e + 3]));
+          }
+          tmem_ld_wait();
+          tmem_ld_32x32b_x32(ts + 64 * (i ^ 1), va);  // the first ones again at the end
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            top0 = max3(top0, __uint_as_float(vb[e]), __uint_as_float(vb[e + 1]));
+            top1 = max3(top1, __uint_as_float(vb[e + 2]), __uint_as_float(vb[e + 3]));
+          }
+          tmem_ld_wait();
+        }
+        const float top = __fmul_rn(fmaxf(top0, top1), c);
         if constexpr (C::kBeside) {  // the last P has been used, and O is that of the steps before
           if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;
           ++pcount;
           tc_fence_after_sync();
         }
-        const bool more = a0 + a1 > kMost || fabsf(m) > kLarge;
-        if (__any_sync(0xffffffffu, more)) {
+        if (r == 0) {
+          m = fmaxf(__fsub_rn(top, kTop), kNoMax);
+        } else if (const bool more = top - m > kGrown; __any_sync(0xffffffffu, more)) {
           // only the rows that need it, so that a row's roundings do not depend on its neighbours
-          const float now = more ? fmaxf(m, row_max()) : m, f = ex2(m - now);
+          const float now = more ? __fsub_rn(top, kTop) : m, f = ex2(m - now);
           m = now;
-          const bool large = fabsf(m) > kLarge;
-          if (__any_sync(0xffffffffu, large)) {
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-              s[i >> 5][i & 31] = __float_as_uint(__fmul_rn(__uint_as_float(s[i >> 5][i & 31]), large ? c : 1.f));
-          }
           l0 *= f, l1 *= f;
-          if (r > 0) {
 #pragma unroll 1
-            for (int i = 0; i < D; i += 32) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(to + i, o);
-              tmem_ld_wait();
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + i, o);
+            tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st_32x32b_x32(to + i, o);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st_32x32b_x32(to + i, o);
           }
-          weights(large ? 1.f : c);
+        }
+        // rows with large scores: the scaled scores rounded before the maximum is subtracted, as it was
+        const bool large = fabsf(m) > kLarge;
+        const float mul = large ? 1.f : c;
+        if (__any_sync(0xffffffffu, large)) {
+#pragma unroll 1
+          for (int i = 0; i < kTile; i += 32) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(ts + i, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), large ? c : 1.f));
+            tmem_st_32x32b_x32(ts + i, v);
+          }
+          tmem_st_wait();
+          tmem_ld_32x32b_x32(ts, va);
+          tmem_ld_wait();
+        }
+        auto weights = [&](uint32_t (&v)[32], int i) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a0 = __uint_as_float(v[2 * e]), a1 = __uint_as_float(v[2 * e + 1]);
+            fma2(a0, a1, mul, -m);
+            a0 = ex2(a0), a1 = ex2(a1);
+            add2(l0, l1, a0, a1);
+            w[e] = pack_h2(a0, a1);
+          }
+          tmem_st_32x32b_x16(tp + 16 * i, w);
+        };
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          tmem_ld_32x32b_x32(ts + 64 * i + 32, vb);
+          weights(va, 2 * i);
+          tmem_ld_wait();
+          if (i == 0) tmem_ld_32x32b_x32(ts + 64, va);
+          weights(vb, 2 * i + 1);
+          tmem_ld_wait();
         }
         if constexpr (C::kBeside) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_st_32x32b_x16(tp + 16 * i, w[i]);
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[x]);
         }
-        l0 += a0, l1 += a1;
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
@@ -696,77 +727,73 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
           if (lane == 0) mbar_arrive(&half);
         }
       } else {
-        uint32_t o[D / 32][32];
-        if (st.count > 0) {
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) tmem_ld_32x32b_x32(to + 32 * i, o[i]);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int i = 0; i < D; ++i) o[i >> 5][i & 31] = 0u;
-        }
+        float f0 = 1.f, f1 = 0.f;
         if (shared) {
           if (!wait(&half, hcount++)) break;
           tc_fence_after_sync();
           const float2 ml = s_ml[it & 1][row];
-          const float now = fmaxf(m, ml.x), f0 = ex2(m - now), f1 = ex2(ml.x - now);
+          const float now = fmaxf(m, ml.x);
+          f0 = ex2(m - now), f1 = ex2(ml.x - now);
           m = now, l = l * f0 + ml.y * f1;
+        }
+        const int mine = (twin ? 0 : x * a.tokens) + tok;  // token of the item
+        const bool there = tok < a.tokens && mine < t.tokens, whole = t.slot < 0;
+        const int last = seen + tok;  // the last key that this row sees
+        const bool nan = last >= s_bad[it & 1];
+        const long long to_row = whole ? (long long)(t.row0 + mine) * a.Hq + t.kvh * a.G + g
+                                       : ((long long)blockIdx.x * 2 + t.slot) * a.part_rows + mine * a.G + g;
+        const float inv = last < 0 ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          if (st.count > 0) {
+            tmem_ld_32x32b_x32(to + i, o);
+            tmem_ld_wait();
+          } else {
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (shared) {
             uint32_t o1[32];
-            tmem_ld_32x32b_x32(to + D + 32 * i, o1);
+            tmem_ld_32x32b_x32(to + D + i, o1);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              o[i][e] = __float_as_uint(__uint_as_float(o[i][e]) * f0 + __uint_as_float(o1[e]) * f1);
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
+          }
+          if (!there) continue;
+          if (nan) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0x7fc00000u;
+          }
+          // channel k of eight stands in column 2 k of theirs (k < 4) or 2 k - 7
+          auto at = [](int ch) { return (ch & ~7) + ((ch & 7) < 4 ? 2 * (ch & 7) : 2 * (ch & 7) - 7); };
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 16) {
+              uint32_t h[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                h[e] = pack_h2(__uint_as_float(o[at(j + 2 * e)]) * inv, __uint_as_float(o[at(j + 2 * e + 1)]) * inv);
+              st_global_32(a.out + to_row * D + i + j, h, sectors);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t h[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) h[e] = o[at(j + e)];
+              st_global_32(a.part + to_row * D + i + j, h, true);
+            }
           }
         }
+        if (there && whole && a.lse) a.lse[to_row] = last < 0 ? -INFINITY : (m + lg2(l)) * 0.6931471805599453f;
+        if (there && !whole) a.ml[to_row] = make_float2(m, l);
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
           if (st.count > 0) mbar_arrive(&ofree[x]);
           if (shared) mbar_arrive(&ofree[1]);
-        }
-        const int mine = (twin ? 0 : x * a.tokens) + tok;  // token of the item
-        if (tok < a.tokens && mine < t.tokens) {
-          const int last = seen + tok;
-          if (last >= s_bad[it & 1]) {
-#pragma unroll
-            for (int i = 0; i < D; ++i) o[i >> 5][i & 31] = 0x7fc00000u;
-          }
-          // channel k of eight stands in column 2 k of theirs (k < 4) or 2 k - 7
-          auto at = [&](int ch) { return (ch & ~7) + ((ch & 7) < 4 ? 2 * (ch & 7) : 2 * (ch & 7) - 7); };
-          if (t.slot < 0) {
-            const long long to_row = (long long)(t.row0 + mine) * a.Hq + t.kvh * a.G + g;
-            const float inv = last < 0 ? 0.f : 1.f / l;
-            __half* dst = a.out + to_row * D;
-#pragma unroll
-            for (int i = 0; i < D; i += 16) {
-              uint32_t h[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int u = at(i + 2 * e), v = at(i + 2 * e + 1);
-                h[e] = pack_h2(__uint_as_float(o[u >> 5][u & 31]) * inv, __uint_as_float(o[v >> 5][v & 31]) * inv);
-              }
-              st_global_32(dst + i, h, sectors);
-            }
-            if (a.lse) {
-              float lg;
-              asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(l));
-              a.lse[to_row] = last < 0 ? -INFINITY : (m + lg) * 0.6931471805599453f;
-            }
-          } else {
-            const long long to_row = ((long long)blockIdx.x * 2 + t.slot) * a.part_rows + mine * a.G + g;
-            a.ml[to_row] = make_float2(m, l);
-            float* dst = a.part + to_row * D;
-#pragma unroll
-            for (int i = 0; i < D; i += 8) {
-              uint32_t h[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) h[e] = o[at(i + e) >> 5][at(i + e) & 31];
-              st_global_32(dst + i, h, true);
-            }
-          }
         }
       }
       __syncwarp();
@@ -833,11 +860,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_chunks_join_kernel(const
       reinterpret_cast<uint2*>(a.out + to * D)[lane] = make_uint2(h[0], h[1]);
     else
       reinterpret_cast<uint32_t*>(a.out + to * D)[lane] = h[0];
-    if (a.lse && lane == 0) {
-      float lg;
-      asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(l));
-      a.lse[to] = none ? -INFINITY : (m + lg) * 0.6931471805599453f;
-    }
+    if (a.lse && lane == 0) a.lse[to] = none ? -INFINITY : (m + lg2(l)) * 0.6931471805599453f;
   }
 }
 
