@@ -477,7 +477,7 @@ wql_status wql_attention_prompt(const uint16_t* q, int64_t q_stride, const uint1
  * workspace: device scratch of at least wql_attention_chunks_kv_i4_workspace_bytes(T, B, Hq, Hkv, D) bytes (the
  * current device's), with no contents to keep; calls that may run at the same time need one each.  out and lse must
  * overlap no input and not each other.  Results are deterministic.
- * Requires B <= 4096, Hq <= 65535, Hq / Hkv <= 128 (WQL_EUNSUPPORTED above).
+ * Requires B <= 4096, Hq <= 65535, Hq / Hkv <= 128, T * Hq < 2^31 (WQL_EUNSUPPORTED above).
  * ---------------------------------------------------------------------------------------- */
 size_t wql_attention_chunks_kv_i4_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
 wql_status wql_attention_chunks_kv_i4(const uint16_t* q, int64_t q_stride, int T, int Hq, int Hkv, int D,
@@ -495,13 +495,15 @@ wql_status wql_attention_chunks_kv_i4(const uint16_t* q, int64_t q_stride, int T
  * as they were.  Each sum is formed in fp32 and added once.  k is what attention_chunks_kv_i4 takes; a row of K whose
  * parameters are not finite makes the sums that it belongs to NaN, and so does a row r whose lse is NaN.
  * Sequences, lengths and pages out of range: as there; the sums of a sequence with a bad page are unspecified.
- * weights must overlap no input.  Results are deterministic.  Requires B <= 4096, Hq <= 65535, Hq / Hkv <= 128
- * (WQL_EUNSUPPORTED above).
+ * workspace: device scratch of at least wql_kv_weights_i4_workspace_bytes() bytes (the current device's), with no contents
+ * to keep; calls that may run at the same time need one each.  weights must overlap no input.  Results are deterministic.
+ * Requires B <= 4096, Hq <= 65535, Hq / Hkv <= 128, T * Hq < 2^31 (WQL_EUNSUPPORTED above).
  * ---------------------------------------------------------------------------------------- */
+size_t wql_kv_weights_i4_workspace_bytes(void);
 wql_status wql_kv_weights_i4(const uint16_t* q, int64_t q_stride, int T, int Hq, int Hkv, int D,
                              const uint8_t* cache, int64_t pages, int page_size, const int32_t* block_table,
                              int table_width, const int32_t* cu_new, const int32_t* kv_lens, int B, float scale,
-                             const float* lse, float* weights, void* stream);
+                             const float* lse, float* weights, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ----------------------------------------------------------------------------------------
  * kv_evict_i4: leave the least attended tokens behind.  Of the n = kv_lens[b] tokens of sequence b each K/V head

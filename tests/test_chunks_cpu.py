@@ -29,8 +29,9 @@ def chunks(lib, T=8, Hq=4, Hkv=2, D=128, qs=512, pages=3, ps=16, width=4, B=2, s
 
 
 def weights(lib, T=8, Hq=4, Hkv=2, D=128, qs=512, pages=3, ps=16, width=4, B=2, scale=0.1, q=P, cache=P, table=P, cu=P, lens=P,
-            lse=P, w=P):
-    return lib.wql_kv_weights_i4(q, qs, T, Hq, Hkv, D, cache, pages, ps, table, width, cu, lens, B, F(scale), lse, w, None)
+            lse=P, w=P, ws=P, n=1 << 40):
+    return lib.wql_kv_weights_i4(q, qs, T, Hq, Hkv, D, cache, pages, ps, table, width, cu, lens, B, F(scale), lse, w, ws, n,
+                                 None)
 
 
 def evict(lib, w=P, cache=P, pages=3, ps=16, H=2, D=128, table=P, width=4, lens=P, B=2, new=P, new_width=2, budget=20, recent=4,
@@ -45,7 +46,7 @@ def evict(lib, w=P, cache=P, pages=3, ps=16, H=2, D=128, table=P, width=4, lens=
     (dict(D=96), EUNSUPPORTED, b"64 or 128"), (dict(ps=24), EINVAL, b"page_size"), (dict(ps=0), EINVAL, b"page_size"),
     (dict(pages=0), EINVAL, b"pages"), (dict(pages=1 << 28), EINVAL, b"2^31"), (dict(width=0), EINVAL, b"table_width"),
     (dict(width=1 << 27, ps=16), EINVAL, b"2^31"), (dict(Hq=258, Hkv=2, qs=258 * 128), EUNSUPPORTED, b"128"),
-    (dict(Hq=65536, Hkv=65536, qs=65536 * 128), EUNSUPPORTED, b"65535"), (dict(scale=math.nan), EINVAL, b"scale"),
+    (dict(T=1 << 30), EUNSUPPORTED, b"2^31"), (dict(Hq=65536, Hkv=65536, qs=65536 * 128), EUNSUPPORTED, b"65535"), (dict(scale=math.nan), EINVAL, b"scale"),
     (dict(scale=-math.inf), EINVAL, b"scale"), (dict(scale=2.0 ** 65), EINVAL, b"scale"), (dict(qs=511), EINVAL, b"stride"),
     (dict(qs=516), EINVAL, b"stride"), (dict(q=None), EINVAL, b"q"), (dict(q=ODD4), EINVAL, b"q"),
     (dict(cache=ODD4), EINVAL, b"cache"), (dict(table=ODD), EINVAL, b"block_table"), (dict(cu=None), EINVAL, b"cu_new"),
@@ -62,12 +63,15 @@ def test_own_refusals(lib):
     assert chunks(lib, n=8) == EINVAL and b"workspace" in lib.wql_last_error()
     for kw in (dict(T=0), dict(B=0)):
         assert chunks(lib, q=None, cache=None, table=None, cu=None, lens=None, out=None, lse=None, ws=None, n=0, **kw) == OK
-        assert weights(lib, q=None, cache=None, table=None, cu=None, lens=None, lse=None, w=None, **kw) == OK
+        assert weights(lib, q=None, cache=None, table=None, cu=None, lens=None, lse=None, w=None, ws=None, n=0, **kw) == OK
     f = lib.wql_attention_chunks_kv_i4_workspace_bytes
     assert f(8, 2, 4, 2, 128) > 0
     assert f(8, 2, 5, 2, 128) == f(0, 2, 4, 2, 128) == f(8, 0, 4, 2, 128) == f(8, 2, 4, 2, 80) == f(8, 2, 258, 2, 64) == 0
     assert weights(lib, lse=None) == EINVAL and weights(lib, lse=ODD) == EINVAL
     assert weights(lib, w=None) == EINVAL and weights(lib, w=ODD4) == EINVAL
+    assert weights(lib, ws=None) == EINVAL and weights(lib, ws=ODD4) == EINVAL
+    assert weights(lib, n=8) == EINVAL and b"workspace" in lib.wql_last_error()
+    assert lib.wql_kv_weights_i4_workspace_bytes() > 0
 
 
 @pytest.mark.parametrize("kw,status,word", [

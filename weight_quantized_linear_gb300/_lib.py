@@ -60,7 +60,8 @@ SIGNATURES = {
     "wql_attention_kv_i4": (_I, [_P, _I64, _I, _I, _I, _I, _I, _P, _I64, _I, _P, _I, _P, _F, _P, _P, _SZ, _P]),
     "wql_attention_chunks_kv_i4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "wql_attention_chunks_kv_i4": (_I, [_P, _I64, _I, _I, _I, _I, _P, _I64, _I, _P, _I, _P, _P, _I, _F, _P, _P, _P, _SZ, _P]),
-    "wql_kv_weights_i4": (_I, [_P, _I64, _I, _I, _I, _I, _P, _I64, _I, _P, _I, _P, _P, _I, _F, _P, _P, _P]),
+    "wql_kv_weights_i4_workspace_bytes": (_SZ, []),
+    "wql_kv_weights_i4": (_I, [_P, _I64, _I, _I, _I, _I, _P, _I64, _I, _P, _I, _P, _P, _I, _F, _P, _P, _P, _SZ, _P]),
     "wql_kv_evict_i4": (_I, [_P, _P, _I64, _I, _I, _I, _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, _P]),
     "wql_attention_prompt": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I, _F, _P, _P]),
 }
@@ -770,23 +771,34 @@ def attention_chunks_kv_i4(q: torch.Tensor, cache: torch.Tensor, block_table: to
     return out
 
 
+def kv_weights_i4_workspace_bytes() -> int:
+    return int(load().wql_kv_weights_i4_workspace_bytes())
+
+
 def kv_weights_i4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, cu_new: torch.Tensor,
-                  kv_lens: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor,
-                  scale: float | None = None) -> torch.Tensor:
+                  kv_lens: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor, scale: float | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Add the attention weight that every cached token gets from packed chunks of rows to weights, fp32
     [B, K/V heads, block_table width * page size]; entries from kv_lens on stay as they are.
 
     q, cu_new, kv_lens, block_table and scale as in attention_chunks_kv_i4, whose lse [T, Hq] it takes (the rows may be
-    any last ones of the sequences, such as a window at a prompt's end).  Returns weights."""
+    any last ones of the sequences, such as a window at a prompt's end).  workspace: uint8,
+    kv_weights_i4_workspace_bytes() of them, allocated here if not given.  Returns weights."""
     pages, Hkv, ps, index, qs, B, width = _chunk_args(q, cache, block_table, cu_new, kv_lens)
     T, Hq, D = q.shape
     if not _is(lse, torch.float32, (T, Hq), index):
         _refuse(lse, "lse", torch.float32, (T, Hq), index)
     if not _is(weights, torch.float32, (B, Hkv, width * ps), index):
         _refuse(weights, "weights", torch.float32, (B, Hkv, width * ps), index)
+    if workspace is None:
+        with torch.cuda.device(cache.device):
+            n = kv_weights_i4_workspace_bytes()
+        workspace = torch.empty((n,), dtype=torch.uint8, device=cache.device)
+    elif not _is(workspace, torch.uint8, (workspace.numel(),), index):
+        _refuse(workspace, "workspace", torch.uint8, (workspace.numel(),), index)
     _run("wql_kv_weights_i4", index, q.data_ptr(), qs, T, Hq, Hkv, D, cache.data_ptr(), pages, ps, block_table.data_ptr(),
          width, cu_new.data_ptr(), kv_lens.data_ptr(), B, D ** -0.5 if scale is None else scale, lse.data_ptr(),
-         weights.data_ptr())
+         weights.data_ptr(), workspace.data_ptr(), workspace.numel())
     return weights
 
 

@@ -633,6 +633,7 @@ wql_status check_chunks(const uint16_t* q, int64_t q_stride, int T, int Hq, int 
   WQL_REQUIRE_CACHE();
   if (B > wql::kPlanMaxB) return fail(WQL_EUNSUPPORTED, "B must be at most 4096");
   if (Hq > 65535 || Hq / Hkv > 128) return fail(WQL_EUNSUPPORTED, "Hq must be at most 65535 and Hq / Hkv at most 128");
+  if ((int64_t)T * Hq > INT_MAX) return fail(WQL_EUNSUPPORTED, "T * Hq must be below 2^31");
   WQL_REQUIRE(table_width >= 1 && (int64_t)table_width * page_size <= INT_MAX,
               "table_width * page_size must be between 16 and 2^31 - 1");
   WQL_REQUIRE(valid_scale(scale), "scale must be finite and at most 2^64 in magnitude");
@@ -679,23 +680,27 @@ wql_status wql_attention_chunks_kv_i4(const uint16_t* q, int64_t q_stride, int T
   return cuda_status(e, "wql_attention_chunks_kv_i4", err);
 }
 
+size_t wql_kv_weights_i4_workspace_bytes(void) { return wql::kv_weights_i4_workspace_bytes(); }
+
 wql_status wql_kv_weights_i4(const uint16_t* q, int64_t q_stride, int T, int Hq, int Hkv, int D, const uint8_t* cache,
                              int64_t pages, int page_size, const int32_t* block_table, int table_width,
                              const int32_t* cu_new, const int32_t* kv_lens, int B, float scale, const float* lse,
-                             float* weights, void* stream) {
+                             float* weights, void* workspace, size_t workspace_bytes, void* stream) {
   bool empty;
   const wql_status st = check_chunks(q, q_stride, T, Hq, Hkv, D, cache, pages, page_size, block_table, table_width, cu_new,
                                      kv_lens, B, scale, &empty);
   if (st != WQL_OK || empty) return st;
   WQL_REQUIRE_PTR4(lse);
   WQL_REQUIRE_PTR(weights);
+  WQL_REQUIRE_PTR(workspace);
+  WQL_REQUIRE(workspace_bytes >= wql::kv_weights_i4_workspace_bytes(),
+              "workspace is smaller than wql_kv_weights_i4_workspace_bytes");
   unsigned* dev_err = device_error_word();
   if (!dev_err) return fail(WQL_ECUDA, "wql_kv_weights_i4: cannot locate the device error word");
-  std::string err;
   const cudaError_t e = wql::launch_kv_weights_i4(q, q_stride, T, Hq, Hkv, D, cache, pages, page_size, block_table,
-                                                  table_width, cu_new, kv_lens, B, scale, lse, weights, dev_err,
-                                                  static_cast<cudaStream_t>(stream), &err);
-  return cuda_status(e, "wql_kv_weights_i4", err);
+                                                  table_width, cu_new, kv_lens, B, scale, lse, weights, workspace, dev_err,
+                                                  static_cast<cudaStream_t>(stream));
+  return cuda_status(e, "wql_kv_weights_i4");
 }
 
 wql_status wql_kv_evict_i4(const float* weights, uint8_t* cache, int64_t pages, int page_size, int H, int D,

@@ -151,10 +151,11 @@ cudaError_t launch_attn_chunks_i4(const uint16_t* q, long long q_stride, int T, 
                                   long long pages, int ps, const int* table, int width, const int* cu, const int* kv_lens,
                                   int B, float scale, uint16_t* out, float* lse, void* workspace, unsigned* dev_err,
                                   cudaStream_t s, std::string* err);
+size_t kv_weights_i4_workspace_bytes();
 cudaError_t launch_kv_weights_i4(const uint16_t* q, long long q_stride, int T, int Hq, int Hkv, int D, const uint8_t* cache,
                                  long long pages, int ps, const int* table, int width, const int* cu, const int* kv_lens, int B,
-                                 float scale, const float* lse, float* weights, unsigned* dev_err, cudaStream_t s,
-                                 std::string* err);
+                                 float scale, const float* lse, float* weights, void* workspace, unsigned* dev_err,
+                                 cudaStream_t s);
 cudaError_t launch_kv_evict_i4(const float* weights, uint8_t* cache, long long pages, int ps, int H, int D, const int* table,
                                int width, const int* kv_lens, int B, const int* new_table, int new_width, int budget,
                                int recent, int* kept, float* new_weights, int* new_lens, unsigned* dev_err, cudaStream_t s);
