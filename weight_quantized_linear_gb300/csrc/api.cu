@@ -697,10 +697,11 @@ wql_status wql_kv_weights_i4(const uint16_t* q, int64_t q_stride, int T, int Hq,
               "workspace is smaller than wql_kv_weights_i4_workspace_bytes");
   unsigned* dev_err = device_error_word();
   if (!dev_err) return fail(WQL_ECUDA, "wql_kv_weights_i4: cannot locate the device error word");
+  std::string err;
   const cudaError_t e = wql::launch_kv_weights_i4(q, q_stride, T, Hq, Hkv, D, cache, pages, page_size, block_table,
                                                   table_width, cu_new, kv_lens, B, scale, lse, weights, workspace, dev_err,
-                                                  static_cast<cudaStream_t>(stream));
-  return cuda_status(e, "wql_kv_weights_i4");
+                                                  static_cast<cudaStream_t>(stream), &err);
+  return cuda_status(e, "wql_kv_weights_i4", err);
 }
 
 wql_status wql_kv_evict_i4(const float* weights, uint8_t* cache, int64_t pages, int page_size, int H, int D,

@@ -155,7 +155,7 @@ size_t kv_weights_i4_workspace_bytes();
 cudaError_t launch_kv_weights_i4(const uint16_t* q, long long q_stride, int T, int Hq, int Hkv, int D, const uint8_t* cache,
                                  long long pages, int ps, const int* table, int width, const int* cu, const int* kv_lens, int B,
                                  float scale, const float* lse, float* weights, void* workspace, unsigned* dev_err,
-                                 cudaStream_t s);
+                                 cudaStream_t s, std::string* err);
 cudaError_t launch_kv_evict_i4(const float* weights, uint8_t* cache, long long pages, int ps, int H, int D, const int* table,
                                int width, const int* kv_lens, int B, const int* new_table, int new_width, int budget,
                                int recent, int* kept, float* new_weights, int* new_lens, unsigned* dev_err, cudaStream_t s);
