@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
           const uint8_t* raw = smem + C::kOffRaw + rs * C::kRawBytes + key_in / kKvBlock * L::kBytes;
           const uint32_t src = smem_u32(raw) + (v ? L::kV : 0) + key_in % kKvBlock * L::kRow;
           const uint32_t dst = smem_u32(smem + C::kOffRing + slot * C::kTileBytes) + row * 128;
-          uint32_t par = key < len ? *reinterpret_cast<const uint32_t*>(raw + (v ? L::kVp : L::kKp) + 4 * (key_in % kKvBlock)) : 0u;
+          uint32_t par = row < len - j * kTile ? *reinterpret_cast<const uint32_t*>(raw + (v ? L::kVp : L::kKp) + 4 * (key_in % kKvBlock)) : 0u;
           if (!kv_finite(par)) {
             if (v) atomicMin(&s_bad[it & 1], key);
             par = v ? 0u : 0x7fff7fffu;

@@ -2,16 +2,16 @@
 //   weights[b, kvh, t] += sum over the rows r of sequence b that see t, and the query heads h of kvh's group, of
 //                         exp(scale q[r, h] . k[t] - lse[r, h]),   k = code * s + lo, rounded to fp16.
 //
-// The sums run over rows, so a warp keeps 32 keys as the first operand of its products (mma.sync, 16 keys x 8 rows x 16
-// channels) in registers, made fp16 there: a lane of the fragment needs two keys' rows, and as the products do not mind the
-// order of the channels, it takes D / 8 contiguous bytes of codes of each, and the same channels of the rows of q.  K is read
-// from memory once.  A lane holds two keys' scores of two rows at a time, turns them into weights and adds them up.
+// The sums run over rows, so the keys are the first operand of the products (tcgen05): 128 of them are the lanes of a tile in
+// tensor memory, where eight warps put them as fp16 numbers, a thread its key's row (no shared memory, and K is read from
+// memory once).  The products of a tile with up to 64 rows (token, query head) put each key's scores into its lane, so a thread
+// turns the scores of one key into weights and adds them up in a register: no exchange at all.
 //
-// A unit is 384 keys of a K/V head, a step a tile of up to 64 rows (token, query head) of a unit.  One warp of a CTA finds the
-// units, looks up their pages and has TMA bring codes and tiles of q into two rings; twelve work on 32 keys each, without
-// waiting for one another.  The steps of all units are divided evenly over the CTAs, one per SM; sums of units that CTAs share
-// go to the workspace, and a second kernel adds them in their order.  What is added to a sum is added by the memory (no load,
-// one operation per sum and call, so the order of CTAs does not show).
+// A unit is 256 keys of a K/V head, two tiles; a step a tile of rows for a unit.  One warp finds the units, looks up their pages
+// and has TMA bring codes and rows of q into two rings, one issues the products, eight convert and eight add up weights.  The
+// steps of all units are divided evenly over the CTAs, one per SM; sums of units that CTAs share go to the workspace, and a
+// second kernel adds them in their order.  What is added to a sum is added by the memory: no load, one operation per sum and
+// call, so the order of CTAs does not show.
 #include <atomic>
 #include <climits>
 #include <type_traits>
@@ -23,22 +23,30 @@
 namespace wql {
 namespace {
 
-constexpr int kWarps = 12, kThreads = 32 * (kWarps + 1);
-constexpr int kUnit = 32 * kWarps;  // keys of a unit
-constexpr int kRows = 64;   // rows of a step, where a token has no more heads than that
-constexpr int kLead = 1;    // steps that stand for a unit's own cost
-constexpr int kKeySlots = 3, kRowSlots = 2;
+constexpr int kTile = 128, kUnit = 2 * kTile;  // keys of a tile in tensor memory, and of a unit
+constexpr int kRows = 64;                      // rows of a step at most
+// warps 0-7: weights, four for each tile; 8-15: conversion, likewise; 16: units and copies; 17: products; 18, 19: none
+constexpr int kThreads = 640, kConvWarp = 8, kLoadWarp = 16, kMmaWarp = 17;
+constexpr int kLead = 1;  // steps that stand for a unit's own cost
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Cfg {
   static constexpr int kCodes = kUnit * KvI4<D>::kRow;                // K's codes of a unit,
   static constexpr int kKeyBytes = kCodes + kUnit / kKvBlock * 128;   // with the parameters of K and V
+  static constexpr int kKeySlots = 6, kRowSlots = 4;
+  static constexpr int kRowBytes = kRows * D * 2, kBox = kRows * 128;  // a tile of q, its boxes of 64 channels
+  static constexpr int kSmem = kRowSlots * kRowBytes + kKeySlots * kKeyBytes + 1024;
+  static_assert(kSmem <= 224 * 1024, "shared memory");
+  // tensor memory: scores [tile][two in turn][kRows], then the keys [two units in turn][tile][D / 2]
+  static constexpr int kColK = 4 * kRows;
+  static_assert(kColK + 4 * (D / 2) <= 512, "tensor memory");
 };
 
 struct Args {
-  int T, Hq, Hkv, G, tokens, rows;  // tokens and rows of a step
-  FastDiv by_g;
+  int T, Hq, Hkv, G;
+  int tokens, heads, groups;  // of a step: tokens, heads of each; steps that a token's heads take
+  FastDiv by_heads;
   int pages, bpp;  // bpp: blocks of a page
   FastDiv by_bpp;
   const int* table;
@@ -48,7 +56,6 @@ struct Args {
   float scale_log2;
   const float* lse;
   float* weights;
-  int row_bytes;  // of a tile of q in shared memory
   // the workspace: the unit that each CTA began and left unfinished {sequence, K/V head, unit of it, 1}, whether it went on
   // with one (1) and ended it (2), and the sums of both [CTA][0: of the one found begun, 1: of the one begun][kUnit]
   int4* begun;
@@ -59,17 +66,17 @@ struct Args {
 
 // Steps of the units of a sequence: unit u takes the row tiles from skip(u) on, those before see none of its keys.
 struct Shape {
-  int units, tiles, per, c;  // per: row tiles that a unit's keys fill as tokens (tokens divides kUnit); c: those before row 0
+  int units, tiles, per;  // per: row tiles that a unit's keys fill as tokens (tokens divides kUnit)
+  long long c;            // row tiles that the tokens before row 0 fill
   __device__ __forceinline__ Shape(const Args& a, const KvChunk& k) {
     units = k.rows > 0 && k.len > 0 ? (k.len - 1) / kUnit + 1 : 0;
-    tiles = k.rows > 0 ? (k.rows - 1) / a.tokens + 1 : 0;
-    per = kUnit / a.tokens;
-    c = k.first >= 0 ? (int)(((unsigned)k.first + a.tokens - 1) / a.tokens) : -(-k.first / a.tokens);
+    tiles = k.rows > 0 ? ((k.rows - 1) / a.tokens + 1) * a.groups : 0;
+    per = kUnit / a.tokens * a.groups;
+    c = (k.first >= 0 ? ((unsigned)k.first + a.tokens - 1) / a.tokens : -(long long)(-k.first / a.tokens)) * a.groups;
   }
   __device__ __forceinline__ int skip(int u) const { return (int)max((long long)per * u - c, 0LL); }
-  __device__ __forceinline__ int cost(int u) const { return kLead + tiles - skip(u); }
   __device__ __forceinline__ long long before(int u) const {  // the cost of units 0 .. u - 1
-    const long long u0 = c < 0 ? 0 : min(c / per + 1, u);  // units that skip nothing
+    const long long u0 = c < 0 ? 0 : min(c / per + 1, (long long)u);  // units that skip nothing
     return (long long)u * (kLead + tiles) - (per * ((long long)u * (u - 1) - u0 * (u0 - 1)) / 2 - c * (u - u0));
   }
 };
@@ -82,12 +89,6 @@ struct Unit {
   int slot;
 };
 
-// D (16 x 8, fp32) = A (16 x 16, fp16) B (16 x 8, fp16)
-__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
 // Two fp32 at once: x, y = (x, y) * m + (a, b).
 __device__ __forceinline__ void fma2v(float& x, float& y, float m, float a, float b) {
   asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n mov.b64 r, {%3, %4};\n"
@@ -102,21 +103,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap tm_par, const Args a) {
   using L = KvI4<D>;
   using C = Cfg<D>;
-  constexpr int kWords = D / 32;  // of codes, per lane and key
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Unit s_unit[kKeySlots];
-  __shared__ __align__(8) float s_z[kRowSlots][128];  // -lse of the rows, times log2 e; minus infinity for none
-  __shared__ uint64_t kfull[kKeySlots], kempty[kKeySlots], qfull[kRowSlots], qempty[kRowSlots];
-  __shared__ long long s_sum[kWarps + 1], s_off;
+  __shared__ Unit s_unit[C::kKeySlots];
+  __shared__ __align__(16) float s_z[C::kRowSlots][kRows];  // -lse of the rows, times log2 e
+  __shared__ uint64_t kfull[C::kKeySlots], kempty[C::kKeySlots];  // codes landed; unit done (17 warps)
+  __shared__ uint64_t qfull[C::kRowSlots], qempty[C::kRowSlots];  // rows landed; products and weights done (1 + 8)
+  __shared__ uint64_t afull[2], aempty[2];                        // keys in tensor memory (8 warps); products of the unit done
+  __shared__ uint64_t sfull[2][2], sempty[2][2];                  // [tile][turn] scores complete; read (4 warps)
+  __shared__ uint64_t done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ long long s_sum[kThreads / 32], s_off;
   __shared__ int s_b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* q_tiles = smem;
-  uint8_t* keys = smem + kRowSlots * a.row_bytes;
+  uint8_t* keys = smem + C::kRowSlots * C::kRowBytes;
   if (tid == 0) {
-    for (int i = 0; i < kKeySlots; ++i) mbar_init(&kfull[i], 1), mbar_init(&kempty[i], kWarps);
-    for (int i = 0; i < kRowSlots; ++i) mbar_init(&qfull[i], 1), mbar_init(&qempty[i], kWarps);
+    for (int i = 0; i < C::kKeySlots; ++i) mbar_init(&kfull[i], 1), mbar_init(&kempty[i], 17);
+    for (int i = 0; i < C::kRowSlots; ++i) mbar_init(&qfull[i], 1), mbar_init(&qempty[i], 9);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&afull[i], 8), mbar_init(&aempty[i], 1);
+      for (int x = 0; x < 2; ++x) mbar_init(&sfull[x][i], 1), mbar_init(&sempty[x][i], 4);
+    }
+    mbar_init(&done, 1);
     fence_mbarrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
   }
   grid_dependency_wait();
   grid_dependents_launch();
@@ -138,9 +152,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane >= d) incl += o;
     }
     if (lane == 31) s_sum[warp] = incl;
+    tc_fence_before_sync();
     __syncthreads();
+    tc_fence_after_sync();
     long long total = 0;
-    for (int w = 0; w <= kWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) incl += s_sum[w];
       total += s_sum[w];
     }
@@ -159,7 +175,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
 
-  if (warp == kWarps) {
+  const uint32_t tmem = tmem_slot;
+
+  // What all warps do with units: wait for the next one, release the last.
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t phase) {
+    if (ok && !mbar_wait_warp(bar, phase & 1)) {
+      if (lane == 0) report_error(a.err, kErrTimeoutFull);
+      ok = false;
+    }
+    return ok;
+  };
+  auto rows_of = [&](const Unit& t, int tile) {
+    return min(t.n - tile / a.groups * a.tokens, a.tokens) * min(a.heads, a.G - tile % a.groups * a.heads);
+  };
+
+  if (warp == kLoadWarp) {
     // ---------------- units, codes, rows ----------------
     if (lane == 0) tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_codes), tma_prefetch_desc(&tm_par);
     constexpr int kBlocks = kUnit / kKvBlock;
@@ -169,14 +200,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int4 begun = make_int4(0, 0, 0, 0);
     int went_on = 0;
     uint32_t n = 0, m = 0;  // units, tiles of rows so far
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t phase) {
-      if (ok && !mbar_wait_warp(bar, phase & 1)) {
-        if (lane == 0) report_error(a.err, kErrTimeoutEmpty);
-        ok = false;
-      }
-      return ok;
-    };
     if (w0 < w1) {
       int b = s_b, kvh, u, s;
       KvChunk k = kv_chunk(a.cu, a.kv_lens, b, a.T, a.cap, nullptr);
@@ -201,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int skip = sh.skip(u), cost = kLead + sh.tiles - skip, take = (int)min((long long)(cost - s), left);
         const int r0 = max(s - kLead, 0), r1 = s + take - kLead;  // row tiles, from skip on
         if (r1 > r0) {
-          const uint32_t ks = n % kKeySlots;
+          const uint32_t ks = n % C::kKeySlots;
           const int gb = u * kBlocks + lane * each, blocks = (k.len - 1) / kKvBlock + 1;
           bool there = lane * each < kBlocks && gb < blocks;
           const int pg = (int)quot((uint32_t)gb, a.by_bpp), page = there ? a.table[(long long)b * a.width + pg] : 0;
@@ -209,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             report_error(a.err, kErrBadIndex);
             there = false;
           }
-          if (!wait(&kempty[ks], n / kKeySlots ^ 1)) break;
+          if (!wait(&kempty[ks], n / C::kKeySlots ^ 1)) break;
           const uint32_t all = __popc(__ballot_sync(0xffffffffu, there)) * bytes;
           if (lane == 0) {
             Unit& t = s_unit[ks];
@@ -234,26 +257,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int tile = skip + r0; tile < skip + r1; ++tile) {
             if (in_b == b && in_h == kvh && in_tile == tile) continue;
             in_b = b, in_h = kvh, in_tile = tile;
-            const uint32_t qs = m % kRowSlots;
-            const int t0 = tile * a.tokens;
+            const uint32_t qs = m % C::kRowSlots;
+            const int t0 = tile / a.groups * a.tokens, h0 = kvh * a.G + tile % a.groups * a.heads;
             // the rows' lse, in registers before the slot is waited for
-            float z[4];
+            float z[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 32 * i + lane, tok = (int)quot((uint32_t)row, a.by_g);
-              z[i] = tok < a.tokens && t0 + tok < k.rows
-                         ? a.lse[(long long)(k.start + t0 + tok) * a.Hq + kvh * a.G + (row - tok * a.G)] * -kLog2e
-                         : -INFINITY;  // of no row: no weights
+            for (int i = 0; i < 2; ++i) {
+              const int row = 32 * i + lane, tok = (int)quot((uint32_t)row, a.by_heads), h = h0 + row - tok * a.heads;
+              z[i] = tok < a.tokens && t0 + tok < k.rows && h < a.Hq ? a.lse[(long long)(k.start + t0 + tok) * a.Hq + h] * -kLog2e
+                                                                     : 0.f;
             }
-            if (!wait(&qempty[qs], m / kRowSlots ^ 1)) break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s_z[qs][32 * i + lane] = z[i];
+            if (!wait(&qempty[qs], m / C::kRowSlots ^ 1)) break;
+            s_z[qs][lane] = z[0], s_z[qs][32 + lane] = z[1];
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive_expect_tx(&qfull[qs], a.rows * D * 2);
+              mbar_arrive_expect_tx(&qfull[qs], a.tokens * a.heads * D * 2);
               for (int i = 0; i < D / 64; ++i)
-                tma_load_3d(q_tiles + qs * a.row_bytes + i * (a.row_bytes / (D / 64)), &tm_q, &qfull[qs], 64 * i, kvh * a.G,
-                            k.start + t0);
+                tma_load_3d(q_tiles + qs * C::kRowBytes + i * C::kBox, &tm_q, &qfull[qs], 64 * i, h0, k.start + t0);
             }
             ++m;
           }
@@ -272,149 +292,176 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (lane == 0) a.begun[blockIdx.x] = begun, a.went_on[blockIdx.x] = went_on;
-    if (wait(&kempty[n % kKeySlots], n / kKeySlots ^ 1) && lane == 0) {
-      s_unit[n % kKeySlots].tile1 = s_unit[n % kKeySlots].tile0 = 0;
-      mbar_arrive(&kfull[n % kKeySlots]);
+    if (wait(&kempty[n % C::kKeySlots], n / C::kKeySlots ^ 1) && lane == 0) {
+      s_unit[n % C::kKeySlots].tile1 = s_unit[n % C::kKeySlots].tile0 = 0;
+      mbar_arrive(&kfull[n % C::kKeySlots]);
     }
     // copies that may still be in flight land before the kernel ends; what was in the slot of the end has been read
     bool landed = true;
-    for (int i = 0; i < kKeySlots - 1 && n > 0 && landed; ++i) --n, landed = mbar_wait_warp(&kfull[n % kKeySlots], n / kKeySlots & 1);
-    for (int i = 0; i < kRowSlots && m > 0 && landed; ++i) --m, landed = mbar_wait_warp(&qfull[m % kRowSlots], m / kRowSlots & 1);
+    for (int i = 0; i < C::kKeySlots - 1 && n > 0 && landed; ++i) {
+      --n;
+      landed = mbar_wait_warp(&kfull[n % C::kKeySlots], n / C::kKeySlots & 1);
+    }
+    for (int i = 0; i < C::kRowSlots && m > 0 && landed; ++i) {
+      --m;
+      landed = mbar_wait_warp(&qfull[m % C::kRowSlots], m / C::kRowSlots & 1);
+    }
     if (!landed && lane == 0) report_error(a.err, kErrTimeoutDrain);
-    return;
-  }
-
-  // ---------------- 32 keys of each unit ----------------
-  const int g = lane >> 2, c = lane & 3;
-  const bool swap = c >= 2;  // lanes 2 and 3 take their words in another order, so that the loads of q meet no bank twice
-  const int half_q = a.row_bytes / (D / 64);  // between the boxes of 64 channels
-  // q in the swizzled tile: chunk 4 c + w of 16 bytes, D = 128; 2 c + w, D = 64
-  const int box = D == 128 ? (c >> 1) * half_q : 0, chunk0 = D == 128 ? 4 * (c & 1) : 2 * c;
-  uint32_t n = 0, m = 0;
-  bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t phase) {
-    if (ok && !mbar_wait_warp(bar, phase & 1)) {
-      if (lane == 0) report_error(a.err, kErrTimeoutFull);
-      ok = false;
-    }
-    return ok;
-  };
-  int in_b = -1, in_h = -1, in_tile = -1;
-  for (; wait(&kfull[n % kKeySlots], n / kKeySlots); ++n) {
-    const uint32_t ks = n % kKeySlots;
-    const Unit t = s_unit[ks];
-    if (t.tile0 == t.tile1) break;
-    const int key0 = t.u * kUnit + 32 * warp, in = 16 * (c >> 1) + 8 * (c & 1) + g;  // this lane's key at the end
-    // fp16 fragments: step 2 w has the pairs (0, 1) and (2, 3) of word w, step 2 w + 1 (4, 5) and (6, 7)
-    uint32_t A[2][2 * kWords][4];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 32 * warp + 16 * mt + 8 * e + g;
-        const uint32_t src = smem_u32(keys + ks * C::kKeyBytes) + row * L::kRow;
-        uint32_t w[kWords];
-        if constexpr (D == 128) {
-          const uint4 v = lds_u128(src + 16 * c);
-          w[0] = swap ? v.z : v.x, w[1] = swap ? v.w : v.y, w[2] = swap ? v.x : v.z, w[3] = swap ? v.y : v.w;
-        } else {
-          const uint2 v = lds_u64(src + 8 * c);
-          w[0] = v.x, w[1] = v.y;
+  } else if (warp == kMmaWarp) {
+    // ---------------- products ----------------
+    const bool leader = elect_one();
+    const uint32_t q_lo = (1u << 16) + (smem_u32(q_tiles) >> 4);
+    uint32_t m = 0, steps = 0;
+    int in_b = -1, in_h = -1, in_tile = -1;
+    for (uint32_t n = 0; wait(&kfull[n % C::kKeySlots], n / C::kKeySlots); ++n) {
+      const Unit t = s_unit[n % C::kKeySlots];
+      __syncwarp();
+      if (leader) mbar_arrive(&kempty[n % C::kKeySlots]);
+      if (t.tile0 == t.tile1 || !wait(&afull[n & 1], n >> 1)) break;
+      tc_fence_after_sync();
+      for (int tile = t.tile0; tile < t.tile1; ++tile, ++steps) {
+        if (in_b != t.b || in_h != t.kvh || in_tile != tile) {  // as the copies go: another tile of rows
+          in_b = t.b, in_h = t.kvh, in_tile = tile;
+          if (m > 0 && leader) umma_commit(&qempty[(m - 1) % C::kRowSlots]);
+          if (!wait(&qfull[m % C::kRowSlots], m / C::kRowSlots)) break;
+          ++m;
         }
-        uint32_t p = lds_u32(smem_u32(keys + ks * C::kKeyBytes) + C::kCodes + row / kKvBlock * 128 + row % kKvBlock * 4);
-        if (t.u * kUnit + row >= t.len) p = 0u;
-        if (!kv_finite(p)) p = 0x7fff7fffu;
-        const uint32_t s2 = prmt(p, 0, 0x1010), lo2 = prmt(p, 0, 0x3232);
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          uint32_t h[4];
-          kv_values8(w[i], s2, lo2, h);
-          if (kv_overflows(p)) {  // rare; of a NaN: no
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = kv_clamp2(h[j]);
-          }
-          A[mt][2 * i][e] = prmt(h[0], h[1], 0x5410), A[mt][2 * i][2 + e] = prmt(h[2], h[3], 0x5410);
-          A[mt][2 * i + 1][e] = prmt(h[0], h[1], 0x7632), A[mt][2 * i + 1][2 + e] = prmt(h[2], h[3], 0x7632);
-        }
-      }
-    fence_proxy_async_smem();  // these reads come before the copies that follow them into the slot
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&kempty[ks]);
-    float sum[2][2][2] = {};  // [keys 16 mt][+ 8 e] of the two rows
-    for (int tile = t.tile0; tile < t.tile1; ++tile) {
-      if (in_b != t.b || in_h != t.kvh || in_tile != tile) {  // as above: another tile
-        in_b = t.b, in_h = t.kvh, in_tile = tile;
-        if (m > 0) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&qempty[(m - 1) % kRowSlots]);
-        }
-        if (!wait(&qfull[m % kRowSlots], m / kRowSlots)) break;
-        ++m;
-      }
-      const uint32_t qs = (m - 1) % kRowSlots, src = smem_u32(q_tiles + qs * a.row_bytes) + box;
-      const int t0 = tile * a.tokens, rows = min(t.n - t0, a.tokens) * a.G;
-      auto eights = [&](auto careful) {  // some row does not see all of the warp's keys, or is not one of this sequence
-        constexpr bool kCareful = decltype(careful)::value;
+        const uint32_t bd = q_lo + (m - 1) % C::kRowSlots * (C::kRowBytes >> 4), turn = steps & 1;
+        const uint32_t idesc = umma_idesc_f16(kTile, (rows_of(t, tile) + 15) & ~15, 0, 0);
 #pragma unroll 1
-        for (int nt = 0; nt < (rows + 7) / 8; ++nt) {
-          float d[2][4];
-          const int row = 8 * nt + g;
+        for (int x = 0; x < 2; ++x) {
+          if (!wait(&sempty[x][turn], (steps >> 1) ^ 1)) break;
+          tc_fence_after_sync();
+          if (leader) {
+            const uint32_t d = tmem + (2 * x + turn) * kRows, ak = tmem + C::kColK + (2 * (n & 1) + x) * (D / 2);
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) {
-            const uint32_t ch = D == 128 ? chunk0 + (w ^ (swap ? 2 : 0)) : chunk0 + w;
-            uint4 bq = make_uint4(0u, 0u, 0u, 0u);
-            if (!kCareful || row < rows) bq = lds_u128(src + row * 128 + ((ch ^ (row & 7)) << 4));
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              if (w == 0)
-                mma_zero(d[mt], A[mt][0], bq.x, bq.y);
-              else
-                mma_f16_16816(d[mt], A[mt][2 * w], bq.x, bq.y);
-              mma_f16_16816(d[mt], A[mt][2 * w + 1], bq.z, bq.w);
-            }
+            for (int s = 0; s < D / 16; ++s)
+              mma_ts(d, ak + 8 * s, bd + (((s >> 2) * C::kBox + (s & 3) * 32) >> 4), idesc, s > 0);
+            umma_commit(&sfull[x][turn]);
           }
-          const float2 z = *reinterpret_cast<const float2*>(&s_z[qs][8 * nt + 2 * c]);
-          const int r = 8 * nt + 2 * c;
-          int tok0 = 0, tok1 = 0;
-          if constexpr (kCareful) tok0 = (int)quot((uint32_t)r, a.by_g), tok1 = (int)quot((uint32_t)r + 1, a.by_g);
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float p0 = d[mt][2 * e], p1 = d[mt][2 * e + 1];
-              fma2v(p0, p1, a.scale_log2, z.x, z.y);
-              p0 = ex2(p0), p1 = ex2(p1);
-              if constexpr (kCareful) {
-                const int last = t.first + t0 - (key0 + 16 * mt + 8 * e + g);
-                if (r >= rows || last + tok0 < 0) p0 = 0.f;
-                if (r + 1 >= rows || last + tok1 < 0) p1 = 0.f;
-              }
-              add2(sum[mt][e][0], sum[mt][e][1], p0, p1);
-            }
         }
-      };
-      if (key0 + 31 > t.first + t0 || rows % 8 != 0)
-        eights(std::true_type());
-      else
-        eights(std::false_type());
-    }
-    // over the four lanes that share a key; lane (g, c) then has key 16 (c >> 1) + 8 (c & 1) + g
-    float s[2][2];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s[mt][e] = sum[mt][e][0] + sum[mt][e][1];
-        s[mt][e] += __shfl_xor_sync(0xffffffffu, s[mt][e], 1);
-        s[mt][e] += __shfl_xor_sync(0xffffffffu, s[mt][e], 2);
       }
-    const float mine = c & 2 ? (c & 1 ? s[1][1] : s[1][0]) : (c & 1 ? s[0][1] : s[0][0]);
-    if (t.slot >= 0)
-      a.part[((long long)blockIdx.x * 2 + t.slot) * kUnit + 32 * warp + in] = mine;
-    else if (key0 + in < t.len)
-      atomicAdd(a.weights + ((long long)t.b * a.Hkv + t.kvh) * a.cap + key0 + in, mine);
+      if (leader) umma_commit(&aempty[n & 1]);
+    }
+    if (ok) {
+      if (leader) umma_commit(&done);
+      wait(&done, 0);
+    }
+  } else if (warp >= kConvWarp && warp < kLoadWarp) {
+    // ---------------- codes to fp16: a thread takes one key's row, a lane of tensor memory ----------------
+    const int x = (warp - kConvWarp) >> 2, row = (tid - 32 * kConvWarp) & (kUnit - 1);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    for (uint32_t n = 0; wait(&kfull[n % C::kKeySlots], n / C::kKeySlots); ++n) {
+      const uint32_t ks = n % C::kKeySlots;
+      const bool end = s_unit[ks].tile0 == s_unit[ks].tile1, inside = row < s_unit[ks].len - s_unit[ks].u * kUnit;
+      if (end || !wait(&aempty[n & 1], (n >> 1) ^ 1)) break;
+      tc_fence_after_sync();
+      const uint32_t raw = smem_u32(keys + ks * C::kKeyBytes);
+      uint32_t p = lds_u32(raw + C::kCodes + row / kKvBlock * 128 + row % kKvBlock * 4);
+      if (!inside) p = 0u;
+      if (!kv_finite(p)) p = 0x7fff7fffu;
+      const uint32_t s2 = prmt(p, 0, 0x1010), lo2 = prmt(p, 0, 0x3232);
+      const bool over = kv_overflows(p);  // rare; of a NaN: no
+      const uint32_t to = tmem + C::kColK + (2 * (n & 1) + x) * (D / 2) + lanes;
+#pragma unroll 1
+      for (int i = 0; i < L::kRow / 16; ++i) {
+        // heads of 128: two keys' codes to a line of 128 bytes, swizzled, so that lanes that read together meet no bank twice
+        const uint4 v = lds_u128(D == 128 ? raw + (row >> 1) * 128 + ((((row & 1) * 4 + i) ^ ((row >> 1) & 7)) << 4)
+                                          : raw + row * L::kRow + 16 * i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t h[4];
+          kv_values8(w[e], s2, lo2, h);
+          o[4 * e] = prmt(h[0], h[1], 0x5410), o[4 * e + 1] = prmt(h[2], h[3], 0x5410);
+          o[4 * e + 2] = prmt(h[0], h[1], 0x7632), o[4 * e + 3] = prmt(h[2], h[3], 0x7632);
+        }
+        if (over) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = kv_clamp2(o[e]);
+        }
+        __syncwarp();
+        tmem_st_32x32b_x16(to + 16 * i, o);
+      }
+      fence_proxy_async_smem();  // these reads come before the copies that follow them into the slot
+      tmem_st_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&afull[n & 1]), mbar_arrive(&kempty[ks]);
+    }
+  } else if (warp < kConvWarp) {
+    // ---------------- weights: a thread takes one key ----------------
+    const int x = warp >> 2, row = tid & (kUnit - 1);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    uint32_t m = 0, steps = 0;
+    int in_b = -1, in_h = -1, in_tile = -1;
+    for (uint32_t n = 0; wait(&kfull[n % C::kKeySlots], n / C::kKeySlots); ++n) {
+      const Unit t = s_unit[n % C::kKeySlots];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&kempty[n % C::kKeySlots]);
+      if (t.tile0 == t.tile1) break;
+      const int key0 = t.u * kUnit;
+      float sum[4] = {};
+      for (int tile = t.tile0; tile < t.tile1; ++tile, ++steps) {
+        if (in_b != t.b || in_h != t.kvh || in_tile != tile) {
+          in_b = t.b, in_h = t.kvh, in_tile = tile;
+          if (m > 0 && lane == 0) mbar_arrive(&qempty[(m - 1) % C::kRowSlots]);
+          if (!wait(&qfull[m % C::kRowSlots], m / C::kRowSlots)) break;  // for s_z
+          ++m;
+        }
+        const float* z = s_z[(m - 1) % C::kRowSlots];
+        const uint32_t turn = steps & 1, from = tmem + (2 * x + turn) * kRows + lanes;
+        const int rows = rows_of(t, tile), first = t.first + tile / a.groups * a.tokens;
+        if (!wait(&sfull[x][turn], steps >> 1)) break;
+        tc_fence_after_sync();
+        auto add = [&](const uint32_t (&v)[32], int col, int lo, int hi, auto careful) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            if (decltype(careful)::value && e >= hi) break;
+            const float4 z4 = *reinterpret_cast<const float4*>(z + col + e);
+            float p0 = __uint_as_float(v[e]), p1 = __uint_as_float(v[e + 1]), p2 = __uint_as_float(v[e + 2]),
+                  p3 = __uint_as_float(v[e + 3]);
+            fma2v(p0, p1, a.scale_log2, z4.x, z4.y);
+            fma2v(p2, p3, a.scale_log2, z4.z, z4.w);
+            p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
+            if constexpr (decltype(careful)::value) {
+              p0 = e >= lo && e < hi ? p0 : 0.f, p1 = e + 1 >= lo && e + 1 < hi ? p1 : 0.f;
+              p2 = e + 2 >= lo && e + 2 < hi ? p2 : 0.f, p3 = e + 3 >= lo && e + 3 < hi ? p3 : 0.f;
+            }
+            add2(sum[0], sum[1], p0, p1);
+            add2(sum[2], sum[3], p2, p3);
+          }
+        };
+        uint32_t v0[32], v1[32];
+        tmem_ld_32x32b_x32(from, v0);
+        tmem_ld_wait();
+        if (rows > 32) tmem_ld_32x32b_x32(from + 32, v1);
+        // columns [lo, rows) are rows that see this key
+        const int lo = min(max(key0 - first + row, 0), kRows) * a.heads;
+        if (key0 - first + (row | 31) > 0 || rows % 32 != 0) {
+          add(v0, 0, lo, rows, std::true_type());
+          tmem_ld_wait();
+          if (rows > 32) add(v1, 32, lo - 32, rows - 32, std::true_type());
+        } else {
+          add(v0, 0, 0, 32, std::false_type());
+          tmem_ld_wait();
+          if (rows > 32) add(v1, 32, 0, 32, std::false_type());
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[x][turn]);
+      }
+      const float mine = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (t.slot >= 0)
+        a.part[((long long)blockIdx.x * 2 + t.slot) * kUnit + row] = mine;
+      else if (row < t.len - key0)
+        atomicAdd(a.weights + ((long long)t.b * a.Hkv + t.kvh) * a.cap + key0 + row, mine);
+    }
   }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 // Adds the sums of the unit that CTA blockIdx.x began and others went on with.
@@ -424,27 +471,25 @@ __global__ void __launch_bounds__(kUnit) kv_weights_join_kernel(const Args a, in
   const int c = blockIdx.x;
   const int4 it = a.begun[c];
   if (it.w == 0) return;
-  const int key = it.z * kUnit + threadIdx.x;
   float sum = a.part[((long long)c * 2 + 1) * kUnit + threadIdx.x];
   for (int i = c + 1; i < ctas; ++i) {
     const int v = a.went_on[i];
     sum += a.part[(long long)i * 2 * kUnit + threadIdx.x];
     if (v != 1) break;
   }
-  if (key < min(max(a.kv_lens[it.x], 0), a.cap)) a.weights[((long long)it.x * a.Hkv + it.y) * a.cap + key] += sum;
+  if ((int)threadIdx.x < min(max(a.kv_lens[it.x], 0), a.cap) - it.z * kUnit)
+    a.weights[((long long)it.x * a.Hkv + it.y) * a.cap + it.z * kUnit + threadIdx.x] += sum;
 }
 
 template <int D>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& codes, const CUtensorMap& par, const Args& a, int ctas,
                    cudaStream_t s) {
-  constexpr int kMost = 2 * (D / 64) * 128 * 128 + kKeySlots * Cfg<D>::kKeyBytes + 1024;  // 128 rows
-  static_assert(kMost <= 220 * 1024, "shared memory");
   static std::atomic<bool> ready[64];  // per device; racing first calls set the same attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(kv_weights_i4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    e = cudaFuncSetAttribute(kv_weights_i4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
   }
@@ -454,7 +499,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& codes, const CUtenso
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kRowSlots * a.row_bytes + kKeySlots * Cfg<D>::kKeyBytes + 1024;
+  cfg.dynamicSmemBytes = Cfg<D>::kSmem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -474,23 +519,25 @@ cudaError_t launch_kv_weights_i4(const uint16_t* q, long long q_stride, int T, i
                                  float scale, const float* lse, float* weights, void* workspace, unsigned* dev_err,
                                  cudaStream_t s, std::string* err) {
   const int ctas = num_sms(), G = Hq / Hkv;
-  int tokens = 1;  // of a step: a power of two, which divides kUnit
-  while (2 * tokens * G <= kRows) tokens *= 2;
-  const int rows = tokens * G, tile_rows = (rows + 7) / 8 * 8;
+  // a step: as many tokens as fit, a power of two, which divides kUnit; where a token has more heads, they take two steps
+  const int heads = G < kRows ? G : kRows, groups = (G + kRows - 1) / kRows;
+  int tokens = 1;
+  while (2 * tokens * heads <= kRows) tokens *= 2;
   const uint64_t piece = 128, block = kKvBlock * (D + 8), blocks = (uint64_t)pages * Hkv * (ps / kKvBlock);
   const uint32_t together = ps % 64 == 0 ? 4 : 1;
   CUtensorMap tq, tc, tp;
-  if (!make_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, D, Hq, T, (uint64_t)D * 2, (uint64_t)q_stride * 2, 64, G, tokens,
+  if (!make_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, D, Hq, T, (uint64_t)D * 2, (uint64_t)q_stride * 2, 64, heads, tokens,
                     CU_TENSOR_MAP_SWIZZLE_128B, err) ||
       !make_tmap_3d(&tc, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache, piece, block / piece, blocks, piece, block, piece,
-                    kKvBlock * D / 2 / piece, together, CU_TENSOR_MAP_SWIZZLE_NONE, err) ||
+                    kKvBlock * D / 2 / piece, together, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    err) ||
       !make_tmap_3d(&tp, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache, piece, block / piece, blocks, piece, block, piece, 1, together,
                     CU_TENSOR_MAP_SWIZZLE_NONE, err))
     return cudaErrorInvalidValue;
   float* part = static_cast<float*>(workspace);
   int4* begun = reinterpret_cast<int4*>(part + (size_t)ctas * 2 * kUnit);
-  Args a{T, Hq, Hkv, G, tokens, rows, fast_div(G), (int)pages, ps / kKvBlock, fast_div(ps / kKvBlock), table, width,
-         width * ps, cu, kv_lens, B, scale * kLog2e, lse, weights, tile_rows * 128 * (D / 64), begun,
+  Args a{T, Hq, Hkv, G, tokens, heads, groups, fast_div(heads), (int)pages, ps / kKvBlock, fast_div(ps / kKvBlock), table, width,
+         width * ps, cu, kv_lens, B, scale * kLog2e, lse, weights, begun,
          reinterpret_cast<int*>(begun + ctas), part, dev_err};
   return D == 128 ? launch<128>(tq, tc, tp, a, ctas, s) : launch<64>(tq, tc, tp, a, ctas, s);
 }
