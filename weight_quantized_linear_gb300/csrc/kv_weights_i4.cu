@@ -45,7 +45,7 @@ struct Cfg {
 
 struct Args {
   int T, Hq, Hkv, G;
-  int tokens, heads, groups;  // of a step: tokens, heads of each; steps that a token's heads take
+  int tokens, heads, two;  // of a step: tokens, heads of each; 1: the heads of a token take two steps, 0: one
   FastDiv by_heads;
   int pages, bpp;  // bpp: blocks of a page
   FastDiv by_bpp;
@@ -70,9 +70,9 @@ struct Shape {
   long long c;            // row tiles that the tokens before row 0 fill
   __device__ __forceinline__ Shape(const Args& a, const KvChunk& k) {
     units = k.rows > 0 && k.len > 0 ? (k.len - 1) / kUnit + 1 : 0;
-    tiles = k.rows > 0 ? ((k.rows - 1) / a.tokens + 1) * a.groups : 0;
-    per = kUnit / a.tokens * a.groups;
-    c = (k.first >= 0 ? ((unsigned)k.first + a.tokens - 1) / a.tokens : -(long long)(-k.first / a.tokens)) * a.groups;
+    tiles = k.rows > 0 ? ((k.rows - 1) / a.tokens + 1) << a.two : 0;
+    per = kUnit / a.tokens << a.two;
+    c = (k.first >= 0 ? ((unsigned)k.first + a.tokens - 1) / a.tokens : -(long long)(-k.first / a.tokens)) * (1 + a.two);
   }
   __device__ __forceinline__ int skip(int u) const { return (int)max((long long)per * u - c, 0LL); }
   __device__ __forceinline__ long long before(int u) const {  // the cost of units 0 .. u - 1
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return ok;
   };
   auto rows_of = [&](const Unit& t, int tile) {
-    return min(t.n - tile / a.groups * a.tokens, a.tokens) * min(a.heads, a.G - tile % a.groups * a.heads);
+    return min(t.n - (tile >> a.two) * a.tokens, a.tokens) * min(a.heads, a.G - (tile & a.two) * a.heads);
   };
 
   if (warp == kLoadWarp) {
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (in_b == b && in_h == kvh && in_tile == tile) continue;
             in_b = b, in_h = kvh, in_tile = tile;
             const uint32_t qs = m % C::kRowSlots;
-            const int t0 = tile / a.groups * a.tokens, h0 = kvh * a.G + tile % a.groups * a.heads;
+            const int t0 = (tile >> a.two) * a.tokens, h0 = kvh * a.G + (tile & a.two) * a.heads;
             // the rows' lse, in registers before the slot is waited for
             float z[2];
 #pragma unroll
@@ -361,29 +361,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!inside) p = 0u;
       if (!kv_finite(p)) p = 0x7fff7fffu;
       const uint32_t s2 = prmt(p, 0, 0x1010), lo2 = prmt(p, 0, 0x3232);
-      const bool over = kv_overflows(p);  // rare; of a NaN: no
       const uint32_t to = tmem + C::kColK + (2 * (n & 1) + x) * (D / 2) + lanes;
+      auto convert = [&](auto clamp) {
 #pragma unroll 1
-      for (int i = 0; i < L::kRow / 16; ++i) {
-        // heads of 128: two keys' codes to a line of 128 bytes, swizzled, so that lanes that read together meet no bank twice
-        const uint4 v = lds_u128(D == 128 ? raw + (row >> 1) * 128 + ((((row & 1) * 4 + i) ^ ((row >> 1) & 7)) << 4)
-                                          : raw + row * L::kRow + 16 * i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[16];
+        for (int i = 0; i < L::kRow / 16; ++i) {
+          // heads of 128: two keys' codes to a line of 128 bytes, swizzled, so that lanes that read together meet no bank twice
+          const uint4 v = lds_u128(D == 128 ? raw + (row >> 1) * 128 + ((((row & 1) * 4 + i) ^ ((row >> 1) & 7)) << 4)
+                                            : raw + row * L::kRow + 16 * i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t h[4];
-          kv_values8(w[e], s2, lo2, h);
-          o[4 * e] = prmt(h[0], h[1], 0x5410), o[4 * e + 1] = prmt(h[2], h[3], 0x5410);
-          o[4 * e + 2] = prmt(h[0], h[1], 0x7632), o[4 * e + 3] = prmt(h[2], h[3], 0x7632);
-        }
-        if (over) {
+          for (int e = 0; e < 4; ++e) {
+            uint32_t h[4];
+            kv_values8(w[e], s2, lo2, h);
+            o[4 * e] = prmt(h[0], h[1], 0x5410), o[4 * e + 1] = prmt(h[2], h[3], 0x5410);
+            o[4 * e + 2] = prmt(h[0], h[1], 0x7632), o[4 * e + 3] = prmt(h[2], h[3], 0x7632);
+          }
+          if constexpr (decltype(clamp)::value) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = kv_clamp2(o[e]);
+            for (int e = 0; e < 16; ++e) o[e] = kv_clamp2(o[e]);
+          }
+          tmem_st_32x32b_x16(to + 16 * i, o);
         }
-        __syncwarp();
-        tmem_st_32x32b_x16(to + 16 * i, o);
-      }
+      };
+      if (__any_sync(0xffffffffu, kv_overflows(p)))  // rare; of a NaN: no
+        convert(std::true_type());
+      else
+        convert(std::false_type());
       fence_proxy_async_smem();  // these reads come before the copies that follow them into the slot
       tmem_st_wait();
       tc_fence_before_sync();
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float* z = s_z[(m - 1) % C::kRowSlots];
         const uint32_t turn = steps & 1, from = tmem + (2 * x + turn) * kRows + lanes;
-        const int rows = rows_of(t, tile), first = t.first + tile / a.groups * a.tokens;
+        const int rows = rows_of(t, tile), first = t.first + (tile >> a.two) * a.tokens;
         if (!wait(&sfull[x][turn], steps >> 1)) break;
         tc_fence_after_sync();
         auto add = [&](const uint32_t (&v)[32], int col, int lo, int hi, auto careful) {
@@ -520,7 +524,7 @@ cudaError_t launch_kv_weights_i4(const uint16_t* q, long long q_stride, int T, i
                                  cudaStream_t s, std::string* err) {
   const int ctas = num_sms(), G = Hq / Hkv;
   // a step: as many tokens as fit, a power of two, which divides kUnit; where a token has more heads, they take two steps
-  const int heads = G < kRows ? G : kRows, groups = (G + kRows - 1) / kRows;
+  const int heads = G < kRows ? G : kRows;
   int tokens = 1;
   while (2 * tokens * heads <= kRows) tokens *= 2;
   const uint64_t piece = 128, block = kKvBlock * (D + 8), blocks = (uint64_t)pages * Hkv * (ps / kKvBlock);
@@ -536,7 +540,7 @@ cudaError_t launch_kv_weights_i4(const uint16_t* q, long long q_stride, int T, i
     return cudaErrorInvalidValue;
   float* part = static_cast<float*>(workspace);
   int4* begun = reinterpret_cast<int4*>(part + (size_t)ctas * 2 * kUnit);
-  Args a{T, Hq, Hkv, G, tokens, heads, groups, fast_div(heads), (int)pages, ps / kKvBlock, fast_div(ps / kKvBlock), table, width,
+  Args a{T, Hq, Hkv, G, tokens, heads, G > kRows, fast_div(heads), (int)pages, ps / kKvBlock, fast_div(ps / kKvBlock), table, width,
          width * ps, cu, kv_lens, B, scale * kLog2e, lse, weights, begun,
          reinterpret_cast<int*>(begun + ctas), part, dev_err};
   return D == 128 ? launch<128>(tq, tc, tp, a, ctas, s) : launch<64>(tq, tc, tp, a, ctas, s);
