@@ -519,8 +519,8 @@ wql_status wql_kv_weights_i4(const uint16_t* q, int64_t q_stride, int T, int Hq,
  * twice in new_table: what such a page then holds is unspecified.  Pages that sequences share may be read by all of them.
  * The old pages stay as they are.  A length beyond table_width * page_size is cut there and recorded; rows whose old or
  * new page number is out of range are not moved and recorded.  Nothing may overlap but the cache with itself.
- * Requires B <= 4096, 1 <= budget <= new_width * page_size, recent >= 0, B * H * ceil(budget / 16) < 2^31
- * (WQL_EUNSUPPORTED above).
+ * Requires B <= 4096, 1 <= budget <= new_width * page_size, recent >= 0, B * H * max(8, ceil(budget / 16)) <
+ * 2^31 (WQL_EUNSUPPORTED above).
  * ---------------------------------------------------------------------------------------- */
 wql_status wql_kv_evict_i4(const float* weights, uint8_t* cache, int64_t pages, int page_size, int H, int D,
                            const int32_t* block_table, int table_width, const int32_t* kv_lens, int B,

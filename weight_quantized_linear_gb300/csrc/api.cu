@@ -718,8 +718,8 @@ wql_status wql_kv_evict_i4(const float* weights, uint8_t* cache, int64_t pages, 
               "new_width * page_size must be between 16 and 2^31 - 1");
   WQL_REQUIRE(budget >= 1 && budget <= (int64_t)new_width * page_size, "budget must be between 1 and new_width * page_size");
   WQL_REQUIRE(recent >= 0, "recent must be >= 0");
-  if ((int64_t)B * H > INT_MAX / (((int64_t)budget + 15) / 16))
-    return fail(WQL_EUNSUPPORTED, "B * H * ceil(budget / 16) must be below 2^31");
+  if ((int64_t)B * H > INT_MAX / (((int64_t)budget + 15) / 16) || (int64_t)B * H > INT_MAX / 8)
+    return fail(WQL_EUNSUPPORTED, "B * H * max(8, ceil(budget / 16)) must be below 2^31");
   if (B == 0) {
     g_last_error.clear();
     return WQL_OK;
