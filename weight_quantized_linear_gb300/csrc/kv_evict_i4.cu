@@ -5,9 +5,9 @@
 // ones go, in their order, into the pages of row b of new_table; their numbers and weights go to kept and new_weights.
 //
 // One kernel, a CTA or a cluster of CTAs for each sequence and head.  A weight is a 32-bit number that orders as the weights
-// do; a thread keeps its run of consecutive ones in registers, so they are read once, whatever follows.  The smallest kept
-// number is found digit by digit: each digit is counted in shared memory (a run of equal ones, as zeros come, at once) and the
-// CTAs add up their counts through distributed shared memory.  Then a scan over threads and CTAs gives every kept token its
+// do; a thread keeps some in registers, so they are read once, whatever follows.  The smallest kept
+// number is found digit by digit: each digit is counted in shared memory (a warp's equal ones, as zeros come, at once), and the
+// first CTA of a cluster adds up what the others have.  Then ballots and a scan over warps and CTAs give every kept token its
 // place, and the warps move the rows, a block of 16 tokens at a time with all its copies in flight at once.  The search is
 // latency and the move bandwidth: where there are many heads, some search while others move.
 // Where a head has more tokens than its CTAs have registers for, they are read again for every digit.
@@ -48,6 +48,13 @@ __device__ __forceinline__ uint32_t ld_peer(const void* p, int rank) {
   return v;
 }
 
+__device__ __forceinline__ void st_peer(void* p, int rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_cluster(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void red_peer(void* p, int rank, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(map_cluster(p, rank)), "r"(v) : "memory");
+}
+
 // Moves the rows of blocks `first`, `first` + `step` .. of 16 kept tokens of a K/V head, a warp each: 16 bytes of codes per
 // lane at a time.
 template <int D>
@@ -56,21 +63,26 @@ __device__ __forceinline__ void move_rows(const Args& a, int b, int h, const int
   constexpr int kChunks = 2 * L::kRow / 16;  // of 16 bytes, per token: K's, then V's
   constexpr int kIter = kKvBlock * kChunks / 32;
   const int lane = threadIdx.x & 31, bpp = a.ps / kKvBlock;
-  for (int blk = first; blk * kKvBlock < keep; blk += step) {
-    const int cnt = min(keep - blk * kKvBlock, kKvBlock);
-    const int pb = (int)quot(blk, a.by_bpp), to = a.new_table[(long long)b * a.new_width + pb];
-    long long from = -1;  // lane: where token lane % 16 is, its block's offset (a multiple of 128) plus its row there
-    if ((lane & 15) < cnt) {
-      const int t = kept[blk * kKvBlock + (lane & 15)];
-      const int pg = (int)quot((uint32_t)t, a.by_ps), at = t - pg * a.ps, page = a.table[(long long)b * a.width + pg];
-      if (page < 0 || page >= a.pages)
-        report_error(a.err, kErrBadIndex);
-      else
-        from = (((long long)page * a.H + h) * bpp + at / kKvBlock) * L::kBytes + at % kKvBlock;
+  // lane: where token lane % 16 of a block is, its block's offset (a multiple of 128) plus its row there; -1: nowhere
+  auto source = [&](int blk) {
+    const int i = blk * kKvBlock + (lane & 15);
+    if (i >= keep) return -1LL;
+    const int t = kept[i], pg = (int)quot((uint32_t)t, a.by_ps), at = t - pg * a.ps, page = a.table[(long long)b * a.width + pg];
+    if (page < 0 || page >= a.pages) {
+      report_error(a.err, kErrBadIndex);
+      return -1LL;
     }
+    return (((long long)page * a.H + h) * bpp + at / kKvBlock) * L::kBytes + at % kKvBlock;
+  };
+  auto target = [&](int blk) { return blk * kKvBlock < keep ? a.new_table[(long long)b * a.new_width + quot(blk, a.by_bpp)] : 0; };
+  long long next = source(first);
+  int next_to = target(first);
+  for (int blk = first; blk * kKvBlock < keep; blk += step) {
+    long long from = next;
+    const int to = next_to, pb = (int)quot(blk, a.by_bpp);
     if (to < 0 || to >= a.pages) {
       report_error(a.err, kErrBadIndex);
-      continue;
+      from = -1;
     }
     uint8_t* dst = a.cache + (((long long)to * a.H + h) * bpp + (blk - pb * bpp)) * L::kBytes;
     uint4 v[kIter];
@@ -85,6 +97,7 @@ __device__ __forceinline__ void move_rows(const Args& a, int b, int h, const int
     // lanes 0-15: K's parameters, 16-31: V's
     const int pr = (int)from & (kKvBlock - 1), ppart = lane < 16 ? L::kKp : L::kVp;
     if (from >= 0) par = __ldcs(reinterpret_cast<const uint32_t*>(a.cache + (from - pr) + ppart + 4 * pr));
+    next = source(blk + step), next_to = target(blk + step);  // while these are under way
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int row = (i * 32 + lane) / kChunks, ch = (i * 32 + lane) % kChunks;
@@ -95,12 +108,12 @@ __device__ __forceinline__ void move_rows(const Args& a, int b, int h, const int
   }
 }
 
-// kPer: consecutive tokens of a thread; kCtas: of a cluster
+// kPer: tokens of a thread; kCtas: of a cluster
 template <int D, int kThreads, int kPer, int kCtas>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : kThreads == 512 ? 2 : 1) kv_evict_kernel(const Args a) {
   constexpr int kWarps = kThreads / 32, kStep = kThreads * kPer;
   __shared__ uint32_t hist[2][kBins];  // two digits' in turn: a CTA may still read the last one's
-  __shared__ uint32_t s_warp[2][kWarps], s_pick[2], s_total[2];
+  __shared__ uint32_t s_warp[2][kWarps], s_pick[2][2], s_total[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = kCtas > 1 ? (int)cluster_ctarank() : 0;
   const int bh = blockIdx.x / kCtas, b = bh / a.H;
@@ -123,21 +136,18 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : kThreads == 51
   int* kept = a.kept + (long long)bh * a.budget;
   float* nw = a.new_weights + (long long)bh * a.new_cap;
   if (rank == 0 && tid == 0 && bh % a.H == 0) a.new_lens[b] = keep;
-  for (int i = keep + rank * kThreads + tid; i < a.budget; i += kCtas * kThreads) kept[i] = -1;
-  for (int i = keep + rank * kThreads + tid; i < a.new_cap; i += kCtas * kThreads) nw[i] = 0.f;
-  const int rounds = (n + kCtas * kStep - 1) / (kCtas * kStep);  // 1: all tokens are in registers
-  // the tokens of a round: thread by thread, CTA by CTA; a row of weights begins at a 16-byte boundary (cap is a multiple of 16)
+  for (long long i = keep + rank * kThreads + tid; i < a.budget; i += kCtas * kThreads) kept[i] = -1;
+  for (long long i = keep + rank * kThreads + tid; i < a.new_cap; i += kCtas * kThreads) nw[i] = 0.f;
+  const int rounds = n > 0 ? (n - 1) / (kCtas * kStep) + 1 : 0;  // 1: all tokens are in registers
+  // the tokens of a round: a warp has 32 kPer consecutive ones, 32 at a time, so that loads and stores are whole lines
   float x[kPer];
   auto load = [&](int round) {
-    const int t0 = ((round * kCtas + rank) * kThreads + tid) * kPer;
+    const uint32_t t = (((uint32_t)(round * kCtas + rank) * kWarps + warp) * kPer) * 32 + lane;  // may pass 2^31
 #pragma unroll
-    for (int i = 0; i < kPer; i += 4) {
-      const float4 v = t0 + i < n ? *reinterpret_cast<const float4*>(w + t0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-    }
-    return t0;
+    for (int i = 0; i < kPer; ++i) x[i] = t + 32 * i < (uint32_t)n ? w[t + 32 * i] : 0.f;
+    return t;
   };
-  int t0 = load(0);
+  uint32_t t0 = load(0);
   uint32_t prefix = 0, ties = 0;  // the smallest kept number; how many of those that have it are kept
   const bool search = places > 0 && places < old;
   if (search) {
@@ -151,37 +161,37 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : kThreads == 51
       __syncthreads();
       for (int r = 0; r < rounds; ++r) {
         if (rounds > 1) t0 = load(r);
-        // a run of equal digits is counted once
-        uint32_t last = 0xffffffffu, cnt = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const uint32_t k = order_of(x[i]);
-          if (t0 + i >= old || (k & mask) != prefix) continue;
-          const uint32_t bin = k >> shift & (bins - 1);
-          if (bin != last) {
-            if (cnt) atomicAdd(&h[last], cnt);
-            last = bin, cnt = 0;
+          const uint32_t k = order_of(x[i]), bin = k >> shift & (bins - 1);
+          const bool in = t0 + 32 * i < (uint32_t)old && (k & mask) == prefix;
+          const unsigned lanes = __ballot_sync(0xffffffffu, in);
+          if (lanes == 0) continue;
+          // where all digits are the same, as those of many zeros, one lane counts them
+          const uint32_t one = __shfl_sync(0xffffffffu, bin, __ffs(lanes) - 1);
+          if (__all_sync(0xffffffffu, !in || bin == one)) {
+            if (lane == 0) atomicAdd(&h[one], (uint32_t)__popc(lanes));
+          } else if (in) {
+            atomicAdd(&h[bin], 1u);
           }
-          ++cnt;
         }
-        if (cnt) atomicAdd(&h[last], cnt);
       }
-      sync_all();
-      // the bin that holds the last kept one, counting from the greatest: a thread's bins, all CTAs' counts
+      if (kCtas > 1) {  // the first CTA adds up the counts that there are
+        cluster_sync();
+        if (rank > 0)
+          for (int i = tid; i < bins; i += kThreads)
+            if (h[i]) red_peer(&h[i], 0, h[i]);
+        cluster_sync();
+      } else {
+        __syncthreads();
+      }
+      // the bin that holds the last kept one, counting from the greatest
       constexpr int kEach = kBins / kThreads;
       uint32_t c[kEach], sum = 0;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const int bin = bins - 1 - (tid * kEach + i);
-        c[i] = 0;
-        if (bin >= 0) {
-          if (kCtas == 1) {
-            c[i] = h[bin];
-          } else {
-#pragma unroll
-            for (int p = 0; p < kCtas; ++p) c[i] += ld_peer(&h[bin], p);
-          }
-        }
+        c[i] = bin >= 0 && rank == 0 ? h[bin] : 0u;
         sum += c[i];
       }
       uint32_t incl = sum;
@@ -197,62 +207,66 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : kThreads == 51
       if (above < need && need <= incl) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-          if (above < need && need <= above + c[i]) s_pick[0] = bins - 1 - (tid * kEach + i), s_pick[1] = need - above;
+          if (above < need && need <= above + c[i]) {
+#pragma unroll
+            for (int p = 0; p < kCtas; ++p) {
+              st_peer(&s_pick[d & 1][0], p, bins - 1 - (tid * kEach + i));
+              st_peer(&s_pick[d & 1][1], p, need - above);
+            }
+          }
           above += c[i];
         }
       }
-      __syncthreads();
-      prefix |= s_pick[0] << shift;
-      need = s_pick[1];
+      sync_all();
+      prefix |= s_pick[d & 1][0] << shift;
+      need = s_pick[d & 1][1];
     }
     ties = need;
   }
-  // counting off: tokens before this thread's that are greater than the smallest kept number or too new to compete, and ties
+  // counting off: how many of the tokens before are greater than the smallest kept number or too new to compete, and ties
   uint32_t done = 0, met = 0;  // of the rounds before
   for (int r = 0; r < rounds; ++r) {
     if (rounds > 1) t0 = load(r);
-    uint32_t sure = 0, tie = 0;  // bits
+    auto is_sure = [&](int i, uint32_t k) {
+      const uint32_t t = t0 + 32 * i;
+      return t < (uint32_t)n && (t >= (uint32_t)old || (search ? k > prefix : places > 0));
+    };
+    auto is_tie = [&](int i, uint32_t k) { return search && t0 + 32 * i < (uint32_t)old && k == prefix; };
+    uint32_t mine = 0;  // of the warp: sure ones, ties in the upper half; a CTA has 2^14 tokens at most
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const uint32_t k = order_of(x[i]);
-      const bool comp = t0 + i < old;
-      if (t0 + i < n && (!comp || (search ? k > prefix : places > 0))) sure |= 1u << i;
-      if (search && comp && k == prefix) tie |= 1u << i;
-    }
-    uint32_t both = __popc(sure) | __popc(tie) << 16, incl = both;  // a CTA has 2^14 tokens at most
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, incl, s);
-      if (lane >= s) incl += o;
+      mine += __popc(__ballot_sync(0xffffffffu, is_sure(i, k))) + (__popc(__ballot_sync(0xffffffffu, is_tie(i, k))) << 16);
     }
     __syncthreads();
-    if (lane == 31) s_warp[r & 1][warp] = incl;
+    if (lane == 0) s_warp[r & 1][warp] = mine;
     __syncthreads();
-    uint32_t total = 0;
-    for (int v = 0; v < kWarps; ++v) {
-      if (v < warp) incl += s_warp[r & 1][v];
-      total += s_warp[r & 1][v];
-    }
-    uint32_t at = done + ((incl - both) & 0xffffu), ties_at = met + ((incl - both) >> 16);
+    uint32_t v = lane < kWarps ? s_warp[r & 1][lane] : 0u, before = lane < warp ? v : 0u;
+    v = __reduce_add_sync(0xffffffffu, v), before = __reduce_add_sync(0xffffffffu, before);
+    uint32_t at = done + (before & 0xffffu), ties_at = met + (before >> 16);
     if (kCtas > 1) {
-      if (tid == 0) s_total[r & 1] = total;
+      if (tid == 0) s_total[r & 1] = v;
       cluster_sync();
 #pragma unroll
       for (int p = 0; p < kCtas; ++p) {
-        const uint32_t v = ld_peer(&s_total[r & 1], p);
-        if (p < rank) at += v & 0xffffu, ties_at += v >> 16;
-        done += v & 0xffffu, met += v >> 16;
+        const uint32_t o = ld_peer(&s_total[r & 1], p);
+        if (p < rank) at += o & 0xffffu, ties_at += o >> 16;
+        done += o & 0xffffu, met += o >> 16;
       }
     } else {
-      done += total & 0xffffu, met += total >> 16;
+      done += v & 0xffffu, met += v >> 16;
     }
-    // of the ties before this thread, as many are kept as there is room for
-    at += min(ties_at, ties);
+    at += min(ties_at, ties);  // of the ties before, as many are kept as there is room for
+    const unsigned below = (1u << lane) - 1;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      bool in = sure >> i & 1;
-      if (tie >> i & 1) in = ties_at++ < ties;
-      if (in) kept[at] = t0 + i, nw[at] = x[i], ++at;
+      const uint32_t k = order_of(x[i]);
+      const unsigned tie = __ballot_sync(0xffffffffu, is_tie(i, k));
+      const bool in = is_sure(i, k) || ((tie >> lane & 1) && ties_at + __popc(tie & below) < ties);
+      const unsigned all = __ballot_sync(0xffffffffu, in);
+      const uint32_t to = at + __popc(all & below);
+      if (in) kept[to] = (int)(t0 + 32 * i), nw[to] = x[i];
+      at += __popc(all), ties_at += __popc(tie);
     }
   }
   sync_all();  // the kept tokens are all listed, and no CTA leaves while another reads its counts
