@@ -428,6 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
             free_tile(k, next);
           }
           if (some && !wait_full(v)) break;
+          // where both tiles read the same keys, the next K is there by now; else what it waits for may come after this step
+          if (!C::kBeside && !twin && some_next && !wait_full(k)) break;
           if (now) {
             if (!wait(&pbar[x], pcount++)) break;
             // the accumulator is taken over when the softmax warps have read that of the item before
@@ -445,8 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
           }
           if (some) free_tile(v, now);
           if (!C::kBeside && some_next) {
-            if (!wait_full(k)) break;
-            tc_fence_after_sync();
+            if (twin) {
+              if (!wait_full(k)) break;
+              tc_fence_after_sync();
+            }
             if (next) qk(q_desc, k);
             free_tile(k, next);
           }
