@@ -34,7 +34,7 @@ constexpr int kThreads = 640;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kNextWarp = 11, kConvWarp = 12;
 constexpr int kLead = 1;          // rounds that stand for an item's own cost
 constexpr float kTop = 7.0f;         // the largest weight after a rescale is 2^7
-constexpr float kGrown = 15.0f;      // and the next rescale comes when one would pass 2^15, as fp16 asks
+constexpr float kMost = 32768.f;     // and a step whose weights come to more than 2^15 asks for the next
 constexpr float kLarge = 1048576.f;  // from here on scores are rounded before the maximum is subtracted, as it was
 constexpr float kNoMax = -3e38f;     // the maximum of keys whose scores are all minus infinity
 // registers per thread: launched with 96; two warpgroups for the softmax, two convert, one does the rest
@@ -625,90 +625,84 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
           }
           tmem_st_wait();
         }
-        // The scores are read twice, 32 at a time and the next ones while the last are worked on: first for the maximum, then
-        // for the weights.  Rolled up, since the eight converting warps' code and this have to stay near their schedulers.
-        uint32_t va[32], vb[32];
-        tmem_ld_32x32b_x32(ts, va);
-        float top0 = -INFINITY, top1 = -INFINITY;
-        tmem_ld_wait();
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          tmem_ld_32x32b_x32(ts + 64 * i + 32, vb);
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            top0 = max3(top0, __uint_as_float(va[e]), __uint_as_float(va[e + 1]));
-            top1 = max3(top1, __uint_as_float(va[e + 2]), __uint_as_float(va[e + 3]));
-          }
-          tmem_ld_wait();
-          tmem_ld_32x32b_x32(ts + 64 * (i ^ 1), va);  // the first ones again at the end
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            top0 = max3(top0, __uint_as_float(vb[e]), __uint_as_float(vb[e + 1]));
-            top1 = max3(top1, __uint_as_float(vb[e + 2]), __uint_as_float(vb[e + 3]));
-          }
-          tmem_ld_wait();
-        }
-        const float top = __fmul_rn(fmaxf(top0, top1), c);
-        if constexpr (C::kBeside) {  // the last P has been used, and O is that of the steps before
-          if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;
-          ++pcount;
-          tc_fence_after_sync();
-        }
-        if (r == 0) {
-          m = fmaxf(__fsub_rn(top, kTop), kNoMax);
-        } else if (const bool more = top - m > kGrown; __any_sync(0xffffffffu, more)) {
-          // only the rows that need it, so that a row's roundings do not depend on its neighbours
-          const float now = more ? __fsub_rn(top, kTop) : m, f = ex2(m - now);
-          m = now;
-          l0 *= f, l1 *= f;
-#pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(to + i, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st_32x32b_x32(to + i, o);
-          }
-        }
-        // rows with large scores: the scaled scores rounded before the maximum is subtracted, as it was
-        const bool large = fabsf(m) > kLarge;
-        const float mul = large ? 1.f : c;
-        if (__any_sync(0xffffffffu, large)) {
+        auto row_max = [&]() {  // of the scaled scores, less kTop
+          float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll 1
           for (int i = 0; i < kTile; i += 32) {
             uint32_t v[32];
             tmem_ld_32x32b_x32(ts + i, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), large ? c : 1.f));
-            tmem_st_32x32b_x32(ts + i, v);
+            for (int e = 0; e < 32; e += 4) {
+              top0 = max3(top0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              top1 = max3(top1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+            }
           }
-          tmem_st_wait();
-          tmem_ld_32x32b_x32(ts, va);
-          tmem_ld_wait();
-        }
-        auto weights = [&](uint32_t (&v)[32], int i) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float a0 = __uint_as_float(v[2 * e]), a1 = __uint_as_float(v[2 * e + 1]);
-            fma2(a0, a1, mul, -m);
-            a0 = ex2(a0), a1 = ex2(a1);
-            add2(l0, l1, a0, a1);
-            w[e] = pack_h2(a0, a1);
-          }
-          tmem_st_32x32b_x16(tp + 16 * i, w);
+          return __fsub_rn(__fmul_rn(fmaxf(top0, top1), c), kTop);
         };
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          tmem_ld_32x32b_x32(ts + 64 * i + 32, vb);
-          weights(va, 2 * i);
-          tmem_ld_wait();
-          if (i == 0) tmem_ld_32x32b_x32(ts + 64, va);
-          weights(vb, 2 * i + 1);
-          tmem_ld_wait();
+        if (r == 0) m = fmaxf(row_max(), kNoMax);
+        // The weights by the maximum as it was, kept until their sum has said that none of them is too large for fp16.
+        uint32_t w[4][16];
+        float a0, a1;  // this step's sums
+        auto weights = [&](float mul) {
+          a0 = a1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(ts + 32 * i, v);
+            tmem_ld_wait();
+            float f[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) fma2(f[e], f[e + 1], mul, -m);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = ex2(f[e]);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) add2(a0, a1, f[e], f[e + 1]), w[i][e / 2] = pack_h2(f[e], f[e + 1]);
+          }
+        };
+        weights(c);
+        if constexpr (C::kBeside) {  // the last P has been used, and O is that of the steps before
+          if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;
+          ++pcount;
+          tc_fence_after_sync();
         }
+        const bool more = a0 + a1 > kMost || fabsf(m) > kLarge;
+        if (__any_sync(0xffffffffu, more)) {
+          // only the rows that need it, so that a row's roundings do not depend on its neighbours
+          const float top = row_max(), now = more ? fmaxf(m, top) : m, f = ex2(m - now);
+          m = now;
+          const bool large = fabsf(m) > kLarge;
+          if (__any_sync(0xffffffffu, large)) {
+#pragma unroll 1
+            for (int i = 0; i < kTile; i += 32) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(ts + i, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__fmul_rn(__uint_as_float(v[e]), large ? c : 1.f));
+              tmem_st_32x32b_x32(ts + i, v);
+            }
+            tmem_st_wait();
+          }
+          l0 *= f, l1 *= f;
+          if (r > 0) {
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(to + i, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x32(to + i, o);
+            }
+          }
+          weights(large ? 1.f : c);
+        }
+        l0 += a0, l1 += a1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_st_32x32b_x16(tp + 16 * i, w[i]);
         if constexpr (C::kBeside) {
           tc_fence_before_sync();
           __syncwarp();
