@@ -34,7 +34,8 @@ constexpr int kThreads = 640;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kNextWarp = 11, kConvWarp = 12;
 constexpr int kLead = 1;          // rounds that stand for an item's own cost
 constexpr float kTop = 7.0f;         // the largest weight after a rescale is 2^7
-constexpr float kMost = 32768.f;     // and a step whose weights come to more than 2^15 asks for the next
+constexpr float kMost = 32768.f;     // and a step whose weights come to more than 2^15 asks for the next,
+constexpr float kGrown = 8.0f;       // or one whose maximum passed the last by 2^8
 constexpr float kLarge = 1048576.f;  // from here on scores are rounded before the maximum is subtracted, as it was
 constexpr float kNoMax = -3e38f;     // the maximum of keys whose scores are all minus infinity
 // registers per thread: launched with 96; two warpgroups for the softmax, two convert, one does the rest
@@ -90,10 +91,22 @@ struct Shape {
   __device__ __forceinline__ int tiles(int p) const { return max(first + p * A + count(p) - 1, 0) / kTile + 1; }  // of keys
   __device__ __forceinline__ bool twin(int p) const { return 2 * count(p) <= A; }
   __device__ __forceinline__ int rounds(int p) const { return twin(p) ? (tiles(p) + 1) / 2 : tiles(p); }
-  // Rounds (kLead more for each) of items 0 .. p - 1, all of them whole, p < items: sum over i of max(1, ceil(x / 128)) with x
-  // = first + A (i + 1).  The sum of floors by Euclid's steps on (A, 128).
+  // Rounds (kLead more for each) of items 0 .. p - 1, all of them whole, p < items: the sum over i of max(1, ceil(x / 128)) with
+  // x = first + A (i + 1).
   __device__ long long before(int p) const {
-    const long long one = min(max(floor_div((long long)kTile - first, A), 0LL), (long long)p);  // items with a single round
+    if ((A & (A - 1)) == 0) {  // the usual numbers of heads, and no division
+      const int a = __ffs(A) - 1;
+      const long long one = min(max(((long long)kTile - first) >> a, 0LL), (long long)p);  // items with a single round
+      const long long y = (long long)first + kTile - 1;
+      long long sum = (long long)p * kLead + one;
+      if (a >= 7)
+        sum += (p - one) * (y >> 7) + ((((long long)p * (p + 1) - one * (one + 1)) / 2) << (a - 7));
+      else
+        sum += floors((y >> a) + p + 1, 7 - a) - floors((y >> a) + one + 1, 7 - a);
+      return sum;
+    }
+    const long long one = min(max(floor_div((long long)kTile - first, A), 0LL), (long long)p);
+    // the sum of floors of (x k + y) / m by Euclid's steps on (A, 128)
     long long sum = (long long)p * kLead + one, n_ = p - one, m = kTile, x = A, y = A * one + (long long)first + A + kTile - 1;
     while (n_ > 0) {
       if (x >= m) sum += n_ * (n_ - 1) / 2 * (x / m), x %= m;
@@ -105,6 +118,11 @@ struct Shape {
       m = x, x = t;
     }
     return sum;
+  }
+  // The sum of x >> s over x = 0 .. n - 1.
+  static __device__ __forceinline__ long long floors(long long n, int s) {
+    const long long q = n >> s;
+    return (q * (q - 1) / 2 << s) + q * (n & ((1LL << s) - 1));
   }
   __device__ long long all() const { return items ? before(items - 1) + rounds(items - 1) + kLead : 0; }
   static __device__ __forceinline__ long long floor_div(long long a, long long b) { return a >= 0 ? a / b : -1; }
@@ -238,7 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
     const long long quota = (total + gridDim.x - 1) / gridDim.x;
     w0 = min(quota * blockIdx.x, total), w1 = min(w0 + quota, total);
     long long at = incl - mine;
-    if (at <= w0 && w0 < incl)
+    if (at <= w0 && w0 < incl && per == 1)
+      s_b = b0, s_off = w0 - at;
+    else if (at <= w0 && w0 < incl)
       for (int b = b0; b < b1; ++b) {
         const long long n = Shape(a, kv_chunk(a.cu, a.kv_lens, b, a.T, a.cap, nullptr)).all() * a.Hkv;
         if (w0 < at + n) {
@@ -640,38 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
           }
           return __fsub_rn(__fmul_rn(fmaxf(top0, top1), c), kTop);
         };
-        if (r == 0) m = fmaxf(row_max(), kNoMax);
-        // The weights by the maximum as it was, kept until their sum has said that none of them is too large for fp16.
-        uint32_t w[4][16];
-        float a0, a1;  // this step's sums
-        auto weights = [&](float mul) {
-          a0 = a1 = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(ts + 32 * i, v);
-            tmem_ld_wait();
-            float f[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) fma2(f[e], f[e + 1], mul, -m);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = ex2(f[e]);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) add2(a0, a1, f[e], f[e + 1]), w[i][e / 2] = pack_h2(f[e], f[e + 1]);
-          }
-        };
-        weights(c);
-        if constexpr (C::kBeside) {  // the last P has been used, and O is that of the steps before
-          if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;
-          ++pcount;
-          tc_fence_after_sync();
-        }
-        const bool more = a0 + a1 > kMost || fabsf(m) > kLarge;
-        if (__any_sync(0xffffffffu, more)) {
-          // only the rows that need it, so that a row's roundings do not depend on its neighbours
-          const float top = row_max(), now = more ? fmaxf(m, top) : m, f = ex2(m - now);
+        // Rows that ask for it take a new maximum: only those, so that a row's roundings do not depend on its neighbours.  Rows
+        // with large scores have them scaled and rounded first.  Returns the factor for the scores.
+        auto raise = [&](float top, bool more) {
+          const float now = more ? fmaxf(m, top) : m, f = ex2(m - now);
           m = now;
           const bool large = fabsf(m) > kLarge;
           if (__any_sync(0xffffffffu, large)) {
@@ -698,16 +690,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
               tmem_st_32x32b_x32(to + i, o);
             }
           }
-          weights(large ? 1.f : c);
+          return large ? 1.f : c;
+        };
+        // The weights, kept until their sum has said that none of them is too large for fp16.
+        uint32_t w[4][16];
+        float a0, a1;  // this step's sums
+        auto weights = [&](float mul) {
+          a0 = a1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(ts + 32 * i, v);
+            tmem_ld_wait();
+            if (C::kBeside && i == 3) {
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sfree[x]);
+            }
+            float f[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) fma2(f[e], f[e + 1], mul, -m);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = ex2(f[e]);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) add2(a0, a1, f[e], f[e + 1]), w[i][e / 2] = pack_h2(f[e], f[e + 1]);
+          }
+        };
+        if constexpr (C::kBeside) {
+          // The next S waits for this one to be read, so the maximum is looked for first and S not needed any more afterwards.
+          const float top = row_max();
+          float mul = c;
+          if (r == 0) m = fmaxf(top, kNoMax);
+          const bool more = top - m > kGrown || fabsf(m) > kLarge;
+          if (__any_sync(0xffffffffu, more)) {
+            if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;  // O is that of the steps before
+            tc_fence_after_sync();
+            mul = raise(top, more);
+          }
+          weights(mul);
+          if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;  // the last P has been used
+          ++pcount;
+          tc_fence_after_sync();
+        } else {
+          if (r == 0) m = fmaxf(row_max(), kNoMax);
+          weights(c);
+          const bool more = a0 + a1 > kMost || fabsf(m) > kLarge;
+          if (__any_sync(0xffffffffu, more)) weights(raise(row_max(), more));
         }
         l0 += a0, l1 += a1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_st_32x32b_x16(tp + 16 * i, w[i]);
-        if constexpr (C::kBeside) {
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sfree[x]);
-        }
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();

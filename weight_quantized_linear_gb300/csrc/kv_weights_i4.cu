@@ -184,7 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long quota = (total + gridDim.x - 1) / gridDim.x;
     w0 = min(quota * blockIdx.x, total), w1 = min(w0 + quota, total);
     long long at = incl - mine;
-    if (at <= w0 && w0 < incl)
+    if (at <= w0 && w0 < incl && per == 1)
+      s_b = b0, s_off = w0 - at;
+    else if (at <= w0 && w0 < incl)
       for (int b = b0; b < b1; ++b) {
         const long long n = all(b, nullptr);
         if (w0 < at + n) {
