@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
           return;
         }
         if (lane == 0) {
-          s_item[it & 1] = t;
+          s_item[it & 1] = t, s_bad[it & 1] = INT_MAX;
           mbar_arrive(&item_full[it & 1]);
         }
         ++it;
@@ -568,11 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
       uint32_t n = 0;  // tiles so far
       for (int it = 0; wait(&item_full[it & 1], it >> 1); ++it) {
         const int j0 = s_item[it & 1].j0, j1 = s_item[it & 1].j1, len = s_item[it & 1].len, tokens = s_item[it & 1].tokens;
-        if (tid == kConvWarp * 32) s_bad[it & 1] = INT_MAX;
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[it & 1]);
         if (tokens == 0) break;
-        named_barrier_sync(1, 256);  // s_bad is reset
         for (int j = j0; j < j1; ++j, ++n) {
           const int row = group * kHalf + key_in, key = j * kTile + row;
           const uint32_t tile = 2 * n + v, slot = tile % C::kSlots, half_n = 2 * n + group, rs = half_n % C::kRaw;
