@@ -468,7 +468,7 @@ wql_status wql_attention_prompt(const uint16_t* q, int64_t q_stride, const uint1
  * request, or fewer tokens than rows).  out [T, Hq, D] fp16 and lse [T, Hq] fp32 are dense; lse may be NULL.  Rows of
  * no sequence are left as they were.
  * k and v are code * s + lo rounded to fp16, as kv_read_i4 gives them, but never infinite: what rounds to infinity is
- * taken as 65504.  A row of V whose parameters are not finite makes the rows that see it NaN.  Sums are fp32, weights
+ * taken as 65504.  A row of K or V whose parameters are not finite makes the rows that see it NaN.  Sums are fp32, weights
  * fp16: a weight is off by 2^-11 of itself (2^-32 of the row's largest one where it is below 2^-21 of that).  A row
  * depends on nothing behind the last token that it sees.  |scale| <= 2^64.
  * A sequence with a negative start, a negative length or an end beyond T is left out and recorded; a length beyond
@@ -495,8 +495,10 @@ wql_status wql_attention_chunks_kv_i4(const uint16_t* q, int64_t q_stride, int T
  * as they were.  Each sum is formed in fp32 and added once.  k is what attention_chunks_kv_i4 takes; a row of K whose
  * parameters are not finite makes the sums that it belongs to NaN, and so does a row r whose lse is NaN.
  * Sequences, lengths and pages out of range: as there; the sums of a sequence with a bad page are unspecified.
+ * A sum, or an entry that one is added to, of less than 2^-126 in magnitude may count as zero.
  * workspace: device scratch of at least wql_kv_weights_i4_workspace_bytes() bytes (the current device's), with no contents
- * to keep; calls that may run at the same time need one each.  weights must overlap no input.  Results are deterministic.
+ * to keep; calls that may run at the same time need a workspace and weights each.  weights must overlap no input.  Results
+ * are deterministic.
  * Requires B <= 4096, Hq <= 65535, Hq / Hkv <= 128, T * Hq < 2^31 (WQL_EUNSUPPORTED above).
  * ---------------------------------------------------------------------------------------- */
 size_t wql_kv_weights_i4_workspace_bytes(void);
@@ -518,7 +520,8 @@ wql_status wql_kv_weights_i4(const uint16_t* q, int64_t q_stride, int T, int Hq,
  * weights is fp32 [B, H, table_width * page_size], dense.  No page of new_table in use may be in use in block_table or
  * twice in new_table: what such a page then holds is unspecified.  Pages that sequences share may be read by all of them.
  * The old pages stay as they are.  A length beyond table_width * page_size is cut there and recorded; rows whose old or
- * new page number is out of range are not moved and recorded.  Nothing may overlap but the cache with itself.
+ * new page number is out of range are not moved and recorded.  Nothing may overlap but the cache with itself; new_table,
+ * new_weights or new_lens that are block_table, weights or kv_lens are refused.
  * Requires B <= 4096, 1 <= budget <= new_width * page_size, recent >= 0, B * H * max(8, ceil(budget / 16)) <
  * 2^31 (WQL_EUNSUPPORTED above).
  * ---------------------------------------------------------------------------------------- */

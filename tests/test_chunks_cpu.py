@@ -160,3 +160,11 @@ def test_evict_restatement_by_hand():
     assert cref.evict(w, [6], 2, 5) == [[[4, 5]]]
     assert cref.evict(w, [3], 8, 1) == [[[0, 1, 2]]] and cref.evict(w, [0], 8, 1) == [[[]]]
     assert cref.evict(torch.tensor([[[-0.0, 0.0, -1.0]]]), [3], 1, 0) == [[[0]]]
+
+
+def test_eviction_into_its_own_tensors_is_refused(lib):
+    A = [ctypes.c_void_p((1 << 20) + 4096 * i) for i in range(1, 9)]
+    kw = dict(w=A[0], cache=A[1], table=A[2], lens=A[3], new=A[4], kept=A[5], nw=A[6], nl=A[7])
+    for own, other in (("new", "table"), ("nw", "w"), ("nl", "lens")):
+        assert evict(lib, **dict(kw, **{own: kw[other]})) == EINVAL
+        assert b"must not be" in lib.wql_last_error()

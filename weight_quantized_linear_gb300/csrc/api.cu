@@ -732,6 +732,8 @@ wql_status wql_kv_evict_i4(const float* weights, uint8_t* cache, int64_t pages, 
   WQL_REQUIRE_PTR4(kept);
   WQL_REQUIRE_PTR(new_weights);
   WQL_REQUIRE_PTR4(new_lens);
+  WQL_REQUIRE(new_table != block_table && new_weights != weights && new_lens != kv_lens,
+              "new_table, new_weights and new_lens must not be block_table, weights and kv_lens");
   unsigned* dev_err = device_error_word();
   if (!dev_err) return fail(WQL_ECUDA, "wql_kv_evict_i4: cannot locate the device error word");
   return cuda_status(wql::launch_kv_evict_i4(weights, cache, pages, page_size, H, D, block_table, table_width, kv_lens, B,

@@ -62,9 +62,10 @@ __device__ __forceinline__ void move_rows(const Args& a, int b, int h, const int
   using L = KvI4<D>;
   constexpr int kChunks = 2 * L::kRow / 16;  // of 16 bytes, per token: K's, then V's
   constexpr int kIter = kKvBlock * kChunks / 32;
-  const int lane = threadIdx.x & 31, bpp = a.ps / kKvBlock;
+  const int lane = threadIdx.x & 31, bpp = a.ps / kKvBlock, blocks = keep > 0 ? (keep - 1) / kKvBlock + 1 : 0;
   // lane: where token lane % 16 of a block is, its block's offset (a multiple of 128) plus its row there; -1: nowhere
   auto source = [&](int blk) {
+    if (blk >= blocks) return -1LL;
     const int i = blk * kKvBlock + (lane & 15);
     if (i >= keep) return -1LL;
     const int t = kept[i], pg = (int)quot((uint32_t)t, a.by_ps), at = t - pg * a.ps, page = a.table[(long long)b * a.width + pg];
@@ -74,10 +75,10 @@ __device__ __forceinline__ void move_rows(const Args& a, int b, int h, const int
     }
     return (((long long)page * a.H + h) * bpp + at / kKvBlock) * L::kBytes + at % kKvBlock;
   };
-  auto target = [&](int blk) { return blk * kKvBlock < keep ? a.new_table[(long long)b * a.new_width + quot(blk, a.by_bpp)] : 0; };
+  auto target = [&](int blk) { return blk < blocks ? a.new_table[(long long)b * a.new_width + quot(blk, a.by_bpp)] : 0; };
   long long next = source(first);
   int next_to = target(first);
-  for (int blk = first; blk * kKvBlock < keep; blk += step) {
+  for (int blk = first; blk < blocks; blk += step) {
     long long from = next;
     const int to = next_to, pb = (int)quot(blk, a.by_bpp);
     if (to < 0 || to >= a.pages) {
