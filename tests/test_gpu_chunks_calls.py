@@ -319,3 +319,152 @@ def test_binding_refusals_on_the_device(wql):
         wql.attention_chunks_kv_i4(many, cache, table, c, n)
     assert not bool(lse.any()) and not bool(sums.any())
     wql.device_status()
+
+
+def test_pool_of_more_than_4_gib(wql):
+    # the same sequences in a small pool and at the end of a large one, whose offsets pass 2^32 bytes
+    lens, new, D, H, ps = [150, 70], [9, 1], 128, 8, 64
+    q, small, table, cu = cref.case(lens, new, 16, H, D, ps, 12)
+    held = small.shape[0]
+    pages = (1 << 32) // (H * ps * (D + 8)) + 40
+    big = torch.empty((pages, H, ps // 16, 16 * (D + 8)), dtype=torch.uint8, device="cuda")
+    big[-held:] = small
+    shift = pages - held
+    c, n = i32(cu), i32(lens)
+    got = []
+    for cache, by, t in ((small, 0, table), (big, shift, torch.where(table < 0, table, table + shift))):
+        lse, sums = torch.zeros((10, 16), device="cuda"), torch.zeros((2, H, table.shape[1] * ps), device="cuda")
+        out = wql.attention_chunks_kv_i4(q, cache, t, c, n, lse=lse)
+        wql.kv_weights_i4(q, cache, t, c, n, lse, sums)
+        room = torch.zeros((2,) + cache.shape[1:], dtype=torch.uint8, device="cuda")
+        pool = torch.cat([cache, room]) if by == 0 else cache
+        to = i32([[held], [held + 1]]) if by == 0 else i32([[0], [pages - held - 1]])  # from the end to the beginning, and at the end
+        kept, kw, kn = wql.kv_evict_i4(sums, pool, t, n, to, 40, 7)
+        moved = [pool[int(p), :, :2].clone() for p in to.flatten()]
+        got.append([out.view(torch.int16), lse.view(torch.int32), sums.view(torch.int32), kept, kw.view(torch.int32), kn] +
+                   [m[:, 0] for m in moved])
+    assert same(got[0], got[1])
+    o, ob, _, _ = cref.chunks(q, small, table, cu, lens)
+    within(got[0][0].view(torch.float16), o, ob)
+    wql.device_status()
+
+
+def test_largest_batch(wql):
+    B, ps, H = 4096, 16, 1
+    lens = [(i * 37) % 47 for i in range(B)]
+    new = [min(n, (1, 1, 2, 5, 0)[i % 5]) for i, n in enumerate(lens)]
+    q, cache, table, cu = cref.case(lens, new, 2, H, 64, ps, 13)
+    c, n = i32(cu), i32(lens)
+    lse, sums = torch.zeros(q.shape[:2], device="cuda"), torch.zeros((B, H, table.shape[1] * ps), device="cuda")
+    out = wql.attention_chunks_kv_i4(q, cache, table, c, n, lse=lse)
+    o, ob, z, zb = cref.chunks(q, cache, table, cu, lens)
+    within(out, o, ob)
+    within(lse, z, zb)
+    wql.kv_weights_i4(q, cache, table, c, n, lse, sums)
+    w, wb = cref.weights(q, cache, table, cu, lens, lse, torch.zeros_like(sums))
+    within(sums, w, wb)
+    pages = cache.shape[0]
+    pool = torch.cat([cache, torch.zeros((B,) + cache.shape[1:], dtype=torch.uint8, device="cuda")])
+    kept, _, kn = wql.kv_evict_i4(sums, pool, table, n, (pages + torch.arange(B)).view(B, 1).int().cuda(), 9, 2)
+    want = cref.evict(sums.cpu(), lens, 9, 2)
+    for b, (k, m) in enumerate(zip(kept.tolist(), kn.tolist())):
+        assert m == min(9, lens[b]) and k[0][:m] == want[b][0] and k[0][m:] == [-1] * (9 - m)
+    wql.device_status()
+
+
+def test_most_heads(wql):
+    # 65535 heads of their own; 128 query heads to each of two
+    for Hq, Hkv, some in ((65535, 65535, [0, 1, 40000, 65534]), (256, 2, [0, 1])):
+        lens, new, G = [21, 9], [2, 1], Hq // Hkv
+        q, cache, table, cu = cref.case(lens, new, Hq, Hkv, 64, 16, 14)
+        c, n = i32(cu), i32(lens)
+        lse, sums = torch.zeros((3, Hq), device="cuda"), torch.zeros((2, Hkv, table.shape[1] * 16), device="cuda")
+        out = wql.attention_chunks_kv_i4(q, cache, table, c, n, lse=lse)
+        wql.kv_weights_i4(q, cache, table, c, n, lse, sums)
+        heads = [h * G + g for h in some for g in range(G)]
+        o, ob, z, zb = cref.chunks(q[:, heads], cache[:, some], table, cu, lens)
+        within(out[:, heads], o, ob, Hq)
+        within(lse[:, heads], z, zb, Hq)
+        w, wb = cref.weights(q[:, heads], cache[:, some], table, cu, lens, lse[:, heads], torch.zeros_like(sums[:, some]))
+        within(sums[:, some], w, wb, Hq)
+        # the weights of a row and head add up to one, to 1e-3 (scores are off by 72 * 2^-23 * scale sum |q k| < 1e-4 here)
+        assert bool(((sums.double().sum(-1) - i32([2 * G, G])[:, None]).abs() < 2 * G * 1e-3).all())
+    wql.device_status()
+
+
+def test_rows_of_two_sequences_and_pages_twice_in_one(wql):
+    # starts 0 5 2 7: rows 0-4 are the first sequence's, 2-6 the third's, the second ends before it begins
+    lens, ps = [60, 30, 45], 16
+    q, cache, table, _ = cref.case(lens, [5, 1, 1], 8, 2, 128, ps, 15)
+    table[0, 2], table[0, 1] = table[0, 0], table[2, 1]  # a page twice, and one of another sequence
+    lse = torch.zeros((7, 8), device="cuda")
+    y = wql.attention_chunks_kv_i4(q, cache, table, i32([0, 5, 2, 7]), i32(lens), lse=lse)
+    with pytest.raises(wql.WQLError):
+        wql.device_status()
+    first, third = cref.chunks(q, cache, table[:1], [0, 5], lens[:1]), cref.chunks(q, cache, table[2:], [2, 7], lens[2:])
+    for got, i in ((y, 0), (lse, 2)):
+        within(got[:2], first[i][:2], first[i + 1][:2])
+        within(got[5:], third[i][5:], third[i + 1][5:])
+        for r in range(2, 5):
+            a = ((got[r].double() - first[i][r]).abs() <= first[i + 1][r]).view(8, -1).all(-1)
+            b = ((got[r].double() - third[i][r]).abs() <= third[i + 1][r]).view(8, -1).all(-1)
+            assert bool((a | b).all())
+    # both add to sums of their own
+    lse0 = torch.where(torch.arange(7, device="cuda")[:, None] < 5, first[2].nan_to_num(), third[2]).float()
+    sums = torch.zeros((3, 2, table.shape[1] * ps), device="cuda")
+    wql.kv_weights_i4(q, cache, table, i32([0, 5, 2, 7]), i32(lens), lse0, sums)
+    with pytest.raises(wql.WQLError):
+        wql.device_status()
+    for b, cu in ((0, [0, 5]), (2, [2, 7])):
+        w, wb = cref.weights(q, cache, table[b:b + 1], cu, lens[b:b + 1], lse0, torch.zeros_like(sums[:1]))
+        within(sums[b:b + 1], w, wb, b)
+    assert not bool(sums[1].any())
+    pool = torch.cat([cache, torch.zeros((2,) + cache.shape[1:], dtype=torch.uint8, device="cuda")])
+    new_table = i32([[cache.shape[0], cache.shape[0] + 1]])
+    kept, _, _ = wql.kv_evict_i4(sums[:1].contiguous(), pool, table[:1].contiguous(), i32(lens[:1]), new_table, 25, 3)
+    i = torch.arange(25, device="cuda")
+    mine = wql.kv_read_i4(pool, (new_table[0].long()[i // ps] * ps + i % ps).int())
+    for h in range(2):
+        at = kept[0, h].long()
+        old = wql.kv_read_i4(cache, (table[0].long()[at // ps] * ps + at % ps).int())
+        for a, b in zip(mine, old):
+            assert torch.equal(a[:, h], b[:, h])
+    wql.device_status()
+
+
+def test_evictions_at_once_and_captured(wql):
+    # on two streams in one pool with pages apart, and in a graph whose weights and lengths change
+    g = torch.Generator().manual_seed(2)
+    H, D, ps, budget = 4, 128, 64, 200
+    _, cache, table, kv_lens = ref.paged_case(4, [3000, 900, 5000, 10], 1, H, H, D, ps, 5)
+    pages, width = cache.shape[0], -(-budget // ps)
+    cache = torch.cat([cache, torch.zeros((4 * width,) + cache.shape[1:], dtype=torch.uint8, device="cuda")])
+    new_table = (pages + torch.arange(4 * width)).view(4, width).int().cuda()
+    w = torch.randn((4, H, table.shape[1] * ps), generator=g).cuda()
+    want = [x.clone() for x in wql.kv_evict_i4(w, cache, table, kv_lens, new_table, budget, 16)]
+    after = cache.clone()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    halves = [[x[2 * i:2 * i + 2].contiguous() for x in (w, table, kv_lens, new_table)] for i in range(2)]
+    cache[pages:] = 0
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                a, t, n, nt = halves[i]
+                got[i].append([x.clone() for x in wql.kv_evict_i4(a, cache, t, n, nt, budget, 16)])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, y[2 * i:2 * i + 2]) for one in got[i] for x, y in zip(one, want))
+    assert torch.equal(cache, after)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept, nw, nl = wql.kv_evict_i4(w, cache, table, kv_lens, new_table, budget, 16)
+    for lens in ([3000, 900, 5000, 10], [1, 0, 4999, 9], [2500, 201, 0, 3]):  # no more than there are pages for
+        w.normal_()
+        kv_lens.copy_(i32(lens))
+        graph.replay()
+        rows = cref.evict(w.cpu(), lens, budget, 16)
+        for b, n in enumerate(lens):
+            m = min(n, budget)
+            assert int(nl[b]) == m and kept[b, :, :m].tolist() == rows[b] and bool((kept[b, :, m:] == -1).all())
+    wql.device_status()
