@@ -405,9 +405,9 @@ def test_rows_of_two_sequences_and_pages_twice_in_one(wql):
     for got, i in ((y, 0), (lse, 2)):
         within(got[:2], first[i][:2], first[i + 1][:2])
         within(got[5:], third[i][5:], third[i + 1][5:])
-        for r in range(2, 5):
-            a = ((got[r].double() - first[i][r]).abs() <= first[i + 1][r]).view(8, -1).all(-1)
-            b = ((got[r].double() - third[i][r]).abs() <= third[i + 1][r]).view(8, -1).all(-1)
+        for r in range(2, 5):  # both write these, 16 or 32 bytes at a time and in no order: each value is one of the two
+            a = (got[r].double() - first[i][r]).abs() <= first[i + 1][r]
+            b = (got[r].double() - third[i][r]).abs() <= third[i + 1][r]
             assert bool((a | b).all())
     # both add to sums of their own
     lse0 = torch.where(torch.arange(7, device="cuda")[:, None] < 5, first[2].nan_to_num(), third[2]).float()
