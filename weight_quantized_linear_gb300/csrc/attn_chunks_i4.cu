@@ -22,8 +22,8 @@
 #include <climits>
 
 #include "attn.cuh"
+#include "attn_chunks.cuh"
 #include "internal.h"
-#include "kv_i4.cuh"
 
 namespace wql {
 namespace {
@@ -50,6 +50,7 @@ struct Cfg {
   static constexpr int kSlots = D == 128 ? 4 : 8;   // of K and V tiles
   static constexpr int kRawBytes = kHalf / kKvBlock * KvI4<D>::kBytes;  // blocks as they are, of half a tile of keys
   static constexpr int kRaw = D == 128 ? 3 : 6;
+  static_assert(kSlots % 2 == 0, "a slot has K or V, so that its warps meet every phase of its barriers");
   // D = 64 leaves room in tensor memory for P beside S, so that the next S is computed while this one's softmax runs
   static constexpr bool kBeside = D == 64;
   static constexpr int kColO = 2 * kTile, kColP = kBeside ? kColO + 2 * D : 0;  // tensor memory columns; S from 0
@@ -72,12 +73,8 @@ struct Args {
   uint32_t negate;  // bit of the instruction descriptor that negates Q, for a negative scale
   __half* out;
   float* lse;
-  // the workspace: what each CTA leaves unfinished, [CTA]; (m, l) and O of up to `part_rows` rows, [CTA][0, 1]
-  int4* begun;   // {row of q, tokens, tokens that the first row sees, K/V head} of the item that it began; no tokens: none
-  int* went_on;  // of the item that it found begun: 0: none, 1: it goes on, 2: it ends here
-  float2* ml;
-  float* part;
-  int part_rows;
+  ChunkParts parts;
+  int few;  // sequences of up to so many rows are not taken here
   unsigned* err;
 };
 
@@ -86,7 +83,7 @@ struct Args {
 struct Shape {
   int first, n, A, items;
   __device__ __forceinline__ Shape(const Args& a, const KvChunk& c)
-      : first(c.first), n(c.rows), A(2 * a.tokens), items(c.rows > 0 ? (c.rows - 1) / (2 * a.tokens) + 1 : 0) {}
+      : first(c.first), n(c.rows), A(2 * a.tokens), items(c.rows > a.few ? (c.rows - 1) / (2 * a.tokens) + 1 : 0) {}
   __device__ __forceinline__ int count(int p) const { return min(n - p * A, A); }
   __device__ __forceinline__ int tiles(int p) const { return max(first + p * A + count(p) - 1, 0) / kTile + 1; }  // of keys
   __device__ __forceinline__ bool twin(int p) const { return 2 * count(p) <= A; }
@@ -150,11 +147,6 @@ struct Steps {
   __device__ __forceinline__ int at(int r) const { return stride * r + offset; }  // key tile, less j0
 };
 
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void sts_u128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -543,13 +535,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
               p = 0;
               do {
                 c = kv_chunk(a.cu, a.kv_lens, ++b, a.T, a.cap, nullptr);
-              } while (c.rows == 0);
+              } while (c.rows <= a.few);
               sh = Shape(a, c);
             }
           }
         }
       }
-      if (lane == 0) a.begun[blockIdx.x] = begun, a.went_on[blockIdx.x] = went_on;
+      if (lane == 0) a.parts.begun[blockIdx.x] = begun, a.parts.went_on[blockIdx.x] = went_on;
       if (ok) {
         Item t = {};
         put(t);
@@ -771,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
         const int last = seen + tok;  // the last key that this row sees
         const bool nan = last >= s_bad[it & 1];
         const long long to_row = whole ? (long long)(t.row0 + mine) * a.Hq + t.kvh * a.G + g
-                                       : ((long long)blockIdx.x * 2 + t.slot) * a.part_rows + mine * a.G + g;
+                                       : ((long long)blockIdx.x * 2 + t.slot) * a.parts.rows + mine * a.G + g;
         const float inv = last < 0 ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
@@ -813,12 +805,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
               uint32_t h[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) h[e] = o[at(j + e)];
-              st_global_32(a.part + to_row * D + i + j, h, true);
+              st_global_32(a.parts.part + to_row * D + i + j, h, true);
             }
           }
         }
         if (there && whole && a.lse) a.lse[to_row] = last < 0 ? -INFINITY : (m + lg2(l)) * 0.6931471805599453f;
-        if (there && !whole) a.ml[to_row] = make_float2(m, l);
+        if (there && !whole) a.parts.ml[to_row] = make_float2(m, l);
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
@@ -835,22 +827,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of items that CTAs shared, in their order: a warp per row of an item that CTA blockIdx.x began.
+// Joins the parts of items that CTAs shared, in their order: a warp per row of an item that CTA blockIdx.x began, of the CTAs
+// of the kernel above and then of those that took sequences of a few rows.
 constexpr int kJoinWarps = 8;
 
+struct JoinArgs {
+  ChunkParts parts[2];
+  int first, ctas, Hq, G;  // first: 1 where there are only the second ones
+  __half* out;
+  float* lse;
+};
+
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_chunks_join_kernel(const Args a, int ctas) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_chunks_join_kernel(const JoinArgs a) {
   constexpr int kPer = D / 32;  // channels per lane
   grid_dependency_wait();
   grid_dependents_launch();
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const int4 it = a.begun[c];
+  const int lane = threadIdx.x & 31, c = blockIdx.x % a.ctas;
+  const ChunkParts& w = a.parts[a.first + blockIdx.x / a.ctas];
+  const int4 it = w.begun[c];
   const int rows = it.y * a.G;
   int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
   if (r >= rows) return;
   int n = 1;  // parts: slot 1 of CTA c, slot 0 of those behind it
-  for (int k0 = c + 1; k0 < ctas; k0 += 32) {
-    const int v = k0 + lane < ctas ? a.went_on[k0 + lane] : 2;
+  for (int k0 = c + 1; k0 < a.ctas; k0 += 32) {
+    const int v = k0 + lane < a.ctas ? w.went_on[k0 + lane] : 2;
     const unsigned stop = __ballot_sync(0xffffffffu, v != 1);
     if (stop) {
       n += __ffs(stop);
@@ -859,18 +860,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_chunks_join_kernel(const
     n += 32;
   }
   for (; r < rows; r += gridDim.y * kJoinWarps) {
-    auto place = [&](int i) { return ((long long)(c + i) * 2 + (i == 0)) * a.part_rows + r; };
+    auto place = [&](int i) { return ((long long)(c + i) * 2 + (i == 0)) * w.rows + r; };
     float m = kNoMax;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, a.ml[place(i)].x);
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, w.ml[place(i)].x);
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     float l = 0.f, o[kPer] = {};
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-      const float2 ml = a.ml[place(i)];
+      const float2 ml = w.ml[place(i)];
       const float f = ex2(ml.x - m);
       l += ml.y * f;
-      const float* src = a.part + place(i) * D + kPer * lane;
+      const float* src = w.part + place(i) * D + kPer * lane;
       float v[kPer];
       if constexpr (kPer == 4)
         *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
@@ -900,7 +901,7 @@ int part_rows(int T, int G) {
 }
 
 template <int D>
-cudaError_t launch(const CUtensorMap& q, const Args& a, int ctas, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap* q, const Args& a, const StepArgs* few, const JoinArgs& j, cudaStream_t s) {
   using C = Cfg<D>;
   static std::atomic<bool> ready[64];  // per device; racing first calls set the same attribute
   int dev = 0;
@@ -915,25 +916,49 @@ cudaError_t launch(const CUtensorMap& q, const Args& a, int ctas, cudaStream_t s
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.gridDim = dim3(j.ctas, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_chunks_i4_kernel<D>, q, a);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(ctas, a.part_rows < 8 * kJoinWarps ? (a.part_rows + kJoinWarps - 1) / kJoinWarps : 8, 1);
+  if (q) {
+    e = cudaLaunchKernelEx(&cfg, attn_chunks_i4_kernel<D>, *q, a);
+    if (e != cudaSuccess) return e;
+  }
+  if (few) {
+    e = launch_attn_steps_i4(*few, D, j.ctas, s);
+    if (e != cudaSuccess) return e;
+  }
+  const int rows = q ? a.parts.rows : few->parts.rows;
+  cfg.gridDim = dim3(q && few ? 2 * j.ctas : j.ctas, rows < 8 * kJoinWarps ? (rows + kJoinWarps - 1) / kJoinWarps : 8, 1);
   cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_chunks_join_kernel<D>, a, ctas);
+  return cudaLaunchKernelEx(&cfg, attn_chunks_join_kernel<D>, j);
+}
+
+// The workspace from `at` on (32-byte aligned; nullptr: to learn its size): O first, then (m, l), then what the CTAs say.
+size_t lay_out(uint8_t* at, int ctas, int rows, int D, ChunkParts* p) {
+  const size_t n = 2 * (size_t)ctas * rows;
+  p->part = reinterpret_cast<float*>(at);
+  p->ml = reinterpret_cast<float2*>(at + n * D * 4);
+  p->begun = reinterpret_cast<int4*>(at + n * (D * 4 + 8));
+  p->went_on = reinterpret_cast<int*>(at + n * (D * 4 + 8) + ctas * 16);
+  p->rows = rows;
+  return (n * (D * 4 + 8) + ctas * 20 + 31) & ~(size_t)31;
+}
+
+int few_rows(int T, int G) {
+  const long long rows = (long long)T * G;
+  return (int)(rows < kFewRows ? rows : kFewRows);
 }
 
 }  // namespace
 
 size_t attn_chunks_i4_workspace_bytes(int T, int, int Hq, int Hkv, int D) {
-  const size_t ctas = num_sms(), rows = 2 * ctas * part_rows(T, Hq / Hkv);
-  return ctas * 32 + rows * (8 + 4 * (size_t)D) + 32;
+  ChunkParts p;
+  const int G = Hq / Hkv, ctas = num_sms();
+  return lay_out(nullptr, ctas, part_rows(T, G), D, &p) + lay_out(nullptr, ctas, few_rows(T, G), D, &p) + 32;
 }
 
 cudaError_t launch_attn_chunks_i4(const uint16_t* q, long long q_stride, int T, int Hq, int Hkv, int D, const uint8_t* cache,
@@ -941,22 +966,29 @@ cudaError_t launch_attn_chunks_i4(const uint16_t* q, long long q_stride, int T, 
                                   int B, float scale, uint16_t* out, float* lse, void* workspace, unsigned* dev_err,
                                   cudaStream_t s, std::string* err) {
   const int G = Hq / Hkv, tokens = kTile / G, ctas = num_sms();
+  // Sequences of a few rows get a kernel of their own where there may be such: not if all rows are one sequence's and too many.
+  // Where there can be no others, theirs is the only one.
+  const int few = B > 1 || T <= kFewRows / G ? kFewRows / G : 0;
+  const bool others = T > few;
   CUtensorMap tq;
-  if (!make_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, D, Hq, T, (uint64_t)D * 2, (uint64_t)q_stride * 2, 64, G, tokens,
-                    CU_TENSOR_MAP_SWIZZLE_128B, err))
+  if (others && !make_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, D, Hq, T, (uint64_t)D * 2, (uint64_t)q_stride * 2, 64, G,
+                              tokens, CU_TENSOR_MAP_SWIZZLE_128B, err))
     return cudaErrorInvalidValue;
-  // O first, at a 32-byte boundary, then (m, l), then what the CTAs say
+  JoinArgs j;
   uint8_t* w = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~(uintptr_t)31);
-  const int rows = part_rows(T, G);
-  float* part = reinterpret_cast<float*>(w);
-  float2* ml = reinterpret_cast<float2*>(part + 2LL * ctas * rows * D);
-  int4* begun = reinterpret_cast<int4*>(ml + 2LL * ctas * rows);
+  w += lay_out(w, ctas, part_rows(T, G), D, &j.parts[0]);
+  lay_out(w, ctas, few_rows(T, G), D, &j.parts[1]);
+  j.first = others ? 0 : 1, j.ctas = ctas, j.Hq = Hq, j.G = G, j.out = reinterpret_cast<__half*>(out), j.lse = lse;
   // a scale of zero keeps a trace of itself, so that masked scores stay minus infinity
-  const float mag = scale < 0.f ? -scale : scale;
-  Args a{cu, kv_lens, B, T, Hq, Hkv, G, tokens, cache, (int)pages, ps / kKvBlock, fast_div(ps / kKvBlock), table, width,
-         width * ps, (mag < 1e-30f ? 1e-30f : mag) * 1.4426950408889634f, scale < 0.f ? 1u << 13 : 0u,
-         reinterpret_cast<__half*>(out), lse, begun, reinterpret_cast<int*>(begun + ctas), ml, part, rows, dev_err};
-  return D == 128 ? launch<128>(tq, a, ctas, s) : launch<64>(tq, a, ctas, s);
+  const float mag = scale < 0.f ? -scale : scale, scale_log2 = (mag < 1e-30f ? 1e-30f : mag) * 1.4426950408889634f;
+  const Args a{cu, kv_lens, B, T, Hq, Hkv, G, tokens, cache, (int)pages, ps / kKvBlock, fast_div(ps / kKvBlock), table, width,
+               width * ps, scale_log2, scale < 0.f ? 1u << 13 : 0u, j.out, lse, j.parts[0], few, dev_err};
+  const StepArgs sa{reinterpret_cast<const __half*>(q), q_stride, cu, kv_lens, B, T, Hq, Hkv, G, few, cache, (int)pages,
+                    fast_div(ps / kKvBlock), table, width, width * ps, scale < 0.f ? -scale_log2 : scale_log2, j.out, lse, j.parts[1],
+                    dev_err};
+  const CUtensorMap* tiles = others ? &tq : nullptr;
+  const StepArgs* steps = few ? &sa : nullptr;
+  return D == 128 ? launch<128>(tiles, a, steps, j, s) : launch<64>(tiles, a, steps, j, s);
 }
 
 }  // namespace wql
