@@ -262,6 +262,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
     __syncthreads();
   }
   const uint32_t tmem = tmem_slot;
+  if (w0 >= w1) {  // nothing to do, as where all sequences have a few rows
+    if (tid == 0) a.parts.begun[blockIdx.x] = make_int4(0, 0, 0, 0), a.parts.went_on[blockIdx.x] = 0;
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    return;
+  }
 
   if (warp >= kLoadWarp) {
     if (warp >= kConvWarp)
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
         }
         ++it;
       };
-      if (w0 < w1) {
+      {
         int b = s_b, p, kvh, s;
         KvChunk c = kv_chunk(a.cu, a.kv_lens, b, a.T, a.cap, nullptr);
         Shape sh(a, c);
@@ -827,13 +832,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of items that CTAs shared, in their order: a warp per row of an item that CTA blockIdx.x began, of the CTAs
-// of the kernel above and then of those that took sequences of a few rows.
-constexpr int kJoinWarps = 8;
+// Joins the parts of items that CTAs shared, in their order: up to kJoinBlocks blocks for each CTA of the kernel above and then
+// one for each of those that took sequences of a few rows, a warp per row.  One pass over a row's parts, kAhead of them in flight
+// at a time.  More of them, or more rows of a warp at once, cost more by their registers than they save: the next kernel's CTAs
+// need all of an SM's (512 tokens behind 15872: 136.7 us, four rows at once 140.4; a block for every eight rows 149.5).
+constexpr int kJoinWarps = 8, kJoinBlocks = 8, kAhead = 4;
 
 struct JoinArgs {
-  ChunkParts parts[2];
-  int first, ctas, Hq, G;  // first: 1 where there are only the second ones
+  ChunkParts parts, few;
+  int blocks, ctas, Hq, G;  // no blocks: there are only the second ones
   __half* out;
   float* lse;
 };
@@ -841,44 +848,62 @@ struct JoinArgs {
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_chunks_join_kernel(const JoinArgs a) {
   constexpr int kPer = D / 32;  // channels per lane
+  const bool few = (int)blockIdx.x >= a.ctas * a.blocks;
+  const ChunkParts w{few ? a.few.begun : a.parts.begun, few ? a.few.went_on : a.parts.went_on, few ? a.few.ml : a.parts.ml,
+                     few ? a.few.part : a.parts.part, few ? a.few.rows : a.parts.rows};
+  const int c = few ? blockIdx.x - a.ctas * a.blocks : blockIdx.x / a.blocks, lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int lane = threadIdx.x & 31, c = blockIdx.x % a.ctas;
-  const ChunkParts& w = a.parts[a.first + blockIdx.x / a.ctas];
   const int4 it = w.begun[c];
-  const int rows = it.y * a.G;
-  int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  int v = c + 1 + lane < a.ctas ? w.went_on[c + 1 + lane] : 2;
+  const int rows = it.y * a.G, step = (few ? 1 : a.blocks) * kJoinWarps;
+  int r = (few ? 0 : blockIdx.x - c * a.blocks) * kJoinWarps + (threadIdx.x >> 5);
   if (r >= rows) return;
   int n = 1;  // parts: slot 1 of CTA c, slot 0 of those behind it
-  for (int k0 = c + 1; k0 < a.ctas; k0 += 32) {
-    const int v = k0 + lane < a.ctas ? w.went_on[k0 + lane] : 2;
+  for (;;) {
     const unsigned stop = __ballot_sync(0xffffffffu, v != 1);
     if (stop) {
       n += __ffs(stop);
       break;
     }
     n += 32;
+    v = c + n + lane < a.ctas ? w.went_on[c + n + lane] : 2;
   }
-  for (; r < rows; r += gridDim.y * kJoinWarps) {
-    auto place = [&](int i) { return ((long long)(c + i) * 2 + (i == 0)) * w.rows + r; };
-    float m = kNoMax;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, w.ml[place(i)].x);
+  for (; r < rows; r += step) {
+    float m = kNoMax, l = 0.f, o[kPer] = {};
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      float2 ml[kAhead];
+      float x[kAhead][kPer];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float l = 0.f, o[kPer] = {};
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float2 ml = w.ml[place(i)];
-      const float f = ex2(ml.x - m);
-      l += ml.y * f;
-      const float* src = w.part + place(i) * D + kPer * lane;
-      float v[kPer];
-      if constexpr (kPer == 4)
-        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-      else
-        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k;
+        const long long at = ((long long)(c + i) * 2 + (i == 0)) * w.rows + r;
+        ml[k] = make_float2(kNoMax, 0.f);
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] += v[e] * f;
+        for (int e = 0; e < kPer; ++e) x[k][e] = 0.f;
+        if (i < n) {
+          ml[k] = w.ml[at];
+          const float* src = w.part + at * D + kPer * lane;
+          if constexpr (kPer == 4)
+            *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(src);
+          else
+            *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(src);
+        }
+      }
+      float now = m;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) now = fmaxf(now, ml[k].x);
+      const float old = ex2(m - now);
+      m = now, l *= old;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] *= old;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float f = ex2(ml[k].x - m);
+        l += ml[k].y * f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] += x[k][e] * f;
+      }
     }
     const int tok = r / a.G;
     const bool none = it.z + tok < 0;  // sees nothing
@@ -930,8 +955,7 @@ cudaError_t launch(const CUtensorMap* q, const Args& a, const StepArgs* few, con
     e = launch_attn_steps_i4(*few, D, j.ctas, s);
     if (e != cudaSuccess) return e;
   }
-  const int rows = q ? a.parts.rows : few->parts.rows;
-  cfg.gridDim = dim3(q && few ? 2 * j.ctas : j.ctas, rows < 8 * kJoinWarps ? (rows + kJoinWarps - 1) / kJoinWarps : 8, 1);
+  cfg.gridDim = dim3(j.ctas * (j.blocks + (few ? 1 : 0)), 1, 1);
   cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_chunks_join_kernel<D>, j);
@@ -976,16 +1000,18 @@ cudaError_t launch_attn_chunks_i4(const uint16_t* q, long long q_stride, int T, 
     return cudaErrorInvalidValue;
   JoinArgs j;
   uint8_t* w = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~(uintptr_t)31);
-  w += lay_out(w, ctas, part_rows(T, G), D, &j.parts[0]);
-  lay_out(w, ctas, few_rows(T, G), D, &j.parts[1]);
-  j.first = others ? 0 : 1, j.ctas = ctas, j.Hq = Hq, j.G = G, j.out = reinterpret_cast<__half*>(out), j.lse = lse;
+  w += lay_out(w, ctas, part_rows(T, G), D, &j.parts);
+  lay_out(w, ctas, few_rows(T, G), D, &j.few);
+  const int blocks = (j.parts.rows + kJoinWarps - 1) / kJoinWarps;
+  j.blocks = !others ? 0 : blocks < kJoinBlocks ? blocks : kJoinBlocks;
+  j.ctas = ctas, j.Hq = Hq, j.G = G, j.out = reinterpret_cast<__half*>(out), j.lse = lse;
   // a scale of zero keeps a trace of itself, so that masked scores stay minus infinity
   const float mag = scale < 0.f ? -scale : scale, scale_log2 = (mag < 1e-30f ? 1e-30f : mag) * 1.4426950408889634f;
   const Args a{cu, kv_lens, B, T, Hq, Hkv, G, tokens, cache, (int)pages, ps / kKvBlock, fast_div(ps / kKvBlock), table, width,
-               width * ps, scale_log2, scale < 0.f ? 1u << 13 : 0u, j.out, lse, j.parts[0], few, dev_err};
+               width * ps, scale_log2, scale < 0.f ? 1u << 13 : 0u, j.out, lse, j.parts, few, dev_err};
   const StepArgs sa{reinterpret_cast<const __half*>(q), q_stride, cu, kv_lens, B, T, Hq, Hkv, G, few, cache, (int)pages,
-                    fast_div(ps / kKvBlock), table, width, width * ps, scale < 0.f ? -scale_log2 : scale_log2, j.out, lse, j.parts[1],
-                    dev_err};
+                    fast_div(ps / kKvBlock), table, width, width * ps, scale < 0.f ? -scale_log2 : scale_log2, j.out, lse, j.few,
+                    others, dev_err};
   const CUtensorMap* tiles = others ? &tq : nullptr;
   const StepArgs* steps = few ? &sa : nullptr;
   return D == 128 ? launch<128>(tiles, a, steps, j, s) : launch<64>(tiles, a, steps, j, s);

@@ -119,7 +119,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
 
   for (int i = tid; i < 2 * kW * kS; i += C::kThreads) mbar_init(&bars[i], 1);
   fence_mbarrier_init();
-  grid_dependency_wait();  // everything before this line overlaps the end of the preceding kernel
+  // Everything before this line overlaps the end of the preceding kernel.  If that is the one for the other sequences, it began
+  // the launch of this one when all before it was complete, and the two work on different rows: this one need not wait for its end
+  // now, only before its own, which the joining kernel waits for.
+  if (!a.second) grid_dependency_wait();
   grid_dependents_launch();
 
   // ---- this CTA's range [n0, n1) of the order of all steps; warp w's run is [run(w), run(w + 1)) ----
@@ -162,6 +165,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
   }
   if (n0 >= n1) {
     if (tid == 0) a.parts.begun[blockIdx.x] = make_int4(0, 0, 0, 0), a.parts.went_on[blockIdx.x] = 0;
+    grid_dependency_wait();
     return;
   }
   const long long each = (n1 - n0 + kW - 1) / kW;
@@ -487,6 +491,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
     a.parts.begun[blockIdx.x] = begun;
     a.parts.went_on[blockIdx.x] = chains & 1u ? (ends_f ? 2 : 1) : 0;
   }
+  grid_dependency_wait();
   if (chains == 0) return;
   float4* fac = reinterpret_cast<float4*>(smem + C::kOffFac);
   for (int i = tid; i < 2 * kW * kFewRows; i += C::kThreads) {
