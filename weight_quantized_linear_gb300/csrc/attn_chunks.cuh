@@ -19,7 +19,7 @@ struct StepArgs {
   const __half* q;
   long long q_stride;
   const int *cu, *kv_lens;
-  int B, T, Hq, Hkv, G, few;  // few: tokens of a chunk at most that are taken here, few * G <= kFewRows
+  int B, T, Hq, Hkv, G, few;  // few: tokens of a chunk at most that are taken here, few * G <= kFewRows; up to 8 of these rows are cheaper
   const uint8_t* cache;
   int pages;
   FastDiv bpp;  // blocks of a page
@@ -32,7 +32,7 @@ struct StepArgs {
   bool second;  // runs behind the kernel for the other sequences, which waits for what came before
   unsigned* err;
 };
-constexpr int kFewRows = 8;
+constexpr int kFewRows = 16;
 cudaError_t launch_attn_steps_i4(const StepArgs& a, int D, int ctas, cudaStream_t s);
 
 __device__ __forceinline__ float lg2(float x) {

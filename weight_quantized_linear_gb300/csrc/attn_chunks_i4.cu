@@ -990,9 +990,12 @@ cudaError_t launch_attn_chunks_i4(const uint16_t* q, long long q_stride, int T, 
                                   int B, float scale, uint16_t* out, float* lse, void* workspace, unsigned* dev_err,
                                   cudaStream_t s, std::string* err) {
   const int G = Hq / Hkv, tokens = kTile / G, ctas = num_sms();
-  // Sequences of a few rows get a kernel of their own where there may be such: not if all rows are one sequence's and too many.
-  // Where there can be no others, theirs is the only one.
-  const int few = B > 1 || T <= kFewRows / G ? kFewRows / G : 0;
+  // Sequences of a few rows of a K/V head get a kernel of their own, where there may be such: not if all rows are one sequence's and
+  // too many.  Up to eight rows if that is what the sequences have on the average, or more than sixteen and so some have many and
+  // others surely few; else, and where a token has more than eight heads, up to sixteen.
+  const long long mean = ((long long)T * G + B - 1) / B;
+  const int most = G > 8 || (mean > 8 && mean <= kFewRows) ? kFewRows : 8;
+  const int few = B > 1 || T <= most / G ? most / G : 0;
   const bool others = T > few;
   CUtensorMap tq;
   if (others && !make_tmap_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, D, Hq, T, (uint64_t)D * 2, (uint64_t)q_stride * 2, 64, G,

@@ -1,6 +1,6 @@
 // attn_steps_i4.cu -- attention over the paged 4-bit KV cache for chunks of a few rows: single tokens, drafted ones.
 //
-// attention_chunks_kv_i4's formulas for the sequences whose rows of a K/V head, tokens times query heads, are kFewRows or fewer.
+// attention_chunks_kv_i4's formulas for the sequences whose rows of a K/V head, tokens times query heads, are 8 NT or fewer.
 // Tiles of 128 rows would be mostly empty and spend their time on them (64 single tokens with four heads each: 195 us), so
 // here rows are the narrow side of mma.sync products, and keys and channels the wide one:
 //   S^T (16 keys x 8 rows) = K Q^T, then O^T (16 channels x 8 rows) += V^T P,
@@ -28,18 +28,19 @@ constexpr float kNoMax = -3e38f;
 // a weight beyond 2^15 asks for a new maximum, which then has the weight 2^7
 constexpr float kTop = 7.0f, kRaise = 15.0f;
 
-template <int D>
+template <int D, int NT>  // NT: rows by eight
 struct Cfg {
-  static constexpr int kWarps = 15, kThreads = 32 * (kWarps + 1);
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kWarps = D == 128 && NT == 2 ? 11 : 15, kThreads = 32 * (kWarps + 1);
   static constexpr int kStepBytes = kStep / kKvBlock * KvI4<D>::kBytes;
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kPitch = D + 4;                                          // floats per row of a part
   static constexpr int kOffJoin = kWarps * kStages * kStepBytes;                // [kWarps][rows][kPitch]: first parts
-  static constexpr int kOffMl = kOffJoin + kWarps * kFewRows * kPitch * 4;      // [first, last part][kWarps][rows] {m, l}
-  static constexpr int kOffFac = kOffMl + 2 * kWarps * kFewRows * 8;            // the same: {factor, its l, maximum}
-  static constexpr int kOffBar = kOffFac + 2 * kWarps * kFewRows * 16;          // [full, empty][kWarps][kStages]
+  static constexpr int kOffMl = kOffJoin + kWarps * kRows * kPitch * 4;      // [first, last part][kWarps][rows] {m, l}
+  static constexpr int kOffFac = kOffMl + 2 * kWarps * kRows * 8;            // the same: {factor, its l, maximum}
+  static constexpr int kOffBar = kOffFac + 2 * kWarps * kRows * 16;          // [full, empty][kWarps][kStages]
   static constexpr int kSmem = kOffBar + 2 * kWarps * kStages * 8;
-  static_assert(kFewRows * kPitch * 4 <= kStages * kStepBytes, "a last part takes the warp's ring");
+  static_assert(kRows * kPitch * 4 <= kStages * kStepBytes, "a last part takes the warp's ring");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -100,9 +101,9 @@ __device__ __forceinline__ int key_of(int r) {
   return 2 * c + (e ^ (D == 128 ? (c & 1) : (c >> 1)));
 }
 
-template <int D>
-__global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(const StepArgs a) {
-  using C = Cfg<D>;
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_steps_i4_kernel(const StepArgs a) {
+  using C = Cfg<D, NT>;
   using L = KvI4<D>;
   constexpr int kW = C::kWarps, kS = C::kStages;
   constexpr int kKw = D / 32;  // words of K codes per thread and key
@@ -254,43 +255,48 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
       const KvChunk k = chunk(a, u.b);
       const int rows = k.rows * a.G;
       // Q: thread (g, c) holds row g's channels of its K words, paired as the codes will be
-      uint32_t qf[kKw][4];
-      {
-        const int r = g / a.G;
-        const __half* src = a.q + (long long)(k.start + r) * a.q_stride + (long long)(u.h * a.G + g - r * a.G) * D + 8 * kKw * c;
+      uint32_t qf[NT][kKw][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int row = 8 * t + g, r = row / a.G;
+        const __half* src = a.q + (long long)(k.start + r) * a.q_stride + (long long)(u.h * a.G + row - r * a.G) * D + 8 * kKw * c;
         uint4 raw[kKw];
 #pragma unroll
         for (int j = 0; j < kKw; ++j)
-          raw[j] = g < rows ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0u, 0u, 0u, 0u);
+          raw[j] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int j = 0; j < kKw; ++j) {
-          qf[j][0] = prmt(raw[j].x, raw[j].z, 0x5410u), qf[j][1] = prmt(raw[j].x, raw[j].z, 0x7632u);
-          qf[j][2] = prmt(raw[j].y, raw[j].w, 0x5410u), qf[j][3] = prmt(raw[j].y, raw[j].w, 0x7632u);
+          qf[t][j][0] = prmt(raw[j].x, raw[j].z, 0x5410u), qf[t][j][1] = prmt(raw[j].x, raw[j].z, 0x7632u);
+          qf[t][j][2] = prmt(raw[j].y, raw[j].w, 0x5410u), qf[t][j][3] = prmt(raw[j].y, raw[j].w, 0x7632u);
         }
       }
-      int lim[2];  // the last keys that rows 2c and 2c + 1 see
+      int lim[NT][2];           // the last keys that rows 2c and 2c + 1 see
+      float o[NT][kMt][4];      // rows 2c and 2c + 1 in [0, 2) and [2, 4)
+      float m[NT][2], l[NT][2]; // l: of this thread's keys
 #pragma unroll
-      for (int e = 0; e < 2; ++e) lim[e] = 2 * c + e < rows ? k.first + (2 * c + e) / a.G : -1;
-      float o[kMt][4];  // rows 2c and 2c + 1 in [0, 2) and [2, 4)
-      float m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};  // l: of this thread's keys
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < kMt; ++i)
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * t + 2 * c + e;
+          lim[t][e] = row < rows ? k.first + row / a.G : -1;
+          m[t][e] = kNoMax, l[t][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+          for (int i = 0; i < kMt; ++i) o[t][i][e] = o[t][i][e + 2] = 0.f;
+        }
 
       // Two blocks of 16 keys from t0.  kCareful: some row may not see them all, or some parameters are infinite, not a number
       // or so large that a value may be.
       auto step = [&](auto careful, const uint8_t* base, int t0) {
         constexpr bool kCareful = decltype(careful)::value;
         constexpr int kB = kStep / kKvBlock;
-        float s[kB][4];  // rows 2c and 2c + 1 of key tok, then of tok + 8
-        bool nan[2] = {false, false};
+        float s[kB][NT][4];  // rows 2c and 2c + 1 of key tok, then of tok + 8
+        int bad = INT_MAX;   // the first of this thread's keys whose row of V is not a number
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
           const uint8_t* blk = base + b * L::kBytes;
           const int left = k.len - t0 - b * kKvBlock;  // keys from this block on
           uint32_t kw[2][kKw], s2[2], lo2[2];
-          float acc[2][4] = {};
+          float acc[NT][2][4] = {};
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const uint32_t ad = smem_u32(blk + (tok + 8 * hh) * L::kRow + 4 * kKw * c);
@@ -305,9 +311,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
             if constexpr (kCareful) {
               if (tok + 8 * hh >= left) par = 0u;
               if (!kv_finite(par)) par = 0x7fff7fffu;
-              const bool bad = !kv_finite(*reinterpret_cast<const uint32_t*>(blk + L::kVp + 4 * (tok + 8 * hh)));
-#pragma unroll
-              for (int e = 0; e < 2; ++e) nan[e] |= bad && t0 + b * kKvBlock + tok + 8 * hh <= lim[e];
+              if (!kv_finite(*reinterpret_cast<const uint32_t*>(blk + L::kVp + 4 * (tok + 8 * hh))))
+                bad = min(bad, t0 + b * kKvBlock + tok + 8 * hh);
             }
             s2[hh] = prmt(par, 0, 0x1010), lo2[hh] = prmt(par, 0, 0x3232);
           }
@@ -319,40 +324,53 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
             if constexpr (kCareful)
 #pragma unroll
               for (int e = 0; e < 4; ++e) x[e] = kv_clamp2(x[e]), y[e] = kv_clamp2(y[e]);
-            mma(acc[0], x[0], y[0], x[1], y[1], qf[j][0], qf[j][1]);
-            mma(acc[1], x[2], y[2], x[3], y[3], qf[j][2], qf[j][3]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma(acc[t][0], x[0], y[0], x[1], y[1], qf[t][j][0], qf[t][j][1]);
+              mma(acc[t][1], x[2], y[2], x[3], y[3], qf[t][j][2], qf[t][j][3]);
+            }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {  // rounded before the maximum is subtracted, so that the largest has the weight 2^7 whatever it is
-            s[b][e] = __fmul_rn(acc[0][e] + acc[1][e], cs);
-            if (kCareful && t0 + b * kKvBlock + tok + 8 * (e >> 1) > lim[e & 1]) s[b][e] = -INFINITY;
-          }
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // rounded before the maximum is subtracted, so that the largest has the weight 2^7 whatever it is
+              s[b][t][e] = __fmul_rn(acc[t][0][e] + acc[t][1][e], cs);
+              if (kCareful && t0 + b * kKvBlock + tok + 8 * (e >> 1) > lim[t][e & 1]) s[b][t][e] = -INFINITY;
+            }
         }
-        const float top0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])) - m[0];
-        const float top1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3])) - m[1];
-        if (__any_sync(0xffffffffu, fmaxf(top0, top1) > kRaise)) {
+        float up = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {  // only the rows that ask for it
-            float x = fmaxf(fmaxf(s[0][e], s[0][e + 2]), fmaxf(s[1][e], s[1][e + 2]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float now = x - m[e] > kRaise ? x - kTop : m[e], f = ex2(m[e] - now);
-            m[e] = now, l[e] *= f;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < kMt; ++i) o[i][e] *= f, o[i][e + 2] *= f;
-          }
+          for (int e = 0; e < 2; ++e)
+            up = fmaxf(up, fmaxf(fmaxf(s[0][t][e], s[0][t][e + 2]), fmaxf(s[1][t][e], s[1][t][e + 2])) - m[t][e]);
+        if (__any_sync(0xffffffffu, up > kRaise)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // only the rows that ask for it
+              float x = fmaxf(fmaxf(s[0][t][e], s[0][t][e + 2]), fmaxf(s[1][t][e], s[1][t][e + 2]));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              const float now = x - m[t][e] > kRaise ? x - kTop : m[t][e], f = ex2(m[t][e] - now);
+              m[t][e] = now, l[t][e] *= f;
+#pragma unroll
+              for (int i = 0; i < kMt; ++i) o[t][i][e] *= f, o[t][i][e + 2] *= f;
+            }
         }
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
           const uint8_t* blk = base + b * L::kBytes;
-          uint32_t w[2];
+          uint32_t w[NT][2];
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const float p0 = ex2(s[b][2 * hh] - m[0]), p1 = ex2(s[b][2 * hh + 1] - m[1]);
-            l[0] += p0, l[1] += p1;
-            w[hh] = movmatrix_trans(pack_h2(p0, p1));
-          }
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const float p0 = ex2(s[b][t][2 * hh] - m[t][0]), p1 = ex2(s[b][t][2 * hh + 1] - m[t][1]);
+              l[t][0] += p0, l[t][1] += p1;
+              w[t][hh] = movmatrix_trans(pack_h2(p0, p1));
+            }
           // words 2g and 2g + 1 (D = 64: word g) of four keys, paired by key: low and high halves
           uint32_t xv[2][2][D / 64], s2[2], lo2[2];
 #pragma unroll
@@ -388,15 +406,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
                   for (int e = 0; e < 4; ++e) v[r][hh][e] = kv_clamp2(v[r][hh][e]);
               }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mma(o[4 * i + e], v[0][0][e], v[1][0][e], v[0][1][e], v[1][1][e], w[0], w[1]);
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma(o[t][4 * i + e], v[0][0][e], v[1][0][e], v[0][1][e], v[1][1][e], w[t][0], w[t][1]);
           }
         }
         if constexpr (kCareful) {  // rows that see a row of V that is not a number
+          bad = __reduce_min_sync(0xffffffffu, bad);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (__ballot_sync(0xffffffffu, nan[e]) >> c & 0x11111111u)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int i = 0; i < kMt; ++i) o[i][e] = o[i][e + 2] = __uint_as_float(0x7fc00000u);
+            for (int e = 0; e < 2; ++e)
+              if (bad <= lim[t][e])
+#pragma unroll
+                for (int i = 0; i < kMt; ++i) o[t][i][e] = o[t][i][e + 2] = __uint_as_float(0x7fc00000u);
         }
       };
 
@@ -429,39 +452,42 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
 
       // ---- the unit's result, or this warp's part of it ----
       const bool open_left = u.s > 0, open_right = here < u.n - u.s, whole = !open_left && !open_right;
-      float* dst = open_left ? join + warp * kFewRows * C::kPitch : const_cast<float*>(reinterpret_cast<const float*>(ring));
-      float2* mld = ml + ((open_left ? 0 : kW) + warp) * kFewRows;
+      float* dst = open_left ? join + warp * C::kRows * C::kPitch : const_cast<float*>(reinterpret_cast<const float*>(ring));
+      float2* mld = ml + ((open_left ? 0 : kW) + warp) * C::kRows;
       if (lane == 0 && !whole) (open_left ? s_first : s_last)[warp] = make_int4(u.b, u.h, 0, open_right ? kPart : kPart | kEnds);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int d = 4; d <= 16; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
-        const int row = 2 * c + e, r = row / a.G;
-        const float inv = lim[e] < 0 ? 0.f : 1.f / l[e];
-        const long long to = (long long)(k.start + r) * a.Hq + u.h * a.G + row - r * a.G;
-        if (!whole && g == 0) mld[row] = make_float2(m[e], l[e]);
-        if (whole && g == 0 && row < rows && a.lse) a.lse[to] = lim[e] < 0 ? -INFINITY : (m[e] + lg2(l[e])) * 0.6931471805599453f;
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-          // D = 128: rows g of tile i are channels 16 g + i, rows g + 8 channels 16 g + 8 + i; D = 64: 8 g + i and 8 g + 4 + i
-          const int ch = (2 * g + hi) * kMt;
-          if (!whole) {
-            float4* d4 = reinterpret_cast<float4*>(dst + row * C::kPitch + ch);
+          for (int d = 4; d <= 16; d <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], d);
+          const int row = 8 * t + 2 * c + e, r = row / a.G;
+          const float inv = lim[t][e] < 0 ? 0.f : 1.f / l[t][e];
+          const long long to = (long long)(k.start + r) * a.Hq + u.h * a.G + row - r * a.G;
+          if (!whole && g == 0) mld[row] = make_float2(m[t][e], l[t][e]);
+          if (whole && g == 0 && row < rows && a.lse)
+            a.lse[to] = lim[t][e] < 0 ? -INFINITY : (m[t][e] + lg2(l[t][e])) * 0.6931471805599453f;
 #pragma unroll
-            for (int i = 0; i < kMt / 4; ++i)
-              d4[i] = make_float4(o[4 * i][e + 2 * hi], o[4 * i + 1][e + 2 * hi], o[4 * i + 2][e + 2 * hi], o[4 * i + 3][e + 2 * hi]);
-          } else if (row < rows) {
-            uint32_t h[kMt / 2];
+          for (int hi = 0; hi < 2; ++hi) {
+            // D = 128: rows g of tile i are channels 16 g + i, rows g + 8 channels 16 g + 8 + i; D = 64: 8 g + i and 8 g + 4 + i
+            const int ch = (2 * g + hi) * kMt, x = e + 2 * hi;
+            if (!whole) {
+              float4* d4 = reinterpret_cast<float4*>(dst + row * C::kPitch + ch);
 #pragma unroll
-            for (int i = 0; i < kMt / 2; ++i) h[i] = pack_h2(o[2 * i][e + 2 * hi] * inv, o[2 * i + 1][e + 2 * hi] * inv);
-            __half* y = a.out + to * D + ch;
-            if constexpr (kMt == 8)
-              *reinterpret_cast<uint4*>(y) = make_uint4(h[0], h[1], h[2], h[3]);
-            else
-              *reinterpret_cast<uint2*>(y) = make_uint2(h[0], h[1]);
+              for (int i = 0; i < kMt / 4; ++i)
+                d4[i] = make_float4(o[t][4 * i][x], o[t][4 * i + 1][x], o[t][4 * i + 2][x], o[t][4 * i + 3][x]);
+            } else if (row < rows) {
+              uint32_t h[kMt / 2];
+#pragma unroll
+              for (int i = 0; i < kMt / 2; ++i) h[i] = pack_h2(o[t][2 * i][x] * inv, o[t][2 * i + 1][x] * inv);
+              __half* y = a.out + to * D + ch;
+              if constexpr (kMt == 8)
+                *reinterpret_cast<uint4*>(y) = make_uint4(h[0], h[1], h[2], h[3]);
+              else
+                *reinterpret_cast<uint2*>(y) = make_uint2(h[0], h[1]);
+            }
           }
         }
-      }
       at += here;
       if (at < r1) {
         u.s = u.n - 1;
@@ -494,21 +520,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
   grid_dependency_wait();
   if (chains == 0) return;
   float4* fac = reinterpret_cast<float4*>(smem + C::kOffFac);
-  for (int i = tid; i < 2 * kW * kFewRows; i += C::kThreads) {
-    const int p = i / kFewRows, row = i % kFewRows, w = p < kW ? p : p - kW;
+  for (int i = tid; i < 2 * kW * C::kRows; i += C::kThreads) {
+    const int p = i / C::kRows, row = i % C::kRows, w = p < kW ? p : p - kW;
     if (!((p < kW ? has_f : has_l) >> w & 1u)) continue;
     const int ch = p < kW ? 31 - __clz(chains & ((2u << w) - 1u)) : w + 1, w_end = chain_end(ch);
     float top = kNoMax;
-    if (ch > 0) top = ml[(kW + ch - 1) * kFewRows + row].x;
+    if (ch > 0) top = ml[(kW + ch - 1) * C::kRows + row].x;
 #pragma unroll 4
-    for (int w2 = ch; w2 <= w_end; ++w2) top = fmaxf(top, ml[w2 * kFewRows + row].x);
+    for (int w2 = ch; w2 <= w_end; ++w2) top = fmaxf(top, ml[w2 * C::kRows + row].x);
     const float2 x = ml[i];
     const float f = ex2(x.x - top);
     fac[i] = make_float4(f, x.y * f, top, 0.f);
   }
   __syncthreads();
-  for (int i = tid; i < __popc(chains) * kFewRows * (D / 4); i += C::kThreads) {
-    const int n = i / (kFewRows * (D / 4)), row = i / (D / 4) % kFewRows, q4 = i % (D / 4) * 4;
+  for (int i = tid; i < __popc(chains) * C::kRows * (D / 4); i += C::kThreads) {
+    const int n = i / (C::kRows * (D / 4)), row = i / (D / 4) % C::kRows, q4 = i % (D / 4) * 4;
     unsigned rest = chains;
     for (int x = 0; x < n; ++x) rest &= rest - 1u;
     const int ch = __ffs(rest) - 1, w_end = chain_end(ch);
@@ -523,9 +549,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
       x.x = fmaf(z.x, f.x, x.x), x.y = fmaf(z.y, f.x, x.y), x.z = fmaf(z.z, f.x, x.z), x.w = fmaf(z.w, f.x, x.w);
       ls += f.y, top = f.z;
     };
-    if (ch > 0) add(fac[(kW + ch - 1) * kFewRows + row], reinterpret_cast<const float*>(smem + (ch - 1) * kS * C::kStepBytes));
+    if (ch > 0) add(fac[(kW + ch - 1) * C::kRows + row], reinterpret_cast<const float*>(smem + (ch - 1) * kS * C::kStepBytes));
 #pragma unroll 4
-    for (int w = ch; w <= w_end; ++w) add(fac[w * kFewRows + row], join + w * kFewRows * C::kPitch);
+    for (int w = ch; w <= w_end; ++w) add(fac[w * C::kRows + row], join + w * C::kRows * C::kPitch);
     if (whole) {
       const int r = row / a.G;
       const bool blind = k.first + r < 0;  // sees nothing
@@ -541,15 +567,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) attn_steps_i4_kernel(cons
   }
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch(const StepArgs& a, int ctas, cudaStream_t s) {
-  using C = Cfg<D>;
+  using C = Cfg<D, NT>;
   static std::atomic<bool> ready[64];  // per device; racing first calls set the same attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(attn_steps_i4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(attn_steps_i4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
   }
@@ -563,13 +589,14 @@ cudaError_t launch(const StepArgs& a, int ctas, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_steps_i4_kernel<D>, a);
+  return cudaLaunchKernelEx(&cfg, attn_steps_i4_kernel<D, NT>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_steps_i4(const StepArgs& a, int D, int ctas, cudaStream_t s) {
-  return D == 128 ? launch<128>(a, ctas, s) : launch<64>(a, ctas, s);
+  if (a.few * a.G <= 8) return D == 128 ? launch<128, 1>(a, ctas, s) : launch<64, 1>(a, ctas, s);
+  return D == 128 ? launch<128, 2>(a, ctas, s) : launch<64, 2>(a, ctas, s);
 }
 
 }  // namespace wql
