@@ -35,7 +35,6 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kNextWarp = 11, kConvWarp = 12;
 constexpr int kLead = 1;          // rounds that stand for an item's own cost
 constexpr float kTop = 7.0f;         // the largest weight after a rescale is 2^7
 constexpr float kMost = 32768.f;     // and a step whose weights come to more than 2^15 asks for the next,
-constexpr float kGrown = 8.0f;       // or one whose maximum passed the last by 2^8
 constexpr float kLarge = 1048576.f;  // from here on scores are rounded before the maximum is subtracted, as it was
 constexpr float kNoMax = -3e38f;     // the maximum of keys whose scores are all minus infinity
 // registers per thread: launched with 96; two warpgroups for the softmax, two convert, one does the rest
@@ -697,11 +696,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
             uint32_t v[32];
             tmem_ld_32x32b_x32(ts + 32 * i, v);
             tmem_ld_wait();
-            if (C::kBeside && i == 3) {
-              tc_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sfree[x]);
-            }
             float f[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
@@ -713,26 +707,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
             for (int e = 0; e < 32; e += 2) add2(a0, a1, f[e], f[e + 1]), w[i][e / 2] = pack_h2(f[e], f[e + 1]);
           }
         };
+        if (r == 0) m = fmaxf(row_max(), kNoMax);
+        weights(c);
+        const bool more = a0 + a1 > kMost || fabsf(m) > kLarge;
+        if (__any_sync(0xffffffffu, more)) {
+          if (C::kBeside && pcount > 0 && !wait(&pfree[x], pcount - 1)) break;  // O is that of the steps before
+          tc_fence_after_sync();
+          weights(raise(row_max(), more));
+        }
         if constexpr (C::kBeside) {
-          // The next S waits for this one to be read, so the maximum is looked for first and S not needed any more afterwards.
-          const float top = row_max();
-          float mul = c;
-          if (r == 0) m = fmaxf(top, kNoMax);
-          const bool more = top - m > kGrown || fabsf(m) > kLarge;
-          if (__any_sync(0xffffffffu, more)) {
-            if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;  // O is that of the steps before
-            tc_fence_after_sync();
-            mul = raise(top, more);
-          }
-          weights(mul);
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[x]);
           if (pcount > 0 && !wait(&pfree[x], pcount - 1)) break;  // the last P has been used
           ++pcount;
           tc_fence_after_sync();
-        } else {
-          if (r == 0) m = fmaxf(row_max(), kNoMax);
-          weights(c);
-          const bool more = a0 + a1 > kMost || fabsf(m) > kLarge;
-          if (__any_sync(0xffffffffu, more)) weights(raise(row_max(), more));
         }
         l0 += a0, l1 += a1;
 #pragma unroll

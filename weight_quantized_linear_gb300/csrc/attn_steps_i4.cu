@@ -31,9 +31,11 @@ constexpr float kTop = 7.0f, kRaise = 15.0f;
 template <int D, int NT>  // NT: rows by eight
 struct Cfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = D == 128 && NT == 2 ? 11 : 15, kThreads = 32 * (kWarps + 1);
+  // As many as registers and rings allow.  Heads of 128: 15 warps with 128 registers and two stages take 80 us for 76 (64 single
+  // tokens), nine with four stages 87; heads of 64: 13 warps 69 us for 65, 11 68.
+  static constexpr int kWarps = D == 128 ? 11 : 15, kThreads = 32 * (kWarps + 1);
   static constexpr int kStepBytes = kStep / kKvBlock * KvI4<D>::kBytes;
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kStages = D == 64 ? 4 : NT == 1 ? 3 : 2;
   static constexpr int kPitch = D + 4;                                          // floats per row of a part
   static constexpr int kOffJoin = kWarps * kStages * kStepBytes;                // [kWarps][rows][kPitch]: first parts
   static constexpr int kOffMl = kOffJoin + kWarps * kRows * kPitch * 4;      // [first, last part][kWarps][rows] {m, l}
@@ -145,8 +147,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_steps_i4_kernel(
       if (w < warp) incl += s_sum[w];
       total += s_sum[w];
     }
-    // at least two steps for every warp: a short batch uses fewer CTAs and has fewer parts to join
-    const long long quota = max((total + gridDim.x - 1) / gridDim.x, (long long)(2 * kW));
+    // at least a step for every warp: a short batch uses fewer CTAs and has fewer parts to join
+    const long long quota = max((total + gridDim.x - 1) / gridDim.x, (long long)kW);
     n0 = min(quota * blockIdx.x, total), n1 = min(n0 + quota, total);
     long long at = incl - mine;
     const long long each = (n1 - n0 + kW - 1) / kW;
