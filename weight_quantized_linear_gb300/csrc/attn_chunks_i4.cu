@@ -5,19 +5,41 @@
 //   out = sum_t softmax_t(scale q . k[t]) v[t],   lse = ln sum_t exp(scale q . k[t]),   t <= kv_len - n + r
 // with k and v of K/V head h / (Hq / Hkv): code * s + lo, rounded to fp16, which is what the matrix product takes.
 //
+// This file has the kernel for chunks of many rows and the one that joins parts; sequences with up to 8 or 16 rows per K/V head
+// (tokens times the G query heads of a group) go to attn_steps_i4.cu, where 128-row tiles would be nearly empty.
+//
 // A tile is 128 / G tokens of one K/V head, each with its G query heads: up to 128 rows, all of which read the same keys.
 // A CTA works on two tiles of consecutive tokens at a time.  Per 128 keys, the tensor cores compute S = Q K^T into tensor
-// memory, the tile's four softmax warps turn it into weights P (thread r owns row r), written over S as fp16, and the tensor
-// cores add P V to the tile's accumulator.  Where a sequence's last tokens fill one tile only, as in a decode step, both
-// halves of the CTA work on that tile, one on the even and one on the odd key tiles, and are joined in tensor memory.
+// memory, the tile's four softmax warps turn it into weights P (thread r owns row r, so neither maximum nor sum needs an
+// exchange) as fp16, and the tensor cores add P V to the tile's accumulator.  With heads of 128 tensor memory is full, P is written
+// over S and the two tiles take turns at the tensor cores, one's softmax beside the other's products; with heads of 64 P has
+// columns of its own and the next S need not wait for it.  Where a sequence's last tokens fill one tile only, both halves of the
+// CTA work on that tile, one on the even and one on the odd key tiles, and are joined in tensor memory.
+//
+// The weights are computed by the maximum as it was and kept in registers until their sum has said that none is too large for
+// fp16; only then is a new maximum looked for and the accumulator rescaled.  Looking for it in every step cost the time of reading
+// S twice (512 tokens behind 15872: 143 -> 135 us; mixed batch with heads of 64: 128 -> 126).
 //
 // K and V reach the tensor cores by way of eight warps that make fp16 numbers of the codes: bulk copies bring the blocks of
-// 64 tokens into a small ring, a thread takes one key's row there, and writes it as a row of a swizzled operand tile.  That is
-// 3.5 instructions per pair of values, done once for the 256 rows of a pair of tiles.
+// 64 tokens as they are into a small ring, a thread takes one key's row there and writes it as a row of a swizzled operand tile.
+// That is 3.5 instructions per pair of values, done once for the 256 rows of a pair of tiles.
 //
 // The rounds (one key tile, or two where both halves share a tile) of all items, one behind the other, are divided evenly
-// over the CTAs, whatever the lengths.  What a CTA computes of an item that it shares with others goes to the workspace as
-// (O, m, l), and a second kernel joins the parts in their order.
+// over the CTAs, one per SM, whatever the lengths: a CTA finds its first item by closed forms for the rounds before an item, not by
+// walking.  What a CTA computes of an item that it shares with others goes to the workspace as (O, m, l), and the joining kernel
+// adds the parts in their order, so results do not depend on who did what.
+//
+// Bound by the tensor cores' and the softmax's chain: with heads of 128 a round of two tiles takes about 3900 cycles for 2048 of
+// products: a tile's softmax 1300, its turn, and 1300 in which its two products hold the tensor cores, since Q K^T and P V read
+// both fp16 operand tiles from shared memory while the converting warps write the next (without the conversion 111 us instead of
+// 136).  With heads of 64 a round takes 3600 for 1024: both softmaxes at once, 1024 of it exponentials.
+// Measured on GB300 through the Python call, rows of 32 query heads:
+//   512 tokens behind 15872, 8 K/V heads of 128     135 us   1000 TFLOP/s, 52 % of the measured peak
+//   4 x 2048 tokens over 2048 to 8190, 32 heads     558 us    985 TFLOP/s
+//   24 requests up to 6000 tokens, three chunks of about 500 among single tokens, 8 K/V heads of 64     126 us
+//   16 tokens behind 700, 32 heads                  14.4 us, launches and latency (attn_steps_i4.cu)
+// What did not pay: the conversion's loop unrolled twice or four times (142 and 150 us for 135: the warps' code no longer stays in
+// the instruction caches), no turns (163), 16-column pieces of the softmax, three operand slots and six raw ones.
 #include <atomic>
 #include <climits>
 

@@ -1,16 +1,27 @@
 // attn_steps_i4.cu -- attention over the paged 4-bit KV cache for chunks of a few rows: single tokens, drafted ones.
 //
 // attention_chunks_kv_i4's formulas for the sequences whose rows of a K/V head, tokens times query heads, are 8 NT or fewer.
-// Tiles of 128 rows would be mostly empty and spend their time on them (64 single tokens with four heads each: 195 us), so
-// here rows are the narrow side of mma.sync products, and keys and channels the wide one:
+// Rows are the narrow side of mma.sync products here, keys and channels the wide one:
 //   S^T (16 keys x 8 rows) = K Q^T, then O^T (16 channels x 8 rows) += V^T P,
-// with K and V converted from codes in registers.  Products' inner indices may be in any order as long as both operands agree:
-// a thread takes its key's codes as they lie in a word (0, 4), (1, 5) .., and Q's channels are put into that order once; for
-// V two keys' words are merged by halves first, which makes the same masks yield pairs of keys.
+// with K and V converted from codes in registers and rounded to fp16, as the formulas ask.  A product's inner indices may be in any
+// order as long as both operands agree: a thread takes its key's codes as they lie in a word, (0, 4), (1, 5) .., and Q's channels
+// are put into that order once; for V two keys' words are merged by halves first, so that the same masks yield pairs of keys.
+// Both products leave rows 2c and 2c + 1 in the threads that hold lane % 4 = c, so the maximum, the sum and the rescaling of the
+// accumulator need an exchange only when a weight passes 2^15 and at the end.
 //
 // A unit is a sequence and K/V head, a step 32 of its keys.  The steps of all units, in order, are divided evenly over the
 // CTAs, one per SM, and a CTA's over its warps, each a run with a ring of copies of its own, which a lane of one more warp
 // keeps filled.  A unit's parts are joined in shared memory at the CTA's end, those of CTAs by the joining kernel.
+//
+// Bound by instructions: about 360 per warp and 16 keys of heads of 128 (208 of them masks, subtractions and multiply-adds that
+// make numbers of codes, 16 products), 59 % of the issue slots used, DRAM at half its rate.  mma.sync, not tcgen05: its operands
+// come out of registers, and they use a fifth of its rate.  Measured on GB300 through the Python call, or in a graph (g):
+//   64 single tokens over up to 8192 (290 MB), 32 / 8 heads of 128          76 us, 3.8 TB/s (in 128-row tiles 197)
+//   4 drafted tokens x 32 over up to 6000, 32 / 8 heads of 64 (66 MB)       37 us g (78)
+//   64 single tokens of 16 heads per K/V head of 128 (89 MB)                43 us g (72)
+//   one row of 700 tokens, 32 heads of 128                                  10.7 us g (14.5), latency of two launches
+// attention_kv_i4, which takes all sequences' rows alike, does not round the values and gives no lse, takes 60, 33, 39 and 6.1.
+// Eight rows where they are enough: with the products for sixteen the first of these takes 100 us.
 #include <atomic>
 #include <climits>
 #include <type_traits>
