@@ -236,3 +236,39 @@ def test_from_planned_pages_to_decode_over_what_is_kept(wql, D, Hq, Hkv):
             slack = float((q[b, h].double().abs() @ kk.abs().T).max()) * D ** -0.5 * 2.0 ** -11 * 2
             assert bool(((y[b, h].double() - oo[0]).abs() <= bb[0] + (slack + 2.0 ** -10) * float(vv.abs().max())).all())
     assert bool((w2[torch.arange(B), :, lens2.long()] > 0).all())  # the new token looked at itself
+
+
+@pytest.mark.parametrize("B,H,n,budget", [(20, 16, 900, 400), (5, 8, 900, 700), (3, 8, 2000, 1500), (30, 16, 2000, 300), (2, 8, 4000, 2000),
+                                          (3, 8, 7000, 3000), (10, 8, 4000, 1000), (10, 8, 20000, 500), (9, 5, 40000, 700), (40, 8, 9000, 200),
+                                          (2, 8, 16000, 16000), (2, 4, 70000, 9000)])
+def test_heads_and_widths_that_choose_the_ctas(wql, B, H, n, budget):
+    # few and many heads with narrow and wide tables, so that heads have one to eight CTAs and read their weights once or again
+    r = random.Random(B * n)
+    lens = [max(1, n - (n * i) // (2 * B) - r.randrange(0, 40)) for i in range(B)]
+    lens[-1] = 5
+    g = torch.Generator().manual_seed(n)
+    D, ps = 64, 64
+    held = [-(-x // ps) for x in lens]
+    width, nw = -(-n // ps), -(-budget // ps)
+    table = torch.full((B, width), -1, dtype=torch.int32)
+    for b, m in enumerate(held):
+        table[b, :m] = torch.randperm(64, generator=g).repeat(m // 64 + 1)[:m].int()  # a pool of 64 pages, read again and again
+    cache = torch.randint(0, 256, (64 + B * nw, H, ps // 16, 16 * (D + 8)), generator=g, dtype=torch.uint8).cuda()
+    before, table = cache.clone(), table.cuda()
+    new_table = (64 + torch.arange(B * nw)).view(B, nw).int().cuda()
+    w = torch.randint(-40, 400, (B, H, width * ps), generator=g).float().cuda() / 16  # many equal ones
+    kept, kw, kn = wql.kv_evict_i4(w, cache, table, i32(lens), new_table, budget, 20)
+    wql.device_status()
+    assert kn.tolist() == [min(x, budget) for x in lens] and torch.equal(cache[:64], before[:64])
+    for b, x in enumerate(lens):
+        m = min(x, budget)
+        new = min(20, budget, x)
+        # of the others the greatest, of equal ones the first: a stable sort
+        order = torch.sort(w[b, :, :x - new], dim=-1, descending=True, stable=True).indices[:, :m - new]
+        want = torch.cat([order.sort(-1).values, torch.arange(x - new, x, device="cuda").expand(H, new)], -1)
+        assert torch.equal(kept[b, :, :m].long(), want) and bool((kept[b, :, m:] == -1).all()), b
+        assert torch.equal(kw[b, :, :m], w[b].gather(1, want)) and not bool(kw[b, :, m:].any())
+        i = torch.arange(m, device="cuda")[:, None].expand(m, H)
+        src = want.T
+        assert torch.equal(rows(cache, new_table[b].long()[i // ps] * ps + i % ps, H, D),
+                           rows(before, table[b].long()[src // ps] * ps + src % ps, H, D)), b

@@ -290,16 +290,31 @@ cudaError_t launch(const Args& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kv_evict_kernel<D, kThreads, kPer, kCtas>, a);
 }
 
-// Tokens as the table's width allows for decide how many threads a head gets, so that they fit the registers.  Many heads get
-// smaller clusters, which read longer contexts again for each digit, rather than wait for room.
+// The table's width, which bounds the lengths, and the number of heads decide.  A head gets as many CTAs as fit the card with those of
+// all heads, two per SM, since a head's search is a chain of latencies and a single CTA moves 16 rows at a time per warp; and
+// registers for all its tokens where it can, else they are read again for each digit.  On GB300, us (threads x tokens of each x CTAs;
+// tokens of a head, half of them kept unless said):
+//     32 heads of  1000, 900 kept   512x2x1  9.7   256x4x1 12.4   256x4x4 12.6   512x4x1 10.5
+//      8 heads of  2000             512x4x1 12.8   256x16x1 22.4  512x4x4 13.4
+//      8 heads of  4000             512x4x4 13.5   512x4x8 12.4   256x16x1 25.7    (32 heads: 13.7, 15.9, 25.7)
+//    128 heads of  4000             512x4x2 23.0   512x4x4 35.4   256x16x1 36.9
+//    512 heads of  4000             256x16x1 78.4  512x4x1 82.5   512x4x2 103.5
+//      8 heads of 16000             512x4x8 17.0   512x16x8 24.0  512x16x2 38.7
+//    128 heads of 16000, 4000 kept  512x16x2 52.4  512x16x4 73.1  512x16x8 112.5
+//     64 heads of 60000, 8000 kept  512x16x4 71.9  512x16x8 83.2  512x16x2 94.3
+//      8 heads of 120001, 16384 kept  1024x16x8 34.4  512x16x8 46.6
 template <int D>
 cudaError_t launch(const Args& a, cudaStream_t s) {
-  const long long heads = (long long)a.B * a.H, sms = num_sms();
-  if (a.cap <= 1024) return launch<D, 256, 4, 1>(a, s);
-  if (a.cap <= 4096) return launch<D, 256, 16, 1>(a, s);
-  if (a.cap <= 16384 || heads * 8 > 4 * sms) return launch<D, 512, 16, 2>(a, s);
-  if (a.cap <= 65536) return launch<D, 512, 16, 8>(a, s);
-  return launch<D, 1024, 16, 8>(a, s);
+  const long long heads = (long long)a.B * a.H, room = 2LL * num_sms();
+  if (a.cap <= 1024) return heads <= room ? launch<D, 512, 2, 1>(a, s) : launch<D, 256, 4, 1>(a, s);
+  if (a.cap <= 2048) return launch<D, 512, 4, 1>(a, s);
+  if (heads * 8 <= room && a.cap > 4096) {
+    if (a.cap <= 16384) return launch<D, 512, 4, 8>(a, s);
+    return a.cap <= 65536 ? launch<D, 512, 16, 8>(a, s) : launch<D, 1024, 16, 8>(a, s);
+  }
+  if (heads * 4 <= room) return a.cap <= 8192 ? launch<D, 512, 4, 4>(a, s) : launch<D, 512, 16, 4>(a, s);
+  if (heads * 2 <= room) return a.cap <= 4096 ? launch<D, 512, 4, 2>(a, s) : launch<D, 512, 16, 2>(a, s);
+  return launch<D, 256, 16, 1>(a, s);
 }
 
 }  // namespace
