@@ -24,9 +24,10 @@
 // 64 tokens as they are into a small ring, a thread takes one key's row there and writes it as a row of a swizzled operand tile.
 // That is 3.5 instructions per pair of values, done once for the 256 rows of a pair of tiles.
 //
-// The rounds (one key tile, or two where both halves share a tile) of all items, one behind the other, are divided evenly
-// over the CTAs, one per SM, whatever the lengths: a CTA finds its first item by closed forms for the rounds before an item, not by
-// walking.  What a CTA computes of an item that it shares with others goes to the workspace as (O, m, l), and the joining kernel
+// The key tiles of all items, one behind the other, are divided evenly over the CTAs, one per SM, whatever the lengths: a CTA finds
+// its first item by closed forms for what is before an item, not by walking.  One of both tiles of rows counts as much as one where
+// the halves share a tile, although two of those are worked on at once: the conversion is the same, and two take 1.6 to 1.7 times as
+// long (counted as one, the CTAs that had them ended last, mixed batch 126 us for 102).  What a CTA computes of an item that it shares with others goes to the workspace as (O, m, l), and the joining kernel
 // adds the parts in their order, so results do not depend on who did what.
 //
 // Bound by the tensor cores' and the softmax's chain: with heads of 128 a round of two tiles takes about 3900 cycles for 2048 of
@@ -35,8 +36,8 @@
 // 136).  With heads of 64 a round takes 3600 for 1024: both softmaxes at once, 1024 of it exponentials.
 // Measured on GB300 through the Python call, rows of 32 query heads:
 //   512 tokens behind 15872, 8 K/V heads of 128     135 us   1000 TFLOP/s, 52 % of the measured peak
-//   4 x 2048 tokens over 2048 to 8190, 32 heads     558 us    985 TFLOP/s
-//   24 requests up to 6000 tokens, three chunks of about 500 among single tokens, 8 K/V heads of 64     126 us
+//   4 x 2048 tokens over 2048 to 8190, 32 heads     550 us   1000 TFLOP/s
+//   24 requests up to 6000 tokens, three chunks of about 500 among single tokens, 8 K/V heads of 64     102 us
 //   16 tokens behind 700, 32 heads                  14.4 us, launches and latency (attn_steps_i4.cu)
 // What did not pay: the conversion's loop unrolled twice or four times (142 and 150 us for 135: the warps' code no longer stays in
 // the instruction caches), no turns (163), 16-column pieces of the softmax, three operand slots and six raw ones.
@@ -54,7 +55,7 @@ constexpr int kTile = 128, kHalf = 64;  // keys of a tile, and rows at most; key
 // warps 0-3, 4-7: softmax of tiles 0, 1; 8: copies; 9, 10: products of tiles 0, 1; 11: next item; 12-19: K and V to fp16
 constexpr int kThreads = 640;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kNextWarp = 11, kConvWarp = 12;
-constexpr int kLead = 1;          // rounds that stand for an item's own cost
+constexpr int kLead = 1;             // key tiles that stand for an item's own cost
 constexpr float kTop = 7.0f;         // the largest weight after a rescale is 2^7
 constexpr float kMost = 32768.f;     // and a step whose weights come to more than 2^15 asks for the next,
 constexpr float kLarge = 1048576.f;  // from here on scores are rounded before the maximum is subtracted, as it was
@@ -99,7 +100,7 @@ struct Args {
   unsigned* err;
 };
 
-// Rounds of an item and what is before it in its sequence.  Tokens [A p, A p + A) of a chunk of n are item p, A = 2 a.tokens;
+// Key tiles of an item and what is before it in its sequence.  Tokens [A p, A p + A) of a chunk of n are item p, A = 2 a.tokens;
 // its last row sees first + A p + (its tokens) keys.
 struct Shape {
   int first, n, A, items;
@@ -108,8 +109,7 @@ struct Shape {
   __device__ __forceinline__ int count(int p) const { return min(n - p * A, A); }
   __device__ __forceinline__ int tiles(int p) const { return max(first + p * A + count(p) - 1, 0) / kTile + 1; }  // of keys
   __device__ __forceinline__ bool twin(int p) const { return 2 * count(p) <= A; }
-  __device__ __forceinline__ int rounds(int p) const { return twin(p) ? (tiles(p) + 1) / 2 : tiles(p); }
-  // Rounds (kLead more for each) of items 0 .. p - 1, all of them whole, p < items: the sum over i of max(1, ceil(x / 128)) with
+  // Key tiles (kLead more for each) of items 0 .. p - 1, all of them whole, p < items: the sum over i of max(1, ceil(x / 128)) with
   // x = first + A (i + 1).
   __device__ long long before(int p) const {
     if ((A & (A - 1)) == 0) {  // the usual numbers of heads, and no division
@@ -142,7 +142,7 @@ struct Shape {
     const long long q = n >> s;
     return (q * (q - 1) / 2 << s) + q * (n & ((1LL << s) - 1));
   }
-  __device__ long long all() const { return items ? before(items - 1) + rounds(items - 1) + kLead : 0; }
+  __device__ long long all() const { return items ? before(items - 1) + tiles(items - 1) + kLead : 0; }
   static __device__ __forceinline__ long long floor_div(long long a, long long b) { return a >= 0 ? a / b : -1; }
 };
 
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
   grid_dependency_wait();  // everything before this line overlaps the end of the preceding kernel
   grid_dependents_launch();
 
-  // ---- this CTA's range [w0, w1) of the rounds of all items, in the order of sequences, their items, K/V heads ----
+  // ---- this CTA's range [w0, w1) of the key tiles of all items, in the order of sequences, their items, K/V heads ----
   long long total, w0, w1;
   {
     const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
@@ -534,23 +534,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
           }
           p = lo;
           const long long rest = s_off - sh.before(p) * a.Hkv;
-          const int cost = sh.rounds(p) + kLead;
+          const int cost = sh.tiles(p) + kLead;
           kvh = (int)(rest / cost), s = (int)(rest % cost);
         }
         long long left = w1 - w0;
         while (left > 0 && ok) {
-          const int rounds = sh.rounds(p), cost = rounds + kLead;
+          const int tiles = sh.tiles(p), cost = tiles + kLead;
           const int take = (int)min((long long)(cost - s), left);
           const int r0 = max(s - kLead, 0), r1 = s + take - kLead;
           if (r1 > r0) {
             Item t;
             t.row0 = c.start + p * sh.A, t.tokens = sh.count(p), t.seen = c.first + p * sh.A, t.len = c.len, t.kvh = kvh, t.b = b;
-            const int tiles = sh.tiles(p), k = sh.twin(p) ? 2 : 1;
             t.twin = sh.twin(p);
-            t.j0 = r0 * k, t.j1 = min(r1 * k, tiles);
+            t.j0 = r0, t.j1 = r1;
             t.n0 = t.twin ? tiles : max(t.seen + a.tokens - 1, 0) / kTile + 1, t.n1 = tiles;
-            t.slot = r0 > 0 ? 0 : r1 < rounds ? 1 : -1;
-            if (t.slot == 0) went_on = r1 == rounds ? 2 : 1;
+            t.slot = r0 > 0 ? 0 : r1 < tiles ? 1 : -1;
+            if (t.slot == 0) went_on = r1 == tiles ? 2 : 1;
             if (t.slot == 1) begun = make_int4(t.row0, t.tokens, t.seen, kvh);
             put(t);
           }

@@ -42,7 +42,7 @@
 // scores, 8 for the values, one for the weights' sum; 9 with heads of 64), which the SM does in a third of the time in
 // which HBM delivers the block.  That holds for decode steps and drafted tokens.  A chunk of a prompt has many more rows, and
 // every 16 of them read the cache again: 512 tokens behind 8192 cached ones take 314 us (128 tokens 87, 16 tokens 25; 32
-// query and 8 K/V heads of 128), where tiles of 128 rows would read it an eighth as often.
+// query and 8 K/V heads of 128); attention_chunks_kv_i4 is for those.
 //
 // Measured on GB300: 64 ragged contexts up to 8192 tokens, 8 K/V heads of 128 (290 MB) 60 us, of which 47 stream the
 // cache at 6.2 TB/s and the rest is finding the range, joining and the launch; one context of 120001 tokens (131 MB) 31 us;
