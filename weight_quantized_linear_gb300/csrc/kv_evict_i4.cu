@@ -12,13 +12,13 @@
 // latency and the move bandwidth: where there are many heads, some search while others move.
 // Where a head has more tokens than its CTAs have registers for, they are read again for every digit.
 //
-// Bound by that chain where heads are few (the search of 4000 tokens about 8 us, a block of rows per warp under 1 us), and by the
-// move where they are many: rows of 64 bytes from all over the cache, 5.2 to 5.5 TB/s while it lasts.  Measured on GB300:
+// Bound by that chain where heads are few, and by the move where they are many: rows of 64 bytes from all over the cache, 5.2 to
+// 5.5 TB/s while it lasts, after a search of about 18 us for heads of 4096 tokens.  Measured on GB300:
 //   64 contexts up to 4096, half of each kept, 8 heads of 128          61 us, 3.7 TB/s over all
 //   one context of 120001, 16384 kept, 8 heads of 128                  35 us
 //   24 contexts up to 3001, 1777 kept, 32 heads of 64                  47 to 49 us
 //   4 contexts of 1024, 960 kept, 8 heads of 128                       10 us on the GPU, 18 to 27 through the Python call
-// The first version, with a launch for each digit's counts, for the places and for the move, took 124, 335, 110 and 39 us.
+// Selecting with one CTA per head, digits of weights read again from memory, and moving in a second kernel took 124, 335, 110 and 39.
 #include "internal.h"
 #include "kv_i4.cuh"
 
