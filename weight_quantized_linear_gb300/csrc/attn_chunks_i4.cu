@@ -27,8 +27,9 @@
 // The key tiles of all items, one behind the other, are divided evenly over the CTAs, one per SM, whatever the lengths: a CTA finds
 // its first item by closed forms for what is before an item, not by walking.  One of both tiles of rows counts as much as one where
 // the halves share a tile, although two of those are worked on at once: the conversion is the same, and two take 1.6 to 1.7 times as
-// long (counted as one, the CTAs that had them ended last, mixed batch 126 us for 102).  What a CTA computes of an item that it shares with others goes to the workspace as (O, m, l), and the joining kernel
-// adds the parts in their order, so results do not depend on who did what.
+// long (counted as one, the CTAs that had them ended last, mixed batch 126 us for 102).  What a CTA computes of an item that it
+// shares with others goes to the workspace as (O, m, l), and the joining kernel adds the parts in their order, so results do not
+// depend on who did what.
 //
 // Bound by the tensor cores' and the softmax's chain: with heads of 128 a round of two tiles takes about 3900 cycles for 2048 of
 // products: a tile's softmax 1300, its turn, and 1300 in which its two products hold the tensor cores, since Q K^T and P V read
@@ -40,7 +41,7 @@
 //   24 requests up to 6000 tokens, three chunks of about 500 among single tokens, 8 K/V heads of 64     102 us
 //   16 tokens behind 700, 32 heads                  14.4 us, launches and latency (attn_steps_i4.cu)
 // What did not pay: the conversion's loop unrolled twice or four times (142 and 150 us for 135: the warps' code no longer stays in
-// the instruction caches), no turns (163), 16-column pieces of the softmax, three operand slots and six raw ones.
+// the instruction caches), no turns (163).
 #include <atomic>
 #include <climits>
 
