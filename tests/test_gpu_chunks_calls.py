@@ -468,3 +468,27 @@ def test_evictions_at_once_and_captured(wql):
             m = min(n, budget)
             assert int(nl[b]) == m and kept[b, :, :m].tolist() == rows[b] and bool((kept[b, :, m:] == -1).all())
     wql.device_status()
+
+
+def test_ragged_prompts_right_after_allocation(wql):
+    # whole prompts of all lengths in small pages, first read from memory that nothing has touched since it was written: copies that
+    # land late and out of order must not be taken for others of the same slot
+    n, B = 587, 38
+    lens = [max(1, n - (n * r) // B - r % 7) for r in range(B)]
+    for D, Hq, Hkv, ps, seed in ((128, 8, 2, 32, 1), (128, 32, 8, 16, 2), (64, 8, 2, 32, 3)):
+        order = torch.randperm(B, generator=torch.Generator().manual_seed(seed)).tolist()
+        some = [lens[i] for i in order]
+        q, cache, table, cu = cref.case(some, some, Hq, Hkv, D, ps, seed, pad=3)
+        o, ob, z, zb = cref.chunks(q, cache, table, cu, some)
+        first = None
+        for _ in range(20):
+            cold, other, lse = cache.clone(), torch.empty((1 << 28,), dtype=torch.uint8, device="cuda"), torch.zeros(q.shape[:2], device="cuda")
+            other.zero_()  # the caches hold something else
+            y = wql.attention_chunks_kv_i4(q, cold, table, i32(cu), i32(some), lse=lse)
+            got = [y[:cu[-1]].view(torch.int16), lse[:cu[-1]].view(torch.int32)]
+            if first is None:
+                first = got
+                within(y[:cu[-1]], o[:cu[-1]], ob[:cu[-1]], D)
+                within(lse[:cu[-1]], z[:cu[-1]], zb[:cu[-1]], D)
+            assert same(got, first)
+    wql.device_status()
