@@ -72,10 +72,10 @@ struct Cfg {
   static constexpr int kTileBytes = kBoxes * kBox;  // a Q, K or V tile
   static constexpr int kSlots = D == 128 ? 4 : 8;   // of K and V tiles
   static constexpr int kRawBytes = kHalf / kKvBlock * KvI4<D>::kBytes;  // blocks as they are, of half a tile of keys
-  static constexpr int kRaw = D == 128 ? 3 : 6;
-  // Where the groups that convert take turns at a raw slot, each would see every other phase of its barrier only, and could take an
-  // old one for the next: there both release every half, the one that does not convert it when it has seen it land.
-  static constexpr bool kBothSee = kRaw % 2 != 0;
+  // One raw slot for each of the two groups that convert, or three.  With an odd number a group would see every other phase of a slot's
+  // barrier only, and could take an old one for the next.
+  static constexpr int kRaw = D == 128 ? 2 : 6;
+  static_assert(kRaw % 2 == 0, "a raw slot is one group's");
   static_assert(kSlots % 2 == 0, "a slot has K or V, so that its warps meet every phase of its barriers");
   // D = 64 leaves room in tensor memory for P beside S, so that the next S is computed while this one's softmax runs
   static constexpr bool kBeside = D == 64;
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
 
   if (tid == 0) {
     mbar_init(&qbar, 1), mbar_init(&qfree, 2), mbar_init(&done, 2), mbar_init(&half, 4);
-    for (int s = 0; s < C::kRaw; ++s) mbar_init(&raw_full[s], 1), mbar_init(&raw_empty[s], C::kBothSee ? 8 : 4);
+    for (int s = 0; s < C::kRaw; ++s) mbar_init(&raw_full[s], 1), mbar_init(&raw_empty[s], 4);
     for (int s = 0; s < C::kSlots; ++s) mbar_init(&full[s], 4), mbar_init(&empty[s], 2);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&turn[x], 1), mbar_init(&sbar[x], 1), mbar_init(&pbar[x], 4), mbar_init(&obar[x], 1), mbar_init(&ofree[x], 4);
@@ -592,14 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[it & 1]);
         if (tokens == 0) break;
-        auto other = [&](uint32_t h) {  // half tile h, the other group's
-          if (!C::kBothSee) return true;
-          const bool r = wait(&raw_full[h % C::kRaw], (int)(h / C::kRaw));
-          if (r && lane == 0) mbar_arrive(&raw_empty[h % C::kRaw]);
-          return r;
-        };
         for (int j = j0; j < j1; ++j, ++n) {
-          if (group == 1 && !other(2 * n)) break;
           const int row = group * kHalf + key_in, key = j * kTile + row;
           const uint32_t tile = 2 * n + v, slot = tile % C::kSlots, half_n = 2 * n + group, rs = half_n % C::kRaw;
           if (!wait(&raw_full[rs], (int)(half_n / C::kRaw)) || !wait(&empty[slot], (int)(tile / C::kSlots) ^ 1)) break;
@@ -626,7 +619,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunks_i4_kernel(const __gri
           fence_proxy_async_smem();  // the tile for the products, and the codes' reads before the next copy
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[slot]), mbar_arrive(&raw_empty[rs]);
-          if (group == 0 && !other(2 * n + 1)) break;
         }
       }
     }
