@@ -18,10 +18,10 @@
 //
 // The weights are computed by the maximum as it was and kept in registers until their sum has said that none is too large for
 // fp16; only then is a new maximum looked for and the accumulator rescaled.  Looking for it in every step cost the time of reading
-// S twice (512 tokens behind 15872: 143 -> 135 us; mixed batch with heads of 64: 128 -> 126).
+// S twice (512 tokens behind 15872: 143 -> 135 us with three raw slots; mixed batch with heads of 64: 128 -> 126).
 //
 // K and V reach the tensor cores by way of eight warps that make fp16 numbers of the codes: bulk copies bring the blocks of
-// 64 tokens as they are into a small ring, a thread takes one key's row there and writes it as a row of a swizzled operand tile.
+// 64 tokens as they are into a slot of the group that converts them, a thread takes one key's row there and writes it as a row of a swizzled operand tile.
 // That is 3.5 instructions per pair of values, done once for the 256 rows of a pair of tiles.
 //
 // The key tiles of all items, one behind the other, are divided evenly over the CTAs, one per SM, whatever the lengths: a CTA finds
@@ -36,12 +36,12 @@
 // both fp16 operand tiles from shared memory while the converting warps write the next (without the conversion 111 us instead of
 // 136).  With heads of 64 a round takes 3600 for 1024: both softmaxes at once, 1024 of it exponentials.
 // Measured on GB300 through the Python call, rows of 32 query heads:
-//   512 tokens behind 15872, 8 K/V heads of 128     135 us   1000 TFLOP/s, 52 % of the measured peak
-//   4 x 2048 tokens over 2048 to 8190, 32 heads     550 us   1000 TFLOP/s
+//   512 tokens behind 15872, 8 K/V heads of 128     142 us    950 TFLOP/s, 50 % of the measured peak
+//   4 x 2048 tokens over 2048 to 8190, 32 heads     586 us    940 TFLOP/s
 //   24 requests up to 6000 tokens, three chunks of about 500 among single tokens, 8 K/V heads of 64     102 us
 //   16 tokens behind 700, 32 heads                  14.4 us, launches and latency (attn_steps_i4.cu)
-// What did not pay: the conversion's loop unrolled twice or four times (142 and 150 us for 135: the warps' code no longer stays in
-// the instruction caches), no turns (163).
+// What did not pay: the conversion's loop unrolled twice or four times (142 and 150 us for 135, with three raw slots: the warps' code no
+// longer stays in the instruction caches), no turns (163).
 #include <atomic>
 #include <climits>
 
