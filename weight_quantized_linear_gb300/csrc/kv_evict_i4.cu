@@ -145,8 +145,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : kThreads == 51
   int* kept = a.kept + (long long)bh * a.budget;
   float* nw = a.new_weights + (long long)bh * a.new_cap;
   if (rank == 0 && tid == 0 && bh % a.H == 0) a.new_lens[b] = keep;
-  for (long long i = keep + rank * kThreads + tid; i < a.budget; i += kCtas * kThreads) kept[i] = -1;
-  for (long long i = keep + rank * kThreads + tid; i < a.new_cap; i += kCtas * kThreads) nw[i] = 0.f;
+  const long long behind = (long long)keep + rank * kThreads + tid;  // may pass 2^31
+  for (long long i = behind; i < a.budget; i += kCtas * kThreads) kept[i] = -1;
+  for (long long i = behind; i < a.new_cap; i += kCtas * kThreads) nw[i] = 0.f;
   const int rounds = n > 0 ? (n - 1) / (kCtas * kStep) + 1 : 0;  // 1: all tokens are in registers
   // the tokens of a round: a warp has 32 kPer consecutive ones, 32 at a time, so that loads and stores are whole lines
   float x[kPer];
