@@ -496,6 +496,11 @@ wql_status wql_attention_chunks_kv_i4(const uint16_t* q, int64_t q_stride, int T
  * parameters are not finite makes the sums that it belongs to NaN, and so does a row r whose lse is NaN.
  * Sequences, lengths and pages out of range: as there; the sums of a sequence with a bad page are unspecified.
  * A sum, or an entry that one is added to, of less than 2^-126 in magnitude may count as zero.
+ * A weight exp(t), t = scale * q . k - lse, is off by a factor of at most e^d with d = 2^-20 + 2^-22 |t| + (D + 8) 2^-23 |scale|
+ * sum_c |q_c k_c| for the lse that it is given.  What that lse is off comes on top, as d does: an fp32 number by 2^-24 of
+ * itself at least, attention_chunks_kv_i4's by up to 2^-22 of it and of the row's largest score, and by the scores' own error.  So from
+ * scores of about 2^18 on weights say which tokens rather than how much, and from 2^26 on one that should be 1 may be
+ * anything, infinity too: sums of such weights are not worth keeping.
  * workspace: device scratch of at least wql_kv_weights_i4_workspace_bytes() bytes (the current device's), with no contents
  * to keep; calls that may run at the same time need a workspace and weights each.  weights must overlap no input.  Results
  * are deterministic.

@@ -68,7 +68,7 @@ struct Args {
   int width, cap;
   const int *cu, *kv_lens;
   int B;
-  float scale_log2;
+  float scale;
   const float* lse;
   float* weights;
   // the workspace: the unit that each CTA began and left unfinished {sequence, K/V head, unit of it, 1}, whether it went on
@@ -471,16 +471,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rows = rows_of(t, tile), first = t.first + (tile >> a.two) * a.tokens;
         if (!wait(&sfull[x][turn], step >> 1)) break;
         tc_fence_after_sync();
-        // In place and each kind of operation for many values at a time, so that none waits for the one before it.
+        // In place and each kind of operation for many values at a time, so that none waits for the one before it.  The difference
+        // of score and lse comes first, in one operation that rounds nothing but it: log2 e in either before that would round
+        // numbers that may be large, and a weight would be off by a factor e^(2^-23 |lse|).
         auto add = [&](float (&v)[32], int col, int lo, int hi, auto careful) {
           constexpr bool kCareful = decltype(careful)::value;
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             if (kCareful && e >= hi) break;
-            float4 z4 = *reinterpret_cast<const float4*>(z + col + e);
-            mul2(z4.x, z4.y, -kLog2e), mul2(z4.z, z4.w, -kLog2e);
-            fma2v(v[e], v[e + 1], a.scale_log2, z4.x, z4.y);
-            fma2v(v[e + 2], v[e + 3], a.scale_log2, z4.z, z4.w);
+            const float4 z4 = *reinterpret_cast<const float4*>(z + col + e);
+            fma2v(v[e], v[e + 1], -a.scale, z4.x, z4.y), mul2(v[e], v[e + 1], -kLog2e);
+            fma2v(v[e + 2], v[e + 3], -a.scale, z4.z, z4.w), mul2(v[e + 2], v[e + 3], -kLog2e);
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
@@ -613,7 +614,7 @@ cudaError_t launch_kv_weights_i4(const uint16_t* q, long long q_stride, int T, i
   float* part = static_cast<float*>(workspace);
   int4* begun = reinterpret_cast<int4*>(part + (size_t)ctas * 2 * kUnit);
   Args a{T, Hq, Hkv, G, log2, tokens, heads, G > kRows, fast_div(heads), (int)pages, ps / kKvBlock, fast_div(ps / kKvBlock), table, width,
-         width * ps, cu, kv_lens, B, scale * kLog2e, lse, weights, begun,
+         width * ps, cu, kv_lens, B, scale, lse, weights, begun,
          reinterpret_cast<int*>(begun + ctas), part, dev_err};
   // From a full step of rows per sequence on, weights are most of the work and two groups add them up, below it the conversion does
   // (one group that adds up / two: 32 tokens over 32768 24.7 / 24.0 us, prompts 271 / 192, 64 single tokens 77 / 94).
