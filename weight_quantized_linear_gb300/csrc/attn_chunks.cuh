@@ -29,7 +29,6 @@ struct StepArgs {
   __half* out;
   float* lse;
   ChunkParts parts;
-  bool second;  // runs behind the kernel for the other sequences, which waits for what came before
   unsigned* err;
 };
 constexpr int kFewRows = 16;

@@ -1028,7 +1028,7 @@ cudaError_t launch_attn_chunks_i4(const uint16_t* q, long long q_stride, int T, 
                width * ps, scale_log2, scale < 0.f ? 1u << 13 : 0u, j.out, lse, j.parts, few, dev_err};
   const StepArgs sa{reinterpret_cast<const __half*>(q), q_stride, cu, kv_lens, B, T, Hq, Hkv, G, few, cache, (int)pages,
                     fast_div(ps / kKvBlock), table, width, width * ps, scale < 0.f ? -scale_log2 : scale_log2, j.out, lse, j.few,
-                    others, dev_err};
+                    dev_err};
   const CUtensorMap* tiles = others ? &tq : nullptr;
   const StepArgs* steps = few ? &sa : nullptr;
   return D == 128 ? launch<128>(tiles, a, steps, j, s) : launch<64>(tiles, a, steps, j, s);

@@ -133,10 +133,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_steps_i4_kernel(
 
   for (int i = tid; i < 2 * kW * kS; i += C::kThreads) mbar_init(&bars[i], 1);
   fence_mbarrier_init();
-  // Everything before this line overlaps the end of the preceding kernel.  If that is the one for the other sequences, it began
-  // the launch of this one when all before it was complete, and the two work on different rows: this one need not wait for its end
-  // now, only before its own, which the joining kernel waits for.
-  if (!a.second) grid_dependency_wait();
+  // Everything before this line overlaps the end of the preceding kernel.  Nothing is read before it, also where that is the kernel
+  // for the other sequences: that it waited for what came before does not make it visible here.
+  grid_dependency_wait();
   grid_dependents_launch();
 
   // ---- this CTA's range [n0, n1) of the order of all steps; warp w's run is [run(w), run(w + 1)) ----
@@ -179,7 +178,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_steps_i4_kernel(
   }
   if (n0 >= n1) {
     if (tid == 0) a.parts.begun[blockIdx.x] = make_int4(0, 0, 0, 0), a.parts.went_on[blockIdx.x] = 0;
-    grid_dependency_wait();
     return;
   }
   const long long each = (n1 - n0 + kW - 1) / kW;
@@ -530,7 +528,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_steps_i4_kernel(
     a.parts.begun[blockIdx.x] = begun;
     a.parts.went_on[blockIdx.x] = chains & 1u ? (ends_f ? 2 : 1) : 0;
   }
-  grid_dependency_wait();
   if (chains == 0) return;
   float4* fac = reinterpret_cast<float4*>(smem + C::kOffFac);
   for (int i = tid; i < 2 * kW * C::kRows; i += C::kThreads) {
