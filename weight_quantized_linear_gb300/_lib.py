@@ -822,6 +822,8 @@ def kv_evict_i4(weights: torch.Tensor, cache: torch.Tensor, block_table: torch.T
             _refuse(t, name, dtype, shape, index)
     if budget < 1 or budget > new_width * ps:
         raise ValueError(f"budget must be between 1 and new_table's width * page size, {new_width * ps}")
+    if recent < 0:
+        raise ValueError(f"recent must be >= 0, got {recent}")
     if kept is None:
         kept = torch.empty((B, H, budget), dtype=i32, device=dev)
     elif not _is(kept, i32, (B, H, budget), index):
@@ -835,6 +837,6 @@ def kv_evict_i4(weights: torch.Tensor, cache: torch.Tensor, block_table: torch.T
     elif not _is(new_lens, i32, (B,), index):
         _refuse(new_lens, "new_lens", i32, (B,), index)
     _run("wql_kv_evict_i4", index, weights.data_ptr(), cache.data_ptr(), pages, ps, H, D, block_table.data_ptr(), width,
-         kv_lens.data_ptr(), B, new_table.data_ptr(), new_width, budget, recent, kept.data_ptr(), new_weights.data_ptr(),
-         new_lens.data_ptr())
+         kv_lens.data_ptr(), B, new_table.data_ptr(), new_width, budget, min(recent, budget), kept.data_ptr(),
+         new_weights.data_ptr(), new_lens.data_ptr())
     return kept, new_weights, new_lens
