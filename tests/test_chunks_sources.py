@@ -35,3 +35,11 @@ def test_kernels_wait_for_what_came_before_them_on_every_path(name, count):
         assert re.search(r"(^|[;}])\s*$", before), (kernel, "the wait is on one path only")
         # nothing that an argument points to is read before it (the pointers themselves are parameters)
         assert not re.search(r"\ba\.[\w.]+\s*\[|chunk\(|__ldg|tma_load|bulk_load|->", before), kernel
+
+
+def test_rings_that_groups_use_in_turn_are_asserted_to_go_round_with_them():
+    # a group that sees every other phase of a slot's barrier can take an old one for the next: each such ring says why it cannot
+    chunks, weights = source("attn_chunks_i4.cu"), source("kv_weights_i4.cu")
+    for text, ring in ((chunks, r"kRaw % 2 == 0"), (chunks, r"kSlots % 2 == 0"), (weights, r"kKeySlots % kConv == 0"), (weights, r"2 % kConv == 0"),
+                       (weights, r"2 % kSoft == 0")):
+        assert re.search(r"static_assert\([^;]*" + ring, text), ring

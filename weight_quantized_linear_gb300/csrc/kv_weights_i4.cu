@@ -50,6 +50,10 @@ struct Cfg {
   static constexpr int kCodes = kUnit * KvI4<D>::kRow;                // K's codes of a unit,
   static constexpr int kKeyBytes = kCodes + kUnit / kKvBlock * 128;   // with the parameters of K and V
   static constexpr int kKeySlots = 6, kRowSlots = 4;
+  // Groups that take turns meet every phase of a barrier only if turns and slots go round together; else one could take an old
+  // phase for the next.  Rows' slots are waited for by warps that take them all.
+  static_assert(kKeySlots % kConv == 0 && 2 % kConv == 0, "key slots, and keys in tensor memory: one converting group's each");
+  static_assert(2 % kSoft == 0, "the two places for scores: one adding group's each");
   static constexpr int kRowBytes = kRows * D * 2, kBox = kRows * 128;  // a tile of q, its boxes of 64 channels
   static constexpr int kSmem = kRowSlots * kRowBytes + kKeySlots * kKeyBytes + 1024;
   static_assert(kSmem <= 224 * 1024, "shared memory");
