@@ -34,10 +34,4 @@ struct StepArgs {
 constexpr int kFewRows = 16;
 cudaError_t launch_attn_steps_i4(const StepArgs& a, int D, int ctas, cudaStream_t s);
 
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 }  // namespace wql

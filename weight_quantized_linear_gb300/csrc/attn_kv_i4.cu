@@ -54,9 +54,9 @@
 #include <climits>
 #include <type_traits>
 
+#include "attn.cuh"
 #include "internal.h"
 #include "kv_i4.cuh"
-#include "tcgen05.cuh"
 
 namespace wql {
 namespace {
@@ -88,30 +88,10 @@ struct Cfg {
   static constexpr int kSmem = kOffBar + 2 * kWarps * kStages * 8;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
-  uint32_t d;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-  return d;
-}
 // (a & b) ^ c in one instruction, b and c in registers.
 __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
@@ -125,16 +105,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 __device__ __forceinline__ float2 h2f2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
-
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 
 // A flag with any other value says that the part is not there, so the workspace may hold anything before a call.
 constexpr unsigned long long kThere = 0x9d6b2f81c35ae704ull;
@@ -220,14 +190,6 @@ __device__ __forceinline__ bool no_codes(const uint8_t* row) {
     any |= x.x | x.y | x.z | x.w;
   }
   return any == 0;
-}
-
-// The token (of 16) that row r of an 8 x 8 block of weights stands for; K's rows, V's reduction index and the
-// params all use it.  Chosen so that the shared-memory loads of K and V hit every bank once.
-template <int D>
-__device__ __forceinline__ int token_of(int r) {
-  const int c = r >> 1, e = r & 1;
-  return 2 * c + (e ^ (D == 128 ? (c & 1) : (c >> 1)));
 }
 
 template <int D, int NT, bool kTwin>

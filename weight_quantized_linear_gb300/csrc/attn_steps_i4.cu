@@ -57,25 +57,11 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
-  uint32_t d;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-  return d;
-}
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 __device__ __forceinline__ KvChunk chunk(const StepArgs& a, int b, unsigned* err = nullptr) {
@@ -105,13 +91,6 @@ __device__ __forceinline__ void advance(const StepArgs& a, Cursor& c, int by) {
       } while (c.n == 0);
     }
   }
-}
-
-// The key (of 16) that row r of a product stands for, chosen so that the loads of K and V hit every bank once.
-template <int D>
-__device__ __forceinline__ int key_of(int r) {
-  const int c = r >> 1, e = r & 1;
-  return 2 * c + (e ^ (D == 128 ? (c & 1) : (c >> 1)));
 }
 
 template <int D, int NT>
@@ -257,8 +236,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_steps_i4_kernel(
     long long at = run(warp);
     const long long r1 = run(warp + 1);
     const float cs = a.scale_log2;
-    const int tok = key_of<D>(g);  // this thread's keys in scores: tok and tok + 8; in values: two neighbours, and those + 8
-    const bool swap = key_of<D>(2 * c) & 1;
+    const int tok = token_of<D>(g);  // this thread's keys in scores: tok and tok + 8; in values: two neighbours, and those + 8
+    const bool swap = token_of<D>(2 * c) & 1;
     const uint32_t sel_s = swap ? 0x1054u : 0x5410u, sel_lo = swap ? 0x3276u : 0x7632u;
     Cursor u = at < r1 ? s_start[warp] : Cursor{0, 0, 0, 0};
     while (at < r1) {
@@ -386,8 +365,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_steps_i4_kernel(
           uint32_t xv[2][2][D / 64], s2[2], lo2[2];
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            const uint8_t* r0 = blk + L::kV + (key_of<D>(2 * c) + 8 * hh) * L::kRow;
-            const uint8_t* r1 = blk + L::kV + (key_of<D>(2 * c + 1) + 8 * hh) * L::kRow;
+            const uint8_t* r0 = blk + L::kV + (token_of<D>(2 * c) + 8 * hh) * L::kRow;
+            const uint8_t* r1 = blk + L::kV + (token_of<D>(2 * c + 1) + 8 * hh) * L::kRow;
             if constexpr (D == 128) {
               const uint2 p = *reinterpret_cast<const uint2*>(r0 + 8 * g), q = *reinterpret_cast<const uint2*>(r1 + 8 * g);
               xv[0][hh][0] = prmt(p.x, q.x, 0x5410u), xv[0][hh][1] = prmt(p.x, q.x, 0x7632u);

@@ -34,6 +34,13 @@ __device__ __forceinline__ void kv_values8(uint32_t w, uint32_t s2, uint32_t lo2
   v[2] = hfma2_u32(hadd2_u32(and_or(w8, 0x000f000fu, 0x64006400u), 0xE400E400u), s2, lo2);
   v[3] = hfma2_u32(hfma2_u32(and_or(w8, 0x00f000f0u, 0x64006400u), 0x2C002C00u, 0xD400D400u), s2, lo2);
 }
+// For mma.sync: the token (of 16) that row r of an 8 x 8 block of weights stands for; K's rows, V's reduction index and the
+// params all use it.  Chosen so that the shared-memory loads of K and V hit every bank once.
+template <int D>
+__device__ __forceinline__ int token_of(int r) {
+  const int c = r >> 1, e = r & 1;
+  return 2 * c + (e ^ (D == 128 ? (c & 1) : (c >> 1)));
+}
 // A finite row may hold values that round to infinity (its s may have been rounded up); attention over fp16 values takes
 // the largest finite number for them.  What of a row's parameters says that.
 __device__ __forceinline__ bool kv_finite(uint32_t par) { return ((par & 0x7c007c00u) + 0x04000400u & 0x80008000u) == 0; }
