@@ -661,7 +661,11 @@ def attention_kv_i4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
     q [B, Hq, D] (one token each) or [B, Lq, Hq, D] fp16, its tokens evenly strided; block_table [B, width] and
     kv_lens [B] int32, the queried tokens counted in.  Row r of Lq sees the tokens up to kv_lens - Lq + r; a row that
     sees none is zero.  scale defaults to D ** -0.5.  workspace: uint8, attention_kv_i4_workspace_bytes() of them,
-    allocated here if not given.  Returns out, dense, of q's shape."""
+    allocated here if not given.  Returns out, dense, of q's shape.
+
+    The call for decode steps, where every sequence has as many new tokens: a fifth faster for single tokens than
+    attention_chunks_kv_i4, which is for tokens of different number and gives log-sums.  This one takes the cache's values
+    code * s + lo as they are, that one rounds them to fp16: outputs of the two differ by up to 2^-11 of the values."""
     pages, Hkv, ps, D = _cache_dims(cache)
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be a tensor [B, Hq, D] or [B, Lq, Hq, D]")
@@ -749,7 +753,11 @@ def attention_chunks_kv_i4(q: torch.Tensor, cache: torch.Tensor, block_table: to
     kv_lens [B] int32 are what kv_plan_pages returns).  A row sees the tokens up to itself; one that sees none is zero.
     scale defaults to D ** -0.5.  lse: fp32 [T, Hq], filled with the logarithm of each row's sum of exponentials.
     workspace: uint8, attention_chunks_kv_i4_workspace_bytes() of them, allocated here if not given.  Returns out
-    [T, Hq, D], dense; rows of no sequence are left as they were (undefined when out is not given)."""
+    [T, Hq, D], dense; rows of no sequence are left as they were (undefined when out is not given).
+
+    Values of the cache are rounded to fp16, as kv_read_i4 gives them, and so are softmax weights.  Where all sequences have
+    one new token, or as many drafted ones, and no log-sums are wanted, attention_kv_i4 is faster and rounds less.  Rows of no
+    sequence cost time where sequences have a few rows each: keep q as short as its sequences allow."""
     pages, Hkv, ps, index, qs, B, width = _chunk_args(q, cache, block_table, cu_new, kv_lens)
     dev, shape = cache.device, q.shape
     T, Hq, D = shape

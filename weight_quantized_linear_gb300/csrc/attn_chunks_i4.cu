@@ -21,7 +21,8 @@
 // S twice (512 tokens behind 15872: 143 -> 135 us with three raw slots; mixed batch with heads of 64: 128 -> 126).
 //
 // K and V reach the tensor cores by way of eight warps that make fp16 numbers of the codes: bulk copies bring the blocks of
-// 64 tokens as they are into a slot of the group that converts them, a thread takes one key's row there and writes it as a row of a swizzled operand tile.
+// 64 tokens as they are into a slot of the group that converts them, a thread takes one key's row there and writes it as a row of
+// a swizzled operand tile.
 // That is 3.5 instructions per pair of values, done once for the 256 rows of a pair of tiles.
 //
 // The key tiles of all items, one behind the other, are divided evenly over the CTAs, one per SM, whatever the lengths: a CTA finds
@@ -35,11 +36,18 @@
 // products: a tile's softmax 1300, its turn, and 1300 in which its two products hold the tensor cores, since Q K^T and P V read
 // both fp16 operand tiles from shared memory while the converting warps write the next (without the conversion 111 us instead of
 // 136).  With heads of 64 a round takes 3600 for 1024: both softmaxes at once, 1024 of it exponentials.
+// Roundings: weights are fp16 because the second product takes them beside V, which the formula has in fp16 anyway.  Outputs are off
+// by 2.5e-4 of their norm, of which 2.1e-4 is their own rounding.  What the rounding leaves as another operand would leave that
+// alone, for another product as large as P V in a kernel that waits for its products.  The sum is taken of the weights before
+// they are rounded, in fp32; exponential and logarithm to base 2 are the GPU's approximations (2^-22), below what fp32 scores are
+// off.  Measured: log-sums within 4e-6.
 // Measured on GB300 through the Python call, rows of 32 query heads:
-//   512 tokens behind 15872, 8 K/V heads of 128     142 us    950 TFLOP/s, 50 % of the measured peak
-//   4 x 2048 tokens over 2048 to 8190, 32 heads     586 us    940 TFLOP/s
-//   24 requests up to 6000 tokens, three chunks of about 500 among single tokens, 8 K/V heads of 64     102 us
-//   16 tokens behind 700, 32 heads                  14.4 us, launches and latency (attn_steps_i4.cu)
+//   512 tokens behind 15872, 8 K/V heads of 128     142 us    955 TFLOP/s, 50 % of the measured peak
+//   4 x 2048 tokens over 2048 to 8190, 32 heads     580 us    950 TFLOP/s
+//   24 requests up to 6000 tokens, three chunks of about 500 among single tokens, 8 K/V heads of 64     104 us
+//   16 tokens behind 700, 32 heads, in a q of 19 rows     15 us, launches and latency
+// The last of these is a case of the rule at the end of this file: in a q of just its 16 rows the kernel for a few rows takes it,
+// 16.3 us for 14.8 in a graph.
 // What did not pay: the conversion's loop unrolled twice or four times (142 and 150 us for 135, with three raw slots: the warps' code no
 // longer stays in the instruction caches), no turns (163).
 #include <atomic>
@@ -1006,7 +1014,9 @@ cudaError_t launch_attn_chunks_i4(const uint16_t* q, long long q_stride, int T, 
   const int G = Hq / Hkv, tokens = kTile / G, ctas = num_sms();
   // Sequences of a few rows of a K/V head get a kernel of their own, where there may be such: not if all rows are one sequence's and
   // too many.  Up to eight rows if that is what the sequences have on the average, or more than sixteen and so some have many and
-  // others surely few; else, and where a token has more than eight heads, up to sixteen.
+  // others surely few; else, and where a token has more than eight heads, up to sixteen.  The lengths are on the device, so rows of
+  // no sequence count too, and a few sequences are judged by all: 32 x 4 drafted tokens of 4 heads (16 rows) take 35 us with heads
+  // of 64 and 55 with heads of 128, but 76 and 100 in a q of twice as many rows, where they go to 128-row tiles.
   const long long mean = ((long long)T * G + B - 1) / B;
   const int most = G > 8 || (mean > 8 && mean <= kFewRows) ? kFewRows : 8;
   const int few = B > 1 || T <= most / G ? most / G : 0;

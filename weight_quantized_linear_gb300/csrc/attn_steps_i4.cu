@@ -16,12 +16,17 @@
 // Bound by instructions: about 360 per warp and 16 keys of heads of 128 (208 of them masks, subtractions and multiply-adds that
 // make numbers of codes, 16 products), 59 % of the issue slots used, DRAM at half its rate.  mma.sync, not tcgen05: its operands
 // come out of registers, and they use a fifth of its rate.  Measured on GB300 through the Python call, or in a graph (g):
-//   64 single tokens over up to 8192 (290 MB), 32 / 8 heads of 128          76 us, 3.8 TB/s (in 128-row tiles 197)
-//   4 drafted tokens x 32 over up to 6000, 32 / 8 heads of 64 (66 MB)       37 us g (78)
-//   64 single tokens of 16 heads per K/V head of 128 (89 MB)                43 us g (72)
-//   one row of 700 tokens, 32 heads of 128                                  10.7 us g (14.5), latency of two launches
-// attention_kv_i4, which takes all sequences' rows alike, does not round the values and gives no lse, takes 60, 33, 39 and 6.1.
+//   64 single tokens over up to 8192 (290 MB), 32 / 8 heads of 128          76 us, 3.8 TB/s, 75 g (in 128-row tiles 197)
+//   4 drafted tokens x 32 over up to 6000, 32 / 8 heads of 64 (57 MB)       35 us g (76)
+//   64 single tokens over up to 5000 of 16 heads per K/V head of 128 (88 MB)   49 us g
+//   one row of 700 tokens, 32 heads of 128                                  11.6 us g, latency of two launches
+// attention_kv_i4, which takes all sequences' rows alike, does not round the values and gives no lse, takes 59, 32, 40 and 7.5 g.
 // Eight rows where they are enough: with the products for sixteen the first of these takes 100 us.
+//
+// Roundings: weights are fp16, as V is by the formula, sums fp32 of weights before they are rounded.  Outputs are off by 2.6e-4 of
+// their norm, of which 2.1e-4 is their own rounding.  For up to four rows that could be all: the columns that they leave free
+// would take what the weights' rounding leaves, as in attention_kv_i4.  Here that would cost 64 single tokens 78 us for 75 (heads of 64: 58
+// for 57) and, by its branch, eight rows 78 for 77, for an error far below that of values in four bits.
 #include <atomic>
 #include <climits>
 #include <type_traits>

@@ -301,17 +301,26 @@ cudaError_t launch(const Args& a, cudaStream_t s) {
 
 // The table's width, which bounds the lengths, and the number of heads decide.  A head gets as many CTAs as fit the card with those of
 // all heads, two per SM, since a head's search is a chain of latencies and a single CTA moves 16 rows at a time per warp; and
-// registers for all its tokens where it can, else they are read again for each digit.  On GB300, us (threads x tokens of each x CTAs;
-// tokens of a head, half of them kept unless said):
+// registers for all its tokens where it can, else they are read again for each digit.  On GB300, us (threads x tokens of each x CTAs,
+// what the rule takes first; tokens of a head, half of them kept unless said):
 //     32 heads of  1000, 900 kept   512x2x1  9.7   256x4x1 12.4   256x4x4 12.6   512x4x1 10.5
 //      8 heads of  2000             512x4x1 12.8   256x16x1 22.4  512x4x4 13.4
-//      8 heads of  4000             512x4x4 13.5   512x4x8 12.4   256x16x1 25.7    (32 heads: 13.7, 15.9, 25.7)
+//      8 heads of  4000             512x4x4 14.1   512x4x8 13.0   256x16x1 25.7
+//     32 heads of  4000             512x4x4 14.5   512x4x8 16.5   512x4x2 16.6   256x16x1 26.5
 //    128 heads of  4000             512x4x2 23.0   512x4x4 35.4   256x16x1 36.9
-//    512 heads of  4000             256x16x1 78.4  512x4x1 82.5   512x4x2 103.5
+//    160 heads of  4000             256x16x1 41.6  512x4x1 30.5   512x4x2 40.9
+//    256 heads of  4000             256x16x1 49.9  512x4x1 39.9   512x4x2 51.5
+//    512 heads of  4000             256x16x1 78.8  512x4x1 82.4   512x4x2 103.3
 //      8 heads of 16000             512x4x8 17.0   512x16x8 24.0  512x16x2 38.7
-//    128 heads of 16000, 4000 kept  512x16x2 52.4  512x16x4 73.1  512x16x8 112.5
+//    128 heads of 16000, 4000 kept  512x16x2 52.4  512x16x4 73.1  512x16x8 112.5  256x16x1 96.2
+//    160 heads of 16000, 4000 kept  256x16x1 108   512x16x2 86.9  512x16x4 96.4   512x16x8 139
+//    256 heads of 16000, 4000 kept  256x16x1 126   512x16x2 108   512x16x4 136
+//    512 heads of 16000, 4000 kept  256x16x1 187   512x16x2 197   512x16x4 259
 //     64 heads of 60000, 8000 kept  512x16x4 71.9  512x16x8 83.2  512x16x2 94.3
+//    160 heads of 60000, 8000 kept  256x16x1 283   512x16x2 209   512x16x4 183
 //      8 heads of 120001, 16384 kept  1024x16x8 34.4  512x16x8 46.6
+// Above 4096 tokens eight CTAs go to a head where they fit, below that four, since 32 heads lose more by eight than 8 heads win.  From 153
+// to some 400 heads the rule's single CTA is not the best: a head with more tokens than its registers hold reads them four times.
 template <int D>
 cudaError_t launch(const Args& a, cudaStream_t s) {
   const long long heads = (long long)a.B * a.H, room = 2LL * num_sms();

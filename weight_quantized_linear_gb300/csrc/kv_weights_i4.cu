@@ -18,9 +18,13 @@
 // brings codes, 2300 cycles per unit, at 31 % of the memory's rate.  One row of a product is one weight in one lane, so nothing is
 // exchanged; the first kernel, mma.sync with K in registers, took 38, 81 and 298 us for the figures below.
 // Measured on GB300 through the Python call:
-//   the last 32 tokens over 32768, 32 / 8 heads of 128          24 us, 22 of them the call's own
-//   64 single tokens over up to 8192, 32 / 8 heads of 128       77 us, 2.1 TB/s
-//   whole prompts up to 4099 tokens, 32 / 8 heads of 64        194 us, 384 TFLOP/s
+//   the last 32 tokens over 32768, 32 / 8 heads of 128          24 us, in a graph as well (the call's host time, beside it: 26)
+//   64 single tokens over up to 8192, 32 / 8 heads of 128       78 us, 2.1 TB/s
+//   whole prompts up to 4099 tokens, 32 / 8 heads of 64        194 us, 382 TFLOP/s
+//
+// Roundings: the difference of score and lse is formed in one fp32 operation, the exponential is the GPU's approximation to base 2
+// (2^-22), sums are fp32.  Weights of whole prompts are off by 2e-7 of themselves, as fp32 scores are; an exact exponential would take
+// several times the one operation that bounds this kernel.
 #include <atomic>
 #include <climits>
 #include <type_traits>
