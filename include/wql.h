@@ -469,7 +469,9 @@ wql_status wql_attention_prompt(const uint16_t* q, int64_t q_stride, const uint1
  * no sequence are left as they were.
  * k and v are code * s + lo rounded to fp16, as kv_read_i4 gives them, but never infinite: what rounds to infinity is
  * taken as 65504.  A row of K or V whose parameters are not finite makes the rows that see it NaN.  Sums are fp32, weights
- * fp16: a weight is off by 2^-11 of itself (2^-32 of the row's largest one where it is below 2^-21 of that).  A row
+ * fp16: a weight is off by 2^-11 of itself (2^-32 of the row's largest one where it is below 2^-21 of that).  Tensor cores cut a
+ * product off at the last place of the sum that it is added to: of n tokens with about the same weight that a CTA adds up (a 152nd of
+ * those of all K/V heads and tiles of rows), up to n 2^-24 of the output is lost.  A row
  * depends on nothing behind the last token that it sees.  |scale| <= 2^64.
  * A sequence with a negative start, a negative length or an end beyond T is left out and recorded; a length beyond
  * table_width * page_size is cut there and recorded; a page number out of range among the pages in use is recorded, and
